@@ -515,6 +515,111 @@ zr_status zr_step_noalloc(const zr_bucket* buckets, int nbuckets, int W, int A, 
                           float loss_scale, int64_t t, int32_t* overflow, void* stream);
 
 /* ------------------------------------------------------------------------- */
+/* 4-bit weights and distillation                                              */
+/* ------------------------------------------------------------------------- */
+
+/* A 4-bit forward pass of the model that the step trains, and the loss it starts from: the
+ * fp32 masters (or any matrix) quantised to microscaled 4-bit floating point (MX4), the
+ * products of such matrices, and a distillation loss whose gradient carries the plan's loss
+ * scale into the ring. [P2] 核心技术 (1)-(3) train in a low precision for the products with
+ * fp32 masters and a loss scale; these are the same roles at 4 bits.
+ *
+ * MX4 (OCP Microscaling Formats v1.0, MXFP4): E2M1 values 0, 0.5, 1, 1.5, 2, 3, 4, 6 and
+ * their negatives, one power-of-two scale for 32 neighbours of a row, 2^(byte - 127). A
+ * matrix of rows x cols takes zr_mx4_bytes of device memory, in tiles of 128 rows x 256
+ * columns, row of tiles by row of tiles, 17,408 bytes each:
+ *   128 rows of 128 bytes of codes: the 16 bytes of columns 32j..32j+31 of row r (in the
+ *   tile) at r*128 + (j ^ (r % 8))*16, the lower column of a byte in its low half;
+ *   then the scale byte of (r, j) at (j/4)*512 + (r % 32)*16 + (r/32)*4 + j % 4.
+ * Rows and columns past the matrix hold zero codes and finite scales; zr_mx4_quantize writes
+ * whole tiles. In memory nothing else belongs to the matrix, so it can be kept, copied and
+ * saved as those bytes. */
+#define ZR_MX4_FEW 16 /* tokens up to which zr_mx4_linear needs no buffer for them */
+
+/* Bytes of a rows x cols MX4 matrix (0 for an empty one, -1 for a negative size). */
+int64_t zr_mx4_bytes(int64_t rows, int64_t cols);
+
+/* Quantises x (device, rows x cols of type dt, row stride ldx elements) to q, blocks along
+ * the columns, and to qt, the MX4 form of x transposed (cols x rows), blocks along the rows
+ * of x; either may be NULL, and both come from one read of x.
+ * A block's scale byte is clamp(e - 2, 0, 254), e the biased fp32 exponent of its largest
+ * magnitude; x * 2^(127 - byte) is rounded to the nearest value, ties to the even code,
+ * magnitudes over 6 to 6. With rand (device, 8 random bits per value, row stride ldr bytes)
+ * it is rounded by chance instead: for neighbours low <= |t| < high to high iff
+ * (|t| - low)/(high - low) > (255.5 - rand)/256, and the byte is one higher where the
+ * largest magnitude would lie over 6, so that nothing is clipped and the mean is kept. A
+ * value's random bits are the same for q and qt. A block with a value that is not finite
+ * gets byte 255: all its values are NaN, so that a product of it is, too, and the step's
+ * overflow flag sees it.
+ * Errors: ZR_ERR_INVALID for a bad dtype, negative sizes, ldx or ldr under cols, no output,
+ * null or misaligned pointers; ZR_ERR_UNSUPPORTED past 2^31 patches of 128 x 128. An empty
+ * matrix is a no-op. */
+zr_status zr_mx4_quantize(const void* x, zr_dtype dt, int64_t rows, int64_t cols, int64_t ldx,
+                          const uint8_t* rand, int64_t ldr, void* q, void* qt, void* stream);
+
+/* The values that q stands for, rounded to nearest even to type dt: exact in F32 and BF16;
+ * (but for 2^128, to which the largest fp32 values may be rounded by chance: infinite); in
+ * F16 values past its range become infinite. out: device, rows x cols, row stride ld.
+ * Errors: ZR_ERR_INVALID for a bad dtype, negative sizes, ld under cols, null or misaligned
+ * pointers. */
+zr_status zr_mx4_dequantize(const void* q, int64_t rows, int64_t cols, void* out, zr_dtype dt, int64_t ld,
+                            void* stream);
+
+/* out = A B^T: a an MX4 matrix of M x K, b of N x K, out device M x N of type dt with row
+ * stride ldo. Products and sums in fp32 on the tensor cores, one rounding to dt. K == 0
+ * gives zeros. The three products of a linear layer y = x W^T are
+ * (x, W), then dx = (dy, W transposed) and dW = (dy transposed, x transposed).
+ * Every wait in the kernel is bounded (2 s); one that gives up leaves out undefined and is
+ * reported by zr_mx4_status. The first call on a device sets kernel attributes there; make it
+ * before any stream capture.
+ * Errors: ZR_ERR_INVALID for a bad dtype, negative sizes, ldo under N, null or misaligned
+ * pointers; ZR_ERR_UNSUPPORTED past 2^30 output tiles. */
+zr_status zr_mx4_matmul(const void* a, int64_t M, const void* b, int64_t N, int64_t K, void* out, zr_dtype dt,
+                        int64_t ldo, void* stream);
+
+/* out = MX4(x) W^T for tokens x (device, M x K of type xdt, row stride ldx), quantised to
+ * nearest in the call as zr_mx4_quantize does, multiplied as zr_mx4_matmul does (the fp32 sums of
+ * few tokens may be split over K and joined, in an order that the sizes decide). Up to ZR_MX4_FEW tokens
+ * take one launch that reads the weights once, and xq may be NULL; more of them need xq, a
+ * device buffer of zr_mx4_bytes(M, K), which then holds MX4(x). (Rows of more than about
+ * 300,000 columns need it for few tokens, too.)
+ * Errors: as the two calls; ZR_ERR_INVALID for a missing xq. */
+zr_status zr_mx4_linear(const void* x, zr_dtype xdt, int64_t M, int64_t ldx, const void* w, int64_t N, int64_t K,
+                        void* out, zr_dtype dt, int64_t ldo, void* xq, void* stream);
+
+/* Synchronises `stream` and returns ZR_ERR_TIMEOUT if a product on this device gave up a wait
+ * since the last call (whose outputs are then not valid), ZR_OK otherwise. */
+zr_status zr_mx4_status(void* stream);
+
+#define ZR_DISTILL_MAX_TOP 1024
+
+/* Distillation from a teacher's top logits, forward and backward in one launch. For row t with
+ * student logits z (V of them), teacher entries k = 0..K-1 of column ids[t][k] and logit
+ * teacher[t][k], p = softmax over the kept entries of teacher/temperature and
+ * q = softmax(z/temperature) over all V:
+ *   loss[t]    = weight[t] temperature^2 sum_k p_k (log p_k - log q_ids[k])
+ *   grad[t][v] = weight[t] temperature s (q_v - sum of p_k with ids[k] = v)
+ * with s = grad_scale times the plan's current loss scale (plan NULL: grad_scale), read on the
+ * device, so a captured graph follows it. The gradient leaves in dt, ready for backward and
+ * the ring; one that overflows dt is what the step's flag is for.
+ * An entry with a negative id, or with a teacher logit of -inf, is not kept. A row without
+ * weight or without kept entries has loss 0 and gradient 0, whatever its logits hold. Logits
+ * of -inf have q = 0. A row with NaN or +inf, with every logit -inf, or with an id >= V has
+ * loss and gradient NaN. An id may stand more than once in a row.
+ * logits: device, T x V of type dt, row stride ldz; ids: device, T x K of int32 (int64 with
+ * ids64), teacher: device, T x K of type teacher_dt, both with row stride ldk; weight: device
+ * fp32[T] or NULL (all 1); loss: device fp32[T]; grad: device, T x V of type dt with row stride
+ * ldg, or NULL for the loss alone; grad may be the logits themselves (with ldg = ldz).
+ * Loads are whole 16-byte words, so up to 15 bytes before and after a row are read with it.
+ * Errors: ZR_ERR_INVALID for bad dtypes, T < 0, V < 1, K outside [1, ZR_DISTILL_MAX_TOP], a row
+ * stride under its row, a temperature outside [1e-6, 1e6], a grad_scale that is not finite,
+ * null or misaligned pointers, a gradient that overlaps the logits without being them. */
+zr_status zr_distill_topk(const void* logits, zr_dtype dt, int64_t T, int64_t V, int64_t ldz, const void* ids,
+                          int ids64, const void* teacher, zr_dtype teacher_dt, int K, int64_t ldk,
+                          const float* weight, float temperature, float grad_scale, const zr_plan* plan, float* loss,
+                          void* grad, int64_t ldg, void* stream);
+
+/* ------------------------------------------------------------------------- */
 /* Accounting                                                                 */
 /* ------------------------------------------------------------------------- */
 

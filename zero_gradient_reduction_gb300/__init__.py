@@ -130,6 +130,14 @@ def lib():
                                          ctypes.POINTER(Hyper), ctypes.c_float, i64, vp, vp]),
                 "zr_plan_checkpoint": (st, [vp, vp, ctypes.POINTER(Checkpoint)]),
                 "zr_plan_restore": (st, [vp, ctypes.POINTER(Checkpoint), vp]),
+                "zr_mx4_bytes": (i64, [i64, i64]),
+                "zr_mx4_quantize": (st, [vp, i32, i64, i64, i64, vp, i64, vp, vp, vp]),
+                "zr_mx4_dequantize": (st, [vp, i64, i64, vp, i32, i64, vp]),
+                "zr_mx4_matmul": (st, [vp, i64, vp, i64, i64, vp, i32, i64, vp]),
+                "zr_mx4_linear": (st, [vp, i32, i64, i64, vp, i64, i64, vp, i32, i64, vp, vp]),
+                "zr_mx4_status": (st, [vp]),
+                "zr_distill_topk": (st, [vp, i32, i64, i64, i64, vp, i32, vp, i32, i32, i64, vp, ctypes.c_float,
+                                         ctypes.c_float, vp, vp, vp, i64, vp]),
                 "zr_model_state_bytes": (i64, [i32, i64, i32]),
                 "zr_ring_traffic": (st, [i64, i32, i32, vp, vp, vp, vp]),
                 "zr_status_str": (ctypes.c_char_p, [st]),
@@ -574,7 +582,135 @@ def step_noalloc(buckets: np.ndarray, W: int, A: int, dtype: int, grads: Sequenc
               int(current), ctypes.byref(h), float(loss_scale), int(t), _ptr(overflow), _stream_handle(stream)))
 
 
+# ----------------------------------------------------------------------------- 4-bit weights and distillation
+MX4_FEW, DISTILL_MAX_TOP = 16, 1024
+
+
+def mx4_bytes(rows: int, cols: int) -> int:
+    """Device bytes of a rows x cols microscaled 4-bit matrix (zr_mx4_bytes)."""
+    return int(lib().zr_mx4_bytes(int(rows), int(cols)))
+
+
+def _refuse(message: str):
+    raise ZrError(1, message)
+
+
+def _matrix(t, what: str):
+    """(pointer, rows, cols, row stride, dtype) of a device matrix whose rows are contiguous."""
+    if t.dim() != 2 or not t.is_cuda:
+        _refuse(f"{what} must be a matrix in device memory")
+    rows, cols = t.shape
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
+        _refuse(f"the rows of {what} must be contiguous")
+    if rows <= 1 or ld < cols:  # a stride that is never taken may be anything
+        if rows > 1:
+            _refuse(f"the rows of {what} overlap")
+        ld = cols
+    return t.data_ptr(), rows, cols, ld, _dt_of(t)
+
+
+class Mx4:
+    """A rows x cols matrix in microscaled 4-bit floating point: its bytes in `data` (layout in include/zr.h)."""
+
+    __slots__ = ("rows", "cols", "data")
+
+    def __init__(self, rows: int, cols: int, data=None, device="cuda"):
+        import torch
+        self.rows, self.cols = int(rows), int(cols)
+        if self.rows < 0 or self.cols < 0:
+            _refuse("Mx4: negative size")
+        need = -(-self.rows // 128) * -(-self.cols // 256) * 17408
+        if data is None:
+            data = torch.empty(need, dtype=torch.uint8, device=device)
+        elif data.dtype != torch.uint8 or data.numel() < need or not data.is_contiguous() or not data.is_cuda:
+            _refuse(f"Mx4: data must be {need} contiguous bytes in device memory")
+        self.data = data
+
+
+def mx4_quantize(x, q: Optional[Mx4] = None, q_t: Optional[Mx4] = None, rand=None, stream=None) -> None:
+    """Quantises matrix x to q, and its transpose to q_t (zr_mx4_quantize); `rand`: uint8 random bits of x's shape
+    for rounding by chance."""
+    p, rows, cols, ld, dt = _matrix(x, "x")
+    if q is not None and (q.rows, q.cols) != (rows, cols):
+        _refuse(f"mx4_quantize: q is {q.rows} x {q.cols}, x {rows} x {cols}")
+    if q_t is not None and (q_t.rows, q_t.cols) != (cols, rows):
+        _refuse(f"mx4_quantize: q_t is {q_t.rows} x {q_t.cols}, x {rows} x {cols}")
+    rp, ldr = None, 0
+    if rand is not None:
+        if rand.element_size() != 1 or rand.shape != x.shape or not rand.is_cuda:
+            _refuse("mx4_quantize: rand must be bytes of x's shape in device memory")
+        if not rand.is_contiguous():
+            _refuse("mx4_quantize: rand must be contiguous")
+        rp, ldr = rand.data_ptr(), cols
+    _check(lib().zr_mx4_quantize(p, dt, rows, cols, ld, rp, ldr, q.data.data_ptr() if q is not None else None,
+                                 q_t.data.data_ptr() if q_t is not None else None, _stream_handle(stream)))
+
+
+def mx4_dequantize(q: Mx4, out, stream=None) -> None:
+    """out = the values that q stands for (zr_mx4_dequantize)."""
+    p, rows, cols, ld, dt = _matrix(out, "out")
+    if (q.rows, q.cols) != (rows, cols):
+        _refuse(f"mx4_dequantize: q is {q.rows} x {q.cols}, out {rows} x {cols}")
+    _check(lib().zr_mx4_dequantize(q.data.data_ptr(), rows, cols, p, dt, ld, _stream_handle(stream)))
+
+
+def mx4_matmul(a: Mx4, b: Mx4, out, stream=None) -> None:
+    """out[M, N] = a[M, K] b[N, K]^T (zr_mx4_matmul)."""
+    p, rows, cols, ld, dt = _matrix(out, "out")
+    if a.cols != b.cols or (a.rows, b.rows) != (rows, cols):
+        _refuse(f"mx4_matmul: a is {a.rows} x {a.cols}, b {b.rows} x {b.cols}, out {rows} x {cols}")
+    _check(lib().zr_mx4_matmul(a.data.data_ptr(), rows, b.data.data_ptr(), cols, a.cols, p, dt, ld,
+                               _stream_handle(stream)))
+
+
+def mx4_linear(x, w: Mx4, out, xq: Optional[Mx4] = None, stream=None) -> None:
+    """out[M, N] = x[M, K] w[N, K]^T with x quantised in the call (zr_mx4_linear); more than MX4_FEW tokens need xq,
+    a buffer for the quantised x."""
+    p, rows, k, ldx, xdt = _matrix(x, "x")
+    o, m, n, ldo, dt = _matrix(out, "out")
+    if w.cols != k or m != rows or w.rows != n:
+        _refuse(f"mx4_linear: x is {rows} x {k}, w {w.rows} x {w.cols}, out {m} x {n}")
+    if xq is not None and (xq.rows, xq.cols) != (rows, k):
+        _refuse(f"mx4_linear: xq is {xq.rows} x {xq.cols}, x {rows} x {k}")
+    _check(lib().zr_mx4_linear(p, xdt, rows, ldx, w.data.data_ptr(), n, k, o, dt, ldo,
+                               xq.data.data_ptr() if xq is not None else None, _stream_handle(stream)))
+
+
+def mx4_status(stream=None) -> None:
+    """Synchronises the stream and raises if a product gave up a wait since the last call (zr_mx4_status)."""
+    _check(lib().zr_mx4_status(_stream_handle(stream)))
+
+
+def distill_topk(logits, ids, teacher, loss, grad=None, weight=None, temperature: float = 1.0,
+                 grad_scale: float = 1.0, plan: Optional[Plan] = None, stream=None) -> None:
+    """The distillation loss of each row against a teacher's top logits, and its gradient times grad_scale and the
+    plan's loss scale (zr_distill_topk). `grad` may be `logits`."""
+    import torch
+    z, rows, vocab, ldz, dt = _matrix(logits, "logits")
+    t, trows, top, ldk, tdt = _matrix(teacher, "teacher")
+    if ids.dtype not in (torch.int32, torch.int64) or ids.shape != teacher.shape or not ids.is_cuda:
+        _refuse("distill_topk: ids must be int32 or int64 of teacher's shape in device memory")
+    if trows != rows:
+        _refuse(f"distill_topk: {rows} rows of logits, {trows} of the teacher")
+    if not ids.is_contiguous() or ldk != top:
+        _refuse("distill_topk: ids and teacher must be contiguous")
+    for name, v in (("loss", loss), ("weight", weight)):
+        if v is not None and (v.dtype != torch.float32 or v.numel() != rows or not v.is_contiguous() or not v.is_cuda):
+            _refuse(f"distill_topk: {name} must be fp32 [{rows}] in device memory")
+    g, ldg = None, 0
+    if grad is not None:
+        if grad.dtype != logits.dtype or grad.shape != logits.shape:
+            _refuse("distill_topk: grad must have the logits' type and shape")
+        g, _, _, ldg, _ = _matrix(grad, "grad")
+    _check(lib().zr_distill_topk(z, dt, rows, vocab, ldz, ids.data_ptr(), int(ids.dtype == torch.int64), t, tdt, top,
+                                 ldk, weight.data_ptr() if weight is not None else None, float(temperature),
+                                 float(grad_scale), plan.handle if plan is not None else None, loss.data_ptr(), g, ldg,
+                                 _stream_handle(stream)))
+
+
 __all__ = ["lib", "ZrError", "chunk_size", "bucket_plan", "model_state_bytes", "ring_traffic", "reduce_scatter",
            "all_reduce", "adamw_shard_step", "accumulate", "offload_adamw", "all_gather", "AdamW", "Scaler",
            "State", "State1", "Plan", "step_noalloc", "F16", "BF16", "F32", "STAGING_REGISTERS", "STAGING_BULK",
-           "STAGING_BULK_IO"]
+           "STAGING_BULK_IO", "Mx4", "mx4_bytes", "mx4_quantize", "mx4_dequantize", "mx4_matmul", "mx4_linear", "mx4_status",
+           "distill_topk", "MX4_FEW", "DISTILL_MAX_TOP"]

@@ -1,0 +1,597 @@
+// Products of microscaled 4-bit matrices on the tensor cores: out = A B^T with both matrices in
+// MX4 tiles, and the few-token form that takes its tokens in 16 or 32 bits.
+//
+// Rows are the contraction's tiles as zr_mx4_quantize lays them out, so a stage is a handful of
+// one-dimensional bulk copies: 128 rows x 256 columns of codes already in the swizzle that the
+// tensor cores read, and their scales already in the order that one copy takes to tensor memory.
+// Products accumulate in fp32.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "zr_internal.h"
+#include "zr_launch.h"
+#include "zr_mx4.cuh"
+#include "zr_nvtx.h"
+#include "zr_tensor.cuh"
+
+using zr::fail;
+
+namespace {
+
+// Set by a kernel whose wait ran out of time; read and cleared by zr_mx4_status.
+__device__ int g_gave_up;
+
+// ------------------------------------------------------------------ the general product
+// One block per streaming multiprocessor, persistent over output tiles of 128 x BN: a producer
+// warp fills a ring of stages (256 columns of K each), one thread issues the products, four warps
+// bring the accumulators out, 32 lanes each.
+constexpr int kGemmThreads = 192;
+constexpr int kStagePad = 1024;  // the operands' swizzle repeats every 1024 bytes
+
+template <int BN>
+struct Gemm {
+  static constexpr int kB = BN / 128;                                  // MX4 tiles along N
+  static constexpr int kStageBytes = zr::kMxTileBytes * (1 + kB);
+  static constexpr int kStages = BN == 256 ? 4 : 6;
+  // accumulators: two of BN columns; at BN = 256 they share 24 columns, or the scales would find
+  // no room in the 512. The shared ones are read first.
+  static constexpr int kD1 = BN == 256 ? 232 : 128;
+  static constexpr int kLag = BN == 256 ? 1 : 2;  // an accumulator waits for the one so many turns before it
+  static constexpr int kScaleA = BN == 256 ? 488 : 256, kScaleB = kScaleA + 8;
+  static constexpr int kStageOut = 32 * 144;                           // an epilogue warp's rows on their way out
+  static constexpr int kSmem = kStages * kStageBytes + 4 * kStageOut + 256 + kStagePad;
+};
+
+struct GemmArgs {
+  const uint8_t* a;
+  const uint8_t* b;
+  void* out;
+  int64_t M, N, ldo;
+  int kt;          // tiles of 256 along K
+  int mt, nt;      // output tiles
+  int vec;         // rows of out are 16-byte aligned
+};
+
+// Output tile of a number: groups of up to 32 tiles of rows, and within a group the rows first, so
+// that the blocks at work at one time share few tiles of B and a band of A.
+__device__ __forceinline__ void tile_of(const GemmArgs& g, int id, int& m, int& n) {
+  constexpr int kBand = 32;
+  const int per = kBand * g.nt, band = id / per, at = id - band * per;
+  const int rows = min(kBand, g.mt - band * kBand);
+  n = at / rows;
+  m = band * kBand + (at - n * rows);
+}
+
+// The values of 128 bytes of a row, out of registers, through this warp's staging rows, to memory.
+template <int DT>
+__device__ __forceinline__ void rows_out(const GemmArgs& g, char* stage, const uint32_t* v, int64_t row0, int64_t col) {
+  constexpr int es = DT == zr::DT_F32 ? 4 : 2, kCols = 128 / es;
+  const int lane = threadIdx.x & 31;
+  uint4* mine = reinterpret_cast<uint4*>(stage + lane * 144);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (DT == zr::DT_F32) {
+      mine[j] = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    } else {
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[8 * j + i]);
+      mine[j] = zr::pack8<DT == zr::DT_F32 ? zr::DT_BF16 : DT>(f);
+    }
+  }
+  __syncwarp();
+  char* out = static_cast<char*>(g.out);
+  if (g.vec && col + kCols <= g.N) {
+    const int r = lane >> 3, c = lane & 7;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t row = row0 + i * 4 + r;
+      if (row < g.M)
+        *reinterpret_cast<uint4*>(out + (row * g.ldo + col) * es + c * 16) =
+            *reinterpret_cast<const uint4*>(stage + (i * 4 + r) * 144 + c * 16);
+    }
+  } else {
+    const int rows = (int)(g.M - row0 < 32 ? g.M - row0 : 32);
+    for (int r = 0; r < rows; ++r)
+#pragma unroll
+      for (int c = lane; c < kCols; c += 32)
+        if (col + c < g.N) {
+          char* to = out + ((row0 + r) * g.ldo + col + c) * es;
+          if (DT == zr::DT_F32)
+            *reinterpret_cast<float*>(to) = *reinterpret_cast<const float*>(stage + r * 144 + c * 4);
+          else
+            *reinterpret_cast<uint16_t*>(to) = *reinterpret_cast<const uint16_t*>(stage + r * 144 + c * 2);
+        }
+  }
+  __syncwarp();
+}
+
+template <int BN, int DT>
+__global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_constant__ GemmArgs g) {
+  using G = Gemm<BN>;
+  extern __shared__ char smem_raw[];
+  char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + kStagePad - 1) & ~(uintptr_t)(kStagePad - 1));
+  const uint32_t stages = zr::smem_u32(smem);
+  char* staging = smem + G::kStages * G::kStageBytes;
+  char* tail = staging + 4 * G::kStageOut;
+  const uint32_t full = zr::smem_u32(tail), empty = full + 8 * G::kStages, done = empty + 8 * G::kStages,
+                 freed = done + 16, drained = freed + 16;
+  volatile int* gave_up = reinterpret_cast<volatile int*>(tail + 192);
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(tail + 200);
+  const int warp = threadIdx.x >> 5;
+
+  if (warp == 0) {
+    zr::tmem_alloc(zr::smem_u32(tmem_at), 512);
+  } else if (threadIdx.x == 32) {
+    for (int s = 0; s < G::kStages; ++s) {
+      zr::bar_init(full + 8 * s, 1);
+      zr::bar_init(empty + 8 * s, 1);
+    }
+    for (int d = 0; d < 2; ++d) {
+      zr::bar_init(done + 8 * d, 1);
+      zr::bar_init(freed + 8 * d, 4);
+    }
+    zr::bar_init(drained, 1);
+    zr::bar_init_fence();
+    *gave_up = 0;
+  }
+  zr::tmem_fence_before();
+  __syncthreads();
+  zr::tmem_fence_after();
+  const uint32_t tmem = *tmem_at;
+  const int tiles = g.mt * g.nt;
+  const int64_t row_bytes = (int64_t)g.kt * zr::kMxTileBytes;  // a row of tiles
+
+  if (warp == 0) {
+    if (zr::elect_one()) {
+      uint32_t it = 0;
+      bool ok = true;
+      for (int id = blockIdx.x; id < tiles && ok; id += gridDim.x) {
+        int m, n;
+        tile_of(g, id, m, n);
+        const uint8_t* a = g.a + m * row_bytes;
+        const uint8_t* b = g.b + (int64_t)n * G::kB * row_bytes;
+        // the last tile of B may reach past its rows: what is missing is not read
+        const bool two = G::kB == 2 && ((int64_t)n * BN + 128 < g.N);
+        const uint32_t bytes = zr::kMxTileBytes * (two ? 3 : 2);
+        for (int k = 0; k < g.kt; ++k, ++it) {
+          const int s = it % G::kStages;
+          if (it >= G::kStages && !(ok = zr::bar_wait(empty + 8 * s, (it / G::kStages - 1) & 1, gave_up))) break;
+          const uint32_t at = stages + s * G::kStageBytes, bar = full + 8 * s;
+          zr::bar_expect(bar, bytes);
+          zr::bulk_copy(at, a + (int64_t)k * zr::kMxTileBytes, zr::kMxTileBytes, bar);
+          const uint8_t* b0 = b + (int64_t)k * zr::kMxTileBytes;
+          const uint32_t bs = at + zr::kMxTileBytes;
+          if (G::kB == 1) {
+            zr::bulk_copy(bs, b0, zr::kMxTileBytes, bar);
+          } else {  // the codes of both tiles first, so that they are one operand of 256 rows
+            zr::bulk_copy(bs, b0, zr::kMxCodeBytes, bar);
+            zr::bulk_copy(bs + 2 * zr::kMxCodeBytes, b0 + zr::kMxCodeBytes, zr::kMxScaleBytes, bar);
+            if (two) {
+              zr::bulk_copy(bs + zr::kMxCodeBytes, b0 + row_bytes, zr::kMxCodeBytes, bar);
+              zr::bulk_copy(bs + 2 * zr::kMxCodeBytes + zr::kMxScaleBytes, b0 + row_bytes + zr::kMxCodeBytes,
+                            zr::kMxScaleBytes, bar);
+            }
+          }
+        }
+      }
+      // nothing may be in flight to this block's shared memory when it ends
+      int never = 0;
+      for (uint32_t i = it < G::kStages ? 0 : it - G::kStages; i < it; ++i)
+        zr::bar_wait(full + 8 * (i % G::kStages), (i / G::kStages) & 1, &never);
+    }
+  } else if (warp == 1) {
+    if (zr::elect_one()) {
+      uint32_t it = 0, turn = 0;
+      bool ok = true;
+      for (int id = blockIdx.x; id < tiles && ok; id += gridDim.x, ++turn) {
+        int m, n;
+        tile_of(g, id, m, n);
+        const bool two = G::kB == 2 && ((int64_t)n * BN + 128 < g.N);
+        const int cols = G::kB == 2 && !two ? 128 : BN;
+        const uint32_t d = tmem + (turn & 1) * G::kD1;
+        // the columns that it shares with the one before have been read, and all of the one before that
+        const uint32_t past = turn - G::kLag;
+        if (turn >= G::kLag && !(ok = zr::bar_wait(freed + 8 * (past & 1), (past >> 1) & 1, gave_up))) break;
+        zr::tmem_fence_after();
+        for (int k = 0; k < g.kt; ++k, ++it) {
+          const int s = it % G::kStages;
+          if (!(ok = zr::bar_wait(full + 8 * s, (it / G::kStages) & 1, gave_up))) break;
+          zr::tmem_fence_after();
+          const uint32_t at = stages + s * G::kStageBytes, bs = at + zr::kMxTileBytes;
+          const uint32_t as = at + zr::kMxCodeBytes, bss = bs + G::kB * zr::kMxCodeBytes;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            zr::copy_scales(tmem + G::kScaleA + 4 * h, zr::scale_rows(as + 512 * h));
+            for (int t = 0; t < (two ? 2 : 1); ++t)
+              zr::copy_scales(tmem + G::kScaleB + 4 * (G::kB * h + t), zr::scale_rows(bss + t * zr::kMxScaleBytes + 512 * h));
+          }
+          const uint64_t da = zr::swizzled_operand(at), db = zr::swizzled_operand(bs);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)  // 64 columns, 32 bytes of each row, at a time
+            zr::mx_mma(d, da + 2 * q, db + 2 * q, zr::mx_product(128, cols, q & 1), tmem + G::kScaleA + 4 * (q >> 1),
+                       tmem + G::kScaleB + 4 * G::kB * (q >> 1), (k | q) != 0);
+          zr::mma_commit(empty + 8 * s);
+        }
+        if (ok) zr::mma_commit(done + 8 * (turn & 1));
+      }
+      if (!ok) {  // no product may be in flight when the tensor memory is given back
+        int never = 0;
+        zr::mma_commit(drained);
+        zr::bar_wait(drained, 0, &never);
+      }
+    }
+  } else {
+    const int lanes = (warp & 3) * 32;  // the lanes of tensor memory that this warp may read
+    char* stage = staging + (warp & 3) * G::kStageOut;
+    constexpr int kOnce = DT == zr::DT_F32 ? 32 : 64, kChunks = BN / kOnce;
+    uint32_t turn = 0;
+    for (int id = blockIdx.x; id < tiles; id += gridDim.x, ++turn) {
+      int m, n;
+      tile_of(g, id, m, n);
+      if (!__all_sync(0xFFFFFFFFu, zr::bar_wait(done + 8 * (turn & 1), (turn >> 1) & 1, gave_up))) break;
+      zr::tmem_fence_after();
+      const uint32_t d = tmem + (turn & 1) * G::kD1 + ((uint32_t)lanes << 16);
+      const int64_t row0 = (int64_t)m * 128 + lanes;
+#pragma unroll 1
+      for (int c = 0; c < kChunks; ++c) {
+        // the first accumulator's last columns are the second's first
+        const int at = (turn & 1) ? c : kChunks - 1 - c;
+        const int64_t col = (int64_t)n * BN + at * kOnce;
+        uint32_t v[kOnce];
+        zr::tmem_load32(d + at * kOnce, *reinterpret_cast<uint32_t(*)[32]>(v));
+        if (kOnce == 64) zr::tmem_load32(d + at * kOnce + 32, *reinterpret_cast<uint32_t(*)[32]>(v + kOnce - 32));
+        if (c == (BN == 256 ? 0 : kChunks - 1)) {
+          zr::tmem_fence_before();
+          __syncwarp();
+          if (zr::elect_one()) zr::bar_arrive(freed + 8 * (turn & 1));
+        }
+        if (row0 < g.M && col < g.N) rows_out<DT>(g, stage, v, row0, col);
+      }
+    }
+  }
+  __syncwarp();
+  zr::tmem_fence_before();
+  __syncthreads();
+  zr::tmem_fence_after();
+  if (threadIdx.x == 0 && *gave_up) g_gave_up = 1;
+  if (warp == 0) zr::tmem_free(tmem, 512);
+}
+
+// ------------------------------------------------------------------ the few-token form
+// The weights are the operand with 128 rows, the tokens the one with 16 columns. A block takes
+// 128 outputs and, in a cluster of S blocks, 1/S of K: it starts its weight copies, quantises its
+// part of the tokens into shared memory meanwhile, and multiplies as the stages arrive. The
+// cluster's partial results are added in the order of its blocks.
+constexpr int kFewTokens = ZR_MX4_FEW, kFewThreads = 256, kFewStages = 5;
+constexpr int kXTileBytes = 3072;  // a 256-column piece of 16 tokens: 2048 of codes, 1024 of scales
+constexpr int kFewTail = 256;
+
+struct FewArgs {
+  const void* x;
+  const uint8_t* w;
+  void* out;
+  int64_t M, K, N, ldx, ldo;
+  int kt, xdt, odt;
+};
+
+__host__ __device__ constexpr int few_smem(int k_tiles) {
+  return kFewStages * zr::kMxTileBytes + k_tiles * kXTileBytes + kFewTail + kStagePad;
+}
+
+// 32 values of a row from column c on as fp32; zeros from column K on.
+__device__ __forceinline__ void load32(const void* x, int dt, int64_t e, int64_t left, float v[32]) {
+  if (left >= 32) {
+    if (dt == zr::DT_F32) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint4 u = zr::load16(reinterpret_cast<const char*>(static_cast<const float*>(x) + e + 4 * i));
+        v[4 * i] = __uint_as_float(u.x);
+        v[4 * i + 1] = __uint_as_float(u.y);
+        v[4 * i + 2] = __uint_as_float(u.z);
+        v[4 * i + 3] = __uint_as_float(u.w);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 u = zr::load16(reinterpret_cast<const char*>(static_cast<const uint16_t*>(x) + e + 8 * i));
+        if (dt == zr::DT_BF16)
+          zr::unpack8<zr::DT_BF16>(u, v + 8 * i);
+        else
+          zr::unpack8<zr::DT_F16>(u, v + 8 * i);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      v[i] = 0.0f;
+      if (i < left)
+        v[i] = dt == zr::DT_F32    ? zr::load1<zr::DT_F32>(x, e + i)
+               : dt == zr::DT_BF16 ? zr::load1<zr::DT_BF16>(x, e + i)
+                                   : zr::load1<zr::DT_F16>(x, e + i);
+    }
+  }
+}
+
+__device__ __forceinline__ void store_as(void* out, int dt, int64_t i, float v) {
+  if (dt == zr::DT_F32)
+    static_cast<float*>(out)[i] = v;
+  else
+    static_cast<uint16_t*>(out)[i] = dt == zr::DT_BF16 ? zr::from_f32<zr::DT_BF16>(v) : zr::from_f32<zr::DT_F16>(v);
+}
+
+template <int S>
+__global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant__ FewArgs g) {
+  extern __shared__ char smem_raw[];
+  char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + kStagePad - 1) & ~(uintptr_t)(kStagePad - 1));
+  const int n = blockIdx.x / S, rank = S > 1 ? (int)zr::cluster_rank() : 0;
+  const int k0 = (int)((int64_t)g.kt * rank / S), nk = (int)((int64_t)g.kt * (rank + 1) / S) - k0;
+  const int k_most = (g.kt + S - 1) / S;
+  char* xq = smem + kFewStages * zr::kMxTileBytes;
+  char* tail = xq + k_most * kXTileBytes;
+  const uint32_t stages = zr::smem_u32(smem), xs = zr::smem_u32(xq);
+  const uint32_t full = zr::smem_u32(tail), empty = full + 8 * kFewStages, done = empty + 8 * kFewStages;
+  volatile int* gave_up = reinterpret_cast<volatile int*>(tail + 192);
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(tail + 200);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint8_t* w = g.w + ((int64_t)n * g.kt + k0) * zr::kMxTileBytes;
+
+  if (warp == 0) {
+    zr::tmem_alloc(zr::smem_u32(tmem_at), 32);
+  } else if (warp == 5 && lane == 0) {
+    for (int s = 0; s < kFewStages; ++s) {
+      zr::bar_init(full + 8 * s, 1);
+      zr::bar_init(empty + 8 * s, 1);
+    }
+    zr::bar_init(done, 1);
+    zr::bar_init_fence();
+    zr::proxy_fence();
+    *gave_up = 0;
+    for (int k = 0; k < nk && k < kFewStages; ++k) {
+      zr::bar_expect(full + 8 * k, zr::kMxTileBytes);
+      zr::bulk_copy(stages + k * zr::kMxTileBytes, w + (int64_t)k * zr::kMxTileBytes, zr::kMxTileBytes, full + 8 * k);
+    }
+  }
+  __syncwarp();
+  // tokens beyond M are left as they are: what they give is not stored
+  const int blocks = nk * 8;
+  for (int t = threadIdx.x; t < blocks * (int)g.M; t += kFewThreads) {
+    const int r = t / blocks, b = t - r * blocks, j = b & 7;
+    const int64_t c = ((int64_t)k0 * 8 + b) * 32;
+    float v[32];
+    load32(g.x, g.xdt, r * g.ldx + c, g.K - c, v);
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    const int byte = zr::mx_scale_byte<false>(m);
+    uint32_t o[4] = {0, 0, 0, 0};
+    if (byte != 255) {
+      const float inv = zr::mx_inverse(byte);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = __fmul_rn(v[i], inv);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = zr::mx_codes8(v + 8 * i);
+    }
+    char* piece = xq + (b >> 3) * kXTileBytes;
+    *reinterpret_cast<uint4*>(piece + r * 128 + ((j ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+    piece[2048 + (j >> 2) * 512 + r * 16 + (j & 3)] = (char)byte;
+  }
+  zr::proxy_fence();
+  zr::tmem_fence_before();
+  __syncthreads();
+  zr::tmem_fence_after();
+  const uint32_t tmem = *tmem_at, scale_a = tmem + 16, scale_b = tmem + 24;
+
+  if (warp == 4) {
+    if (zr::elect_one()) {
+      int k = 0;
+      for (; k < nk; ++k) {
+        const int s = k % kFewStages;
+        if (!zr::bar_wait(full + 8 * s, (k / kFewStages) & 1, gave_up)) break;
+        zr::tmem_fence_after();
+        const uint32_t at = stages + s * zr::kMxTileBytes, xt = xs + k * kXTileBytes;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          zr::copy_scales(scale_a + 4 * h, zr::scale_rows(at + zr::kMxCodeBytes + 512 * h));
+          zr::copy_scales(scale_b + 4 * h, zr::scale_rows(xt + 2048 + 512 * h));
+        }
+        const uint64_t da = zr::swizzled_operand(at), db = zr::swizzled_operand(xt);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          zr::mx_mma(tmem, da + 2 * q, db + 2 * q, zr::mx_product(128, 16, q & 1), scale_a + 4 * (q >> 1),
+                     scale_b + 4 * (q >> 1), (k | q) != 0);
+        zr::mma_commit(empty + 8 * s);
+      }
+      zr::mma_commit(done);  // after a wait that gave up too: nothing may be in flight at the end
+    }
+  } else if (warp == 5 && nk > kFewStages) {
+    if (zr::elect_one()) {
+      int k = kFewStages;
+      for (; k < nk; ++k) {
+        const int s = k % kFewStages;
+        if (!zr::bar_wait(empty + 8 * s, (k / kFewStages - 1) & 1, gave_up)) break;
+        zr::bar_expect(full + 8 * s, zr::kMxTileBytes);
+        zr::bulk_copy(stages + s * zr::kMxTileBytes, w + (int64_t)k * zr::kMxTileBytes, zr::kMxTileBytes, full + 8 * s);
+      }
+      int never = 0;
+      for (int i = k - kFewStages; i < k; ++i) zr::bar_wait(full + 8 * (i % kFewStages), (i / kFewStages) & 1, &never);
+    }
+  }
+  __syncwarp();
+
+  float* part = reinterpret_cast<float*>(smem);  // [token][128], over the stages once they are used up
+  if (warp < 4) {
+    uint32_t v[16];
+    const bool ok = __all_sync(0xFFFFFFFFu, zr::bar_wait(done, 0, gave_up));
+    zr::tmem_fence_after();
+    if (ok) {
+      zr::tmem_load16(tmem + ((uint32_t)(warp * 32) << 16), v);
+      const int64_t col = (int64_t)n * 128 + warp * 32 + lane;
+#pragma unroll
+      for (int t = 0; t < kFewTokens; ++t)
+        if (t < g.M) {
+          if (S > 1)
+            part[t * 128 + warp * 32 + lane] = __uint_as_float(v[t]);
+          else if (col < g.N)
+            store_as(g.out, g.odt, t * g.ldo + col, __uint_as_float(v[t]));
+        }
+    }
+    zr::tmem_fence_before();
+  }
+  __syncwarp();
+  if (S > 1) {
+    zr::cluster_sync();
+    constexpr int kShare = 128 / S;
+    for (int e = threadIdx.x; e < (int)g.M * kShare; e += kFewThreads) {
+      const int t = e / kShare, c = rank * kShare + e % kShare;
+      const uint32_t at = zr::smem_u32(part + t * 128 + c);
+      float sum = 0.0f;
+#pragma unroll
+      for (int r = 0; r < S; ++r) {
+        const float p = zr::cluster_load(zr::cluster_addr(at, r));
+        sum = r ? sum + p : p;
+      }
+      const int64_t col = (int64_t)n * 128 + c;
+      if (col < g.N) store_as(g.out, g.odt, t * g.ldo + col, sum);
+    }
+    __syncwarp();
+    zr::cluster_sync();  // a block's shared memory stays until the others have read it
+  } else {
+    __syncthreads();
+  }
+  zr::tmem_fence_after();
+  if (threadIdx.x == 0 && *gave_up) g_gave_up = 1;
+  if (warp == 0) zr::tmem_free(tmem, 32);
+}
+
+template <int BN, int DT>
+zr_status launch_gemm(const GemmArgs& g, int grid, cudaStream_t s) {
+  static zr::SmemAllowance allowance;
+  if (zr_status st = allowance.allow("zr_mx4_matmul", (const void*)gemm_kernel<BN, DT>, Gemm<BN>::kSmem)) return st;
+  gemm_kernel<BN, DT><<<grid, kGemmThreads, Gemm<BN>::kSmem, s>>>(g);
+  return zr::launch_status("zr_mx4_matmul");
+}
+
+zr_status matmul(const char* what, const void* a, int64_t M, const void* b, int64_t N, int64_t K, void* out, zr_dtype dt,
+                 int64_t ldo, cudaStream_t s) {
+  const int es = dt == ZR_F32 ? 4 : 2;
+  if (K == 0) {  // a sum of nothing
+    cudaError_t e = cudaMemset2DAsync(out, (size_t)ldo * es, 0, (size_t)N * es, (size_t)M, s);
+    return e == cudaSuccess ? ZR_OK : fail(ZR_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+  }
+  const int sms = zr::sm_count(what);
+  if (sms == 0) return ZR_ERR_CUDA;
+  GemmArgs g{};
+  g.a = static_cast<const uint8_t*>(a);
+  g.b = static_cast<const uint8_t*>(b);
+  g.out = out;
+  g.M = M; g.N = N; g.ldo = ldo;
+  const int64_t mt = zr::mx_tiles(M, 128), kt = zr::mx_tiles(K, zr::kMxCols);
+  const bool wide = mt * zr::mx_tiles(N, 256) >= sms;
+  const int64_t nt = zr::mx_tiles(N, wide ? 256 : 128);
+  if (kt > 0x7FFFFFFF || nt > (1 << 25) || mt > 0x3FFFFFFF / nt)
+    return fail(ZR_ERR_UNSUPPORTED, "%s: the product has too many tiles", what);
+  g.kt = (int)kt; g.mt = (int)mt; g.nt = (int)nt;
+  g.vec = ldo * es % 16 == 0;
+  const int grid = (int)(mt * nt < sms ? mt * nt : sms);
+  if (wide) {
+    if (dt == ZR_F16) return launch_gemm<256, zr::DT_F16>(g, grid, s);
+    if (dt == ZR_BF16) return launch_gemm<256, zr::DT_BF16>(g, grid, s);
+    return launch_gemm<256, zr::DT_F32>(g, grid, s);
+  }
+  if (dt == ZR_F16) return launch_gemm<128, zr::DT_F16>(g, grid, s);
+  if (dt == ZR_BF16) return launch_gemm<128, zr::DT_BF16>(g, grid, s);
+  return launch_gemm<128, zr::DT_F32>(g, grid, s);
+}
+
+template <int S>
+zr_status launch_few(const FewArgs& g, int blocks, int smem, cudaStream_t s) {
+  static zr::SmemAllowance allowance;
+  if (zr_status st = allowance.allow("zr_mx4_linear", (const void*)few_kernel<S>, zr::kSmemMost)) return st;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3((unsigned)blocks);
+  c.blockDim = dim3(kFewThreads);
+  c.dynamicSmemBytes = (size_t)smem;
+  c.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim = {S, 1, 1};
+  c.attrs = &at;
+  c.numAttrs = S > 1 ? 1 : 0;
+  cudaError_t e = cudaLaunchKernelEx(&c, few_kernel<S>, g);
+  if (e != cudaSuccess) return fail(ZR_ERR_CUDA, "zr_mx4_linear: launch failed: %s", cudaGetErrorString(e));
+  return ZR_OK;
+}
+
+}  // namespace
+
+extern "C" zr_status zr_mx4_matmul(const void* a, int64_t M, const void* b, int64_t N, int64_t K, void* out,
+                                   zr_dtype dt, int64_t ldo, void* stream) {
+  zr::clear_error();
+  zr::Range range("zr_mx4_matmul");
+  if (!zr::dtype_ok(dt)) return fail(ZR_ERR_INVALID, "zr_mx4_matmul: bad dtype %d", (int)dt);
+  if (M < 0 || N < 0 || K < 0) return fail(ZR_ERR_INVALID, "zr_mx4_matmul: negative size");
+  if (ldo < N) return fail(ZR_ERR_INVALID, "zr_mx4_matmul: the row stride of out is under N");
+  if (M == 0 || N == 0) return ZR_OK;
+  if (!out || (K > 0 && (!a || !b))) return fail(ZR_ERR_INVALID, "zr_mx4_matmul: null pointer");
+  if (!zr::aligned16(a) || !zr::aligned16(b) || !zr::aligned16(out))
+    return fail(ZR_ERR_INVALID, "zr_mx4_matmul: a pointer is not 16-byte aligned");
+  return matmul("zr_mx4_matmul", a, M, b, N, K, out, dt, ldo, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" zr_status zr_mx4_linear(const void* x, zr_dtype xdt, int64_t M, int64_t ldx, const void* w, int64_t N,
+                                   int64_t K, void* out, zr_dtype dt, int64_t ldo, void* xq, void* stream) {
+  zr::clear_error();
+  zr::Range range("zr_mx4_linear");
+  if (!zr::dtype_ok(xdt) || !zr::dtype_ok(dt)) return fail(ZR_ERR_INVALID, "zr_mx4_linear: bad dtype");
+  if (M < 0 || N < 0 || K < 0) return fail(ZR_ERR_INVALID, "zr_mx4_linear: negative size");
+  if (ldx < K || ldo < N) return fail(ZR_ERR_INVALID, "zr_mx4_linear: a row stride is under the row");
+  if (M == 0 || N == 0) return ZR_OK;
+  if (!out || (K > 0 && (!x || !w))) return fail(ZR_ERR_INVALID, "zr_mx4_linear: null pointer");
+  if (!zr::aligned16(x) || !zr::aligned16(w) || !zr::aligned16(out) || !zr::aligned16(xq))
+    return fail(ZR_ERR_INVALID, "zr_mx4_linear: a pointer is not 16-byte aligned");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int64_t kt = zr::mx_tiles(K, zr::kMxCols), nt = zr::mx_tiles(N, 128);
+  // blocks of a cluster share K where the outputs alone would leave multiprocessors idle: two blocks
+  // fit on one, so up to twice their number
+  const int sms = zr::sm_count("zr_mx4_linear");
+  if (sms == 0) return ZR_ERR_CUDA;
+  int split = 1;
+  while (split < 8 && nt * split * 2 <= 2 * sms && split * 2 <= kt) split *= 2;
+  while (split < 8 && split * 2 <= kt && few_smem((int)(zr::mx_tiles(kt, split) < 4096 ? zr::mx_tiles(kt, split) : 4096)) > zr::kSmemMost) split *= 2;
+  const int64_t most = kt > 0 ? zr::mx_tiles(kt, split) : 0;
+  const bool few = M <= kFewTokens && K > 0 && most < 4096 && few_smem((int)most) <= zr::kSmemMost && nt * split <= 0x7FFFFFFF;
+  if (few) {
+    FewArgs g{};
+    g.x = x; g.w = static_cast<const uint8_t*>(w); g.out = out;
+    g.M = M; g.K = K; g.N = N; g.ldx = ldx; g.ldo = ldo;
+    g.kt = (int)kt; g.xdt = (int)xdt; g.odt = (int)dt;
+    const int blocks = (int)(nt * split), smem = few_smem((int)most);
+    if (split == 8) return launch_few<8>(g, blocks, smem, s);
+    if (split == 4) return launch_few<4>(g, blocks, smem, s);
+    if (split == 2) return launch_few<2>(g, blocks, smem, s);
+    return launch_few<1>(g, blocks, smem, s);
+  }
+  if (K > 0) {
+    if (!xq) return fail(ZR_ERR_INVALID, "zr_mx4_linear: more than %d tokens (or a very long K) need xq", kFewTokens);
+    if (zr_status st = zr_mx4_quantize(x, xdt, M, K, ldx, nullptr, 0, xq, nullptr, stream)) return st;
+  }
+  return matmul("zr_mx4_linear", xq, M, w, N, K, out, dt, ldo, s);
+}
+
+extern "C" zr_status zr_mx4_status(void* stream) {
+  zr::clear_error();
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int gave_up = 0;
+  cudaError_t e = cudaMemcpyFromSymbolAsync(&gave_up, g_gave_up, sizeof gave_up, 0, cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e == cudaSuccess && gave_up) {
+    const int zero = 0;
+    e = cudaMemcpyToSymbolAsync(g_gave_up, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e == cudaSuccess)
+      return fail(ZR_ERR_TIMEOUT, "zr_mx4_status: a product gave up a wait; outputs since the last check are not valid");
+  }
+  return e == cudaSuccess ? ZR_OK : fail(ZR_ERR_CUDA, "zr_mx4_status: %s", cudaGetErrorString(e));
+}

@@ -1,0 +1,383 @@
+// Quantisation of a matrix to the microscaled 4-bit format (by its rows, by its columns, or
+// both from one read) and back to the values that the codes stand for.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "zr_internal.h"
+#include "zr_launch.h"
+#include "zr_mx4.cuh"
+#include "zr_nvtx.h"
+
+using zr::fail;
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kPatch = 128;  // a block quantises 128 x 128 values
+
+struct QuantArgs {
+  const void* x;
+  const uint8_t* rand;  // 8 random bits per value, or null (to nearest)
+  uint8_t* q;           // rows x cols, or null
+  uint8_t* qt;          // cols x rows, or null
+  int64_t rows, cols, ldx, ldr;
+  int64_t q_tiles, qt_tiles;  // tiles along the columns of q, of qt
+  int64_t col_patches;        // patches along the columns of x
+  int q_row_patches, qt_col_patches;  // patches that q has along its rows, qt along x's columns
+};
+
+template <int DT>
+struct Shape {
+  static constexpr int es = DT == zr::DT_F32 ? 4 : 2;
+  static constexpr int pitch = kPatch * es + 16;
+  // Rows 16 bytes apart in their banks, blocks of 32 rows another 32 bytes: so the 8 rows' or
+  // the 4 row blocks' worth of lanes that one access serves fall on different banks.
+  __device__ static int at(int r) { return r * pitch + (r >> 5) * 32; }
+  static constexpr int bytes = kPatch * pitch + 4 * 32;
+};
+constexpr int kRandPitch = kPatch + 8;
+
+// |x| of the patch's words: the bits of the largest magnitude so far. As integers the bits of
+// magnitudes are ordered like the magnitudes, and infinities and NaN lie over all of them.
+template <int DT>
+__device__ __forceinline__ uint32_t amax_word(uint32_t m, uint32_t w) {
+  if (DT == zr::DT_F32) {
+    w &= 0x7FFFFFFFu;
+    return w > m ? w : m;
+  }
+  return __vmaxu2(m, w & 0x7FFF7FFFu);
+}
+
+template <int DT>
+__device__ __forceinline__ uint32_t bits_of_half(uint32_t h) {  // 16-bit pattern -> fp32 bits
+  return __float_as_uint(zr::to_f32<DT>((uint16_t)h));
+}
+
+template <bool CHANCE>
+__device__ __forceinline__ uint32_t codes_of(const float t[8], uint64_t r) {
+  if (!CHANCE) return zr::mx_codes8(t);
+  uint32_t c = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) c |= zr::mx_code_by_chance(t[j], (uint32_t)(r >> (8 * j)) & 255u) << (4 * j);
+  return c;
+}
+
+// Combines the scale bytes of a quad of lanes (lane % 4 = byte) into a word.
+__device__ __forceinline__ uint32_t quad_bytes(int byte) {
+  uint32_t w = (uint32_t)byte << (8 * (threadIdx.x & 3));
+  w |= __shfl_xor_sync(0xFFFFFFFFu, w, 1);
+  w |= __shfl_xor_sync(0xFFFFFFFFu, w, 2);
+  return w;
+}
+
+template <int DT, bool CHANCE>
+__global__ void __launch_bounds__(kThreads) quant_kernel(const __grid_constant__ QuantArgs a) {
+  using S = Shape<DT>;
+  extern __shared__ __align__(16) char smem[];
+  uint8_t* srand = reinterpret_cast<uint8_t*>(smem + S::bytes);
+  const int tid = threadIdx.x;
+  const int64_t pr = blockIdx.x / a.col_patches, pc = blockIdx.x - pr * a.col_patches;
+  const int64_t r0 = pr * kPatch, c0 = pc * kPatch;
+
+  // ---- the patch to shared memory as it is, zeros outside the matrix
+  constexpr int kPer = 16 / S::es, kVecs = kPatch / kPer, kLoads = kPatch * kVecs / kThreads;
+  const char* xb = static_cast<const char*>(a.x);
+#pragma unroll
+  for (int half = 0; half < kLoads; half += 8) {
+    uint4 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int k = tid + (half + i) * kThreads, r = k / kVecs, c = (k % kVecs) * kPer;
+      v[i] = make_uint4(0, 0, 0, 0);
+      if (r0 + r < a.rows && c0 + c < a.cols) {
+        const int64_t e = (r0 + r) * a.ldx + c0 + c;
+        if (c0 + c + kPer <= a.cols) {
+          v[i] = zr::load16(xb + e * S::es);
+        } else {
+          uint32_t w[4] = {0, 0, 0, 0};
+          const int left = (int)(a.cols - c0 - c);
+#pragma unroll
+          for (int j = 0; j < kPer; ++j)
+            if (j < left) {
+              if (S::es == 4)
+                w[j] = static_cast<const uint32_t*>(a.x)[e + j];
+              else
+                w[j / 2] |= (uint32_t)static_cast<const uint16_t*>(a.x)[e + j] << (16 * (j & 1));
+            }
+          v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int k = tid + (half + i) * kThreads, r = k / kVecs, c = k % kVecs;
+      *reinterpret_cast<uint4*>(smem + S::at(r) + c * 16) = v[i];
+    }
+  }
+  if (CHANCE) {
+#pragma unroll
+    for (int i = 0; i < kPatch * kPatch / 16 / kThreads; ++i) {
+      const int k = tid + i * kThreads, r = k / 8, c = (k % 8) * 16;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (r0 + r < a.rows && c0 + c < a.cols) {
+        const uint8_t* p = a.rand + (r0 + r) * a.ldr + c0 + c;
+        if (c0 + c + 16 <= a.cols) {
+          v = zr::load16(reinterpret_cast<const char*>(p));
+        } else {
+          uint32_t w[4] = {0, 0, 0, 0};
+          const int left = (int)(a.cols - c0 - c);
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (j < left) w[j / 4] |= (uint32_t)p[j] << (8 * (j & 3));
+          v = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      uint2* d = reinterpret_cast<uint2*>(srand + r * kRandPitch + c);
+      d[0] = make_uint2(v.x, v.y);
+      d[1] = make_uint2(v.z, v.w);
+    }
+  }
+  __syncthreads();
+
+  // ---- by rows: a thread takes 32 neighbours of a row, a quad of lanes a row's four blocks
+  if (a.q && pr < a.q_row_patches) {
+    uint8_t* tile = a.q + (pr * a.q_tiles + (pc >> 1)) * zr::kMxTileBytes;
+#pragma unroll 1
+    for (int it = 0; it < 2; ++it) {
+      const int task = tid + it * kThreads, r = task >> 2, b = task & 3;
+      // the four 8-value words of the block in an order that differs between the lanes of a
+      // quad, so that they read different banks: word (i + rot) % 4 comes i-th
+      const int rot = DT == zr::DT_F32 ? b : (b & 2);
+      const char* row = smem + S::at(r) + b * 32 * S::es;
+      uint4 raw[4][S::es / 2];
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int w = (i + rot) & 3;
+#pragma unroll
+        for (int h = 0; h < S::es / 2; ++h) {
+          const uint4 u = *reinterpret_cast<const uint4*>(row + w * 8 * S::es + h * 16);
+          raw[i][h] = u;
+          m = amax_word<DT>(amax_word<DT>(amax_word<DT>(amax_word<DT>(m, u.x), u.y), u.z), u.w);
+        }
+      }
+      if (DT != zr::DT_F32) m = bits_of_half<DT>((m >> 16) > (m & 0xFFFFu) ? m >> 16 : m & 0xFFFFu);
+      const int byte = zr::mx_scale_byte<CHANCE>(m);
+      uint32_t o[4];
+      if (byte == 255) {
+        o[0] = o[1] = o[2] = o[3] = 0;
+      } else {
+        const float inv = zr::mx_inverse(byte);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float t[8];
+          if (DT == zr::DT_F32) {
+            const uint4 u = raw[i][0], w = raw[i][S::es / 2 - 1];
+            const uint32_t f[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) t[j] = __uint_as_float(f[j]);
+          } else {
+            zr::unpack8<DT>(raw[i][0], t);
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) t[j] = __fmul_rn(t[j], inv);
+          uint64_t rnd = 0;
+          if (CHANCE) rnd = *reinterpret_cast<const uint64_t*>(srand + r * kRandPitch + b * 32 + ((i + rot) & 3) * 8);
+          o[i] = codes_of<CHANCE>(t, rnd);
+        }
+      }
+      if (rot & 1) {
+        const uint32_t z = o[3];
+        o[3] = o[2]; o[2] = o[1]; o[1] = o[0]; o[0] = z;
+      }
+      if (rot & 2) {
+        uint32_t z = o[0];
+        o[0] = o[2]; o[2] = z;
+        z = o[1];
+        o[1] = o[3]; o[3] = z;
+      }
+      const int j = (int)(pc & 1) * 4 + b;
+      *reinterpret_cast<uint4*>(tile + zr::mx_chunk_at(r, j)) = make_uint4(o[0], o[1], o[2], o[3]);
+      const uint32_t bytes = quad_bytes(byte);
+      if (b == 0) *reinterpret_cast<uint32_t*>(tile + zr::mx_scale_at(r, j)) = bytes;
+    }
+  }
+
+  // ---- by columns: a thread takes 32 neighbours of one column (of two in 16 bits), a quad of
+  // lanes a column's four blocks
+  if (a.qt && pc < a.qt_col_patches) {
+    uint8_t* tile = a.qt + (pc * a.qt_tiles + (pr >> 1)) * zr::kMxTileBytes;
+    constexpr int kCols = DT == zr::DT_F32 ? 1 : 2;
+#pragma unroll 1
+    for (int it = 0; it < 2 / kCols; ++it) {
+      const int task = tid + it * kThreads, c = (task >> 2) * kCols, b = task & 3;
+      const char* col = smem + S::at(b * 32) + c * S::es;
+      uint32_t raw[32];
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        raw[i] = *reinterpret_cast<const uint32_t*>(col + i * S::pitch);
+        m = amax_word<DT>(m, raw[i]);
+      }
+#pragma unroll
+      for (int k = 0; k < kCols; ++k) {
+        uint32_t mk = m;
+        if (DT != zr::DT_F32) mk = bits_of_half<DT>(k ? m >> 16 : m & 0xFFFFu);
+        const int byte = zr::mx_scale_byte<CHANCE>(mk);
+        uint32_t o[4];
+        if (byte == 255) {
+          o[0] = o[1] = o[2] = o[3] = 0;
+        } else {
+          const float inv = zr::mx_inverse(byte);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float t[8];
+            uint64_t rnd = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const uint32_t w = raw[i * 8 + j];
+              const float f = DT == zr::DT_F32    ? __uint_as_float(w)
+                              : DT == zr::DT_BF16 ? __uint_as_float(k ? w & 0xFFFF0000u : w << 16)
+                                                  : zr::to_f32<DT>((uint16_t)(k ? w >> 16 : w));
+              t[j] = __fmul_rn(f, inv);
+              if (CHANCE) rnd |= (uint64_t)srand[(b * 32 + i * 8 + j) * kRandPitch + c + k] << (8 * j);
+            }
+            o[i] = codes_of<CHANCE>(t, rnd);
+          }
+        }
+        const int j = (int)(pr & 1) * 4 + b;
+        *reinterpret_cast<uint4*>(tile + zr::mx_chunk_at(c + k, j)) = make_uint4(o[0], o[1], o[2], o[3]);
+        const uint32_t bytes = quad_bytes(byte);
+        if (b == 0) *reinterpret_cast<uint32_t*>(tile + zr::mx_scale_at(c + k, j)) = bytes;
+      }
+    }
+  }
+}
+
+struct DequantArgs {
+  const uint8_t* q;
+  void* out;
+  int64_t rows, cols, ld, tiles;  // tiles along the columns
+  int vec;                        // the rows of out are 16-byte aligned
+};
+
+// A warp takes a row of a tile (128 bytes of codes), a lane eight of its values; a block the
+// 128 rows of a tile.
+template <int DT>
+__global__ void __launch_bounds__(kThreads) dequant_kernel(const __grid_constant__ DequantArgs a) {
+  const int64_t rt = blockIdx.x / a.tiles, ct = blockIdx.x - rt * a.tiles;
+  const uint8_t* tile = a.q + (int64_t)blockIdx.x * zr::kMxTileBytes;
+  const int lane = threadIdx.x & 31, j = lane >> 2;
+  const int64_t c = ct * zr::kMxCols + lane * 8;
+  if (c >= a.cols) return;
+#pragma unroll 4
+  for (int r = threadIdx.x >> 5; r < zr::kMxRows; r += kThreads / 32) {
+    const int64_t row = rt * zr::kMxRows + r;
+    if (row >= a.rows) return;
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(tile + zr::mx_chunk_at(r, j) + (lane & 3) * 4);
+    const float s = zr::mx_scale_value(tile[zr::mx_scale_at(r, j)]);
+    float v[8];
+    zr::mx_decode8(w, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], s);
+    const int64_t e = row * a.ld + c;
+    if (a.vec && c + 8 <= a.cols) {
+      if (DT == zr::DT_F32) {
+        float* o = static_cast<float*>(a.out) + e;
+        zr::st_once_f4(o, make_float4(v[0], v[1], v[2], v[3]));
+        zr::st_once_f4(o + 4, make_float4(v[4], v[5], v[6], v[7]));
+      } else {
+        zr::st_once(static_cast<uint16_t*>(a.out) + e, zr::pack8<DT>(v));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c + i < a.cols) {
+          if (DT == zr::DT_F32)
+            static_cast<float*>(a.out)[e + i] = v[i];
+          else
+            static_cast<uint16_t*>(a.out)[e + i] = zr::from_f32<DT>(v[i]);
+        }
+    }
+  }
+}
+
+template <int DT, bool CHANCE>
+zr_status launch_quant(const QuantArgs& a, int64_t patches, cudaStream_t s) {
+  constexpr int smem = Shape<DT>::bytes + (CHANCE ? kPatch * kRandPitch : 0);
+  static zr::SmemAllowance allowance;
+  if (zr_status st = allowance.allow("zr_mx4_quantize", (const void*)quant_kernel<DT, CHANCE>, smem)) return st;
+  quant_kernel<DT, CHANCE><<<(unsigned)patches, kThreads, smem, s>>>(a);
+  return zr::launch_status("zr_mx4_quantize");
+}
+
+}  // namespace
+
+extern "C" int64_t zr_mx4_bytes(int64_t rows, int64_t cols) {
+  if (rows < 0 || cols < 0) return -1;
+  return zr::mx_tiles(rows, zr::kMxRows) * zr::mx_tiles(cols, zr::kMxCols) * zr::kMxTileBytes;
+}
+
+extern "C" zr_status zr_mx4_quantize(const void* x, zr_dtype dt, int64_t rows, int64_t cols, int64_t ldx,
+                                     const uint8_t* rand, int64_t ldr, void* q, void* qt, void* stream) {
+  zr::clear_error();
+  zr::Range range("zr_mx4_quantize");
+  if (!zr::dtype_ok(dt)) return fail(ZR_ERR_INVALID, "zr_mx4_quantize: bad dtype %d", (int)dt);
+  if (rows < 0 || cols < 0) return fail(ZR_ERR_INVALID, "zr_mx4_quantize: negative size");
+  if (ldx < cols || (rand && ldr < cols)) return fail(ZR_ERR_INVALID, "zr_mx4_quantize: a row stride is under cols");
+  if (rows == 0 || cols == 0) return ZR_OK;
+  if (!q && !qt) return fail(ZR_ERR_INVALID, "zr_mx4_quantize: neither q nor qt given");
+  if (!x) return fail(ZR_ERR_INVALID, "zr_mx4_quantize: null x");
+  if (!zr::aligned16(x) || !zr::aligned16(rand) || !zr::aligned16(q) || !zr::aligned16(qt))
+    return fail(ZR_ERR_INVALID, "zr_mx4_quantize: a pointer is not 16-byte aligned");
+  QuantArgs a{};
+  a.x = x; a.rand = rand;
+  a.q = static_cast<uint8_t*>(q); a.qt = static_cast<uint8_t*>(qt);
+  a.rows = rows; a.cols = cols; a.ldx = ldx; a.ldr = ldr;
+  a.q_tiles = zr::mx_tiles(cols, zr::kMxCols);
+  a.qt_tiles = zr::mx_tiles(rows, zr::kMxCols);
+  // patches to the end of both outputs' tiles: 128 rows by 256 columns of q, 128 columns by 256 rows for qt
+  const int64_t row128 = zr::mx_tiles(rows, kPatch), col128 = zr::mx_tiles(cols, kPatch);
+  const int64_t row_patches = qt ? 2 * a.qt_tiles : row128;
+  a.col_patches = q ? 2 * a.q_tiles : col128;
+  const int64_t patches = row_patches * a.col_patches;
+  if (patches > 0x7FFFFFFF) return fail(ZR_ERR_UNSUPPORTED, "zr_mx4_quantize: matrix too large for one launch");
+  a.q_row_patches = (int)row128;
+  a.qt_col_patches = (int)col128;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (rand) {
+    if (dt == ZR_F16) return launch_quant<zr::DT_F16, true>(a, patches, s);
+    if (dt == ZR_BF16) return launch_quant<zr::DT_BF16, true>(a, patches, s);
+    return launch_quant<zr::DT_F32, true>(a, patches, s);
+  }
+  if (dt == ZR_F16) return launch_quant<zr::DT_F16, false>(a, patches, s);
+  if (dt == ZR_BF16) return launch_quant<zr::DT_BF16, false>(a, patches, s);
+  return launch_quant<zr::DT_F32, false>(a, patches, s);
+}
+
+extern "C" zr_status zr_mx4_dequantize(const void* q, int64_t rows, int64_t cols, void* out, zr_dtype dt, int64_t ld,
+                                       void* stream) {
+  zr::clear_error();
+  zr::Range range("zr_mx4_dequantize");
+  if (!zr::dtype_ok(dt)) return fail(ZR_ERR_INVALID, "zr_mx4_dequantize: bad dtype %d", (int)dt);
+  if (rows < 0 || cols < 0) return fail(ZR_ERR_INVALID, "zr_mx4_dequantize: negative size");
+  if (ld < cols) return fail(ZR_ERR_INVALID, "zr_mx4_dequantize: the row stride is under cols");
+  if (rows == 0 || cols == 0) return ZR_OK;
+  if (!q || !out) return fail(ZR_ERR_INVALID, "zr_mx4_dequantize: null pointer");
+  if (!zr::aligned16(q) || !zr::aligned16(out))
+    return fail(ZR_ERR_INVALID, "zr_mx4_dequantize: a pointer is not 16-byte aligned");
+  DequantArgs a{};
+  a.q = static_cast<const uint8_t*>(q);
+  a.out = out;
+  a.rows = rows; a.cols = cols; a.ld = ld;
+  a.tiles = zr::mx_tiles(cols, zr::kMxCols);
+  a.vec = ld * (dt == ZR_F32 ? 4 : 2) % 16 == 0;
+  const int64_t tiles = zr::mx_tiles(rows, zr::kMxRows) * a.tiles;
+  if (tiles > 0x7FFFFFFF) return fail(ZR_ERR_UNSUPPORTED, "zr_mx4_dequantize: matrix too large for one launch");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (dt == ZR_F16) dequant_kernel<zr::DT_F16><<<(unsigned)tiles, kThreads, 0, s>>>(a);
+  else if (dt == ZR_BF16) dequant_kernel<zr::DT_BF16><<<(unsigned)tiles, kThreads, 0, s>>>(a);
+  else dequant_kernel<zr::DT_F32><<<(unsigned)tiles, kThreads, 0, s>>>(a);
+  return zr::launch_status("zr_mx4_dequantize");
+}
