@@ -611,7 +611,7 @@ zr_status zr_mx4_status(void* stream);
  * fp32[T] or NULL (all 1); loss: device fp32[T]; grad: device, T x V of type dt with row stride
  * ldg, or NULL for the loss alone; grad may be the logits themselves (with ldg = ldz).
  * Loads are whole 16-byte words, so up to 15 bytes before and after a row are read with it.
- * Errors: ZR_ERR_INVALID for bad dtypes, T < 0, V < 1, K outside [1, ZR_DISTILL_MAX_TOP], a row
+ * Errors: ZR_ERR_INVALID for bad dtypes, T < 0, V outside [1, 2^31 - 256], K outside [1, ZR_DISTILL_MAX_TOP], a row
  * stride under its row, a temperature outside [1e-6, 1e6], a grad_scale that is not finite,
  * null or misaligned pointers, a gradient that overlaps the logits without being them. */
 zr_status zr_distill_topk(const void* logits, zr_dtype dt, int64_t T, int64_t V, int64_t ldz, const void* ids,

@@ -595,11 +595,41 @@ def _refuse(message: str):
     raise ZrError(1, message)
 
 
+# A small call costs a few microseconds on the GPU, so these calls look their parts up once: the library's functions,
+# torch's types, the current stream's handle without a Stream object around it.
+_fns = {}
+_types = {}
+
+
+def _fn(name: str):
+    f = _fns.get(name)
+    if f is None:
+        import torch
+        _types.update({torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32})
+        f = _fns[name] = getattr(lib(), name)
+    return f
+
+
+def _raw_stream(stream, device: int) -> int:
+    if stream is not None:
+        return int(stream.cuda_stream)
+    import torch
+    global _raw_stream_of
+    if _raw_stream_of is None:
+        _raw_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda d: torch.cuda.current_stream(d).cuda_stream)
+    return _raw_stream_of(device)
+
+
+_raw_stream_of = None
+
+
 def _matrix(t, what: str):
     """(pointer, rows, cols, row stride, dtype) of a device matrix whose rows are contiguous."""
-    if t.dim() != 2 or not t.is_cuda:
+    shape = t.shape
+    if len(shape) != 2 or not t.is_cuda:
         _refuse(f"{what} must be a matrix in device memory")
-    rows, cols = t.shape
+    rows, cols = shape
     ld, step = t.stride()
     if step != 1 and cols > 1:
         _refuse(f"the rows of {what} must be contiguous")
@@ -607,34 +637,37 @@ def _matrix(t, what: str):
         if rows > 1:
             _refuse(f"the rows of {what} overlap")
         ld = cols
-    return t.data_ptr(), rows, cols, ld, _dt_of(t)
+    dt = _types.get(t.dtype)
+    if dt is None:
+        _refuse(f"{what} must be fp32, fp16 or bf16, not {t.dtype}")
+    return t.data_ptr(), rows, cols, ld, dt
 
 
 class Mx4:
     """A rows x cols matrix in microscaled 4-bit floating point: its bytes in `data` (layout in include/zr.h)."""
 
-    __slots__ = ("rows", "cols", "data")
+    __slots__ = ("rows", "cols", "data", "ptr")
 
     def __init__(self, rows: int, cols: int, data=None, device="cuda"):
         import torch
-        self.rows, self.cols = int(rows), int(cols)
-        if self.rows < 0 or self.cols < 0:
+        if rows < 0 or cols < 0:
             _refuse("Mx4: negative size")
-        need = -(-self.rows // 128) * -(-self.cols // 256) * 17408
+        need = -(-rows // 128) * -(-cols // 256) * 17408
         if data is None:
             data = torch.empty(need, dtype=torch.uint8, device=device)
-        elif data.dtype != torch.uint8 or data.numel() < need or not data.is_contiguous() or not data.is_cuda:
+        elif data.dtype is not torch.uint8 or data.numel() < need or not data.is_contiguous() or not data.is_cuda:
             _refuse(f"Mx4: data must be {need} contiguous bytes in device memory")
-        self.data = data
+        self.rows, self.cols, self.data, self.ptr = rows, cols, data, data.data_ptr()
 
 
 def mx4_quantize(x, q: Optional[Mx4] = None, q_t: Optional[Mx4] = None, rand=None, stream=None) -> None:
     """Quantises matrix x to q, and its transpose to q_t (zr_mx4_quantize); `rand`: uint8 random bits of x's shape
     for rounding by chance."""
+    fn = _fn("zr_mx4_quantize")
     p, rows, cols, ld, dt = _matrix(x, "x")
-    if q is not None and (q.rows, q.cols) != (rows, cols):
+    if q is not None and (q.rows != rows or q.cols != cols):
         _refuse(f"mx4_quantize: q is {q.rows} x {q.cols}, x {rows} x {cols}")
-    if q_t is not None and (q_t.rows, q_t.cols) != (cols, rows):
+    if q_t is not None and (q_t.rows != cols or q_t.cols != rows):
         _refuse(f"mx4_quantize: q_t is {q_t.rows} x {q_t.cols}, x {rows} x {cols}")
     rp, ldr = None, 0
     if rand is not None:
@@ -643,38 +676,38 @@ def mx4_quantize(x, q: Optional[Mx4] = None, q_t: Optional[Mx4] = None, rand=Non
         if not rand.is_contiguous():
             _refuse("mx4_quantize: rand must be contiguous")
         rp, ldr = rand.data_ptr(), cols
-    _check(lib().zr_mx4_quantize(p, dt, rows, cols, ld, rp, ldr, q.data.data_ptr() if q is not None else None,
-                                 q_t.data.data_ptr() if q_t is not None else None, _stream_handle(stream)))
+    _check(fn(p, dt, rows, cols, ld, rp, ldr, q and q.ptr, q_t and q_t.ptr, _raw_stream(stream, x.get_device())))
 
 
 def mx4_dequantize(q: Mx4, out, stream=None) -> None:
     """out = the values that q stands for (zr_mx4_dequantize)."""
+    fn = _fn("zr_mx4_dequantize")
     p, rows, cols, ld, dt = _matrix(out, "out")
-    if (q.rows, q.cols) != (rows, cols):
+    if q.rows != rows or q.cols != cols:
         _refuse(f"mx4_dequantize: q is {q.rows} x {q.cols}, out {rows} x {cols}")
-    _check(lib().zr_mx4_dequantize(q.data.data_ptr(), rows, cols, p, dt, ld, _stream_handle(stream)))
+    _check(fn(q.ptr, rows, cols, p, dt, ld, _raw_stream(stream, out.get_device())))
 
 
 def mx4_matmul(a: Mx4, b: Mx4, out, stream=None) -> None:
     """out[M, N] = a[M, K] b[N, K]^T (zr_mx4_matmul)."""
+    fn = _fn("zr_mx4_matmul")
     p, rows, cols, ld, dt = _matrix(out, "out")
-    if a.cols != b.cols or (a.rows, b.rows) != (rows, cols):
+    if a.cols != b.cols or a.rows != rows or b.rows != cols:
         _refuse(f"mx4_matmul: a is {a.rows} x {a.cols}, b {b.rows} x {b.cols}, out {rows} x {cols}")
-    _check(lib().zr_mx4_matmul(a.data.data_ptr(), rows, b.data.data_ptr(), cols, a.cols, p, dt, ld,
-                               _stream_handle(stream)))
+    _check(fn(a.ptr, rows, b.ptr, cols, a.cols, p, dt, ld, _raw_stream(stream, out.get_device())))
 
 
 def mx4_linear(x, w: Mx4, out, xq: Optional[Mx4] = None, stream=None) -> None:
     """out[M, N] = x[M, K] w[N, K]^T with x quantised in the call (zr_mx4_linear); more than MX4_FEW tokens need xq,
     a buffer for the quantised x."""
+    fn = _fn("zr_mx4_linear")
     p, rows, k, ldx, xdt = _matrix(x, "x")
     o, m, n, ldo, dt = _matrix(out, "out")
     if w.cols != k or m != rows or w.rows != n:
         _refuse(f"mx4_linear: x is {rows} x {k}, w {w.rows} x {w.cols}, out {m} x {n}")
-    if xq is not None and (xq.rows, xq.cols) != (rows, k):
+    if xq is not None and (xq.rows != rows or xq.cols != k):
         _refuse(f"mx4_linear: xq is {xq.rows} x {xq.cols}, x {rows} x {k}")
-    _check(lib().zr_mx4_linear(p, xdt, rows, ldx, w.data.data_ptr(), n, k, o, dt, ldo,
-                               xq.data.data_ptr() if xq is not None else None, _stream_handle(stream)))
+    _check(fn(p, xdt, rows, ldx, w.ptr, n, k, o, dt, ldo, xq and xq.ptr, _raw_stream(stream, out.get_device())))
 
 
 def mx4_status(stream=None) -> None:
@@ -687,6 +720,7 @@ def distill_topk(logits, ids, teacher, loss, grad=None, weight=None, temperature
     """The distillation loss of each row against a teacher's top logits, and its gradient times grad_scale and the
     plan's loss scale (zr_distill_topk). `grad` may be `logits`."""
     import torch
+    fn = _fn("zr_distill_topk")
     z, rows, vocab, ldz, dt = _matrix(logits, "logits")
     t, trows, top, ldk, tdt = _matrix(teacher, "teacher")
     if ids.dtype not in (torch.int32, torch.int64) or ids.shape != teacher.shape or not ids.is_cuda:
@@ -703,10 +737,10 @@ def distill_topk(logits, ids, teacher, loss, grad=None, weight=None, temperature
         if grad.dtype != logits.dtype or grad.shape != logits.shape:
             _refuse("distill_topk: grad must have the logits' type and shape")
         g, _, _, ldg, _ = _matrix(grad, "grad")
-    _check(lib().zr_distill_topk(z, dt, rows, vocab, ldz, ids.data_ptr(), int(ids.dtype == torch.int64), t, tdt, top,
-                                 ldk, weight.data_ptr() if weight is not None else None, float(temperature),
-                                 float(grad_scale), plan.handle if plan is not None else None, loss.data_ptr(), g, ldg,
-                                 _stream_handle(stream)))
+    _check(fn(z, dt, rows, vocab, ldz, ids.data_ptr(), int(ids.dtype == torch.int64), t, tdt, top, ldk,
+              weight.data_ptr() if weight is not None else None, temperature, grad_scale,
+              plan.handle if plan is not None else None, loss.data_ptr(), g, ldg,
+              _raw_stream(stream, logits.get_device())))
 
 
 __all__ = ["lib", "ZrError", "chunk_size", "bucket_plan", "model_state_bytes", "ring_traffic", "reduce_scatter",

@@ -21,7 +21,7 @@ using zr::fail;
 
 namespace {
 
-constexpr int kMaxThreads = 512;
+constexpr int kMaxThreads = 512;  // 15 warps for a row's words and one for the teacher's entries
 constexpr float kLog2E = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
 
 struct DistillArgs {
@@ -34,7 +34,7 @@ struct DistillArgs {
   void* grad;           // null: the loss alone
   int64_t T, V, ldz, ldg, ldk;
   int64_t share;        // columns of each block of a row's cluster
-  int K, wide_ids, tdt;
+  int K, K4, wide_ids, tdt;  // K4: K to a multiple of 4
   int room;             // 16-byte words of a row's share that shared memory holds
   float tau, grad_scale;
 };
@@ -49,10 +49,35 @@ __device__ __forceinline__ uint4 ld_row(const uint4* p) {
   return r;
 }
 
-__device__ __forceinline__ float exp2_fast(float x) {  // 2 ulp; 2^-inf = 0
+// 2^x to 2 ulp, results under 2^-126 to zero.
+__device__ __forceinline__ float exp2_fast(float x) {
   float y;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Two fp32 operations in one instruction.
+struct Two {
+  uint64_t v;
+  __device__ Two(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+  __device__ explicit Two(uint64_t w) : v(w) {}
+  __device__ float lo() const { return __uint_as_float((uint32_t)v); }
+  __device__ float hi() const { return __uint_as_float((uint32_t)(v >> 32)); }
+};
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return Two(r);
+}
+__device__ __forceinline__ Two add2(Two a, Two b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a.v), "l"(b.v));
+  return Two(r);
+}
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a.v), "l"(b.v));
+  return Two(r);
 }
 
 template <int DT>
@@ -65,6 +90,30 @@ struct Word {
     } else {
       zr::unpack8<DT>(u, f);
     }
+  }
+  // The larger of m and the word's values, two at a time in 16 bits; `m` starts as lowest().
+  __device__ static uint32_t lowest() {
+    return DT == zr::DT_F32 ? 0xFF800000u : DT == zr::DT_BF16 ? 0xFF80FF80u : 0xFC00FC00u;
+  }
+  __device__ static uint32_t larger(uint32_t a, uint32_t b) {
+    if constexpr (DT == zr::DT_F32) {
+      return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    } else if constexpr (DT == zr::DT_BF16) {
+      const __nv_bfloat162 r = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+      return *reinterpret_cast<const uint32_t*>(&r);
+    } else {
+      const __half2 r = __hmax2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+      return *reinterpret_cast<const uint32_t*>(&r);
+    }
+  }
+  __device__ static uint32_t larger(uint32_t m, uint4 u) {
+    return larger(larger(m, larger(u.x, u.y)), larger(u.z, u.w));
+  }
+  __device__ static float largest(uint32_t m) {
+    if constexpr (DT == zr::DT_F32)
+      return __uint_as_float(m);
+    else
+      return fmaxf(zr::to_f32<DT>((uint16_t)m), zr::to_f32<DT>((uint16_t)(m >> 16)));
   }
   __device__ static uint4 close(const float f[per]) {
     if constexpr (DT == zr::DT_F32)
@@ -82,246 +131,306 @@ __device__ __forceinline__ void store1(void* p, int64_t i, float v) {
     static_cast<uint16_t*>(p)[i] = zr::from_f32<DT == zr::DT_F32 ? zr::DT_BF16 : DT>(v);
 }
 
-struct Sum {
-  __device__ static float of(float a, float b) { return __fadd_rn(a, b); }
-};
-struct Max {
-  __device__ static float of(float a, float b) { return fmaxf(a, b); }
-};
+// 16 bytes from global to shared memory without a register on the way.
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(zr::smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// The block's sum or maximum in every thread; `slots`: 32 floats that no one else uses meanwhile.
-template <class OP>
-__device__ float block_all(float v, float none, float* slots) {
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) v = OP::of(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-  if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = (threadIdx.x & 31) < (blockDim.x >> 5) ? slots[threadIdx.x & 31] : none;
+  for (int o = 16; o; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) v = OP::of(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-  __syncthreads();
+  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
   return v;
 }
 
+// A sum of exponentials is kept relative to the maximum m of its z, in base 2 and as one
+// multiply-add: sum of 2^(z c - mc), mc = m c rounded. That rounding multiplies every term by the
+// same factor, which cancels in q and in log q. Where m c is not a usable number (a mask of the
+// type's lowest value, which times c overflows) the terms are 2^((z - m) c). A part that is all
+// masked has m = -inf; its terms are taken relative to 0: 0, or NaN where z is.
+struct Base {
+  float m, mc, c;
+  bool fused;
+  __device__ Base(float largest, float c_) : c(c_) {
+    m = largest == -INFINITY ? 0.0f : largest;
+    mc = __fmul_rn(m, c);
+    fused = fabsf(mc) < 1e37f;  // not where m is NaN or infinite either
+  }
+  __device__ float exponent(float z) const { return fused ? __fmaf_rn(z, c, -mc) : __fmul_rn(z - m, c); }
+};
+// A sum relative to the maximum m, relative to a larger one.
+__device__ __forceinline__ float rescaled(float m, float sum, const Base& to) {
+  if (m == -INFINITY) return sum;
+  const Base from(m, to.c);
+  return __fmul_rn(sum, exp2_fast(from.fused && to.fused ? from.mc - to.mc : __fmul_rn(m - to.m, to.c)));
+}
+
+struct Shared {      // what the block's warps, and the cluster's blocks, tell each other
+  float m[16], sum[16], loss[16];  // of each warp
+  float row_m, row_sum, row_loss;  // of the block
+  int some, beyond;
+};
+
 // A row is handled in the 16-byte words of memory that hold it: word 0 begins at the boundary at
 // or before its first value, so every load is aligned whatever the row stride; `lead` values of
-// word 0 belong to the row before, and the last word may end past the row.
+// word 0 belong to the row before, and the last word may end past the row. A thread copies, sums
+// and stores the same words, so the passes need no barrier between them; the last warp has no words
+// and reads the teacher's entries while the row is on its way.
 template <int DT, int C>
-__global__ void __launch_bounds__(kMaxThreads) distill_kernel(const __grid_constant__ DistillArgs a) {
+__global__ void __launch_bounds__(kMaxThreads, 2) distill_kernel(const __grid_constant__ DistillArgs a) {
   using W = Word<DT>;
   constexpr int per = W::per, es = 16 / per;
   extern __shared__ __align__(16) char smem[];
   uint4* words = reinterpret_cast<uint4*>(smem);
-  float* sp = reinterpret_cast<float*>(words + a.room);            // p of each entry
-  int64_t* sid = reinterpret_cast<int64_t*>(sp + ((a.K + 1) & ~1));  // its column, or -1
-  float* own = reinterpret_cast<float*>(sid + a.K);                // the gradient at that column
-  float* slots = own + a.K;                                        // 32
-  float* mine = slots + 32;                                        // what the cluster reads: max, sum, loss
-  const int tid = threadIdx.x, nthr = blockDim.x;
+  int* sid = reinterpret_cast<int*>(words + a.room);  // an entry's column, or -1
+  float* sp = reinterpret_cast<float*>(sid + a.K4);   // its p
+  float* own = sp + a.K4;                             // its log2 p, then the gradient at its column
+  Shared& sh = *reinterpret_cast<Shared*>(own + a.K4);
+  const int tid = threadIdx.x, nthr = blockDim.x - 32, lane = tid & 31, warp = tid >> 5;  // nthr: those that share the words
   const int64_t row = blockIdx.x / C;
   const int rank = C > 1 ? (int)zr::cluster_rank() : 0;
-  const int64_t v0 = rank * a.share, v1 = v0 + a.share < a.V ? v0 + a.share : a.V;  // may be empty: v0 >= v1
-  const int64_t n = v1 > v0 ? v1 - v0 : 0;
+  const int64_t v0 = rank * a.share, v1 = v0 + a.share < a.V ? v0 + a.share : a.V;
+  const int n = v1 > v0 ? (int)(v1 - v0) : 0;  // this block's columns; the last blocks may have none
 
   const float w = a.weight ? a.weight[row] : 1.0f;
   const float c = __fdiv_rn(kLog2E, a.tau);
-
-  // ---- the teacher's entries: p over the kept ones
-  bool some = false, beyond = false;
-  float t_max = -INFINITY;
-  if (w != 0.0f)
-    for (int k = tid; k < a.K; k += nthr) {
-      const int64_t at = row * a.ldk + k;
-      const int64_t id = a.wide_ids ? static_cast<const int64_t*>(a.ids)[at] : static_cast<const int32_t*>(a.ids)[at];
-      const float t = a.tdt == zr::DT_F32    ? zr::load1<zr::DT_F32>(a.teacher, at)
-                      : a.tdt == zr::DT_BF16 ? zr::load1<zr::DT_BF16>(a.teacher, at)
-                                             : zr::load1<zr::DT_F16>(a.teacher, at);
-      sid[k] = id;
-      sp[k] = t;
-      some |= id >= 0 && !(t == -INFINITY);  // a masked entry is none
-      beyond |= id >= a.V;
-      if (id >= 0) t_max = fmaxf(t_max, t);
-    }
-  some = __syncthreads_or(some);
-  void* grad = a.grad ? static_cast<char*>(a.grad) + (row * a.ldg + v0) * es : nullptr;
+  char* grad = a.grad ? static_cast<char*>(a.grad) + (row * a.ldg + v0) * es : nullptr;
   const char* zrow = static_cast<const char*>(a.z) + (row * a.ldz + v0) * es;
   const int lead = (int)(reinterpret_cast<uintptr_t>(zrow) & 15) / es;
   const uint4* zw = reinterpret_cast<const uint4*>(zrow - lead * es);
-  const int64_t nw = n > 0 ? (lead + n + per - 1) / per : 0;
+  const int nw = n > 0 ? (lead + n + per - 1) / per : 0;
   // the gradient's words are the logits' words, shifted: stored whole only where they coincide
-  const bool same = grad && ((reinterpret_cast<uintptr_t>(grad) & 15) / es) == (uintptr_t)lead;
+  const bool same = grad && (int)(reinterpret_cast<uintptr_t>(grad) & 15) / es == lead;
 
-  if (!some) {  // no weight, or nothing kept: no loss and no gradient (uniform over the cluster)
-    if (rank == 0 && tid == 0) a.loss[row] = 0.0f;
-    if (grad)
-      for (int64_t j = tid; j < nw; j += nthr) {
-        const int64_t i0 = j * per - lead;
-        if (same && i0 >= 0 && i0 + per <= n)
-          *reinterpret_cast<uint4*>(static_cast<char*>(grad) + i0 * es) = make_uint4(0, 0, 0, 0);
-        else
-          for (int i = 0; i < per; ++i)
-            if (i0 + i >= 0 && i0 + i < n) store1<DT>(grad, i0 + i, 0.0f);
+  // whole words [first, last) and, before and behind them, under a word's worth of single values:
+  // those go to one thread each, which keeps its value in a register
+  const int first = lead > 0 ? 1 : 0, last = (lead + n) / per;
+  const int head = lead > 0 ? min(n, per - lead) : 0, behind = max(head, last * per - lead);
+  const int single = tid < head ? tid : tid >= 32 && tid - 32 < n - behind ? behind + tid - 32 : -1;
+  float z_single = -INFINITY;
+
+  bool some = w != 0.0f;
+  if (some) {
+    for (int j = first + tid; tid < nthr && j < min(last, a.room); j += nthr) copy16(words + j, zw + j);
+    if (single >= 0) {
+      if (single == 0 && first == 1) copy16(words, zw);
+      if (single == n - 1 && last >= first && last < min(nw, a.room)) copy16(words + last, zw + last);
+      z_single = zr::load1<DT>(zrow, single);
+    }
+    if (tid >= nthr) {
+      // ---- the teacher's entries: p over the kept ones
+      float t_max = -INFINITY;
+      int any = 0, past = 0;
+      for (int k = lane; k < a.K4; k += 32) {
+        int64_t id = -1;
+        float t = 0.0f;
+        if (k < a.K) {
+          const int64_t at = row * a.ldk + k;
+          id = a.wide_ids ? static_cast<const int64_t*>(a.ids)[at] : static_cast<const int32_t*>(a.ids)[at];
+          t = a.tdt == zr::DT_F32    ? zr::load1<zr::DT_F32>(a.teacher, at)
+              : a.tdt == zr::DT_BF16 ? zr::load1<zr::DT_BF16>(a.teacher, at)
+                                     : zr::load1<zr::DT_F16>(a.teacher, at);
+        }
+        const bool kept = id >= 0;
+        past |= id >= a.V;
+        any |= kept && !(t == -INFINITY);  // a masked entry is none
+        if (kept) t_max = fmaxf(t_max, t);
+        sid[k] = kept && id < a.V ? (int)id : -1;
+        own[k] = kept ? t : -INFINITY;
       }
+      any = __any_sync(0xFFFFFFFFu, any);
+      past = __any_sync(0xFFFFFFFFu, past);
+      t_max = warp_max(t_max);
+      // an entry of -inf has p = 0; +inf or NaN leaves every p not a number
+      float p_sum = 0.0f;
+      for (int k = lane; k < a.K4; k += 32) p_sum += sp[k] = exp2_fast(own[k] = (own[k] - t_max) * c);
+      p_sum = warp_sum(p_sum);
+      const float log_p = log2f(p_sum);
+      for (int k = lane; k < a.K4; k += 32) {
+        sp[k] = __fdiv_rn(sp[k], p_sum);
+        own[k] -= log_p;
+      }
+      if (lane == 0) {
+        sh.some = any;
+        sh.beyond = past;
+      }
+    }
+    copies_done();
+  }
+
+  auto word = [&](int j) { return j < a.room ? words[j] : ld_row(zw + j); };
+  auto value = [&](int i) {  // the i-th logit of this block's columns
+    i += lead;
+    return i / per < a.room ? zr::load1<DT>(smem, i) : zr::load1<DT>(zw, i);
+  };
+
+  if (some && tid < nthr) {
+    // ---- each thread's maximum, and its sum relative to it
+    uint32_t most = W::lowest();
+    for (int j = first + tid; j < last; j += nthr) most = W::larger(most, word(j));
+    const float m = fmaxf(W::largest(most), z_single);
+    const Base mine(m, c);
+    float sum = 0.0f;
+    if (mine.fused) {
+      const Two cc(c, c), less(-mine.mc, -mine.mc);
+      Two total(0.0f, 0.0f);
+      for (int j = first + tid; j < last; j += nthr) {
+        float f[per];
+        W::open(word(j), f);
+        Two part(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < per; i += 2) {
+          const Two x = fma2(Two(f[i], f[i + 1]), cc, less);
+          part = add2(part, Two(exp2_fast(x.lo()), exp2_fast(x.hi())));
+        }
+        total = add2(total, part);
+      }
+      sum = __fadd_rn(total.lo(), total.hi());
+    } else {
+      for (int j = first + tid; j < last; j += nthr) {
+        float f[per];
+        W::open(word(j), f);
+#pragma unroll
+        for (int i = 0; i < per; ++i) sum = __fadd_rn(sum, exp2_fast(mine.exponent(f[i])));
+      }
+    }
+    sum = __fadd_rn(sum, exp2_fast(mine.exponent(z_single)));
+    const float wm = warp_max(m);
+    sum = warp_sum(rescaled(m, sum, Base(wm, c)));
+    if (lane == 0) {
+      sh.m[warp] = wm;
+      sh.sum[warp] = sum;
+    }
+  }
+  if (some) {
+    __syncthreads();
+    some = sh.some;
+  }
+
+  if (!some) {  // no weight, or nothing kept: no loss and no gradient (the same in the whole cluster)
+    if (rank == 0 && tid == 0) a.loss[row] = 0.0f;
+    if (grad && tid < nthr) {
+      for (int j = first + tid; j < last; j += nthr) {
+        char* to = grad + (int64_t)(j * per - lead) * es;
+        if (same)
+          zr::st_once(to, make_uint4(0, 0, 0, 0));
+        else
+          for (int i = 0; i < per; ++i) store1<DT>(to, i, 0.0f);
+      }
+      if (single >= 0) store1<DT>(grad, single, 0.0f);
+    }
     return;
   }
-  beyond = __syncthreads_or(beyond);
 
-  // ---- the row into shared memory, and its maximum
-  float m = -INFINITY;
-  auto value_max = [&](int64_t j, uint4 u) {
-    float f[per];
-    W::open(u, f);
-    const int64_t i0 = j * per - lead;
-    if (i0 >= 0 && i0 + per <= n) {
-#pragma unroll
-      for (int i = 0; i < per; ++i) m = fmaxf(m, f[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < per; ++i)
-        if (i0 + i >= 0 && i0 + i < n) m = fmaxf(m, f[i]);
-    }
-  };
-  {
-    constexpr int kAhead = 8;
-    int64_t j = tid;
-    for (; j + (kAhead - 1) * nthr < nw; j += kAhead * nthr) {
-      uint4 u[kAhead];
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) u[i] = ld_row(zw + j + i * nthr);
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        if (j + i * nthr < a.room) words[j + i * nthr] = u[i];
-        value_max(j + i * nthr, u[i]);
-      }
-    }
-    for (; j < nw; j += nthr) {
-      const uint4 u = ld_row(zw + j);
-      if (j < a.room) words[j] = u;
-      value_max(j, u);
-    }
-  }
-  auto word = [&](int64_t j) { return j < a.room ? words[j] : ld_row(zw + j); };
-  t_max = block_all<Max>(t_max, -INFINITY, slots);
-  float p_sum = 0.0f;
-  for (int k = tid; k < a.K; k += nthr) {
-    // an entry of -inf has p = 0; +inf or NaN leaves every p not a number
-    const float e = sid[k] >= 0 ? exp2_fast((sp[k] - t_max) * c) : 0.0f;
-    p_sum += e;
-  }
-  p_sum = block_all<Sum>(p_sum, 0.0f, slots);
-  m = block_all<Max>(m, -INFINITY, slots);
-
-  // ---- sum of 2^(z c - m c). The rounding of m c multiplies every term by the same factor, which
-  // cancels in q and in log q.
-  float mc = m == -INFINITY ? 0.0f : __fmul_rn(m, c);  // all masked so far: the terms are 0, or NaN where z is
-  float sum = 0.0f;
-  for (int64_t j = tid; j < nw; j += nthr) {
-    float f[per];
-    W::open(word(j), f);
-    const int64_t i0 = j * per - lead;
-    float part = 0.0f;
-    if (i0 >= 0 && i0 + per <= n) {
-#pragma unroll
-      for (int i = 0; i < per; ++i) part = __fadd_rn(part, exp2_fast(__fmaf_rn(f[i], c, -mc)));
-    } else {
-#pragma unroll
-      for (int i = 0; i < per; ++i)
-        if (i0 + i >= 0 && i0 + i < n) part = __fadd_rn(part, exp2_fast(__fmaf_rn(f[i], c, -mc)));
-    }
-    sum = __fadd_rn(sum, part);
-  }
-  sum = block_all<Sum>(sum, 0.0f, slots);
+  const bool has = lane < (nthr >> 5);
+  float wm = has ? sh.m[lane & 15] : -INFINITY, m = warp_max(wm);
+  float sum = warp_sum(has ? rescaled(wm, sh.sum[lane & 15], Base(m, c)) : 0.0f);
   if (C > 1) {
     if (tid == 0) {
-      mine[0] = m;
-      mine[1] = sum;
+      sh.row_m = m;
+      sh.row_sum = sum;
     }
     __syncwarp();
     zr::cluster_sync();
-    const uint32_t at = zr::smem_u32(mine);
-    float ms[C], all = -INFINITY;
+    float ms[C];
+    m = -INFINITY;
 #pragma unroll
     for (int r = 0; r < C; ++r) {
-      ms[r] = zr::cluster_load(zr::cluster_addr(at, r));
-      all = fmaxf(all, ms[r]);
+      ms[r] = zr::cluster_load(zr::cluster_addr(zr::smem_u32(&sh.row_m), r));
+      m = fmaxf(m, ms[r]);
     }
-    mc = all == -INFINITY ? 0.0f : __fmul_rn(all, c);
     sum = 0.0f;
 #pragma unroll
-    for (int r = 0; r < C; ++r) {
-      const float s = zr::cluster_load(zr::cluster_addr(at + 4, r));
-      sum = __fadd_rn(sum, ms[r] == -INFINITY ? s : __fmul_rn(s, exp2_fast(__fmul_rn(ms[r], c) - mc)));
-    }
+    for (int r = 0; r < C; ++r)
+      sum = __fadd_rn(sum, rescaled(ms[r], zr::cluster_load(zr::cluster_addr(zr::smem_u32(&sh.row_sum), r)), Base(m, c)));
   }
-  if (beyond) sum = NAN;  // an entry past the vocabulary: the row says so in its loss and its gradient
+  const Base base(m, c);
+  if (sh.beyond) sum = NAN;  // an entry past the vocabulary: the row says so in its loss and its gradient
 
-  // ---- the loss, by the entries in this block's columns; p stays in shared memory
-  const float log_q = log2f(sum), log_p = log2f(p_sum);
+  // ---- the entries in this block's columns: their loss, and the gradient there
+  const float scale = a.scale ? __fmul_rn(a.grad_scale, *a.scale) : a.grad_scale;
+  const float f = __fmul_rn(w, __fmul_rn(a.tau, scale));
+  const float log_q = log2f(sum);
   float loss = 0.0f;
-  for (int k = tid; k < a.K; k += nthr) {
-    const int64_t id = sid[k];
-    const float t = (sp[k] - t_max) * c;
-    const float p = id >= 0 ? __fdiv_rn(exp2_fast(t), p_sum) : 0.0f;
-    sp[k] = p;
-    if (id >= v0 && id < v1 && !(p == 0.0f)) {
-      const int64_t i = lead + (id - v0), j = i / per;
-      const float z = j < a.room ? zr::load1<DT>(smem, i) : zr::load1<DT>(zw, i);
-      loss += p * ((t - log_p) - (__fmaf_rn(z, c, -mc) - log_q)) * kLn2;
+  for (int k = tid; k < a.K; k += blockDim.x) {
+    const int id = sid[k];
+    if (id >= v0 && id < v1) {
+      const float zc = base.exponent(value((int)(id - v0)));
+      if (!(sp[k] == 0.0f)) loss += sp[k] * (own[k] - (zc - log_q)) * kLn2;
+      float p = 0.0f;  // an id may stand twice: each of its entries finds the same sum
+      for (int i = 0; i < a.K4; i += 4) {
+        const int4 four = *reinterpret_cast<const int4*>(sid + i);
+        if (four.x == id) p += sp[i];
+        if (four.y == id) p += sp[i + 1];
+        if (four.z == id) p += sp[i + 2];
+        if (four.w == id) p += sp[i + 3];
+      }
+      own[k] = __fmul_rn(f, __fdiv_rn(exp2_fast(zc), sum) - p);
     }
   }
-  if (beyond) loss = NAN;
-  loss = block_all<Sum>(loss, 0.0f, slots);  // and every p is written
+  loss = warp_sum(loss);
+  if (lane == 0) sh.loss[warp] = loss;
 
-  // ---- the gradient
+  // ---- the gradient: all columns, then the entries' own
   if (grad) {
-    const float scale = a.scale ? __fmul_rn(a.grad_scale, *a.scale) : a.grad_scale;
-    const float f = __fmul_rn(w, __fmul_rn(a.tau, scale));
+    if (nw > a.room) __syncthreads();  // the entries' logits are read before the gradient may replace them
     const float fq = __fdiv_rn(f, sum);
-    // the entries' own columns first, from the logits as they were; stored behind the others
-    for (int k = tid; k < a.K; k += nthr) {
-      const int64_t id = sid[k];
-      if (!(id >= v0 && id < v1)) continue;
-      float p = 0.0f;
-      for (int i = 0; i < a.K; ++i)
-        if (sid[i] == id) p += sp[i];  // an id may stand twice: each of its entries finds the same sum
-      const int64_t i = lead + (id - v0), j = i / per;
-      const float z = j < a.room ? zr::load1<DT>(smem, i) : zr::load1<DT>(zw, i);
-      own[k] = __fmul_rn(f, __fdiv_rn(exp2_fast(__fmaf_rn(z, c, -mc)), sum) - p);
-    }
-    __syncthreads();
-    for (int64_t j = tid; j < nw; j += nthr) {
+    const Two cc(c, c), less(-base.mc, -base.mc), by(fq, fq);
+    for (int j = first + tid; tid < nthr && j < last; j += nthr) {
       float v[per];
       W::open(word(j), v);
+      if (base.fused) {
 #pragma unroll
-      for (int i = 0; i < per; ++i) v[i] = __fmul_rn(exp2_fast(__fmaf_rn(v[i], c, -mc)), fq);
-      const int64_t i0 = j * per - lead;
-      if (same && i0 >= 0 && i0 + per <= n) {
-        zr::st_once(static_cast<char*>(grad) + i0 * es, W::close(v));
+        for (int i = 0; i < per; i += 2) {
+          const Two x = fma2(Two(v[i], v[i + 1]), cc, less);
+          const Two y = mul2(Two(exp2_fast(x.lo()), exp2_fast(x.hi())), by);
+          v[i] = y.lo();
+          v[i + 1] = y.hi();
+        }
       } else {
 #pragma unroll
-        for (int i = 0; i < per; ++i)
-          if (i0 + i >= 0 && i0 + i < n) store1<DT>(grad, i0 + i, v[i]);
+        for (int i = 0; i < per; ++i) v[i] = __fmul_rn(exp2_fast(base.exponent(v[i])), fq);
+      }
+      char* to = grad + (int64_t)(j * per - lead) * es;
+      if (same) {
+        zr::st_once(to, W::close(v));
+      } else {
+#pragma unroll
+        for (int i = 0; i < per; ++i) store1<DT>(to, i, v[i]);
       }
     }
-    __syncthreads();
-    for (int k = tid; k < a.K; k += nthr)
-      if (sid[k] >= v0 && sid[k] < v1) store1<DT>(grad, sid[k] - v0, own[k]);
+    if (single >= 0) store1<DT>(grad, single, __fmul_rn(exp2_fast(base.exponent(z_single)), fq));
   }
-  loss = __fmul_rn(loss, __fmul_rn(w, __fmul_rn(a.tau, a.tau)));
+  __syncthreads();
+  if (grad)
+    for (int k = tid; k < a.K; k += blockDim.x)
+      if (sid[k] >= v0 && sid[k] < v1) store1<DT>(grad, sid[k] - v0, own[k]);
+  if (warp == 0) {
+    loss = warp_sum(lane <= (nthr >> 5) ? sh.loss[lane & 15] : 0.0f);
+    loss = sh.beyond ? NAN : __fmul_rn(loss, __fmul_rn(w, __fmul_rn(a.tau, a.tau)));
+    if (lane == 0) {
+      if (C > 1)
+        sh.row_loss = loss;
+      else
+        a.loss[row] = loss;
+    }
+  }
   if (C > 1) {
-    if (tid == 0) mine[2] = loss;
     __syncwarp();
     zr::cluster_sync();
     if (rank == 0 && tid == 0) {
       loss = 0.0f;
 #pragma unroll
-      for (int r = 0; r < C; ++r) loss += zr::cluster_load(zr::cluster_addr(zr::smem_u32(mine + 2), r));
+      for (int r = 0; r < C; ++r) loss += zr::cluster_load(zr::cluster_addr(zr::smem_u32(&sh.row_loss), r));
       a.loss[row] = loss;
     }
     __syncwarp();
     zr::cluster_sync();  // a block's shared memory stays until rank 0 has read it
-  } else if (tid == 0) {
-    a.loss[row] = loss;
   }
 }
 
@@ -361,7 +470,7 @@ extern "C" zr_status zr_distill_topk(const void* logits, zr_dtype dt, int64_t T,
   zr::clear_error();
   zr::Range range("zr_distill_topk");
   if (!zr::dtype_ok(dt) || !zr::dtype_ok(teacher_dt)) return fail(ZR_ERR_INVALID, "zr_distill_topk: bad dtype");
-  if (T < 0 || V < 1) return fail(ZR_ERR_INVALID, "zr_distill_topk: T must be >= 0 and V >= 1");
+  if (T < 0 || V < 1 || V > 0x7FFFFF00) return fail(ZR_ERR_INVALID, "zr_distill_topk: T must be >= 0 and V in [1, 2^31 - 256]");
   if (K < 1 || K > ZR_DISTILL_MAX_TOP)
     return fail(ZR_ERR_INVALID, "zr_distill_topk: K=%d outside [1, %d]", K, ZR_DISTILL_MAX_TOP);
   if (ldz < V || ldk < K || (grad && ldg < V)) return fail(ZR_ERR_INVALID, "zr_distill_topk: a row stride is under the row");
@@ -386,11 +495,11 @@ extern "C" zr_status zr_distill_topk(const void* logits, zr_dtype dt, int64_t T,
   a.scale = plan ? &plan->ctrl_dev->scale : nullptr;
   a.loss = loss; a.grad = grad;
   a.T = T; a.V = V; a.ldz = ldz; a.ldg = ldg; a.ldk = ldk;
-  a.K = K; a.wide_ids = ids64; a.tdt = (int)teacher_dt;
+  a.K = K; a.K4 = (K + 3) & ~3; a.wide_ids = ids64; a.tdt = (int)teacher_dt;
   a.tau = temperature; a.grad_scale = grad_scale;
   // A row goes to one block where two rows fit an SM's shared memory and there are rows for every
   // SM; longer rows, or few of them, are shared by a cluster.
-  const int fixed = ((K + 1) & ~1) * 4 + K * 12 + 36 * 4;
+  const int fixed = ((K + 3) & ~3) * 12 + (int)sizeof(Shared);
   const int64_t half = zr::kSmemMost / 2 - 1024 - fixed;
   int split = 1;
   while (split < 8 && ((V / split) * es > half || (T * split <= sms && V / split >= 4096))) split *= 2;
@@ -401,7 +510,8 @@ extern "C" zr_status zr_distill_topk(const void* logits, zr_dtype dt, int64_t T,
   const int64_t most = (zr::kSmemMost - fixed) / 16;
   a.room = (int)(room < most ? room : most);  // what does not fit is read again
   int threads = 64;
-  while (threads < kMaxThreads && threads * 4 < room) threads *= 2;
+  while (threads < 256 && threads * 4 < room) threads *= 2;
+  threads = threads * 4 < room ? kMaxThreads : threads + 32;
   const int smem = a.room * 16 + fixed;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dt == ZR_F16) return launch_split<zr::DT_F16>(a, split, threads, smem, s);

@@ -101,19 +101,11 @@ __device__ __forceinline__ void mx_decode8(uint32_t w, float v[8]) {
   }
 }
 
-// 16 bytes at any address that is a multiple of 2, out of the one or two aligned words that
-// hold them; no word is read that holds none of the 16 bytes.
-__device__ __forceinline__ uint4 load16(const char* p) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-  const uint32_t sh = (uint32_t)a & 15u;
-  const uint4* w = reinterpret_cast<const uint4*>(a - sh);
-  const uint4 lo = ld_once(w);
-  if (sh == 0) return lo;
-  const uint4 hi = ld_once(w + 1);
+// Bytes sh .. sh + 15 of the 32 bytes lo, hi (sh even, 0 to 15).
+__device__ __forceinline__ uint4 shift16(uint4 lo, uint4 hi, uint32_t sh) {
   uint32_t v[7] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z};
-  uint32_t last = hi.w;
   if (sh & 8) {
-    v[0] = v[2]; v[1] = v[3]; v[2] = v[4]; v[3] = v[5]; v[4] = v[6]; v[5] = last;
+    v[0] = v[2]; v[1] = v[3]; v[2] = v[4]; v[3] = v[5]; v[4] = v[6]; v[5] = hi.w;
   }
   if (sh & 4) {
     v[0] = v[1]; v[1] = v[2]; v[2] = v[3]; v[3] = v[4]; v[4] = v[5];
@@ -121,6 +113,17 @@ __device__ __forceinline__ uint4 load16(const char* p) {
   const uint32_t bits = (sh & 3u) * 8u;
   return make_uint4(__funnelshift_r(v[0], v[1], bits), __funnelshift_r(v[1], v[2], bits),
                     __funnelshift_r(v[2], v[3], bits), __funnelshift_r(v[3], v[4], bits));
+}
+
+// 16 bytes at any address, out of the one or two aligned words that hold them; no word is read
+// that holds none of the 16 bytes.
+__device__ __forceinline__ uint4 load16(const char* p) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  const uint32_t sh = (uint32_t)a & 15u;
+  const uint4* w = reinterpret_cast<const uint4*>(a - sh);
+  const uint4 lo = ld_once(w);
+  if (sh == 0) return lo;
+  return shift16(lo, ld_once(w + 1), sh);
 }
 
 }  // namespace zr

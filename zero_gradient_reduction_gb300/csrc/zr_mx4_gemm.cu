@@ -5,9 +5,12 @@
 // one-dimensional bulk copies: 128 rows x 256 columns of codes already in the swizzle that the
 // tensor cores read, and their scales already in the order that one copy takes to tensor memory.
 // Products accumulate in fp32.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "zr_internal.h"
 #include "zr_launch.h"
@@ -23,23 +26,29 @@ namespace {
 __device__ int g_gave_up;
 
 // ------------------------------------------------------------------ the general product
-// One block per streaming multiprocessor, persistent over output tiles of 128 x BN: a producer
-// warp fills a ring of stages (256 columns of K each), one thread issues the products, four warps
-// bring the accumulators out, 32 lanes each.
+// Persistent blocks of six warps: a producer fills a ring of stages (256 columns of K each), one
+// thread issues the products, four warps bring the accumulators out, 32 lanes each, while the next
+// tile's products run. Two forms, PAIR or not:
+//   a block alone takes 128 x 128 of the output;
+//   a pair of blocks (a cluster of two on neighbouring multiprocessors) takes 256 x 256 as one
+//   product of M = 256: each holds 128 rows of A and half of the rows of B, so that 32 KB of codes
+//   come in for 128 x 256 of output where a block alone would need 48 KB.
 constexpr int kGemmThreads = 192;
 constexpr int kStagePad = 1024;  // the operands' swizzle repeats every 1024 bytes
 
-template <int BN>
+template <bool PAIR>
 struct Gemm {
-  static constexpr int kB = BN / 128;                                  // MX4 tiles along N
-  static constexpr int kStageBytes = zr::kMxTileBytes * (1 + kB);
-  static constexpr int kStages = BN == 256 ? 4 : 6;
-  // accumulators: two of BN columns; at BN = 256 they share 24 columns, or the scales would find
-  // no room in the 512. The shared ones are read first.
-  static constexpr int kD1 = BN == 256 ? 232 : 128;
-  static constexpr int kLag = BN == 256 ? 1 : 2;  // an accumulator waits for the one so many turns before it
-  static constexpr int kScaleA = BN == 256 ? 488 : 256, kScaleB = kScaleA + 8;
-  static constexpr int kStageOut = 32 * 144;                           // an epilogue warp's rows on their way out
+  static constexpr int kRows = PAIR ? 256 : 128, kCols = PAIR ? 256 : 128;  // output tile
+  // a stage: A codes and scales, this block's B codes, the scales of all of the tile's B rows
+  static constexpr int kBCodes = zr::kMxTileBytes, kBScales = kBCodes + zr::kMxCodeBytes;
+  static constexpr int kStageBytes = kBScales + (PAIR ? 2 : 1) * zr::kMxScaleBytes;
+  static constexpr int kStages = PAIR ? 5 : 6;
+  // Tensor memory: two accumulators of kCols columns, 8 columns of A's scales, and B's. The pair's
+  // accumulators share 24 columns, or the scales would find no room in the 512: those are read
+  // first, and the next tile's products wait for them alone.
+  static constexpr int kD1 = PAIR ? 232 : 128, kScaleA = PAIR ? 488 : 256, kScaleB = kScaleA + 8;
+  static constexpr int kLag = PAIR ? 1 : 2;  // an accumulator waits for the one so many turns before it
+  static constexpr int kStageOut = 32 * 144;  // an epilogue warp's rows on their way out
   static constexpr int kSmem = kStages * kStageBytes + 4 * kStageOut + 256 + kStagePad;
 };
 
@@ -52,6 +61,15 @@ struct GemmArgs {
   int mt, nt;      // output tiles
   int vec;         // rows of out are 16-byte aligned
 };
+
+// How a pair's copies see the two matrices: rows of 128 bytes, 136 to an MX4 tile (128 of codes, 8 of
+// scales), and how many rows a copy takes. A copy through a map may report to the other block's
+// barrier; the tile's bytes are in their place already, so the maps say nothing of swizzles.
+constexpr int kTileLines = zr::kMxTileBytes / 128;
+struct PairMaps {
+  CUtensorMap a_tile, b_codes, b_scales;
+};
+struct NoMaps {};
 
 // Output tile of a number: groups of up to 32 tiles of rows, and within a group the rows first, so
 // that the blocks at work at one time share few tiles of B and a band of A.
@@ -107,22 +125,31 @@ __device__ __forceinline__ void rows_out(const GemmArgs& g, char* stage, const u
   __syncwarp();
 }
 
-template <int BN, int DT>
-__global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_constant__ GemmArgs g) {
-  using G = Gemm<BN>;
+template <bool PAIR>
+using Maps = typename std::conditional<PAIR, PairMaps, NoMaps>::type;
+
+template <bool PAIR, int DT>
+__global__ void __launch_bounds__(kGemmThreads, 1)
+    gemm_kernel(const __grid_constant__ GemmArgs g, const __grid_constant__ Maps<PAIR> maps) {
+  using G = Gemm<PAIR>;
   extern __shared__ char smem_raw[];
-  char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + kStagePad - 1) & ~(uintptr_t)(kStagePad - 1));
+  // the same offset in both blocks of a pair: the dynamic part begins at the same address in each
+  char* smem = smem_raw + ((kStagePad - (zr::smem_u32(smem_raw) & (kStagePad - 1))) & (kStagePad - 1));
   const uint32_t stages = zr::smem_u32(smem);
   char* staging = smem + G::kStages * G::kStageBytes;
   char* tail = staging + 4 * G::kStageOut;
+  // full: a stage's copies have landed (a pair's, in both blocks: the first block's barrier counts them
+  // all); empty: its products are done; done: an accumulator is complete; freed: it may be written again
   const uint32_t full = zr::smem_u32(tail), empty = full + 8 * G::kStages, done = empty + 8 * G::kStages,
                  freed = done + 16, drained = freed + 16;
-  volatile int* gave_up = reinterpret_cast<volatile int*>(tail + 192);
-  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(tail + 200);
+  volatile int* gave_up = reinterpret_cast<volatile int*>(tail + 224);
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(tail + 232);
   const int warp = threadIdx.x >> 5;
+  const int rank = PAIR ? (int)zr::cluster_rank() : 0;
+  const int first = PAIR ? blockIdx.x >> 1 : blockIdx.x, step = PAIR ? gridDim.x >> 1 : gridDim.x;
 
   if (warp == 0) {
-    zr::tmem_alloc(zr::smem_u32(tmem_at), 512);
+    zr::tmem_alloc<PAIR>(zr::smem_u32(tmem_at), 512);
   } else if (threadIdx.x == 32) {
     for (int s = 0; s < G::kStages; ++s) {
       zr::bar_init(full + 8 * s, 1);
@@ -130,122 +157,152 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
     }
     for (int d = 0; d < 2; ++d) {
       zr::bar_init(done + 8 * d, 1);
-      zr::bar_init(freed + 8 * d, 4);
+      zr::bar_init(freed + 8 * d, PAIR ? 8 : 4);
     }
     zr::bar_init(drained, 1);
     zr::bar_init_fence();
     *gave_up = 0;
   }
+  __syncwarp();
   zr::tmem_fence_before();
-  __syncthreads();
+  if (PAIR)
+    zr::cluster_sync();
+  else
+    __syncthreads();
   zr::tmem_fence_after();
   const uint32_t tmem = *tmem_at;
   const int tiles = g.mt * g.nt;
-  const int64_t row_bytes = (int64_t)g.kt * zr::kMxTileBytes;  // a row of tiles
+  const int64_t row_bytes = (int64_t)g.kt * zr::kMxTileBytes;  // a row of MX4 tiles
 
   if (warp == 0) {
     if (zr::elect_one()) {
       uint32_t it = 0;
       bool ok = true;
-      for (int id = blockIdx.x; id < tiles && ok; id += gridDim.x) {
+      for (int id = first; id < tiles && ok; id += step) {
         int m, n;
         tile_of(g, id, m, n);
-        const uint8_t* a = g.a + m * row_bytes;
-        const uint8_t* b = g.b + (int64_t)n * G::kB * row_bytes;
-        // the last tile of B may reach past its rows: what is missing is not read
-        const bool two = G::kB == 2 && ((int64_t)n * BN + 128 < g.N);
-        const uint32_t bytes = zr::kMxTileBytes * (two ? 3 : 2);
+        // a pair's tile may reach past the rows of A or B by an MX4 tile, which is not read then:
+        // what the products make of the bytes in its place is not stored
+        const int64_t am = PAIR ? 2 * (int64_t)m + rank : m, bn = PAIR ? 2 * (int64_t)n : n;
+        const bool has_a = !PAIR || am * 128 < g.M, second = PAIR && (bn + 1) * 128 < g.N;
+        const bool has_b = !PAIR || rank == 0 || second;
+        const uint8_t *a = g.a + am * row_bytes, *b = g.b + bn * row_bytes;
+        const int a_line = (int)(am * g.kt) * kTileLines, b_line = (int)(bn * g.kt) * kTileLines;
+        // the first block expects the pair's bytes
+        const bool peer_a = PAIR && (am + 1) * 128 < g.M;
+        const uint32_t bytes = PAIR ? zr::kMxTileBytes * (peer_a ? 2 : 1) + (zr::kMxCodeBytes + 2 * zr::kMxScaleBytes) * (second ? 2 : 1)
+                                    : 2 * zr::kMxTileBytes;
         for (int k = 0; k < g.kt; ++k, ++it) {
           const int s = it % G::kStages;
-          if (it >= G::kStages && !(ok = zr::bar_wait(empty + 8 * s, (it / G::kStages - 1) & 1, gave_up))) break;
-          const uint32_t at = stages + s * G::kStageBytes, bar = full + 8 * s;
-          zr::bar_expect(bar, bytes);
-          zr::bulk_copy(at, a + (int64_t)k * zr::kMxTileBytes, zr::kMxTileBytes, bar);
-          const uint8_t* b0 = b + (int64_t)k * zr::kMxTileBytes;
-          const uint32_t bs = at + zr::kMxTileBytes;
-          if (G::kB == 1) {
-            zr::bulk_copy(bs, b0, zr::kMxTileBytes, bar);
-          } else {  // the codes of both tiles first, so that they are one operand of 256 rows
-            zr::bulk_copy(bs, b0, zr::kMxCodeBytes, bar);
-            zr::bulk_copy(bs + 2 * zr::kMxCodeBytes, b0 + zr::kMxCodeBytes, zr::kMxScaleBytes, bar);
-            if (two) {
-              zr::bulk_copy(bs + zr::kMxCodeBytes, b0 + row_bytes, zr::kMxCodeBytes, bar);
-              zr::bulk_copy(bs + 2 * zr::kMxCodeBytes + zr::kMxScaleBytes, b0 + row_bytes + zr::kMxCodeBytes,
-                            zr::kMxScaleBytes, bar);
-            }
+          if (it >= G::kStages && !(ok = zr::bar_wait<PAIR>(empty + 8 * s, (it / G::kStages - 1) & 1, gave_up))) break;
+          const uint32_t at = stages + s * G::kStageBytes;
+          if constexpr (PAIR) {
+            const uint32_t bar = zr::cluster_addr(full + 8 * s, 0);
+            const int line = k * kTileLines;
+            if (rank == 0) zr::bar_expect(full + 8 * s, bytes);
+            if (has_a) zr::pair_copy(at, &maps.a_tile, 0, a_line + line, bar);
+            if (has_b) zr::pair_copy(at + G::kBCodes, &maps.b_codes, 0, b_line + (rank * g.kt + k) * kTileLines, bar);
+            zr::pair_copy(at + G::kBScales, &maps.b_scales, 0, b_line + line + 128, bar);
+            if (second)
+              zr::pair_copy(at + G::kBScales + zr::kMxScaleBytes, &maps.b_scales, 0,
+                            b_line + (g.kt + k) * kTileLines + 128, bar);
+          } else {
+            const int64_t ko = (int64_t)k * zr::kMxTileBytes;
+            zr::bar_expect(full + 8 * s, bytes);
+            zr::bulk_copy(at, a + ko, zr::kMxTileBytes, full + 8 * s);
+            zr::bulk_copy(at + G::kBCodes, b + ko, zr::kMxTileBytes, full + 8 * s);
           }
         }
       }
-      // nothing may be in flight to this block's shared memory when it ends
-      int never = 0;
-      for (uint32_t i = it < G::kStages ? 0 : it - G::kStages; i < it; ++i)
-        zr::bar_wait(full + 8 * (i % G::kStages), (i / G::kStages) & 1, &never);
+      // the block may end once its copies have landed and its stages' products are done
+      const uint32_t from = it < G::kStages ? 0 : it - G::kStages;
+      for (uint32_t i = from; i < it && ok; ++i)
+        ok = zr::bar_wait<PAIR>(empty + 8 * (i % G::kStages), (i / G::kStages) & 1, gave_up);
+      if (!ok && rank == 0) {  // (the first block waits for the pair's copies; the other ends after it)
+        int never = 0;
+        for (uint32_t i = from; i < it; ++i) zr::bar_wait(full + 8 * (i % G::kStages), (i / G::kStages) & 1, &never);
+      }
     }
   } else if (warp == 1) {
-    if (zr::elect_one()) {
+    if (rank == 0 && zr::elect_one()) {  // a pair's products are issued by its first block
       uint32_t it = 0, turn = 0;
       bool ok = true;
-      for (int id = blockIdx.x; id < tiles && ok; id += gridDim.x, ++turn) {
-        int m, n;
-        tile_of(g, id, m, n);
-        const bool two = G::kB == 2 && ((int64_t)n * BN + 128 < g.N);
-        const int cols = G::kB == 2 && !two ? 128 : BN;
+      for (int id = first; id < tiles && ok; id += step, ++turn) {
         const uint32_t d = tmem + (turn & 1) * G::kD1;
         // the columns that it shares with the one before have been read, and all of the one before that
         const uint32_t past = turn - G::kLag;
-        if (turn >= G::kLag && !(ok = zr::bar_wait(freed + 8 * (past & 1), (past >> 1) & 1, gave_up))) break;
+        if (turn >= G::kLag && !(ok = zr::bar_wait<PAIR>(freed + 8 * (past & 1), (past >> 1) & 1, gave_up))) break;
         zr::tmem_fence_after();
         for (int k = 0; k < g.kt; ++k, ++it) {
           const int s = it % G::kStages;
-          if (!(ok = zr::bar_wait(full + 8 * s, (it / G::kStages) & 1, gave_up))) break;
+          if (!(ok = zr::bar_wait<PAIR>(full + 8 * s, (it / G::kStages) & 1, gave_up))) break;
           zr::tmem_fence_after();
-          const uint32_t at = stages + s * G::kStageBytes, bs = at + zr::kMxTileBytes;
-          const uint32_t as = at + zr::kMxCodeBytes, bss = bs + G::kB * zr::kMxCodeBytes;
+          const uint32_t at = stages + s * G::kStageBytes;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            zr::copy_scales(tmem + G::kScaleA + 4 * h, zr::scale_rows(as + 512 * h));
-            for (int t = 0; t < (two ? 2 : 1); ++t)
-              zr::copy_scales(tmem + G::kScaleB + 4 * (G::kB * h + t), zr::scale_rows(bss + t * zr::kMxScaleBytes + 512 * h));
+            zr::copy_scales<PAIR>(tmem + G::kScaleA + 4 * h, zr::scale_rows(at + zr::kMxCodeBytes + 512 * h));
+#pragma unroll
+            for (int t = 0; t < (PAIR ? 2 : 1); ++t)
+              zr::copy_scales<PAIR>(tmem + G::kScaleB + 4 * ((PAIR ? 2 : 1) * h + t),
+                                    zr::scale_rows(at + G::kBScales + t * zr::kMxScaleBytes + 512 * h));
           }
-          const uint64_t da = zr::swizzled_operand(at), db = zr::swizzled_operand(bs);
+          const uint64_t da = zr::swizzled_operand(at), db = zr::swizzled_operand(at + G::kBCodes);
 #pragma unroll
           for (int q = 0; q < 4; ++q)  // 64 columns, 32 bytes of each row, at a time
-            zr::mx_mma(d, da + 2 * q, db + 2 * q, zr::mx_product(128, cols, q & 1), tmem + G::kScaleA + 4 * (q >> 1),
-                       tmem + G::kScaleB + 4 * G::kB * (q >> 1), (k | q) != 0);
-          zr::mma_commit(empty + 8 * s);
+            zr::mx_mma<PAIR>(d, da + 2 * q, db + 2 * q, zr::mx_product(G::kRows, G::kCols, q & 1),
+                             tmem + G::kScaleA + 4 * (q >> 1), tmem + G::kScaleB + 4 * (PAIR ? 2 : 1) * (q >> 1),
+                             (k | q) != 0);
+          if (PAIR)
+            zr::pair_commit(empty + 8 * s, 3);
+          else
+            zr::mma_commit(empty + 8 * s);
         }
-        if (ok) zr::mma_commit(done + 8 * (turn & 1));
+        if (ok) {
+          if (PAIR)
+            zr::pair_commit(done + 8 * (turn & 1), 3);
+          else
+            zr::mma_commit(done + 8 * (turn & 1));
+        }
       }
       if (!ok) {  // no product may be in flight when the tensor memory is given back
         int never = 0;
-        zr::mma_commit(drained);
+        if (PAIR)
+          zr::pair_commit(drained, 1);
+        else
+          zr::mma_commit(drained);
         zr::bar_wait(drained, 0, &never);
       }
     }
   } else {
     const int lanes = (warp & 3) * 32;  // the lanes of tensor memory that this warp may read
     char* stage = staging + (warp & 3) * G::kStageOut;
-    constexpr int kOnce = DT == zr::DT_F32 ? 32 : 64, kChunks = BN / kOnce;
+    constexpr int kOnce = DT == zr::DT_F32 ? 32 : 64, kChunks = G::kCols / kOnce;
+    const uint32_t freed_at = PAIR ? zr::cluster_addr(freed, 0) : freed;
     uint32_t turn = 0;
-    for (int id = blockIdx.x; id < tiles; id += gridDim.x, ++turn) {
+    for (int id = first; id < tiles; id += step, ++turn) {
       int m, n;
       tile_of(g, id, m, n);
-      if (!__all_sync(0xFFFFFFFFu, zr::bar_wait(done + 8 * (turn & 1), (turn >> 1) & 1, gave_up))) break;
+      if (!__all_sync(0xFFFFFFFFu, zr::bar_wait<PAIR>(done + 8 * (turn & 1), (turn >> 1) & 1, gave_up))) break;
       zr::tmem_fence_after();
       const uint32_t d = tmem + (turn & 1) * G::kD1 + ((uint32_t)lanes << 16);
-      const int64_t row0 = (int64_t)m * 128 + lanes;
+      const int64_t row0 = (int64_t)m * G::kRows + rank * 128 + lanes;
 #pragma unroll 1
       for (int c = 0; c < kChunks; ++c) {
         // the first accumulator's last columns are the second's first
         const int at = (turn & 1) ? c : kChunks - 1 - c;
-        const int64_t col = (int64_t)n * BN + at * kOnce;
+        const int64_t col = (int64_t)n * G::kCols + at * kOnce;
         uint32_t v[kOnce];
         zr::tmem_load32(d + at * kOnce, *reinterpret_cast<uint32_t(*)[32]>(v));
         if (kOnce == 64) zr::tmem_load32(d + at * kOnce + 32, *reinterpret_cast<uint32_t(*)[32]>(v + kOnce - 32));
-        if (c == (BN == 256 ? 0 : kChunks - 1)) {
+        if (c == (PAIR ? 0 : kChunks - 1)) {
           zr::tmem_fence_before();
           __syncwarp();
-          if (zr::elect_one()) zr::bar_arrive(freed + 8 * (turn & 1));
+          if (zr::elect_one()) {
+            if (PAIR)
+              zr::cluster_arrive(freed_at + 8 * (turn & 1));
+            else
+              zr::bar_arrive(freed_at + 8 * (turn & 1));
+          }
         }
         if (row0 < g.M && col < g.N) rows_out<DT>(g, stage, v, row0, col);
       }
@@ -253,10 +310,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
   }
   __syncwarp();
   zr::tmem_fence_before();
-  __syncthreads();
+  if (PAIR)
+    zr::cluster_sync();  // neither block's shared or tensor memory goes before the other is done with it
+  else
+    __syncthreads();
   zr::tmem_fence_after();
   if (threadIdx.x == 0 && *gave_up) g_gave_up = 1;
-  if (warp == 0) zr::tmem_free(tmem, 512);
+  if (warp == 0) zr::tmem_free<PAIR>(tmem, 512);
 }
 
 // ------------------------------------------------------------------ the few-token form
@@ -401,7 +461,7 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
         for (int q = 0; q < 4; ++q)
           zr::mx_mma(tmem, da + 2 * q, db + 2 * q, zr::mx_product(128, 16, q & 1), scale_a + 4 * (q >> 1),
                      scale_b + 4 * (q >> 1), (k | q) != 0);
-        zr::mma_commit(empty + 8 * s);
+        if (k + kFewStages < nk) zr::mma_commit(empty + 8 * s);
       }
       zr::mma_commit(done);  // after a wait that gave up too: nothing may be in flight at the end
     }
@@ -465,12 +525,51 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
   if (warp == 0) zr::tmem_free(tmem, 32);
 }
 
-template <int BN, int DT>
-zr_status launch_gemm(const GemmArgs& g, int grid, cudaStream_t s) {
+// The driver's encoder of tensor maps, looked up once.
+PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found);
+    return (PFN_cuTensorMapEncodeTiled_v12000)(e == cudaSuccess && found == cudaDriverEntryPointSuccess ? p : nullptr);
+  }();
+  return fn;
+}
+
+// A map of an MX4 matrix's `tiles` tiles as lines of 128 bytes, copied `lines` at a time.
+bool encode_lines(CUtensorMap* map, const void* q, int64_t tiles, int lines) {
+  const cuuint64_t size[2] = {128, (cuuint64_t)(tiles * kTileLines)}, stride[1] = {128};
+  const cuuint32_t box[2] = {128, (cuuint32_t)lines}, step[2] = {1, 1};
+  return map_encoder()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(q), size, stride, box, step,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool PAIR, int DT>
+zr_status launch_gemm(const GemmArgs& g, int blocks, cudaStream_t s) {
   static zr::SmemAllowance allowance;
-  if (zr_status st = allowance.allow("zr_mx4_matmul", (const void*)gemm_kernel<BN, DT>, Gemm<BN>::kSmem)) return st;
-  gemm_kernel<BN, DT><<<grid, kGemmThreads, Gemm<BN>::kSmem, s>>>(g);
-  return zr::launch_status("zr_mx4_matmul");
+  if (zr_status st = allowance.allow("zr_mx4_matmul", (const void*)gemm_kernel<PAIR, DT>, Gemm<PAIR>::kSmem)) return st;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3((unsigned)blocks);
+  c.blockDim = dim3(kGemmThreads);
+  c.dynamicSmemBytes = (size_t)Gemm<PAIR>::kSmem;
+  c.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim = {2, 1, 1};
+  c.attrs = &at;
+  c.numAttrs = PAIR ? 1 : 0;
+  Maps<PAIR> maps;
+  if constexpr (PAIR) {
+    const int64_t a_tiles = zr::mx_tiles(g.M, zr::kMxRows) * g.kt, b_tiles = zr::mx_tiles(g.N, zr::kMxRows) * g.kt;
+    if (!map_encoder() || !encode_lines(&maps.a_tile, g.a, a_tiles, kTileLines) ||
+        !encode_lines(&maps.b_codes, g.b, b_tiles, zr::kMxRows) ||
+        !encode_lines(&maps.b_scales, g.b, b_tiles, zr::kMxScaleBytes / 128))
+      return fail(ZR_ERR_CUDA, "zr_mx4_matmul: the driver gave no tensor map");
+  }
+  cudaError_t e = cudaLaunchKernelEx(&c, gemm_kernel<PAIR, DT>, g, maps);
+  if (e != cudaSuccess) return fail(ZR_ERR_CUDA, "zr_mx4_matmul: launch failed: %s", cudaGetErrorString(e));
+  return ZR_OK;
 }
 
 zr_status matmul(const char* what, const void* a, int64_t M, const void* b, int64_t N, int64_t K, void* out, zr_dtype dt,
@@ -487,22 +586,26 @@ zr_status matmul(const char* what, const void* a, int64_t M, const void* b, int6
   g.b = static_cast<const uint8_t*>(b);
   g.out = out;
   g.M = M; g.N = N; g.ldo = ldo;
-  const int64_t mt = zr::mx_tiles(M, 128), kt = zr::mx_tiles(K, zr::kMxCols);
-  const bool wide = mt * zr::mx_tiles(N, 256) >= sms;
-  const int64_t nt = zr::mx_tiles(N, wide ? 256 : 128);
+  const int64_t kt = zr::mx_tiles(K, zr::kMxCols);
+  // pairs where each gets a tile (and 32 bits hold a matrix's lines)
+  const int64_t most = 0x7FFFFFFF / kTileLines;
+  const bool pair = zr::mx_tiles(M, 256) * zr::mx_tiles(N, 256) >= sms / 2 && zr::mx_tiles(M, 128) <= most / kt &&
+                    zr::mx_tiles(N, 128) <= most / kt;
+  const int64_t mt = zr::mx_tiles(M, pair ? 256 : 128), nt = zr::mx_tiles(N, pair ? 256 : 128);
   if (kt > 0x7FFFFFFF || nt > (1 << 25) || mt > 0x3FFFFFFF / nt)
     return fail(ZR_ERR_UNSUPPORTED, "%s: the product has too many tiles", what);
   g.kt = (int)kt; g.mt = (int)mt; g.nt = (int)nt;
   g.vec = ldo * es % 16 == 0;
-  const int grid = (int)(mt * nt < sms ? mt * nt : sms);
-  if (wide) {
-    if (dt == ZR_F16) return launch_gemm<256, zr::DT_F16>(g, grid, s);
-    if (dt == ZR_BF16) return launch_gemm<256, zr::DT_BF16>(g, grid, s);
-    return launch_gemm<256, zr::DT_F32>(g, grid, s);
+  if (pair) {
+    const int blocks = 2 * (int)(mt * nt < sms / 2 ? mt * nt : sms / 2);
+    if (dt == ZR_F16) return launch_gemm<true, zr::DT_F16>(g, blocks, s);
+    if (dt == ZR_BF16) return launch_gemm<true, zr::DT_BF16>(g, blocks, s);
+    return launch_gemm<true, zr::DT_F32>(g, blocks, s);
   }
-  if (dt == ZR_F16) return launch_gemm<128, zr::DT_F16>(g, grid, s);
-  if (dt == ZR_BF16) return launch_gemm<128, zr::DT_BF16>(g, grid, s);
-  return launch_gemm<128, zr::DT_F32>(g, grid, s);
+  const int blocks = (int)(mt * nt < sms ? mt * nt : sms);
+  if (dt == ZR_F16) return launch_gemm<false, zr::DT_F16>(g, blocks, s);
+  if (dt == ZR_BF16) return launch_gemm<false, zr::DT_BF16>(g, blocks, s);
+  return launch_gemm<false, zr::DT_F32>(g, blocks, s);
 }
 
 template <int S>

@@ -259,47 +259,75 @@ struct DequantArgs {
   const uint8_t* q;
   void* out;
   int64_t rows, cols, ld, tiles;  // tiles along the columns
-  int vec;                        // the rows of out are 16-byte aligned
 };
 
-// A warp takes a row of a tile (128 bytes of codes), a lane eight of its values; a block the
-// 128 rows of a tile.
+constexpr int kDequantRows = 32, kRowsPerWarp = kDequantRows / (kThreads / 32);
+
+// A block takes 32 rows of a tile, a warp four of them at once (their loads in flight together), a
+// lane eight values of a row. A row that does not begin on a 16-byte boundary goes through shared
+// memory, so that it still leaves in whole aligned words but for its ends.
 template <int DT>
 __global__ void __launch_bounds__(kThreads) dequant_kernel(const __grid_constant__ DequantArgs a) {
-  const int64_t rt = blockIdx.x / a.tiles, ct = blockIdx.x - rt * a.tiles;
-  const uint8_t* tile = a.q + (int64_t)blockIdx.x * zr::kMxTileBytes;
-  const int lane = threadIdx.x & 31, j = lane >> 2;
-  const int64_t c = ct * zr::kMxCols + lane * 8;
-  if (c >= a.cols) return;
-#pragma unroll 4
-  for (int r = threadIdx.x >> 5; r < zr::kMxRows; r += kThreads / 32) {
-    const int64_t row = rt * zr::kMxRows + r;
+  constexpr int es = DT == zr::DT_F32 ? 4 : 2, kRowBytes = zr::kMxCols * es;
+  __shared__ __align__(16) char staging[kThreads / 32][kRowBytes + 16];
+  const int64_t t = blockIdx.x >> 2, rt = t / a.tiles, ct = t - rt * a.tiles;
+  const uint8_t* tile = a.q + t * zr::kMxTileBytes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane >> 2;
+  const int64_t c0 = ct * zr::kMxCols;
+  const int n = (int)(a.cols - c0 < zr::kMxCols ? a.cols - c0 : zr::kMxCols);  // columns of this tile
+  const int r0 = (int)(blockIdx.x & 3) * kDequantRows + warp;
+  uint32_t codes[kRowsPerWarp];
+  int byte[kRowsPerWarp];
+#pragma unroll
+  for (int i = 0; i < kRowsPerWarp; ++i) {
+    const int r = r0 + i * (kThreads / 32);
+    codes[i] = *reinterpret_cast<const uint32_t*>(tile + zr::mx_chunk_at(r, j) + (lane & 3) * 4);
+    byte[i] = tile[zr::mx_scale_at(r, j)];
+  }
+#pragma unroll
+  for (int i = 0; i < kRowsPerWarp; ++i) {
+    const int64_t row = rt * zr::kMxRows + r0 + i * (kThreads / 32);
     if (row >= a.rows) return;
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(tile + zr::mx_chunk_at(r, j) + (lane & 3) * 4);
-    const float s = zr::mx_scale_value(tile[zr::mx_scale_at(r, j)]);
     float v[8];
-    zr::mx_decode8(w, v);
+    zr::mx_decode8(codes[i], v);
+    const float s = zr::mx_scale_value(byte[i]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], s);
-    const int64_t e = row * a.ld + c;
-    if (a.vec && c + 8 <= a.cols) {
-      if (DT == zr::DT_F32) {
-        float* o = static_cast<float*>(a.out) + e;
-        zr::st_once_f4(o, make_float4(v[0], v[1], v[2], v[3]));
-        zr::st_once_f4(o + 4, make_float4(v[4], v[5], v[6], v[7]));
-      } else {
-        zr::st_once(static_cast<uint16_t*>(a.out) + e, zr::pack8<DT>(v));
-      }
+    for (int k = 0; k < 8; ++k) v[k] = __fmul_rn(v[k], s);
+    uint4 w[es / 2];
+    if constexpr (DT == zr::DT_F32) {
+      w[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+      w[1] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
     } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c + i < a.cols) {
-          if (DT == zr::DT_F32)
-            static_cast<float*>(a.out)[e + i] = v[i];
-          else
-            static_cast<uint16_t*>(a.out)[e + i] = zr::from_f32<DT>(v[i]);
-        }
+      w[0] = zr::pack8<DT>(v);
     }
+    char* out = static_cast<char*>(a.out) + (row * a.ld + c0) * es;
+    const int lead = (int)(reinterpret_cast<uintptr_t>(out) & 15);
+    if (lead == 0 && n == zr::kMxCols) {
+#pragma unroll
+      for (int k = 0; k < es / 2; ++k) zr::st_once(out + (lane * (es / 2) + k) * 16, w[k]);
+      continue;
+    }
+    char* stage = staging[warp];
+#pragma unroll
+    for (int k = 0; k < es / 2; ++k) *reinterpret_cast<uint4*>(stage + (lane * (es / 2) + k) * 16) = w[k];
+    __syncwarp();
+    // words of memory that the row covers: the k-th holds bytes 16k - lead .. of it
+    const int bytes = n * es;
+    for (int k = lane; k * 16 < lead + bytes; k += 32) {
+      const int from = k * 16 - lead;
+      if (from >= 0 && from + 16 <= bytes) {
+        const uint4* at = reinterpret_cast<const uint4*>(stage + (from & ~15));
+        zr::st_once(out + from, zr::shift16(at[0], at[1], (uint32_t)from & 15u));
+      } else {
+        for (int b = from < 0 ? 0 : from; b < from + 16 && b < bytes; b += es) {
+          if (es == 4)
+            *reinterpret_cast<uint32_t*>(out + b) = *reinterpret_cast<const uint32_t*>(stage + b);
+          else
+            *reinterpret_cast<uint16_t*>(out + b) = *reinterpret_cast<const uint16_t*>(stage + b);
+        }
+      }
+    }
+    __syncwarp();
   }
 }
 
@@ -372,12 +400,11 @@ extern "C" zr_status zr_mx4_dequantize(const void* q, int64_t rows, int64_t cols
   a.out = out;
   a.rows = rows; a.cols = cols; a.ld = ld;
   a.tiles = zr::mx_tiles(cols, zr::kMxCols);
-  a.vec = ld * (dt == ZR_F32 ? 4 : 2) % 16 == 0;
-  const int64_t tiles = zr::mx_tiles(rows, zr::kMxRows) * a.tiles;
-  if (tiles > 0x7FFFFFFF) return fail(ZR_ERR_UNSUPPORTED, "zr_mx4_dequantize: matrix too large for one launch");
+  const int64_t blocks = zr::mx_tiles(rows, zr::kMxRows) * a.tiles * (zr::kMxRows / kDequantRows);
+  if (blocks > 0x7FFFFFFF) return fail(ZR_ERR_UNSUPPORTED, "zr_mx4_dequantize: matrix too large for one launch");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (dt == ZR_F16) dequant_kernel<zr::DT_F16><<<(unsigned)tiles, kThreads, 0, s>>>(a);
-  else if (dt == ZR_BF16) dequant_kernel<zr::DT_BF16><<<(unsigned)tiles, kThreads, 0, s>>>(a);
-  else dequant_kernel<zr::DT_F32><<<(unsigned)tiles, kThreads, 0, s>>>(a);
+  if (dt == ZR_F16) dequant_kernel<zr::DT_F16><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+  else if (dt == ZR_BF16) dequant_kernel<zr::DT_BF16><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+  else dequant_kernel<zr::DT_F32><<<(unsigned)blocks, kThreads, 0, s>>>(a);
   return zr::launch_status("zr_mx4_dequantize");
 }
