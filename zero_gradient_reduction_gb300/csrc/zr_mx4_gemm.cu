@@ -30,27 +30,31 @@ __device__ int g_gave_up;
 // thread issues the products, four warps bring the accumulators out, 32 lanes each, while the next
 // tile's products run. Two forms, PAIR or not:
 //   a block alone takes 128 x 128 of the output;
-//   a pair of blocks (a cluster of two on neighbouring multiprocessors) takes 256 x 256 as one
-//   product of M = 256: each holds 128 rows of A and half of the rows of B, so that 32 KB of codes
-//   come in for 128 x 256 of output where a block alone would need 48 KB.
-constexpr int kGemmThreads = 192;
-constexpr int kStagePad = 1024;  // the operands' swizzle repeats every 1024 bytes
+//   a pair of blocks (a cluster of two on neighbouring multiprocessors) takes 256 x 256 with products
+//   of M = 256, N = 128: each holds 128 rows of A and 64 of each half's rows of B, so that 32 KB of
+//   codes come in for 128 x 256 of output where a block alone would need 48 KB.
+constexpr int kOutWarps = 4, kGemmThreads = 64 + 32 * kOutWarps;
+constexpr int kSwizzle = 1024;  // the operands' swizzle repeats every 1024 bytes
 
 template <bool PAIR>
 struct Gemm {
-  static constexpr int kRows = PAIR ? 256 : 128, kCols = PAIR ? 256 : 128;  // output tile
+  static constexpr int kHalves = PAIR ? 2 : 1;                     // of 128 columns each
+  static constexpr int kRows = 128 * kHalves, kCols = 128 * kHalves;  // output tile
   // a stage: A codes and scales, this block's B codes, the scales of all of the tile's B rows
   static constexpr int kBCodes = zr::kMxTileBytes, kBScales = kBCodes + zr::kMxCodeBytes;
-  static constexpr int kStageBytes = kBScales + (PAIR ? 2 : 1) * zr::kMxScaleBytes;
-  static constexpr int kStages = PAIR ? 5 : 6;
-  // Tensor memory: two accumulators of kCols columns, 8 columns of A's scales, and B's. The pair's
-  // accumulators share 24 columns, or the scales would find no room in the 512: those are read
-  // first, and the next tile's products wait for them alone.
+  static constexpr int kBHalf = zr::kMxCodeBytes / kHalves;
+  static constexpr int kStageBytes = kBScales + kHalves * zr::kMxScaleBytes;
+  static constexpr int kStages = 6;
+  // Tensor memory: two accumulators of kCols columns, 8 columns of A's scales, 8 for each half of B's.
+  // The pair's accumulators share 24 columns, or the scales would find no room in the 512: the second
+  // half of the even turns' and the first half of the odd turns'.
   static constexpr int kD1 = PAIR ? 232 : 128, kScaleA = PAIR ? 488 : 256, kScaleB = kScaleA + 8;
-  static constexpr int kLag = PAIR ? 1 : 2;  // an accumulator waits for the one so many turns before it
-  static constexpr int kStageOut = 32 * 144;  // an epilogue warp's rows on their way out
-  static constexpr int kSmem = kStages * kStageBytes + 4 * kStageOut + 256 + kStagePad;
+  static constexpr int kStageOut = 32 * 128;  // an epilogue warp's rows on their way out
+  static constexpr int kSmem = kStages * kStageBytes + kOutWarps * kStageOut + 256;
 };
+// Stages that a tile's products may run ahead in the half that it does not share while the shared
+// columns are still being read; more of them would hold up the ring.
+constexpr int kAhead = 4;
 
 struct GemmArgs {
   const uint8_t* a;
@@ -59,7 +63,7 @@ struct GemmArgs {
   int64_t M, N, ldo;
   int kt;          // tiles of 256 along K
   int mt, nt;      // output tiles
-  int vec;         // rows of out are 16-byte aligned
+  int vec;         // rows of out begin on 16-byte boundaries, and a map can address it
 };
 
 // How a pair's copies see the two matrices: rows of 128 bytes, 136 to an MX4 tile (128 of codes, 8 of
@@ -67,9 +71,12 @@ struct GemmArgs {
 // barrier; the tile's bytes are in their place already, so the maps say nothing of swizzles.
 constexpr int kTileLines = zr::kMxTileBytes / 128;
 struct PairMaps {
-  CUtensorMap a_tile, b_codes, b_scales;
+  CUtensorMap out, a_tile, b_codes, b_scales;
 };
-struct NoMaps {};
+// The output as a box of 32 rows of 128 bytes takes it, swizzled (unused where vec is 0).
+struct OutMap {
+  CUtensorMap out;
+};
 
 // Output tile of a number: groups of up to 32 tiles of rows, and within a group the rows first, so
 // that the blocks at work at one time share few tiles of B and a band of A.
@@ -81,67 +88,70 @@ __device__ __forceinline__ void tile_of(const GemmArgs& g, int id, int& m, int& 
   m = band * kBand + (at - n * rows);
 }
 
-// The values of 128 bytes of a row, out of registers, through this warp's staging rows, to memory.
+// The values of 128 bytes of 32 rows, a row in each lane's registers, to memory. They go through this
+// warp's staging rows in the order of the 128-byte swizzle (16-byte word j of a row at j ^ (row % 8),
+// so that no two lanes write to a bank), from where one copy takes them; where the rows of out do not
+// begin on 16-byte boundaries, a row at a time by the lanes.
 template <int DT>
-__device__ __forceinline__ void rows_out(const GemmArgs& g, char* stage, const uint32_t* v, int64_t row0, int64_t col) {
+__device__ __forceinline__ void rows_out(const GemmArgs& g, const CUtensorMap* map, char* stage, const uint32_t* v,
+                                         int64_t row0, int64_t col) {
   constexpr int es = DT == zr::DT_F32 ? 4 : 2, kCols = 128 / es;
   const int lane = threadIdx.x & 31;
-  uint4* mine = reinterpret_cast<uint4*>(stage + lane * 144);
+  if (g.vec) {  // the copy before has read the staging rows
+    if (lane == 0) zr::stores_read();
+    __syncwarp();
+  }
+  uint4* mine = reinterpret_cast<uint4*>(stage + lane * 128);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     if (DT == zr::DT_F32) {
-      mine[j] = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+      mine[j ^ (lane & 7)] = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
     } else {
       float f[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[8 * j + i]);
-      mine[j] = zr::pack8<DT == zr::DT_F32 ? zr::DT_BF16 : DT>(f);
+      mine[j ^ (lane & 7)] = zr::pack8<DT == zr::DT_F32 ? zr::DT_BF16 : DT>(f);
     }
+  }
+  if (g.vec && (col + kCols <= g.N || g.N * es % 16 == 0)) {  // (copies write whole 16-byte words)
+    zr::proxy_fence();
+    __syncwarp();
+    if (lane == 0) zr::box_store(map, (int)col, (int)row0, zr::smem_u32(stage));
+    return;
   }
   __syncwarp();
   char* out = static_cast<char*>(g.out);
-  if (g.vec && col + kCols <= g.N) {
-    const int r = lane >> 3, c = lane & 7;
+  const int rows = (int)(g.M - row0 < 32 ? g.M - row0 : 32);
+  for (int r = 0; r < rows; ++r)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t row = row0 + i * 4 + r;
-      if (row < g.M)
-        *reinterpret_cast<uint4*>(out + (row * g.ldo + col) * es + c * 16) =
-            *reinterpret_cast<const uint4*>(stage + (i * 4 + r) * 144 + c * 16);
-    }
-  } else {
-    const int rows = (int)(g.M - row0 < 32 ? g.M - row0 : 32);
-    for (int r = 0; r < rows; ++r)
-#pragma unroll
-      for (int c = lane; c < kCols; c += 32)
-        if (col + c < g.N) {
-          char* to = out + ((row0 + r) * g.ldo + col + c) * es;
-          if (DT == zr::DT_F32)
-            *reinterpret_cast<float*>(to) = *reinterpret_cast<const float*>(stage + r * 144 + c * 4);
-          else
-            *reinterpret_cast<uint16_t*>(to) = *reinterpret_cast<const uint16_t*>(stage + r * 144 + c * 2);
-        }
-  }
+    for (int c = lane; c < kCols; c += 32)
+      if (col + c < g.N) {
+        char* to = out + ((row0 + r) * g.ldo + col + c) * es;
+        const char* from = stage + r * 128 + ((c * es) ^ ((r & 7) << 4));
+        if (DT == zr::DT_F32)
+          *reinterpret_cast<float*>(to) = *reinterpret_cast<const float*>(from);
+        else
+          *reinterpret_cast<uint16_t*>(to) = *reinterpret_cast<const uint16_t*>(from);
+      }
   __syncwarp();
 }
 
 template <bool PAIR>
-using Maps = typename std::conditional<PAIR, PairMaps, NoMaps>::type;
+using Maps = typename std::conditional<PAIR, PairMaps, OutMap>::type;
 
 template <bool PAIR, int DT>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     gemm_kernel(const __grid_constant__ GemmArgs g, const __grid_constant__ Maps<PAIR> maps) {
   using G = Gemm<PAIR>;
-  extern __shared__ char smem_raw[];
-  // the same offset in both blocks of a pair: the dynamic part begins at the same address in each
-  char* smem = smem_raw + ((kStagePad - (zr::smem_u32(smem_raw) & (kStagePad - 1))) & (kStagePad - 1));
+  extern __shared__ __align__(kSwizzle) char smem[];
   const uint32_t stages = zr::smem_u32(smem);
-  char* staging = smem + G::kStages * G::kStageBytes;
-  char* tail = staging + 4 * G::kStageOut;
+  char* staging = smem + G::kStages * G::kStageBytes;  // (a multiple of the swizzle, too)
+  char* tail = staging + kOutWarps * G::kStageOut;
   // full: a stage's copies have landed (a pair's, in both blocks: the first block's barrier counts them
-  // all); empty: its products are done; done: an accumulator is complete; freed: it may be written again
+  // all); empty: its products are done; done: an accumulator is complete; opened: the columns that it
+  // shares with the next have been read; freed: all of it has
   const uint32_t full = zr::smem_u32(tail), empty = full + 8 * G::kStages, done = empty + 8 * G::kStages,
-                 freed = done + 16, drained = freed + 16;
+                 opened = done + 16, freed = opened + 16, drained = freed + 16;
   volatile int* gave_up = reinterpret_cast<volatile int*>(tail + 224);
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(tail + 232);
   const int warp = threadIdx.x >> 5;
@@ -157,7 +167,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     for (int d = 0; d < 2; ++d) {
       zr::bar_init(done + 8 * d, 1);
-      zr::bar_init(freed + 8 * d, PAIR ? 8 : 4);
+      zr::bar_init(opened + 8 * d, G::kHalves * kOutWarps);
+      zr::bar_init(freed + 8 * d, G::kHalves * kOutWarps);
     }
     zr::bar_init(drained, 1);
     zr::bar_init_fence();
@@ -182,15 +193,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         int m, n;
         tile_of(g, id, m, n);
         // a pair's tile may reach past the rows of A or B by an MX4 tile, which is not read then:
-        // what the products make of the bytes in its place is not stored
+        // what the products make of the bytes in A's place is not stored, a half of B is left out
         const int64_t am = PAIR ? 2 * (int64_t)m + rank : m, bn = PAIR ? 2 * (int64_t)n : n;
         const bool has_a = !PAIR || am * 128 < g.M, second = PAIR && (bn + 1) * 128 < g.N;
-        const bool has_b = !PAIR || rank == 0 || second;
         const uint8_t *a = g.a + am * row_bytes, *b = g.b + bn * row_bytes;
         const int a_line = (int)(am * g.kt) * kTileLines, b_line = (int)(bn * g.kt) * kTileLines;
         // the first block expects the pair's bytes
         const bool peer_a = PAIR && (am + 1) * 128 < g.M;
-        const uint32_t bytes = PAIR ? zr::kMxTileBytes * (peer_a ? 2 : 1) + (zr::kMxCodeBytes + 2 * zr::kMxScaleBytes) * (second ? 2 : 1)
+        const uint32_t bytes = PAIR ? zr::kMxTileBytes * (peer_a ? 2 : 1) +
+                                          (zr::kMxCodeBytes + 2 * zr::kMxScaleBytes) * (second ? 2 : 1)
                                     : 2 * zr::kMxTileBytes;
         for (int k = 0; k < g.kt; ++k, ++it) {
           const int s = it % G::kStages;
@@ -201,11 +212,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const int line = k * kTileLines;
             if (rank == 0) zr::bar_expect(full + 8 * s, bytes);
             if (has_a) zr::pair_copy(at, &maps.a_tile, 0, a_line + line, bar);
-            if (has_b) zr::pair_copy(at + G::kBCodes, &maps.b_codes, 0, b_line + (rank * g.kt + k) * kTileLines, bar);
+            zr::pair_copy(at + G::kBCodes, &maps.b_codes, 0, b_line + line + rank * 64, bar);
             zr::pair_copy(at + G::kBScales, &maps.b_scales, 0, b_line + line + 128, bar);
-            if (second)
+            if (second) {
+              zr::pair_copy(at + G::kBCodes + G::kBHalf, &maps.b_codes, 0, b_line + g.kt * kTileLines + line + rank * 64, bar);
               zr::pair_copy(at + G::kBScales + zr::kMxScaleBytes, &maps.b_scales, 0,
-                            b_line + (g.kt + k) * kTileLines + 128, bar);
+                            b_line + g.kt * kTileLines + line + 128, bar);
+            }
           } else {
             const int64_t ko = (int64_t)k * zr::kMxTileBytes;
             zr::bar_expect(full + 8 * s, bytes);
@@ -227,42 +240,60 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     if (rank == 0 && zr::elect_one()) {  // a pair's products are issued by its first block
       uint32_t it = 0, turn = 0;
       bool ok = true;
-      for (int id = first; id < tiles && ok; id += step, ++turn) {
-        const uint32_t d = tmem + (turn & 1) * G::kD1;
-        // the columns that it shares with the one before have been read, and all of the one before that
-        const uint32_t past = turn - G::kLag;
-        if (turn >= G::kLag && !(ok = zr::bar_wait<PAIR>(freed + 8 * (past & 1), (past >> 1) & 1, gave_up))) break;
+      // The products of a half of B's rows over the stage of a number, and before them its scales.
+      auto multiply = [&](uint32_t stage, uint32_t d, int half, bool scales_a, bool more) {
+        const uint32_t at = stages + stage % G::kStages * G::kStageBytes;
+        const uint32_t sb = tmem + G::kScaleB + 8 * half;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (scales_a) zr::copy_scales<PAIR>(tmem + G::kScaleA + 4 * h, zr::scale_rows(at + zr::kMxCodeBytes + 512 * h));
+          zr::copy_scales<PAIR>(sb + 4 * h, zr::scale_rows(at + G::kBScales + half * zr::kMxScaleBytes + 512 * h));
+        }
+        const uint64_t da = zr::swizzled_operand(at), db = zr::swizzled_operand(at + G::kBCodes + half * G::kBHalf);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)  // 64 columns, 32 bytes of each row, at a time
+          zr::mx_mma<PAIR>(d + 128 * half, da + 2 * q, db + 2 * q, zr::mx_product(G::kRows, 128, q & 1),
+                           tmem + G::kScaleA + 4 * (q >> 1), sb + 4 * (q >> 1), more || q > 0);
+      };
+      auto landed = [&](uint32_t stage) {
+        ok = zr::bar_wait<PAIR>(full + 8 * (stage % G::kStages), (stage / G::kStages) & 1, gave_up);
         zr::tmem_fence_after();
-        for (int k = 0; k < g.kt; ++k, ++it) {
-          const int s = it % G::kStages;
-          if (!(ok = zr::bar_wait<PAIR>(full + 8 * s, (it / G::kStages) & 1, gave_up))) break;
+        return ok;
+      };
+      auto release = [&](uint32_t bar) {
+        if (PAIR)
+          zr::pair_commit(bar, 3);
+        else
+          zr::mma_commit(bar);
+      };
+      for (int id = first; id < tiles; id += step, ++turn) {
+        int m, n;
+        tile_of(g, id, m, n);
+        const uint32_t buffer = turn & 1, d = tmem + buffer * G::kD1;
+        const bool second = PAIR && (int64_t)n * 256 + 128 < g.N;
+        if (turn >= 2 && !(ok = zr::bar_wait<PAIR>(freed + 8 * buffer, ((turn >> 1) - 1) & 1, gave_up))) break;
+        zr::tmem_fence_after();
+        int k = 0;
+        if (PAIR && turn >= 1) {
+          // the half that the tile before does not share, some stages ahead; the other when its columns are read
+          const int own = buffer, shared = own ^ 1, ahead = min(kAhead, g.kt);
+          for (; k < ahead && landed(it + k); ++k)
+            if (own == 0 || second) multiply(it + k, d, own, true, k > 0);
+          if (!ok || !(ok = zr::bar_wait<PAIR>(opened + 8 * (buffer ^ 1), ((turn - 1) >> 1) & 1, gave_up))) break;
           zr::tmem_fence_after();
-          const uint32_t at = stages + s * G::kStageBytes;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            zr::copy_scales<PAIR>(tmem + G::kScaleA + 4 * h, zr::scale_rows(at + zr::kMxCodeBytes + 512 * h));
-#pragma unroll
-            for (int t = 0; t < (PAIR ? 2 : 1); ++t)
-              zr::copy_scales<PAIR>(tmem + G::kScaleB + 4 * ((PAIR ? 2 : 1) * h + t),
-                                    zr::scale_rows(at + G::kBScales + t * zr::kMxScaleBytes + 512 * h));
+          for (k = 0; k < ahead; ++k) {
+            if (shared == 0 || second) multiply(it + k, d, shared, true, k > 0);
+            release(empty + 8 * ((it + k) % G::kStages));
           }
-          const uint64_t da = zr::swizzled_operand(at), db = zr::swizzled_operand(at + G::kBCodes);
-#pragma unroll
-          for (int q = 0; q < 4; ++q)  // 64 columns, 32 bytes of each row, at a time
-            zr::mx_mma<PAIR>(d, da + 2 * q, db + 2 * q, zr::mx_product(G::kRows, G::kCols, q & 1),
-                             tmem + G::kScaleA + 4 * (q >> 1), tmem + G::kScaleB + 4 * (PAIR ? 2 : 1) * (q >> 1),
-                             (k | q) != 0);
-          if (PAIR)
-            zr::pair_commit(empty + 8 * s, 3);
-          else
-            zr::mma_commit(empty + 8 * s);
         }
-        if (ok) {
-          if (PAIR)
-            zr::pair_commit(done + 8 * (turn & 1), 3);
-          else
-            zr::mma_commit(done + 8 * (turn & 1));
+        for (; k < g.kt && landed(it + k); ++k) {
+          multiply(it + k, d, 0, true, k > 0);
+          if (second) multiply(it + k, d, 1, false, k > 0);
+          release(empty + 8 * ((it + k) % G::kStages));
         }
+        it += k;
+        if (!ok) break;
+        release(done + 8 * buffer);
       }
       if (!ok) {  // no product may be in flight when the tensor memory is given back
         int never = 0;
@@ -277,7 +308,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const int lanes = (warp & 3) * 32;  // the lanes of tensor memory that this warp may read
     char* stage = staging + (warp & 3) * G::kStageOut;
     constexpr int kOnce = DT == zr::DT_F32 ? 32 : 64, kChunks = G::kCols / kOnce;
-    const uint32_t freed_at = PAIR ? zr::cluster_addr(freed, 0) : freed;
+    auto tell = [&](uint32_t bar) {  // the thread that issues the products
+      zr::tmem_fence_before();
+      __syncwarp();
+      if (zr::elect_one()) {
+        if (PAIR)
+          zr::cluster_arrive(zr::cluster_addr(bar, 0));
+        else
+          zr::bar_arrive(bar);
+      }
+    };
     uint32_t turn = 0;
     for (int id = first; id < tiles; id += step, ++turn) {
       int m, n;
@@ -292,21 +332,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const int at = (turn & 1) ? c : kChunks - 1 - c;
         const int64_t col = (int64_t)n * G::kCols + at * kOnce;
         uint32_t v[kOnce];
-        zr::tmem_load32(d + at * kOnce, *reinterpret_cast<uint32_t(*)[32]>(v));
-        if (kOnce == 64) zr::tmem_load32(d + at * kOnce + 32, *reinterpret_cast<uint32_t(*)[32]>(v + kOnce - 32));
-        if (c == (PAIR ? 0 : kChunks - 1)) {
-          zr::tmem_fence_before();
-          __syncwarp();
-          if (zr::elect_one()) {
-            if (PAIR)
-              zr::cluster_arrive(freed_at + 8 * (turn & 1));
-            else
-              zr::bar_arrive(freed_at + 8 * (turn & 1));
-          }
-        }
-        if (row0 < g.M && col < g.N) rows_out<DT>(g, stage, v, row0, col);
+        if constexpr (kOnce == 32)
+          zr::tmem_load32(d + at * kOnce, v);
+        else
+          zr::tmem_load64(d + at * kOnce, v);
+        if (PAIR && c == 0) tell(opened + 8 * (turn & 1));
+        if (c == kChunks - 1) tell(freed + 8 * (turn & 1));
+        if (row0 < g.M && col < g.N) rows_out<DT>(g, &maps.out, stage, v, row0, col);
       }
     }
+    if ((threadIdx.x & 31) == 0) zr::stores_done();  // out of this block's shared memory
   }
   __syncwarp();
   zr::tmem_fence_before();
@@ -337,7 +372,7 @@ struct FewArgs {
 };
 
 __host__ __device__ constexpr int few_smem(int k_tiles) {
-  return kFewStages * zr::kMxTileBytes + k_tiles * kXTileBytes + kFewTail + kStagePad;
+  return kFewStages * zr::kMxTileBytes + k_tiles * kXTileBytes + kFewTail;
 }
 
 // 32 values of a row from column c on as fp32; zeros from column K on.
@@ -383,8 +418,7 @@ __device__ __forceinline__ void store_as(void* out, int dt, int64_t i, float v) 
 
 template <int S>
 __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant__ FewArgs g) {
-  extern __shared__ char smem_raw[];
-  char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + kStagePad - 1) & ~(uintptr_t)(kStagePad - 1));
+  extern __shared__ __align__(kSwizzle) char smem[];
   const int n = blockIdx.x / S, rank = S > 1 ? (int)zr::cluster_rank() : 0;
   const int k0 = (int)((int64_t)g.kt * rank / S), nk = (int)((int64_t)g.kt * (rank + 1) / S) - k0;
   const int k_most = (g.kt + S - 1) / S;
@@ -545,6 +579,19 @@ bool encode_lines(CUtensorMap* map, const void* q, int64_t tiles, int lines) {
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A map of the output.
+bool encode_out(CUtensorMap* map, const GemmArgs& g, int dt) {
+  const int es = dt == zr::DT_F32 ? 4 : 2;
+  const CUtensorMapDataType type = dt == zr::DT_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : dt == zr::DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const cuuint64_t size[2] = {(cuuint64_t)g.N, (cuuint64_t)g.M}, stride[1] = {(cuuint64_t)g.ldo * es};
+  const cuuint32_t box[2] = {(cuuint32_t)(128 / es), 32}, step[2] = {1, 1};
+  return map_encoder()(map, type, 2, g.out, size, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <bool PAIR, int DT>
 zr_status launch_gemm(const GemmArgs& g, int blocks, cudaStream_t s) {
   static zr::SmemAllowance allowance;
@@ -560,10 +607,12 @@ zr_status launch_gemm(const GemmArgs& g, int blocks, cudaStream_t s) {
   c.attrs = &at;
   c.numAttrs = PAIR ? 1 : 0;
   Maps<PAIR> maps;
+  if (!map_encoder() || (g.vec && !encode_out(&maps.out, g, DT)))
+    return fail(ZR_ERR_CUDA, "zr_mx4_matmul: the driver gave no tensor map");
   if constexpr (PAIR) {
     const int64_t a_tiles = zr::mx_tiles(g.M, zr::kMxRows) * g.kt, b_tiles = zr::mx_tiles(g.N, zr::kMxRows) * g.kt;
-    if (!map_encoder() || !encode_lines(&maps.a_tile, g.a, a_tiles, kTileLines) ||
-        !encode_lines(&maps.b_codes, g.b, b_tiles, zr::kMxRows) ||
+    if (!encode_lines(&maps.a_tile, g.a, a_tiles, kTileLines) ||
+        !encode_lines(&maps.b_codes, g.b, b_tiles, zr::kMxRows / 2) ||
         !encode_lines(&maps.b_scales, g.b, b_tiles, zr::kMxScaleBytes / 128))
       return fail(ZR_ERR_CUDA, "zr_mx4_matmul: the driver gave no tensor map");
   }
@@ -595,7 +644,7 @@ zr_status matmul(const char* what, const void* a, int64_t M, const void* b, int6
   if (kt > 0x7FFFFFFF || nt > (1 << 25) || mt > 0x3FFFFFFF / nt)
     return fail(ZR_ERR_UNSUPPORTED, "%s: the product has too many tiles", what);
   g.kt = (int)kt; g.mt = (int)mt; g.nt = (int)nt;
-  g.vec = ldo * es % 16 == 0;
+  g.vec = ldo * es % 16 == 0 && ldo < (int64_t)1 << 36 && M <= 0x7FFFFFFF && N <= 0x7FFFFFFF;
   if (pair) {
     const int blocks = 2 * (int)(mt * nt < sms / 2 ? mt * nt : sms / 2);
     if (dt == ZR_F16) return launch_gemm<true, zr::DT_F16>(g, blocks, s);
