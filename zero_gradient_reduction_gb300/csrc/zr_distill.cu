@@ -131,12 +131,6 @@ __device__ __forceinline__ void store1(void* p, int64_t i, float v) {
     static_cast<uint16_t*>(p)[i] = zr::from_f32<DT == zr::DT_F32 ? zr::DT_BF16 : DT>(v);
 }
 
-// 16 bytes from global to shared memory without a register on the way.
-__device__ __forceinline__ void copy16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(zr::smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
@@ -216,10 +210,10 @@ __global__ void __launch_bounds__(kMaxThreads, 2) distill_kernel(const __grid_co
 
   bool some = w != 0.0f;
   if (some) {
-    for (int j = first + tid; tid < nthr && j < min(last, a.room); j += nthr) copy16(words + j, zw + j);
+    for (int j = first + tid; tid < nthr && j < min(last, a.room); j += nthr) zr::copy16(zr::smem_u32(words + j), zw + j);
     if (single >= 0) {
-      if (single == 0 && first == 1) copy16(words, zw);
-      if (single == n - 1 && last >= first && last < min(nw, a.room)) copy16(words + last, zw + last);
+      if (single == 0 && first == 1) zr::copy16(zr::smem_u32(words), zw);
+      if (single == n - 1 && last >= first && last < min(nw, a.room)) zr::copy16(zr::smem_u32(words + last), zw + last);
       z_single = zr::load1<DT>(zrow, single);
     }
     if (tid >= nthr) {
@@ -260,7 +254,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) distill_kernel(const __grid_co
         sh.beyond = past;
       }
     }
-    copies_done();
+    zr::copies_done();
   }
 
   auto word = [&](int j) { return j < a.room ? words[j] : ld_row(zw + j); };

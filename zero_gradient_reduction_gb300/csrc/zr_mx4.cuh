@@ -58,20 +58,33 @@ __device__ __forceinline__ uint32_t mx_codes8(const float t[8]) {
   return r;
 }
 
-// One value to its code, rounded by chance: with the two neighbours low <= |t| < high and
-// f = (|t| - low) / (high - low), to high iff f > (255.5 - r) / 256. From 1 on a value's
-// neighbours are its leading two significand bits and the next, so with b the 22 bits below
-// them the condition is b > (255.5 - r) 2^14, that is, b + 2^14 r + 2^13 - 1 carries. Below
-// 1 the spacing is 1/2, which is what |t| + 1 has; that sum is rounded up, which keeps the
-// condition's sign because the thresholds plus 1 are representable.
-__device__ __forceinline__ uint32_t mx_code_by_chance(float t, uint32_t r) {
-  const uint32_t b = __float_as_uint(t);
-  const float a = fabsf(t);
-  const bool one = a >= 1.0f;
-  const uint32_t y = __float_as_uint(one ? a : __fadd_ru(a, 1.0f));
-  const uint32_t c = ((y + (r << 14) + 0x1FFFu) >> 22) - (one ? 252u : 254u);
-  return (c < 7u ? c : 7u) | ((b >> 28) & 8u);
+// Eight values to codes, rounded by chance; quarter: a quarter of 2^(127 - byte). With the neighbours
+// low <= t < high of the magnitude t <= 6 under its scale and f = (t - low) / (high - low), to high iff
+// f > (255.5 - r) / 256. From 1 on the neighbours are a value's leading two significand bits and the
+// next, so with b the 22 bits below them the condition is b > (255.5 - r) 2^14: b + 2^14 r + 2^13 - 1
+// carries, or, moved up by two bits, where the byte r lies in byte 2, 4 b + 2^16 r + 2^15 - 4. Below 1
+// the spacing is 1/2, which is what t/2 + 1/2 has in its leading two bits, with the exponents that
+// continue the others'; that sum is the larger of the two exactly there, and it is rounded up, which
+// keeps the condition's sign because the thresholds are representable. On t/4 the leading bits run
+// from 248 (for 0) to 255 (for 6) without a wrap in their byte.
+__device__ __forceinline__ uint32_t mx_codes8_by_chance(const float x[8], float quarter, const uint32_t dither[8]) {
+  uint32_t c = 0u - 248u * 0x11111111u;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float t = __fmul_rn(fabsf(x[j]), quarter);
+    const uint32_t y = __float_as_uint(fmaxf(t, __fmaf_ru(t, 0.5f, 0.125f)));
+    c += ((y * 4u + dither[j]) >> 24) << (4 * j);
+  }
+  // the signs: the upper bytes of the even values and of the odd ones, a byte to each pair of codes
+  auto upper = [&](int j) {
+    const uint32_t a = __byte_perm(__float_as_uint(x[j]), __float_as_uint(x[j + 2]), 0x0073);
+    const uint32_t b = __byte_perm(__float_as_uint(x[j + 4]), __float_as_uint(x[j + 6]), 0x7300);
+    return __byte_perm(a, b, 0x7610);
+  };
+  return c | (upper(0) >> 4 & 0x08080808u) | (upper(1) & 0x80808080u);
 }
+// 2^16 r + 2^15 - 4 for r = byte k of w.
+__device__ __forceinline__ uint32_t mx_dither(uint32_t w, int k) { return __byte_perm(w, 0x7FFCu, 0x6054 | k << 8); }
 
 // The scale byte of a block from the bits of its largest magnitude. By chance nothing may be
 // clipped, or the rounding would lose its mean: a block whose largest value would lie over 6

@@ -189,6 +189,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     if (zr::elect_one()) {
       uint32_t it = 0;
       bool ok = true;
+      zr::wait_for_previous();
       for (int id = first; id < tiles && ok; id += step) {
         int m, n;
         tile_of(g, id, m, n);
@@ -319,6 +320,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       }
     };
     uint32_t turn = 0;
+    zr::wait_for_previous();
     for (int id = first; id < tiles; id += step, ++turn) {
       int m, n;
       tile_of(g, id, m, n);
@@ -357,55 +359,65 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 // ------------------------------------------------------------------ the few-token form
 // The weights are the operand with 128 rows, the tokens the one with 16 columns. A block takes
 // 128 outputs and, in a cluster of S blocks, 1/S of K: it starts its weight copies, quantises its
-// part of the tokens into shared memory meanwhile, and multiplies as the stages arrive. The
-// cluster's partial results are added in the order of its blocks.
-constexpr int kFewTokens = ZR_MX4_FEW, kFewThreads = 256, kFewStages = 5;
-constexpr int kXTileBytes = 3072;  // a 256-column piece of 16 tokens: 2048 of codes, 1024 of scales
+// part of the tokens into shared memory meanwhile (or copies them, quantised once by a launch
+// before it whose end only this part awaits), and multiplies as the stages arrive. The cluster's
+// partial results are added in the order of its blocks.
+constexpr int kFewTokens = ZR_MX4_FEW, kFewThreads = 256, kFewStages = 5;  // at most
+// A 256-column piece of 16 tokens: 2048 bytes of codes and, behind the codes of all pieces, twice 256
+// of scales (what a copy of 512 brings of the next piece's stands for tokens past the 16th).
+constexpr int kXCodes = 2048, kXScales = 512;
 constexpr int kFewTail = 256;
 
 struct FewArgs {
   const void* x;
+  const uint8_t* xq;  // the tokens as an MX4 matrix, or null: quantised here from x
   const uint8_t* w;
   void* out;
   int64_t M, K, N, ldx, ldo;
   int kt, xdt, odt;
+  int stages;  // of a block's ring
 };
 
-__host__ __device__ constexpr int few_smem(int k_tiles) {
-  return kFewStages * zr::kMxTileBytes + k_tiles * kXTileBytes + kFewTail;
+__host__ __device__ constexpr int few_smem(int k_tiles, int stages) {
+  return stages * zr::kMxTileBytes + k_tiles * (kXCodes + kXScales) + 256 + kFewTail;
 }
 
-// 32 values of a row from column c on as fp32; zeros from column K on.
-__device__ __forceinline__ void load32(const void* x, int dt, int64_t e, int64_t left, float v[32]) {
-  if (left >= 32) {
-    if (dt == zr::DT_F32) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint4 u = zr::load16(reinterpret_cast<const char*>(static_cast<const float*>(x) + e + 4 * i));
-        v[4 * i] = __uint_as_float(u.x);
-        v[4 * i + 1] = __uint_as_float(u.y);
-        v[4 * i + 2] = __uint_as_float(u.z);
-        v[4 * i + 3] = __uint_as_float(u.w);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4 u = zr::load16(reinterpret_cast<const char*>(static_cast<const uint16_t*>(x) + e + 8 * i));
-        if (dt == zr::DT_BF16)
-          zr::unpack8<zr::DT_BF16>(u, v + 8 * i);
-        else
-          zr::unpack8<zr::DT_F16>(u, v + 8 * i);
-      }
-    }
+// Eight values of a row from element e on, as they are (the upper eight bytes pair only in fp32);
+// zeros past the `left` that the row still has.
+struct Eight {
+  uint4 lo, hi;
+};
+__device__ __forceinline__ Eight load_eight(const void* x, int dt, int64_t e, int64_t left) {
+  const int es = dt == zr::DT_F32 ? 4 : 2;
+  const char* p = static_cast<const char*>(x) + e * es;
+  Eight r{};
+  if (left >= 8) {
+    r.lo = zr::load16(p);
+    if (dt == zr::DT_F32) r.hi = zr::load16(p + 16);
   } else {
+    uint32_t w[8] = {};
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      v[i] = 0.0f;
-      if (i < left)
-        v[i] = dt == zr::DT_F32    ? zr::load1<zr::DT_F32>(x, e + i)
-               : dt == zr::DT_BF16 ? zr::load1<zr::DT_BF16>(x, e + i)
-                                   : zr::load1<zr::DT_F16>(x, e + i);
-    }
+    for (int i = 0; i < 8; ++i)
+      if (i < left) {
+        if (dt == zr::DT_F32)
+          w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+        else
+          w[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i & 1));
+      }
+    r.lo = make_uint4(w[0], w[1], w[2], w[3]);
+    r.hi = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+  return r;
+}
+__device__ __forceinline__ void open_eight(const Eight& u, int dt, float v[8]) {
+  if (dt == zr::DT_F32) {
+    const uint32_t w[8] = {u.lo.x, u.lo.y, u.lo.z, u.lo.w, u.hi.x, u.hi.y, u.hi.z, u.hi.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+  } else if (dt == zr::DT_BF16) {
+    zr::unpack8<zr::DT_BF16>(u.lo, v);
+  } else {
+    zr::unpack8<zr::DT_F16>(u.lo, v);
   }
 }
 
@@ -422,10 +434,11 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
   const int n = blockIdx.x / S, rank = S > 1 ? (int)zr::cluster_rank() : 0;
   const int k0 = (int)((int64_t)g.kt * rank / S), nk = (int)((int64_t)g.kt * (rank + 1) / S) - k0;
   const int k_most = (g.kt + S - 1) / S;
-  char* xq = smem + kFewStages * zr::kMxTileBytes;
-  char* tail = xq + k_most * kXTileBytes;
-  const uint32_t stages = zr::smem_u32(smem), xs = zr::smem_u32(xq);
-  const uint32_t full = zr::smem_u32(tail), empty = full + 8 * kFewStages, done = empty + 8 * kFewStages;
+  char* xq = smem + g.stages * zr::kMxTileBytes;
+  char* xscale = xq + k_most * kXCodes;
+  char* tail = xscale + k_most * kXScales + 256;
+  const uint32_t stages = zr::smem_u32(smem);
+  const uint32_t full = zr::smem_u32(tail), empty = full + 8 * kFewStages, done = empty + 8 * kFewStages, tokens = done + 8;
   volatile int* gave_up = reinterpret_cast<volatile int*>(tail + 192);
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(tail + 200);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -439,38 +452,65 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
       zr::bar_init(empty + 8 * s, 1);
     }
     zr::bar_init(done, 1);
+    zr::bar_init(tokens, 1);
     zr::bar_init_fence();
     zr::proxy_fence();
     *gave_up = 0;
-    for (int k = 0; k < nk && k < kFewStages; ++k) {
+    for (int k = 0; k < nk && k < g.stages; ++k) {
       zr::bar_expect(full + 8 * k, zr::kMxTileBytes);
       zr::bulk_copy(stages + k * zr::kMxTileBytes, w + (int64_t)k * zr::kMxTileBytes, zr::kMxTileBytes, full + 8 * k);
     }
   }
   __syncwarp();
-  // tokens beyond M are left as they are: what they give is not stored
-  const int blocks = nk * 8;
-  for (int t = threadIdx.x; t < blocks * (int)g.M; t += kFewThreads) {
-    const int r = t / blocks, b = t - r * blocks, j = b & 7;
-    const int64_t c = ((int64_t)k0 * 8 + b) * 32;
-    float v[32];
-    load32(g.x, g.xdt, r * g.ldx + c, g.K - c, v);
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-    const int byte = zr::mx_scale_byte<false>(m);
-    uint32_t o[4] = {0, 0, 0, 0};
-    if (byte != 255) {
-      const float inv = zr::mx_inverse(byte);
-#pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = __fmul_rn(v[i], inv);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = zr::mx_codes8(v + 8 * i);
+  if (g.xq) {
+    if (warp == 5 && lane == 0) {  // the first 16 rows of each tile and of its scales
+      zr::wait_for_previous();
+      zr::bar_expect(tokens, nk * (kXCodes + kXScales));
+      for (int k = 0; k < nk; ++k) {
+        const uint8_t* tile = g.xq + (int64_t)(k0 + k) * zr::kMxTileBytes;
+        zr::bulk_copy(zr::smem_u32(xq + k * kXCodes), tile, kXCodes, tokens);
+        for (int h = 0; h < 2; ++h)
+          zr::bulk_copy(zr::smem_u32(xscale + k * kXScales + h * 256), tile + zr::kMxCodeBytes + h * 512, 256, tokens);
+      }
     }
-    char* piece = xq + (b >> 3) * kXTileBytes;
-    *reinterpret_cast<uint4*>(piece + r * 128 + ((j ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-    piece[2048 + (j >> 2) * 512 + r * 16 + (j & 3)] = (char)byte;
+  } else {
+    // four lanes to a block of 32 values, a warp to 256 of a row, several rows' loads in flight. What
+    // lies in the place of tokens beyond M is left as it is: what it gives is not stored.
+    constexpr int kBatch = 4, kWarps = kFewThreads / 32;
+    const int j = lane >> 2;
+    for (int t0 = warp; t0 < nk * (int)g.M; t0 += kBatch * kWarps) {
+      Eight u[kBatch];
+      int row[kBatch], piece[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int t = t0 + i * kWarps;
+        row[i] = t / nk;
+        piece[i] = t - row[i] * nk;
+        const int64_t c = (int64_t)(k0 + piece[i]) * 256 + lane * 8;
+        u[i] = row[i] < g.M && c < g.K ? load_eight(g.x, g.xdt, row[i] * g.ldx + c, g.K - c) : Eight{};
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int r = row[i], k = piece[i];
+        if (r >= g.M) break;
+        float v[8];
+        open_eight(u[i], g.xdt, v);
+        uint32_t m = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+        const int byte = zr::mx_scale_byte<false>(m);
+        const float inv = byte == 255 ? 0.0f : zr::mx_inverse(byte);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = __fmul_rn(v[e], inv);
+        const uint32_t codes = byte == 255 ? 0u : zr::mx_codes8(v);
+        *reinterpret_cast<uint32_t*>(xq + k * kXCodes + r * 128 + ((j ^ (r & 7)) << 4) + (lane & 3) * 4) = codes;
+        if ((lane & 3) == 0) xscale[k * kXScales + (j >> 2) * 256 + r * 16 + (j & 3)] = (char)byte;
+      }
+    }
   }
+  __syncwarp();
   zr::proxy_fence();
   zr::tmem_fence_before();
   __syncthreads();
@@ -479,37 +519,42 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
 
   if (warp == 4) {
     if (zr::elect_one()) {
-      int k = 0;
+      int k = g.xq && !zr::bar_wait(tokens, 0, gave_up) ? nk : 0;
       for (; k < nk; ++k) {
-        const int s = k % kFewStages;
-        if (!zr::bar_wait(full + 8 * s, (k / kFewStages) & 1, gave_up)) break;
+        const int s = k % g.stages;
+        if (!zr::bar_wait(full + 8 * s, (k / g.stages) & 1, gave_up)) break;
         zr::tmem_fence_after();
-        const uint32_t at = stages + s * zr::kMxTileBytes, xt = xs + k * kXTileBytes;
+        const uint32_t at = stages + s * zr::kMxTileBytes, xt = zr::smem_u32(xq + k * kXCodes);
+        const uint32_t xsc = zr::smem_u32(xscale + k * kXScales);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           zr::copy_scales(scale_a + 4 * h, zr::scale_rows(at + zr::kMxCodeBytes + 512 * h));
-          zr::copy_scales(scale_b + 4 * h, zr::scale_rows(xt + 2048 + 512 * h));
+          zr::copy_scales(scale_b + 4 * h, zr::scale_rows(xsc + 256 * h));
         }
         const uint64_t da = zr::swizzled_operand(at), db = zr::swizzled_operand(xt);
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           zr::mx_mma(tmem, da + 2 * q, db + 2 * q, zr::mx_product(128, 16, q & 1), scale_a + 4 * (q >> 1),
                      scale_b + 4 * (q >> 1), (k | q) != 0);
-        if (k + kFewStages < nk) zr::mma_commit(empty + 8 * s);
+        if (k + g.stages < nk) zr::mma_commit(empty + 8 * s);
+      }
+      if (*gave_up && g.xq) {  // nothing may be in flight at the end: the tokens, too
+        int never = 0;
+        zr::bar_wait(tokens, 0, &never);
       }
       zr::mma_commit(done);  // after a wait that gave up too: nothing may be in flight at the end
     }
-  } else if (warp == 5 && nk > kFewStages) {
+  } else if (warp == 5 && nk > g.stages) {
     if (zr::elect_one()) {
-      int k = kFewStages;
+      int k = g.stages;
       for (; k < nk; ++k) {
-        const int s = k % kFewStages;
-        if (!zr::bar_wait(empty + 8 * s, (k / kFewStages - 1) & 1, gave_up)) break;
+        const int s = k % g.stages;
+        if (!zr::bar_wait(empty + 8 * s, (k / g.stages - 1) & 1, gave_up)) break;
         zr::bar_expect(full + 8 * s, zr::kMxTileBytes);
         zr::bulk_copy(stages + s * zr::kMxTileBytes, w + (int64_t)k * zr::kMxTileBytes, zr::kMxTileBytes, full + 8 * s);
       }
       int never = 0;
-      for (int i = k - kFewStages; i < k; ++i) zr::bar_wait(full + 8 * (i % kFewStages), (i / kFewStages) & 1, &never);
+      for (int i = k - g.stages; i < k; ++i) zr::bar_wait(full + 8 * (i % g.stages), (i / g.stages) & 1, &never);
     }
   }
   __syncwarp();
@@ -559,6 +604,30 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
   if (warp == 0) zr::tmem_free(tmem, 32);
 }
 
+// A launch of clusters that may begin while the launch before it (in the same call) still runs.
+template <class Kernel, class... Args>
+cudaError_t launch(Kernel kernel, int blocks, int threads, int smem, int cluster, bool early, cudaStream_t s,
+                   const Args&... args) {
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3((unsigned)blocks);
+  c.blockDim = dim3((unsigned)threads);
+  c.dynamicSmemBytes = (size_t)smem;
+  c.stream = s;
+  cudaLaunchAttribute at[2] = {};
+  int n = 0;
+  if (cluster > 1) {
+    at[n].id = cudaLaunchAttributeClusterDimension;
+    at[n++].val.clusterDim = {(unsigned)cluster, 1, 1};
+  }
+  if (early) {
+    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  c.attrs = at;
+  c.numAttrs = n;
+  return cudaLaunchKernelEx(&c, kernel, args...);
+}
+
 // The driver's encoder of tensor maps, looked up once.
 PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
   static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
@@ -593,19 +662,9 @@ bool encode_out(CUtensorMap* map, const GemmArgs& g, int dt) {
 }
 
 template <bool PAIR, int DT>
-zr_status launch_gemm(const GemmArgs& g, int blocks, cudaStream_t s) {
+zr_status launch_gemm(const GemmArgs& g, int blocks, bool early, cudaStream_t s) {
   static zr::SmemAllowance allowance;
   if (zr_status st = allowance.allow("zr_mx4_matmul", (const void*)gemm_kernel<PAIR, DT>, Gemm<PAIR>::kSmem)) return st;
-  cudaLaunchConfig_t c{};
-  c.gridDim = dim3((unsigned)blocks);
-  c.blockDim = dim3(kGemmThreads);
-  c.dynamicSmemBytes = (size_t)Gemm<PAIR>::kSmem;
-  c.stream = s;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim = {2, 1, 1};
-  c.attrs = &at;
-  c.numAttrs = PAIR ? 1 : 0;
   Maps<PAIR> maps;
   if (!map_encoder() || (g.vec && !encode_out(&maps.out, g, DT)))
     return fail(ZR_ERR_CUDA, "zr_mx4_matmul: the driver gave no tensor map");
@@ -616,13 +675,14 @@ zr_status launch_gemm(const GemmArgs& g, int blocks, cudaStream_t s) {
         !encode_lines(&maps.b_scales, g.b, b_tiles, zr::kMxScaleBytes / 128))
       return fail(ZR_ERR_CUDA, "zr_mx4_matmul: the driver gave no tensor map");
   }
-  cudaError_t e = cudaLaunchKernelEx(&c, gemm_kernel<PAIR, DT>, g, maps);
+  cudaError_t e = launch(gemm_kernel<PAIR, DT>, blocks, kGemmThreads, Gemm<PAIR>::kSmem, PAIR ? 2 : 1, early, s, g, maps);
   if (e != cudaSuccess) return fail(ZR_ERR_CUDA, "zr_mx4_matmul: launch failed: %s", cudaGetErrorString(e));
   return ZR_OK;
 }
 
+// early: the launch before it is the quantisation of a, in the same call.
 zr_status matmul(const char* what, const void* a, int64_t M, const void* b, int64_t N, int64_t K, void* out, zr_dtype dt,
-                 int64_t ldo, cudaStream_t s) {
+                 int64_t ldo, bool early, cudaStream_t s) {
   const int es = dt == ZR_F32 ? 4 : 2;
   if (K == 0) {  // a sum of nothing
     cudaError_t e = cudaMemset2DAsync(out, (size_t)ldo * es, 0, (size_t)N * es, (size_t)M, s);
@@ -647,31 +707,21 @@ zr_status matmul(const char* what, const void* a, int64_t M, const void* b, int6
   g.vec = ldo * es % 16 == 0 && ldo < (int64_t)1 << 36 && M <= 0x7FFFFFFF && N <= 0x7FFFFFFF;
   if (pair) {
     const int blocks = 2 * (int)(mt * nt < sms / 2 ? mt * nt : sms / 2);
-    if (dt == ZR_F16) return launch_gemm<true, zr::DT_F16>(g, blocks, s);
-    if (dt == ZR_BF16) return launch_gemm<true, zr::DT_BF16>(g, blocks, s);
-    return launch_gemm<true, zr::DT_F32>(g, blocks, s);
+    if (dt == ZR_F16) return launch_gemm<true, zr::DT_F16>(g, blocks, early, s);
+    if (dt == ZR_BF16) return launch_gemm<true, zr::DT_BF16>(g, blocks, early, s);
+    return launch_gemm<true, zr::DT_F32>(g, blocks, early, s);
   }
   const int blocks = (int)(mt * nt < sms ? mt * nt : sms);
-  if (dt == ZR_F16) return launch_gemm<false, zr::DT_F16>(g, blocks, s);
-  if (dt == ZR_BF16) return launch_gemm<false, zr::DT_BF16>(g, blocks, s);
-  return launch_gemm<false, zr::DT_F32>(g, blocks, s);
+  if (dt == ZR_F16) return launch_gemm<false, zr::DT_F16>(g, blocks, early, s);
+  if (dt == ZR_BF16) return launch_gemm<false, zr::DT_BF16>(g, blocks, early, s);
+  return launch_gemm<false, zr::DT_F32>(g, blocks, early, s);
 }
 
 template <int S>
 zr_status launch_few(const FewArgs& g, int blocks, int smem, cudaStream_t s) {
   static zr::SmemAllowance allowance;
   if (zr_status st = allowance.allow("zr_mx4_linear", (const void*)few_kernel<S>, zr::kSmemMost)) return st;
-  cudaLaunchConfig_t c{};
-  c.gridDim = dim3((unsigned)blocks);
-  c.blockDim = dim3(kFewThreads);
-  c.dynamicSmemBytes = (size_t)smem;
-  c.stream = s;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim = {S, 1, 1};
-  c.attrs = &at;
-  c.numAttrs = S > 1 ? 1 : 0;
-  cudaError_t e = cudaLaunchKernelEx(&c, few_kernel<S>, g);
+  cudaError_t e = launch(few_kernel<S>, blocks, kFewThreads, smem, S, g.xq != nullptr, s, g);
   if (e != cudaSuccess) return fail(ZR_ERR_CUDA, "zr_mx4_linear: launch failed: %s", cudaGetErrorString(e));
   return ZR_OK;
 }
@@ -689,7 +739,7 @@ extern "C" zr_status zr_mx4_matmul(const void* a, int64_t M, const void* b, int6
   if (!out || (K > 0 && (!a || !b))) return fail(ZR_ERR_INVALID, "zr_mx4_matmul: null pointer");
   if (!zr::aligned16(a) || !zr::aligned16(b) || !zr::aligned16(out))
     return fail(ZR_ERR_INVALID, "zr_mx4_matmul: a pointer is not 16-byte aligned");
-  return matmul("zr_mx4_matmul", a, M, b, N, K, out, dt, ldo, static_cast<cudaStream_t>(stream));
+  return matmul("zr_mx4_matmul", a, M, b, N, K, out, dt, ldo, false, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" zr_status zr_mx4_linear(const void* x, zr_dtype xdt, int64_t M, int64_t ldx, const void* w, int64_t N,
@@ -711,15 +761,28 @@ extern "C" zr_status zr_mx4_linear(const void* x, zr_dtype xdt, int64_t M, int64
   if (sms == 0) return ZR_ERR_CUDA;
   int split = 1;
   while (split < 8 && nt * split * 2 <= 2 * sms && split * 2 <= kt) split *= 2;
-  while (split < 8 && split * 2 <= kt && few_smem((int)(zr::mx_tiles(kt, split) < 4096 ? zr::mx_tiles(kt, split) : 4096)) > zr::kSmemMost) split *= 2;
-  const int64_t most = kt > 0 ? zr::mx_tiles(kt, split) : 0;
-  const bool few = M <= kFewTokens && K > 0 && most < 4096 && few_smem((int)most) <= zr::kSmemMost && nt * split <= 0x7FFFFFFF;
-  if (few) {
+  auto pieces = [&](int by) { return (int)(zr::mx_tiles(kt, by) < 4096 ? zr::mx_tiles(kt, by) : 4096); };
+  while (split < 8 && split * 2 <= kt && few_smem(pieces(split), 1) > zr::kSmemMost) split *= 2;
+  const int most = pieces(split);
+  if (M <= kFewTokens && K > 0 && few_smem(most, 1) <= zr::kSmemMost && nt * split <= 0x7FFFFFFF) {
     FewArgs g{};
     g.x = x; g.w = static_cast<const uint8_t*>(w); g.out = out;
     g.M = M; g.K = K; g.N = N; g.ldx = ldx; g.ldo = ldo;
     g.kt = (int)kt; g.xdt = (int)xdt; g.odt = (int)dt;
-    const int blocks = (int)(nt * split), smem = few_smem((int)most);
+    const int blocks = (int)(nt * split);
+    // as many stages as fit where every block that there is, up to three to a multiprocessor, is resident
+    // at once: one more wave costs more than a shorter ring
+    const int resident = blocks <= sms ? 1 : blocks <= 2 * sms ? 2 : 3;
+    g.stages = kFewStages < most ? kFewStages : most;
+    while (g.stages > 2 && few_smem(most, g.stages) > (zr::kSmemMost + 1024) / resident - 1024) --g.stages;
+    while (g.stages > 1 && few_smem(most, g.stages) > zr::kSmemMost) --g.stages;
+    const int smem = few_smem(most, g.stages);
+    // Every block quantises its part of the tokens anew, in a time that its warps' pieces of 256 values
+    // decide; past four each (8 tokens of 2048: 15.3 us for 50304 outputs, against 12.4) a launch that does it once is faster.
+    if (xq && M * most > 4 * (kFewThreads / 32)) {
+      if (zr_status st = zr_mx4_quantize(x, xdt, M, K, ldx, nullptr, 0, xq, nullptr, stream)) return st;
+      g.xq = static_cast<const uint8_t*>(xq);
+    }
     if (split == 8) return launch_few<8>(g, blocks, smem, s);
     if (split == 4) return launch_few<4>(g, blocks, smem, s);
     if (split == 2) return launch_few<2>(g, blocks, smem, s);
@@ -729,7 +792,7 @@ extern "C" zr_status zr_mx4_linear(const void* x, zr_dtype xdt, int64_t M, int64
     if (!xq) return fail(ZR_ERR_INVALID, "zr_mx4_linear: more than %d tokens (or a very long K) need xq", kFewTokens);
     if (zr_status st = zr_mx4_quantize(x, xdt, M, K, ldx, nullptr, 0, xq, nullptr, stream)) return st;
   }
-  return matmul("zr_mx4_linear", xq, M, w, N, K, out, dt, ldo, s);
+  return matmul("zr_mx4_linear", xq, M, w, N, K, out, dt, ldo, true, s);
 }
 
 extern "C" zr_status zr_mx4_status(void* stream) {

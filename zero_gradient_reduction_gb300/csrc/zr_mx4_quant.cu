@@ -8,6 +8,7 @@
 #include "zr_launch.h"
 #include "zr_mx4.cuh"
 #include "zr_nvtx.h"
+#include "zr_tensor.cuh"
 
 using zr::fail;
 
@@ -24,6 +25,7 @@ struct QuantArgs {
   int64_t rows, cols, ldx, ldr;
   int64_t q_tiles, qt_tiles;  // tiles along the columns of q, of qt
   int64_t col_patches;        // patches along the columns of x
+  int whole;                  // the rows of x and of rand begin on 16-byte boundaries
   int q_row_patches, qt_col_patches;  // patches that q has along its rows, qt along x's columns
 };
 
@@ -38,29 +40,34 @@ struct Shape {
 };
 constexpr int kRandPitch = kPatch + 8;
 
-// |x| of the patch's words: the bits of the largest magnitude so far. As integers the bits of
-// magnitudes are ordered like the magnitudes, and infinities and NaN lie over all of them.
+// The largest magnitude so far and those of a word of the patch (one fp32 value, or two of 16 bits
+// apart). NaN, if there is one.
 template <int DT>
 __device__ __forceinline__ uint32_t amax_word(uint32_t m, uint32_t w) {
-  if (DT == zr::DT_F32) {
-    w &= 0x7FFFFFFFu;
-    return w > m ? w : m;
-  }
-  return __vmaxu2(m, w & 0x7FFF7FFFu);
+  uint32_t r;
+  if (DT == zr::DT_F32)
+    asm("{\n .reg .f32 a;\n abs.f32 a, %2;\n max.NaN.f32 %0, %1, a;\n}\n" : "=f"(*reinterpret_cast<float*>(&r)) : "f"(__uint_as_float(m)), "f"(__uint_as_float(w)));
+  else if (DT == zr::DT_BF16)
+    asm("{\n .reg .b32 a;\n abs.bf16x2 a, %2;\n max.NaN.bf16x2 %0, %1, a;\n}\n" : "=r"(r) : "r"(m), "r"(w));
+  else
+    asm("{\n .reg .b32 a;\n abs.f16x2 a, %2;\n max.NaN.f16x2 %0, %1, a;\n}\n" : "=r"(r) : "r"(m), "r"(w));
+  return r;
 }
 
+// The fp32 bits of a magnitude's 16-bit pattern.
 template <int DT>
-__device__ __forceinline__ uint32_t bits_of_half(uint32_t h) {  // 16-bit pattern -> fp32 bits
+__device__ __forceinline__ uint32_t bits_of_half(uint32_t h) {
   return __float_as_uint(zr::to_f32<DT>((uint16_t)h));
 }
 
+// Eight values to codes; `dither` only by chance.
 template <bool CHANCE>
-__device__ __forceinline__ uint32_t codes_of(const float t[8], uint64_t r) {
-  if (!CHANCE) return zr::mx_codes8(t);
-  uint32_t c = 0;
+__device__ __forceinline__ uint32_t codes_of(const float x[8], float inv, const uint32_t dither[8]) {
+  if (CHANCE) return zr::mx_codes8_by_chance(x, __fmul_rn(inv, 0.25f), dither);
+  float t[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) c |= zr::mx_code_by_chance(t[j], (uint32_t)(r >> (8 * j)) & 255u) << (4 * j);
-  return c;
+  for (int j = 0; j < 8; ++j) t[j] = __fmul_rn(x[j], inv);
+  return zr::mx_codes8(t);
 }
 
 // Combines the scale bytes of a quad of lanes (lane % 4 = byte) into a word.
@@ -72,17 +79,34 @@ __device__ __forceinline__ uint32_t quad_bytes(int byte) {
 }
 
 template <int DT, bool CHANCE>
-__global__ void __launch_bounds__(kThreads) quant_kernel(const __grid_constant__ QuantArgs a) {
+__global__ void __launch_bounds__(kThreads, DT == zr::DT_F32 ? (CHANCE ? 2 : 3) : 4) quant_kernel(const __grid_constant__ QuantArgs a) {
   using S = Shape<DT>;
   extern __shared__ __align__(16) char smem[];
   uint8_t* srand = reinterpret_cast<uint8_t*>(smem + S::bytes);
   const int tid = threadIdx.x;
   const int64_t pr = blockIdx.x / a.col_patches, pc = blockIdx.x - pr * a.col_patches;
   const int64_t r0 = pr * kPatch, c0 = pc * kPatch;
+  zr::let_next_begin();  // a product of what this writes (it waits for that before it reads)
 
   // ---- the patch to shared memory as it is, zeros outside the matrix
   constexpr int kPer = 16 / S::es, kVecs = kPatch / kPer, kLoads = kPatch * kVecs / kThreads;
   const char* xb = static_cast<const char*>(a.x);
+  if (a.whole && r0 + kPatch <= a.rows && c0 + kPatch <= a.cols) {
+    // a patch inside a matrix of aligned rows: copies, all of them in flight
+    constexpr int kStep = kThreads / kVecs;  // rows between a thread's words; a divisor of 32
+    const char* from = xb + ((r0 + tid / kVecs) * a.ldx + c0) * S::es + (tid % kVecs) * 16;
+    const uint32_t to = zr::smem_u32(smem) + (tid / kVecs) * S::pitch + (tid % kVecs) * 16;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      zr::copy16(to + i * kStep * S::pitch + (i * kStep >> 5) * 32, from + i * kStep * a.ldx * S::es);
+    if (CHANCE) {
+      const uint8_t* rfrom = a.rand + (r0 + (tid >> 4)) * a.ldr + c0 + (tid & 15) * 8;
+      const uint32_t rto = zr::smem_u32(srand) + (tid >> 4) * kRandPitch + (tid & 15) * 8;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) zr::copy8(rto + i * 16 * kRandPitch, rfrom + i * 16 * a.ldr);
+    }
+    zr::copies_done();
+  } else {
 #pragma unroll
   for (int half = 0; half < kLoads; half += 8) {
     uint4 v[8];
@@ -138,6 +162,7 @@ __global__ void __launch_bounds__(kThreads) quant_kernel(const __grid_constant__
       d[1] = make_uint2(v.z, v.w);
     }
   }
+  }
   __syncthreads();
 
   // ---- by rows: a thread takes 32 neighbours of a row, a quad of lanes a row's four blocks
@@ -162,7 +187,7 @@ __global__ void __launch_bounds__(kThreads) quant_kernel(const __grid_constant__
           m = amax_word<DT>(amax_word<DT>(amax_word<DT>(amax_word<DT>(m, u.x), u.y), u.z), u.w);
         }
       }
-      if (DT != zr::DT_F32) m = bits_of_half<DT>((m >> 16) > (m & 0xFFFFu) ? m >> 16 : m & 0xFFFFu);
+      if (DT != zr::DT_F32) m = bits_of_half<DT>((m >> 16) > (m & 0xFFFFu) ? m >> 16 : m & 0xFFFFu);  // (as whole numbers, NaN on top)
       const int byte = zr::mx_scale_byte<CHANCE>(m);
       uint32_t o[4];
       if (byte == 255) {
@@ -171,20 +196,22 @@ __global__ void __launch_bounds__(kThreads) quant_kernel(const __grid_constant__
         const float inv = zr::mx_inverse(byte);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float t[8];
+          float x[8];
           if (DT == zr::DT_F32) {
             const uint4 u = raw[i][0], w = raw[i][S::es / 2 - 1];
             const uint32_t f[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int j = 0; j < 8; ++j) t[j] = __uint_as_float(f[j]);
+            for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(f[j]);
           } else {
-            zr::unpack8<DT>(raw[i][0], t);
+            zr::unpack8<DT>(raw[i][0], x);
           }
+          uint32_t dither[8];
+          if (CHANCE) {
+            const uint2 r8 = *reinterpret_cast<const uint2*>(srand + r * kRandPitch + b * 32 + ((i + rot) & 3) * 8);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) t[j] = __fmul_rn(t[j], inv);
-          uint64_t rnd = 0;
-          if (CHANCE) rnd = *reinterpret_cast<const uint64_t*>(srand + r * kRandPitch + b * 32 + ((i + rot) & 3) * 8);
-          o[i] = codes_of<CHANCE>(t, rnd);
+            for (int j = 0; j < 8; ++j) dither[j] = zr::mx_dither(j < 4 ? r8.x : r8.y, j & 3);
+          }
+          o[i] = codes_of<CHANCE>(x, inv, dither);
         }
       }
       if (rot & 1) {
@@ -220,35 +247,46 @@ __global__ void __launch_bounds__(kThreads) quant_kernel(const __grid_constant__
         raw[i] = *reinterpret_cast<const uint32_t*>(col + i * S::pitch);
         m = amax_word<DT>(m, raw[i]);
       }
+      int byte[kCols];
+      float inv[kCols];
 #pragma unroll
       for (int k = 0; k < kCols; ++k) {
-        uint32_t mk = m;
-        if (DT != zr::DT_F32) mk = bits_of_half<DT>(k ? m >> 16 : m & 0xFFFFu);
-        const int byte = zr::mx_scale_byte<CHANCE>(mk);
-        uint32_t o[4];
-        if (byte == 255) {
-          o[0] = o[1] = o[2] = o[3] = 0;
-        } else {
-          const float inv = zr::mx_inverse(byte);
+        byte[k] = zr::mx_scale_byte<CHANCE>(DT == zr::DT_F32 ? m : bits_of_half<DT>(k ? m >> 16 : m & 0xFFFFu));
+        inv[k] = byte[k] == 255 ? 0.0f : zr::mx_inverse(byte[k]);
+      }
+      uint32_t o[kCols][4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float t[8];
-            uint64_t rnd = 0;
+      for (int i = 0; i < 4; ++i) {
+        uint32_t rnd[8];
+        if (CHANCE) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const uint32_t w = raw[i * 8 + j];
-              const float f = DT == zr::DT_F32    ? __uint_as_float(w)
-                              : DT == zr::DT_BF16 ? __uint_as_float(k ? w & 0xFFFF0000u : w << 16)
-                                                  : zr::to_f32<DT>((uint16_t)(k ? w >> 16 : w));
-              t[j] = __fmul_rn(f, inv);
-              if (CHANCE) rnd |= (uint64_t)srand[(b * 32 + i * 8 + j) * kRandPitch + c + k] << (8 * j);
-            }
-            o[i] = codes_of<CHANCE>(t, rnd);
+          for (int j = 0; j < 8; ++j) {  // the random bytes of this thread's one or two columns
+            const uint8_t* at = srand + (b * 32 + i * 8 + j) * kRandPitch + c;
+            rnd[j] = kCols == 2 ? *reinterpret_cast<const uint16_t*>(at) : *at;
           }
         }
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) {
+          float x[8];
+          uint32_t dither[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t w = raw[i * 8 + j];
+            x[j] = DT == zr::DT_F32    ? __uint_as_float(w)
+                   : DT == zr::DT_BF16 ? __uint_as_float(k ? w & 0xFFFF0000u : w << 16)
+                                       : zr::to_f32<DT>((uint16_t)(k ? w >> 16 : w));
+            if (CHANCE) dither[j] = zr::mx_dither(rnd[j], k);
+          }
+          o[k][i] = codes_of<CHANCE>(x, inv[k], dither);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kCols; ++k) {
         const int j = (int)(pr & 1) * 4 + b;
-        *reinterpret_cast<uint4*>(tile + zr::mx_chunk_at(c + k, j)) = make_uint4(o[0], o[1], o[2], o[3]);
-        const uint32_t bytes = quad_bytes(byte);
+        const bool bad = byte[k] == 255;
+        *reinterpret_cast<uint4*>(tile + zr::mx_chunk_at(c + k, j)) =
+            bad ? make_uint4(0, 0, 0, 0) : make_uint4(o[k][0], o[k][1], o[k][2], o[k][3]);
+        const uint32_t bytes = quad_bytes(byte[k]);
         if (b == 0) *reinterpret_cast<uint32_t*>(tile + zr::mx_scale_at(c + k, j)) = bytes;
       }
     }
@@ -363,6 +401,7 @@ extern "C" zr_status zr_mx4_quantize(const void* x, zr_dtype dt, int64_t rows, i
   a.x = x; a.rand = rand;
   a.q = static_cast<uint8_t*>(q); a.qt = static_cast<uint8_t*>(qt);
   a.rows = rows; a.cols = cols; a.ldx = ldx; a.ldr = ldr;
+  a.whole = ldx * (dt == ZR_F32 ? 4 : 2) % 16 == 0 && (!rand || ldr % 16 == 0);
   a.q_tiles = zr::mx_tiles(cols, zr::kMxCols);
   a.qt_tiles = zr::mx_tiles(rows, zr::kMxCols);
   // patches to the end of both outputs' tiles: 128 rows by 256 columns of q, 128 columns by 256 rows for qt

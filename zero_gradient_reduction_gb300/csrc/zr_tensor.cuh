@@ -75,6 +75,16 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_
                : "memory");
 }
 
+// 16 (8) bytes from global to shared memory without a register on the way, and the wait for all of
+// this thread's.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global.L2::256B [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // A box of a tensor map (x = column, y = row of its first element) to shared memory of this block of
 // a pair, counted on a barrier of either block of it (an address from cluster_addr).
 __device__ __forceinline__ void pair_copy(uint32_t dst, const void* map, int x, int y, uint32_t bar) {
@@ -230,6 +240,12 @@ __device__ __forceinline__ void pair_commit(uint32_t bar, uint16_t blocks) {
                "h"(blocks)
                : "memory");
 }
+
+// ---- a launch that may begin before the one before it in the stream has ended (both no-ops otherwise)
+// Lets the next one begin.
+__device__ __forceinline__ void let_next_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// Waits until the one before has ended and its writes can be read.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ---- clusters
 __device__ __forceinline__ uint32_t cluster_rank() {
