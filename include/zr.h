@@ -552,7 +552,7 @@ int64_t zr_mx4_bytes(int64_t rows, int64_t cols);
  * gets byte 255: all its values are NaN, so that a product of it is, too, and the step's
  * overflow flag sees it.
  * Errors: ZR_ERR_INVALID for a bad dtype, negative sizes, ldx or ldr under cols, no output,
- * null or misaligned pointers; ZR_ERR_UNSUPPORTED past 2^31 patches of 128 x 128. An empty
+ * null or misaligned pointers; ZR_ERR_UNSUPPORTED past 2^31 patches of 64 x 128. An empty
  * matrix is a no-op. */
 zr_status zr_mx4_quantize(const void* x, zr_dtype dt, int64_t rows, int64_t cols, int64_t ldx,
                           const uint8_t* rand, int64_t ldr, void* q, void* qt, void* stream);

@@ -166,7 +166,7 @@ __device__ __forceinline__ float rescaled(float m, float sum, const Base& to) {
 
 struct Shared {      // what the block's warps, and the cluster's blocks, tell each other
   float m[16], sum[16], loss[16];  // of each warp
-  float row_m, row_sum, row_loss;  // of the block
+  float row_m[8], row_sum[8], row_loss[8];  // of the cluster's blocks: each tells all, the loss the first
   int some, beyond;
 };
 
@@ -325,23 +325,18 @@ __global__ void __launch_bounds__(kMaxThreads, 2) distill_kernel(const __grid_co
   float wm = has ? sh.m[lane & 15] : -INFINITY, m = warp_max(wm);
   float sum = warp_sum(has ? rescaled(wm, sh.sum[lane & 15], Base(m, c)) : 0.0f);
   if (C > 1) {
-    if (tid == 0) {
-      sh.row_m = m;
-      sh.row_sum = sum;
+    if (tid < C) {
+      zr::cluster_store(zr::cluster_addr(zr::smem_u32(&sh.row_m[rank]), tid), m);
+      zr::cluster_store(zr::cluster_addr(zr::smem_u32(&sh.row_sum[rank]), tid), sum);
     }
     __syncwarp();
     zr::cluster_sync();
-    float ms[C];
     m = -INFINITY;
 #pragma unroll
-    for (int r = 0; r < C; ++r) {
-      ms[r] = zr::cluster_load(zr::cluster_addr(zr::smem_u32(&sh.row_m), r));
-      m = fmaxf(m, ms[r]);
-    }
+    for (int r = 0; r < C; ++r) m = fmaxf(m, sh.row_m[r]);
     sum = 0.0f;
 #pragma unroll
-    for (int r = 0; r < C; ++r)
-      sum = __fadd_rn(sum, rescaled(ms[r], zr::cluster_load(zr::cluster_addr(zr::smem_u32(&sh.row_sum), r)), Base(m, c)));
+    for (int r = 0; r < C; ++r) sum = __fadd_rn(sum, rescaled(sh.row_m[r], sh.row_sum[r], Base(m, c)));
   }
   const Base base(m, c);
   if (sh.beyond) sum = NAN;  // an entry past the vocabulary: the row says so in its loss and its gradient
@@ -369,10 +364,18 @@ __global__ void __launch_bounds__(kMaxThreads, 2) distill_kernel(const __grid_co
   }
   loss = warp_sum(loss);
   if (lane == 0) sh.loss[warp] = loss;
+  if (C > 1 || nw > a.room) __syncthreads();  // the entries' logits are read before the gradient may replace them
+  if (C > 1) {  // the blocks' parts of the loss travel while the gradient is written
+    if (warp == 0) {
+      loss = warp_sum(lane <= (nthr >> 5) ? sh.loss[lane & 15] : 0.0f);
+      if (lane == 0) zr::cluster_store(zr::cluster_addr(zr::smem_u32(&sh.row_loss[rank]), 0), loss);
+    }
+    __syncwarp();
+    zr::cluster_arrived();
+  }
 
   // ---- the gradient: all columns, then the entries' own
   if (grad) {
-    if (nw > a.room) __syncthreads();  // the entries' logits are read before the gradient may replace them
     const float fq = __fdiv_rn(f, sum);
     const Two cc(c, c), less(-base.mc, -base.mc), by(fq, fq);
     for (int j = first + tid; tid < nthr && j < last; j += nthr) {
@@ -404,27 +407,19 @@ __global__ void __launch_bounds__(kMaxThreads, 2) distill_kernel(const __grid_co
   if (grad)
     for (int k = tid; k < a.K; k += blockDim.x)
       if (sid[k] >= v0 && sid[k] < v1) store1<DT>(grad, sid[k] - v0, own[k]);
-  if (warp == 0) {
-    loss = warp_sum(lane <= (nthr >> 5) ? sh.loss[lane & 15] : 0.0f);
-    loss = sh.beyond ? NAN : __fmul_rn(loss, __fmul_rn(w, __fmul_rn(a.tau, a.tau)));
-    if (lane == 0) {
-      if (C > 1)
-        sh.row_loss = loss;
-      else
-        a.loss[row] = loss;
-    }
-  }
   if (C > 1) {
     __syncwarp();
-    zr::cluster_sync();
-    if (rank == 0 && tid == 0) {
+    zr::cluster_wait();
+  }
+  if (rank == 0 && warp == 0) {
+    if (C > 1) {
       loss = 0.0f;
 #pragma unroll
-      for (int r = 0; r < C; ++r) loss += zr::cluster_load(zr::cluster_addr(zr::smem_u32(&sh.row_loss), r));
-      a.loss[row] = loss;
+      for (int r = 0; r < C; ++r) loss = __fadd_rn(loss, sh.row_loss[r]);
+    } else {
+      loss = warp_sum(lane <= (nthr >> 5) ? sh.loss[lane & 15] : 0.0f);
     }
-    __syncwarp();
-    zr::cluster_sync();  // a block's shared memory stays until rank 0 has read it
+    if (lane == 0) a.loss[row] = sh.beyond ? NAN : __fmul_rn(loss, __fmul_rn(w, __fmul_rn(a.tau, a.tau)));
   }
 }
 

@@ -114,7 +114,7 @@ __device__ __forceinline__ void mx_decode8(uint32_t w, float v[8]) {
   }
 }
 
-// Bytes sh .. sh + 15 of the 32 bytes lo, hi (sh even, 0 to 15).
+// Bytes sh .. sh + 15 of the 32 bytes lo, hi (sh 0 to 15).
 __device__ __forceinline__ uint4 shift16(uint4 lo, uint4 hi, uint32_t sh) {
   uint32_t v[7] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z};
   if (sh & 8) {
@@ -134,9 +134,8 @@ __device__ __forceinline__ uint4 load16(const char* p) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(p);
   const uint32_t sh = (uint32_t)a & 15u;
   const uint4* w = reinterpret_cast<const uint4*>(a - sh);
-  const uint4 lo = ld_once(w);
-  if (sh == 0) return lo;
-  return shift16(lo, ld_once(w + 1), sh);
+  if (sh == 0) return ld_once(w);
+  return shift16(__ldg(w), __ldg(w + 1), sh);  // (the next lane's first word: from the nearest cache)
 }
 
 }  // namespace zr

@@ -14,8 +14,11 @@ using zr::fail;
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kPatch = 128;  // a block quantises 128 x 128 values
+// A block quantises 64 x 128 values: half a tile's rows by half its columns in q, half a tile's rows by
+// a quarter of its columns in qt. Blocks of twice the rows and threads left a longer last wave (4099 x
+// 2049 in bf16 by chance both ways 21.1 us; now XXX).
+constexpr int kThreads = 128, kRows = 64, kCols = 128;
+constexpr int kDequantThreads = 256;
 
 struct QuantArgs {
   const void* x;
@@ -32,13 +35,15 @@ struct QuantArgs {
 template <int DT>
 struct Shape {
   static constexpr int es = DT == zr::DT_F32 ? 4 : 2;
-  static constexpr int pitch = kPatch * es + 16;
-  // Rows 16 bytes apart in their banks, blocks of 32 rows another 32 bytes: so the 8 rows' or
-  // the 4 row blocks' worth of lanes that one access serves fall on different banks.
-  __device__ static int at(int r) { return r * pitch + (r >> 5) * 32; }
-  static constexpr int bytes = kPatch * pitch + 4 * 32;
+  static constexpr int pitch = kCols * es + 16;
+  // Rows 16 bytes apart in their banks, the two blocks of 32 rows another 64 bytes: so the 8 rows' or
+  // the 2 row blocks' worth of lanes that one access serves fall on different banks.
+  __host__ __device__ static constexpr int at(int r) { return r * pitch + (r >> 5) * 64; }
+  static constexpr int bytes = kRows * pitch + 64;
 };
-constexpr int kRandPitch = kPatch + 8;
+constexpr int kRandPitch = kCols + 8;
+__host__ __device__ constexpr int rand_at(int r) { return r * kRandPitch + (r >> 5) * 32; }
+constexpr int kRandBytes = kRows * kRandPitch + 32;
 
 // The largest magnitude so far and those of a word of the patch (one fp32 value, or two of 16 bits
 // apart). NaN, if there is one.
@@ -63,47 +68,51 @@ __device__ __forceinline__ uint32_t bits_of_half(uint32_t h) {
 // Eight values to codes; `dither` only by chance.
 template <bool CHANCE>
 __device__ __forceinline__ uint32_t codes_of(const float x[8], float inv, const uint32_t dither[8]) {
-  if (CHANCE) return zr::mx_codes8_by_chance(x, __fmul_rn(inv, 0.25f), dither);
-  float t[8];
+  if constexpr (CHANCE) {
+    return zr::mx_codes8_by_chance(x, __fmul_rn(inv, 0.25f), dither);
+  } else {
+    float t[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) t[j] = __fmul_rn(x[j], inv);
-  return zr::mx_codes8(t);
+    for (int j = 0; j < 8; ++j) t[j] = __fmul_rn(x[j], inv);
+    return zr::mx_codes8(t);
+  }
 }
 
-// Combines the scale bytes of a quad of lanes (lane % 4 = byte) into a word.
-__device__ __forceinline__ uint32_t quad_bytes(int byte) {
-  uint32_t w = (uint32_t)byte << (8 * (threadIdx.x & 3));
+// Combines the scale bytes of N lanes (lane % N = byte) into a word.
+template <int N>
+__device__ __forceinline__ uint32_t lane_bytes(int byte) {
+  uint32_t w = (uint32_t)byte << (8 * (threadIdx.x & (N - 1)));
   w |= __shfl_xor_sync(0xFFFFFFFFu, w, 1);
-  w |= __shfl_xor_sync(0xFFFFFFFFu, w, 2);
+  if (N == 4) w |= __shfl_xor_sync(0xFFFFFFFFu, w, 2);
   return w;
 }
 
 template <int DT, bool CHANCE>
-__global__ void __launch_bounds__(kThreads, DT == zr::DT_F32 ? (CHANCE ? 2 : 3) : 4) quant_kernel(const __grid_constant__ QuantArgs a) {
+__global__ void __launch_bounds__(kThreads, DT == zr::DT_F32 ? (CHANCE ? 5 : 6) : 8) quant_kernel(const __grid_constant__ QuantArgs a) {
   using S = Shape<DT>;
   extern __shared__ __align__(16) char smem[];
   uint8_t* srand = reinterpret_cast<uint8_t*>(smem + S::bytes);
   const int tid = threadIdx.x;
   const int64_t pr = blockIdx.x / a.col_patches, pc = blockIdx.x - pr * a.col_patches;
-  const int64_t r0 = pr * kPatch, c0 = pc * kPatch;
+  const int64_t r0 = pr * kRows, c0 = pc * kCols;
   zr::let_next_begin();  // a product of what this writes (it waits for that before it reads)
 
   // ---- the patch to shared memory as it is, zeros outside the matrix
-  constexpr int kPer = 16 / S::es, kVecs = kPatch / kPer, kLoads = kPatch * kVecs / kThreads;
+  constexpr int kPer = 16 / S::es, kVecs = kCols / kPer, kLoads = kRows * kVecs / kThreads;
   const char* xb = static_cast<const char*>(a.x);
-  if (a.whole && r0 + kPatch <= a.rows && c0 + kPatch <= a.cols) {
+  if (a.whole && r0 + kRows <= a.rows && c0 + kCols <= a.cols) {
     // a patch inside a matrix of aligned rows: copies, all of them in flight
     constexpr int kStep = kThreads / kVecs;  // rows between a thread's words; a divisor of 32
     const char* from = xb + ((r0 + tid / kVecs) * a.ldx + c0) * S::es + (tid % kVecs) * 16;
     const uint32_t to = zr::smem_u32(smem) + (tid / kVecs) * S::pitch + (tid % kVecs) * 16;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
-      zr::copy16(to + i * kStep * S::pitch + (i * kStep >> 5) * 32, from + i * kStep * a.ldx * S::es);
+      zr::copy16(to + S::at(i * kStep), from + i * kStep * a.ldx * S::es);
     if (CHANCE) {
       const uint8_t* rfrom = a.rand + (r0 + (tid >> 4)) * a.ldr + c0 + (tid & 15) * 8;
       const uint32_t rto = zr::smem_u32(srand) + (tid >> 4) * kRandPitch + (tid & 15) * 8;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) zr::copy8(rto + i * 16 * kRandPitch, rfrom + i * 16 * a.ldr);
+      for (int i = 0; i < 8; ++i) zr::copy8(rto + rand_at(i * 8), rfrom + i * 8 * a.ldr);
     }
     zr::copies_done();
   } else {
@@ -141,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, DT == zr::DT_F32 ? (CHANCE ? 2 : 3) 
   }
   if (CHANCE) {
 #pragma unroll
-    for (int i = 0; i < kPatch * kPatch / 16 / kThreads; ++i) {
+    for (int i = 0; i < kRows * kCols / 16 / kThreads; ++i) {
       const int k = tid + i * kThreads, r = k / 8, c = (k % 8) * 16;
       uint4 v = make_uint4(0, 0, 0, 0);
       if (r0 + r < a.rows && c0 + c < a.cols) {
@@ -157,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, DT == zr::DT_F32 ? (CHANCE ? 2 : 3) 
           v = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
-      uint2* d = reinterpret_cast<uint2*>(srand + r * kRandPitch + c);
+      uint2* d = reinterpret_cast<uint2*>(srand + rand_at(r) + c);
       d[0] = make_uint2(v.x, v.y);
       d[1] = make_uint2(v.z, v.w);
     }
@@ -167,7 +176,8 @@ __global__ void __launch_bounds__(kThreads, DT == zr::DT_F32 ? (CHANCE ? 2 : 3) 
 
   // ---- by rows: a thread takes 32 neighbours of a row, a quad of lanes a row's four blocks
   if (a.q && pr < a.q_row_patches) {
-    uint8_t* tile = a.q + (pr * a.q_tiles + (pc >> 1)) * zr::kMxTileBytes;
+    uint8_t* tile = a.q + ((pr >> 1) * a.q_tiles + (pc >> 1)) * zr::kMxTileBytes;
+    const int tr = (int)(pr & 1) * kRows;  // the patch's first row in its tile
 #pragma unroll 1
     for (int it = 0; it < 2; ++it) {
       const int task = tid + it * kThreads, r = task >> 2, b = task & 3;
@@ -207,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, DT == zr::DT_F32 ? (CHANCE ? 2 : 3) 
           }
           uint32_t dither[8];
           if (CHANCE) {
-            const uint2 r8 = *reinterpret_cast<const uint2*>(srand + r * kRandPitch + b * 32 + ((i + rot) & 3) * 8);
+            const uint2 r8 = *reinterpret_cast<const uint2*>(srand + rand_at(r) + b * 32 + ((i + rot) & 3) * 8);
 #pragma unroll
             for (int j = 0; j < 8; ++j) dither[j] = zr::mx_dither(j < 4 ? r8.x : r8.y, j & 3);
           }
@@ -225,20 +235,20 @@ __global__ void __launch_bounds__(kThreads, DT == zr::DT_F32 ? (CHANCE ? 2 : 3) 
         o[1] = o[3]; o[3] = z;
       }
       const int j = (int)(pc & 1) * 4 + b;
-      *reinterpret_cast<uint4*>(tile + zr::mx_chunk_at(r, j)) = make_uint4(o[0], o[1], o[2], o[3]);
-      const uint32_t bytes = quad_bytes(byte);
-      if (b == 0) *reinterpret_cast<uint32_t*>(tile + zr::mx_scale_at(r, j)) = bytes;
+      *reinterpret_cast<uint4*>(tile + zr::mx_chunk_at(tr + r, j)) = make_uint4(o[0], o[1], o[2], o[3]);
+      const uint32_t bytes = lane_bytes<4>(byte);
+      if (b == 0) *reinterpret_cast<uint32_t*>(tile + zr::mx_scale_at(tr + r, j)) = bytes;
     }
   }
 
-  // ---- by columns: a thread takes 32 neighbours of one column (of two in 16 bits), a quad of
-  // lanes a column's four blocks
+  // ---- by columns: a thread takes 32 neighbours of one column (of two in 16 bits), a pair of
+  // lanes a column's two blocks
   if (a.qt && pc < a.qt_col_patches) {
-    uint8_t* tile = a.qt + (pc * a.qt_tiles + (pr >> 1)) * zr::kMxTileBytes;
-    constexpr int kCols = DT == zr::DT_F32 ? 1 : 2;
+    uint8_t* tile = a.qt + (pc * a.qt_tiles + (pr >> 2)) * zr::kMxTileBytes;
+    constexpr int kOwn = DT == zr::DT_F32 ? 1 : 2;
 #pragma unroll 1
-    for (int it = 0; it < 2 / kCols; ++it) {
-      const int task = tid + it * kThreads, c = (task >> 2) * kCols, b = task & 3;
+    for (int it = 0; it < 2 / kOwn; ++it) {
+      const int task = tid + it * kThreads, c = (task >> 1) * kOwn, b = task & 1;
       const char* col = smem + S::at(b * 32) + c * S::es;
       uint32_t raw[32];
       uint32_t m = 0;
@@ -247,26 +257,26 @@ __global__ void __launch_bounds__(kThreads, DT == zr::DT_F32 ? (CHANCE ? 2 : 3) 
         raw[i] = *reinterpret_cast<const uint32_t*>(col + i * S::pitch);
         m = amax_word<DT>(m, raw[i]);
       }
-      int byte[kCols];
-      float inv[kCols];
+      int byte[kOwn];
+      float inv[kOwn];
 #pragma unroll
-      for (int k = 0; k < kCols; ++k) {
+      for (int k = 0; k < kOwn; ++k) {
         byte[k] = zr::mx_scale_byte<CHANCE>(DT == zr::DT_F32 ? m : bits_of_half<DT>(k ? m >> 16 : m & 0xFFFFu));
         inv[k] = byte[k] == 255 ? 0.0f : zr::mx_inverse(byte[k]);
       }
-      uint32_t o[kCols][4];
+      uint32_t o[kOwn][4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         uint32_t rnd[8];
         if (CHANCE) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {  // the random bytes of this thread's one or two columns
-            const uint8_t* at = srand + (b * 32 + i * 8 + j) * kRandPitch + c;
-            rnd[j] = kCols == 2 ? *reinterpret_cast<const uint16_t*>(at) : *at;
+            const uint8_t* at = srand + rand_at(b * 32) + (i * 8 + j) * kRandPitch + c;
+            rnd[j] = kOwn == 2 ? *reinterpret_cast<const uint16_t*>(at) : *at;
           }
         }
 #pragma unroll
-        for (int k = 0; k < kCols; ++k) {
+        for (int k = 0; k < kOwn; ++k) {
           float x[8];
           uint32_t dither[8];
 #pragma unroll
@@ -281,13 +291,13 @@ __global__ void __launch_bounds__(kThreads, DT == zr::DT_F32 ? (CHANCE ? 2 : 3) 
         }
       }
 #pragma unroll
-      for (int k = 0; k < kCols; ++k) {
-        const int j = (int)(pr & 1) * 4 + b;
+      for (int k = 0; k < kOwn; ++k) {
+        const int j = (int)(pr & 3) * 2 + b;
         const bool bad = byte[k] == 255;
         *reinterpret_cast<uint4*>(tile + zr::mx_chunk_at(c + k, j)) =
             bad ? make_uint4(0, 0, 0, 0) : make_uint4(o[k][0], o[k][1], o[k][2], o[k][3]);
-        const uint32_t bytes = quad_bytes(byte[k]);
-        if (b == 0) *reinterpret_cast<uint32_t*>(tile + zr::mx_scale_at(c + k, j)) = bytes;
+        const uint32_t bytes = lane_bytes<2>(byte[k]);
+        if (b == 0) *reinterpret_cast<uint16_t*>(tile + zr::mx_scale_at(c + k, j)) = (uint16_t)bytes;
       }
     }
   }
@@ -299,15 +309,15 @@ struct DequantArgs {
   int64_t rows, cols, ld, tiles;  // tiles along the columns
 };
 
-constexpr int kDequantRows = 32, kRowsPerWarp = kDequantRows / (kThreads / 32);
+constexpr int kDequantRows = 32, kRowsPerWarp = kDequantRows / (kDequantThreads / 32);
 
 // A block takes 32 rows of a tile, a warp four of them at once (their loads in flight together), a
 // lane eight values of a row. A row that does not begin on a 16-byte boundary goes through shared
 // memory, so that it still leaves in whole aligned words but for its ends.
 template <int DT>
-__global__ void __launch_bounds__(kThreads) dequant_kernel(const __grid_constant__ DequantArgs a) {
+__global__ void __launch_bounds__(kDequantThreads) dequant_kernel(const __grid_constant__ DequantArgs a) {
   constexpr int es = DT == zr::DT_F32 ? 4 : 2, kRowBytes = zr::kMxCols * es;
-  __shared__ __align__(16) char staging[kThreads / 32][kRowBytes + 16];
+  __shared__ __align__(16) char staging[kDequantThreads / 32][kRowBytes + 16];
   const int64_t t = blockIdx.x >> 2, rt = t / a.tiles, ct = t - rt * a.tiles;
   const uint8_t* tile = a.q + t * zr::kMxTileBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane >> 2;
@@ -318,13 +328,13 @@ __global__ void __launch_bounds__(kThreads) dequant_kernel(const __grid_constant
   int byte[kRowsPerWarp];
 #pragma unroll
   for (int i = 0; i < kRowsPerWarp; ++i) {
-    const int r = r0 + i * (kThreads / 32);
+    const int r = r0 + i * (kDequantThreads / 32);
     codes[i] = *reinterpret_cast<const uint32_t*>(tile + zr::mx_chunk_at(r, j) + (lane & 3) * 4);
     byte[i] = tile[zr::mx_scale_at(r, j)];
   }
 #pragma unroll
   for (int i = 0; i < kRowsPerWarp; ++i) {
-    const int64_t row = rt * zr::kMxRows + r0 + i * (kThreads / 32);
+    const int64_t row = rt * zr::kMxRows + r0 + i * (kDequantThreads / 32);
     if (row >= a.rows) return;
     float v[8];
     zr::mx_decode8(codes[i], v);
@@ -371,7 +381,7 @@ __global__ void __launch_bounds__(kThreads) dequant_kernel(const __grid_constant
 
 template <int DT, bool CHANCE>
 zr_status launch_quant(const QuantArgs& a, int64_t patches, cudaStream_t s) {
-  constexpr int smem = Shape<DT>::bytes + (CHANCE ? kPatch * kRandPitch : 0);
+  constexpr int smem = Shape<DT>::bytes + (CHANCE ? kRandBytes : 0);
   static zr::SmemAllowance allowance;
   if (zr_status st = allowance.allow("zr_mx4_quantize", (const void*)quant_kernel<DT, CHANCE>, smem)) return st;
   quant_kernel<DT, CHANCE><<<(unsigned)patches, kThreads, smem, s>>>(a);
@@ -405,8 +415,8 @@ extern "C" zr_status zr_mx4_quantize(const void* x, zr_dtype dt, int64_t rows, i
   a.q_tiles = zr::mx_tiles(cols, zr::kMxCols);
   a.qt_tiles = zr::mx_tiles(rows, zr::kMxCols);
   // patches to the end of both outputs' tiles: 128 rows by 256 columns of q, 128 columns by 256 rows for qt
-  const int64_t row128 = zr::mx_tiles(rows, kPatch), col128 = zr::mx_tiles(cols, kPatch);
-  const int64_t row_patches = qt ? 2 * a.qt_tiles : row128;
+  const int64_t row128 = 2 * zr::mx_tiles(rows, 128), col128 = zr::mx_tiles(cols, kCols);
+  const int64_t row_patches = qt ? 4 * a.qt_tiles : row128;
   a.col_patches = q ? 2 * a.q_tiles : col128;
   const int64_t patches = row_patches * a.col_patches;
   if (patches > 0x7FFFFFFF) return fail(ZR_ERR_UNSUPPORTED, "zr_mx4_quantize: matrix too large for one launch");
@@ -442,8 +452,8 @@ extern "C" zr_status zr_mx4_dequantize(const void* q, int64_t rows, int64_t cols
   const int64_t blocks = zr::mx_tiles(rows, zr::kMxRows) * a.tiles * (zr::kMxRows / kDequantRows);
   if (blocks > 0x7FFFFFFF) return fail(ZR_ERR_UNSUPPORTED, "zr_mx4_dequantize: matrix too large for one launch");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (dt == ZR_F16) dequant_kernel<zr::DT_F16><<<(unsigned)blocks, kThreads, 0, s>>>(a);
-  else if (dt == ZR_BF16) dequant_kernel<zr::DT_BF16><<<(unsigned)blocks, kThreads, 0, s>>>(a);
-  else dequant_kernel<zr::DT_F32><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+  if (dt == ZR_F16) dequant_kernel<zr::DT_F16><<<(unsigned)blocks, kDequantThreads, 0, s>>>(a);
+  else if (dt == ZR_BF16) dequant_kernel<zr::DT_BF16><<<(unsigned)blocks, kDequantThreads, 0, s>>>(a);
+  else dequant_kernel<zr::DT_F32><<<(unsigned)blocks, kDequantThreads, 0, s>>>(a);
   return zr::launch_status("zr_mx4_dequantize");
 }
