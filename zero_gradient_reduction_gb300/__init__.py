@@ -153,7 +153,7 @@ def lib():
 
 
 def _check(status: int) -> None:
-    if status != 0:
+    if status:
         raise ZrError(status, lib().zr_last_error().decode(errors="replace"))
 
 
@@ -613,15 +613,12 @@ def _fn(name: str):
 def _raw_stream(stream, device: int) -> int:
     if stream is not None:
         return int(stream.cuda_stream)
-    import torch
-    global _raw_stream_of
-    if _raw_stream_of is None:
-        _raw_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    of = _fns.get("stream")
+    if of is None:
+        import torch
+        of = _fns["stream"] = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda d: torch.cuda.current_stream(d).cuda_stream)
-    return _raw_stream_of(device)
-
-
-_raw_stream_of = None
+    return of(device)
 
 
 def _matrix(t, what: str):
@@ -649,13 +646,13 @@ class Mx4:
     __slots__ = ("rows", "cols", "data", "ptr")
 
     def __init__(self, rows: int, cols: int, data=None, device="cuda"):
-        import torch
         if rows < 0 or cols < 0:
             _refuse("Mx4: negative size")
         need = -(-rows // 128) * -(-cols // 256) * 17408
         if data is None:
+            import torch
             data = torch.empty(need, dtype=torch.uint8, device=device)
-        elif data.dtype is not torch.uint8 or data.numel() < need or not data.is_contiguous() or not data.is_cuda:
+        elif data.element_size() != 1 or data.numel() < need or not data.is_cuda or not data.is_contiguous():
             _refuse(f"Mx4: data must be {need} contiguous bytes in device memory")
         self.rows, self.cols, self.data, self.ptr = rows, cols, data, data.data_ptr()
 

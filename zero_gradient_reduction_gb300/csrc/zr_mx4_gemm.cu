@@ -30,31 +30,28 @@ __device__ int g_gave_up;
 // thread issues the products, four warps bring the accumulators out, 32 lanes each, while the next
 // tile's products run. Two forms, PAIR or not:
 //   a block alone takes 128 x 128 of the output;
-//   a pair of blocks (a cluster of two on neighbouring multiprocessors) takes 256 x 256 with products
-//   of M = 256, N = 128: each holds 128 rows of A and 64 of each half's rows of B, so that 32 KB of
+//   a pair of blocks (a cluster of two on neighbouring multiprocessors) takes 256 x 256 as one
+//   product of M = 256: each holds 128 rows of A and 128 of the tile's rows of B, so that 32 KB of
 //   codes come in for 128 x 256 of output where a block alone would need 48 KB.
 constexpr int kOutWarps = 4, kGemmThreads = 64 + 32 * kOutWarps;
 constexpr int kSwizzle = 1024;  // the operands' swizzle repeats every 1024 bytes
 
 template <bool PAIR>
 struct Gemm {
-  static constexpr int kHalves = PAIR ? 2 : 1;                     // of 128 columns each
-  static constexpr int kRows = 128 * kHalves, kCols = 128 * kHalves;  // output tile
+  static constexpr int kTiles = PAIR ? 2 : 1;                       // MX4 tiles along M and along N
+  static constexpr int kRows = 128 * kTiles, kCols = 128 * kTiles;  // output tile
   // a stage: A codes and scales, this block's B codes, the scales of all of the tile's B rows
   static constexpr int kBCodes = zr::kMxTileBytes, kBScales = kBCodes + zr::kMxCodeBytes;
-  static constexpr int kBHalf = zr::kMxCodeBytes / kHalves;
-  static constexpr int kStageBytes = kBScales + kHalves * zr::kMxScaleBytes;
+  static constexpr int kStageBytes = kBScales + kTiles * zr::kMxScaleBytes;
   static constexpr int kStages = 6;
-  // Tensor memory: two accumulators of kCols columns, 8 columns of A's scales, 8 for each half of B's.
-  // The pair's accumulators share 24 columns, or the scales would find no room in the 512: the second
-  // half of the even turns' and the first half of the odd turns'.
+  // Tensor memory: two accumulators of kCols columns, 8 columns of A's scales, 8 for each tile of B's.
+  // The pair's accumulators share 24 columns, or the scales would find no room in the 512: those are
+  // read first, and the next tile's products wait for them alone.
   static constexpr int kD1 = PAIR ? 232 : 128, kScaleA = PAIR ? 488 : 256, kScaleB = kScaleA + 8;
+  static constexpr int kLag = PAIR ? 1 : 2;   // an accumulator waits for the one so many turns before it
   static constexpr int kStageOut = 32 * 128;  // an epilogue warp's rows on their way out
   static constexpr int kSmem = kStages * kStageBytes + kOutWarps * kStageOut + 256;
 };
-// Stages that a tile's products may run ahead in the half that it does not share while the shared
-// columns are still being read; more of them would hold up the ring.
-constexpr int kAhead = 4;
 
 struct GemmArgs {
   const uint8_t* a;
@@ -148,10 +145,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   char* staging = smem + G::kStages * G::kStageBytes;  // (a multiple of the swizzle, too)
   char* tail = staging + kOutWarps * G::kStageOut;
   // full: a stage's copies have landed (a pair's, in both blocks: the first block's barrier counts them
-  // all); empty: its products are done; done: an accumulator is complete; opened: the columns that it
-  // shares with the next have been read; freed: all of it has
+  // all); empty: its products are done; done: an accumulator is complete; freed: the turn kLag later
+  // may begin
   const uint32_t full = zr::smem_u32(tail), empty = full + 8 * G::kStages, done = empty + 8 * G::kStages,
-                 opened = done + 16, freed = opened + 16, drained = freed + 16;
+                 freed = done + 16, drained = freed + 16;
   volatile int* gave_up = reinterpret_cast<volatile int*>(tail + 224);
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(tail + 232);
   const int warp = threadIdx.x >> 5;
@@ -167,8 +164,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     for (int d = 0; d < 2; ++d) {
       zr::bar_init(done + 8 * d, 1);
-      zr::bar_init(opened + 8 * d, G::kHalves * kOutWarps);
-      zr::bar_init(freed + 8 * d, G::kHalves * kOutWarps);
+      zr::bar_init(freed + 8 * d, G::kTiles * kOutWarps);
     }
     zr::bar_init(drained, 1);
     zr::bar_init_fence();
@@ -194,7 +190,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         int m, n;
         tile_of(g, id, m, n);
         // a pair's tile may reach past the rows of A or B by an MX4 tile, which is not read then:
-        // what the products make of the bytes in A's place is not stored, a half of B is left out
+        // what the products make of the bytes in its place is not stored
         const int64_t am = PAIR ? 2 * (int64_t)m + rank : m, bn = PAIR ? 2 * (int64_t)n : n;
         const bool has_a = !PAIR || am * 128 < g.M, second = PAIR && (bn + 1) * 128 < g.N;
         const uint8_t *a = g.a + am * row_bytes, *b = g.b + bn * row_bytes;
@@ -206,20 +202,18 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                                     : 2 * zr::kMxTileBytes;
         for (int k = 0; k < g.kt; ++k, ++it) {
           const int s = it % G::kStages;
-          if (it >= G::kStages && !(ok = zr::bar_wait<PAIR>(empty + 8 * s, (it / G::kStages - 1) & 1, gave_up))) break;
+          if (it >= G::kStages && !(ok = zr::bar_wait(empty + 8 * s, (it / G::kStages - 1) & 1, gave_up))) break;
           const uint32_t at = stages + s * G::kStageBytes;
           if constexpr (PAIR) {
             const uint32_t bar = zr::cluster_addr(full + 8 * s, 0);
             const int line = k * kTileLines;
             if (rank == 0) zr::bar_expect(full + 8 * s, bytes);
             if (has_a) zr::pair_copy(at, &maps.a_tile, 0, a_line + line, bar);
-            zr::pair_copy(at + G::kBCodes, &maps.b_codes, 0, b_line + line + rank * 64, bar);
+            const int next = g.kt * kTileLines;  // the tile's second rows of B
+            if (rank == 0 || second) zr::pair_copy(at + G::kBCodes, &maps.b_codes, 0, b_line + line + rank * next, bar);
             zr::pair_copy(at + G::kBScales, &maps.b_scales, 0, b_line + line + 128, bar);
-            if (second) {
-              zr::pair_copy(at + G::kBCodes + G::kBHalf, &maps.b_codes, 0, b_line + g.kt * kTileLines + line + rank * 64, bar);
-              zr::pair_copy(at + G::kBScales + zr::kMxScaleBytes, &maps.b_scales, 0,
-                            b_line + g.kt * kTileLines + line + 128, bar);
-            }
+            if (second)
+              zr::pair_copy(at + G::kBScales + zr::kMxScaleBytes, &maps.b_scales, 0, b_line + next + line + 128, bar);
           } else {
             const int64_t ko = (int64_t)k * zr::kMxTileBytes;
             zr::bar_expect(full + 8 * s, bytes);
@@ -231,7 +225,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       // the block may end once its copies have landed and its stages' products are done
       const uint32_t from = it < G::kStages ? 0 : it - G::kStages;
       for (uint32_t i = from; i < it && ok; ++i)
-        ok = zr::bar_wait<PAIR>(empty + 8 * (i % G::kStages), (i / G::kStages) & 1, gave_up);
+        ok = zr::bar_wait(empty + 8 * (i % G::kStages), (i / G::kStages) & 1, gave_up);
       if (!ok && rank == 0) {  // (the first block waits for the pair's copies; the other ends after it)
         int never = 0;
         for (uint32_t i = from; i < it; ++i) zr::bar_wait(full + 8 * (i % G::kStages), (i / G::kStages) & 1, &never);
@@ -241,60 +235,37 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     if (rank == 0 && zr::elect_one()) {  // a pair's products are issued by its first block
       uint32_t it = 0, turn = 0;
       bool ok = true;
-      // The products of a half of B's rows over the stage of a number, and before them its scales.
-      auto multiply = [&](uint32_t stage, uint32_t d, int half, bool scales_a, bool more) {
-        const uint32_t at = stages + stage % G::kStages * G::kStageBytes;
-        const uint32_t sb = tmem + G::kScaleB + 8 * half;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (scales_a) zr::copy_scales<PAIR>(tmem + G::kScaleA + 4 * h, zr::scale_rows(at + zr::kMxCodeBytes + 512 * h));
-          zr::copy_scales<PAIR>(sb + 4 * h, zr::scale_rows(at + G::kBScales + half * zr::kMxScaleBytes + 512 * h));
-        }
-        const uint64_t da = zr::swizzled_operand(at), db = zr::swizzled_operand(at + G::kBCodes + half * G::kBHalf);
-#pragma unroll
-        for (int q = 0; q < 4; ++q)  // 64 columns, 32 bytes of each row, at a time
-          zr::mx_mma<PAIR>(d + 128 * half, da + 2 * q, db + 2 * q, zr::mx_product(G::kRows, 128, q & 1),
-                           tmem + G::kScaleA + 4 * (q >> 1), sb + 4 * (q >> 1), more || q > 0);
-      };
-      auto landed = [&](uint32_t stage) {
-        ok = zr::bar_wait<PAIR>(full + 8 * (stage % G::kStages), (stage / G::kStages) & 1, gave_up);
-        zr::tmem_fence_after();
-        return ok;
-      };
       auto release = [&](uint32_t bar) {
         if (PAIR)
           zr::pair_commit(bar, 3);
         else
           zr::mma_commit(bar);
       };
-      for (int id = first; id < tiles; id += step, ++turn) {
-        int m, n;
-        tile_of(g, id, m, n);
-        const uint32_t buffer = turn & 1, d = tmem + buffer * G::kD1;
-        const bool second = PAIR && (int64_t)n * 256 + 128 < g.N;
-        if (turn >= 2 && !(ok = zr::bar_wait<PAIR>(freed + 8 * buffer, ((turn >> 1) - 1) & 1, gave_up))) break;
+      for (int id = first; id < tiles && ok; id += step, ++turn) {
+        const uint32_t d = tmem + (turn & 1) * G::kD1, past = turn - G::kLag;
+        if (turn >= G::kLag && !(ok = zr::bar_wait(freed + 8 * (past & 1), (past >> 1) & 1, gave_up))) break;
         zr::tmem_fence_after();
-        int k = 0;
-        if (PAIR && turn >= 1) {
-          // the half that the tile before does not share, some stages ahead; the other when its columns are read
-          const int own = buffer, shared = own ^ 1, ahead = min(kAhead, g.kt);
-          for (; k < ahead && landed(it + k); ++k)
-            if (own == 0 || second) multiply(it + k, d, own, true, k > 0);
-          if (!ok || !(ok = zr::bar_wait<PAIR>(opened + 8 * (buffer ^ 1), ((turn - 1) >> 1) & 1, gave_up))) break;
+        for (int k = 0; k < g.kt; ++k, ++it) {
+          const int s = it % G::kStages;
+          if (!(ok = zr::bar_wait(full + 8 * s, (it / G::kStages) & 1, gave_up))) break;
           zr::tmem_fence_after();
-          for (k = 0; k < ahead; ++k) {
-            if (shared == 0 || second) multiply(it + k, d, shared, true, k > 0);
-            release(empty + 8 * ((it + k) % G::kStages));
+          const uint32_t at = stages + s * G::kStageBytes;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            zr::copy_scales<PAIR>(tmem + G::kScaleA + 4 * h, zr::scale_rows(at + zr::kMxCodeBytes + 512 * h));
+#pragma unroll
+            for (int t = 0; t < G::kTiles; ++t)
+              zr::copy_scales<PAIR>(tmem + G::kScaleB + 4 * (G::kTiles * h + t),
+                                    zr::scale_rows(at + G::kBScales + t * zr::kMxScaleBytes + 512 * h));
           }
+          const uint64_t da = zr::swizzled_operand(at), db = zr::swizzled_operand(at + G::kBCodes);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)  // 64 columns, 32 bytes of each row, at a time
+            zr::mx_mma<PAIR>(d, da + 2 * q, db + 2 * q, zr::mx_product(G::kRows, G::kCols, q & 1),
+                             tmem + G::kScaleA + 4 * (q >> 1), tmem + G::kScaleB + 4 * G::kTiles * (q >> 1), (k | q) != 0);
+          release(empty + 8 * s);
         }
-        for (; k < g.kt && landed(it + k); ++k) {
-          multiply(it + k, d, 0, true, k > 0);
-          if (second) multiply(it + k, d, 1, false, k > 0);
-          release(empty + 8 * ((it + k) % G::kStages));
-        }
-        it += k;
-        if (!ok) break;
-        release(done + 8 * buffer);
+        if (ok) release(done + 8 * (turn & 1));
       }
       if (!ok) {  // no product may be in flight when the tensor memory is given back
         int never = 0;
@@ -324,7 +295,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     for (int id = first; id < tiles; id += step, ++turn) {
       int m, n;
       tile_of(g, id, m, n);
-      if (!__all_sync(0xFFFFFFFFu, zr::bar_wait<PAIR>(done + 8 * (turn & 1), (turn >> 1) & 1, gave_up))) break;
+      if (!__all_sync(0xFFFFFFFFu, zr::bar_wait(done + 8 * (turn & 1), (turn >> 1) & 1, gave_up))) break;
       zr::tmem_fence_after();
       const uint32_t d = tmem + (turn & 1) * G::kD1 + ((uint32_t)lanes << 16);
       const int64_t row0 = (int64_t)m * G::kRows + rank * 128 + lanes;
@@ -338,8 +309,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           zr::tmem_load32(d + at * kOnce, v);
         else
           zr::tmem_load64(d + at * kOnce, v);
-        if (PAIR && c == 0) tell(opened + 8 * (turn & 1));
-        if (c == kChunks - 1) tell(freed + 8 * (turn & 1));
+        if (c == (PAIR ? 0 : kChunks - 1)) tell(freed + 8 * (turn & 1));
         if (row0 < g.M && col < g.N) rows_out<DT>(g, &maps.out, stage, v, row0, col);
       }
     }
@@ -671,7 +641,7 @@ zr_status launch_gemm(const GemmArgs& g, int blocks, bool early, cudaStream_t s)
   if constexpr (PAIR) {
     const int64_t a_tiles = zr::mx_tiles(g.M, zr::kMxRows) * g.kt, b_tiles = zr::mx_tiles(g.N, zr::kMxRows) * g.kt;
     if (!encode_lines(&maps.a_tile, g.a, a_tiles, kTileLines) ||
-        !encode_lines(&maps.b_codes, g.b, b_tiles, zr::kMxRows / 2) ||
+        !encode_lines(&maps.b_codes, g.b, b_tiles, zr::kMxRows) ||
         !encode_lines(&maps.b_scales, g.b, b_tiles, zr::kMxScaleBytes / 128))
       return fail(ZR_ERR_CUDA, "zr_mx4_matmul: the driver gave no tensor map");
   }

@@ -31,35 +31,28 @@ __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// CLUSTER: the arrivals may come from another block of the cluster.
-template <bool CLUSTER = false>
+// The barriers' default order, within the block, is enough between the blocks of a pair, too: what
+// they guard is read and written by copies, products and tensor-memory loads, whose own completion
+// and fences order them. Waits and arrivals of cluster scope cost 15 % of a product.
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
-  if constexpr (CLUSTER)
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-  else
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
   return ok != 0;
 }
 
 // Waits until the phase of `bar` with this parity is complete. Gives up after kTensorWaitNs, or
-// soon after another thread of the block gave up (`gave_up`, in shared memory), and says false.
-template <bool CLUSTER = false>
+// soon after another thread of the block gave up (`gave_up`, in shared memory), and says false. The
+// clock is read at every 64th try only: reading it takes longer than the barriers' own latency.
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
-  if (bar_try<CLUSTER>(bar, parity)) return true;
-  uint64_t t0, t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
-  while (!bar_try<CLUSTER>(bar, parity)) {
+  uint64_t t0 = 0, t;
+  for (uint32_t n = 1; !bar_try(bar, parity); ++n) {
+    if (n & 63) continue;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    if (t0 == 0) t0 = t;
     if (*gave_up || t - t0 > kTensorWaitNs) {
       *gave_up = 1;
       return false;
@@ -269,7 +262,7 @@ __device__ __forceinline__ void cluster_store(uint32_t addr, float v) {
 }
 // An arrival on a barrier of another block of the cluster (an address from cluster_addr).
 __device__ __forceinline__ void cluster_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ float cluster_load(uint32_t addr) {
   float v;
