@@ -119,6 +119,7 @@ __device__ __forceinline__ void rows_out(const GemmArgs& g, const CUtensorMap* m
   __syncwarp();
   char* out = static_cast<char*>(g.out);
   const int rows = (int)(g.M - row0 < 32 ? g.M - row0 : 32);
+#pragma unroll 4
   for (int r = 0; r < rows; ++r)
 #pragma unroll
     for (int c = lane; c < kCols; c += 32)

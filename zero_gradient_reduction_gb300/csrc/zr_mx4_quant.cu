@@ -359,21 +359,20 @@ __global__ void __launch_bounds__(kDequantThreads) dequant_kernel(const __grid_c
 #pragma unroll
     for (int k = 0; k < es / 2; ++k) *reinterpret_cast<uint4*>(stage + (lane * (es / 2) + k) * 16) = w[k];
     __syncwarp();
-    // words of memory that the row covers: the k-th holds bytes 16k - lead .. of it
-    const int bytes = n * es;
-    for (int k = lane; k * 16 < lead + bytes; k += 32) {
-      const int from = k * 16 - lead;
-      if (from >= 0 && from + 16 <= bytes) {
-        const uint4* at = reinterpret_cast<const uint4*>(stage + (from & ~15));
-        zr::st_once(out + from, zr::shift16(at[0], at[1], (uint32_t)from & 15u));
-      } else {
-        for (int b = from < 0 ? 0 : from; b < from + 16 && b < bytes; b += es) {
-          if (es == 4)
-            *reinterpret_cast<uint32_t*>(out + b) = *reinterpret_cast<const uint32_t*>(stage + b);
-          else
-            *reinterpret_cast<uint16_t*>(out + b) = *reinterpret_cast<const uint16_t*>(stage + b);
-        }
-      }
+    // the values before the first boundary, whole words from there, the values behind the last
+    const int head = lead ? (16 - lead) / es < n ? (16 - lead) / es : n : 0;
+    const int whole = (n - head) * es / 16, tail = n - head - whole * (16 / es);
+    for (int k = lane; k < whole; k += 32) {
+      const int from = head * es + k * 16;
+      const uint4* at = reinterpret_cast<const uint4*>(stage + (from & ~15));
+      zr::st_once(out + from, zr::shift16(at[0], at[1], (uint32_t)from & 15u));
+    }
+    const int one = lane < head ? lane : lane >= 16 && lane - 16 < tail ? n - tail + lane - 16 : -1;
+    if (one >= 0) {
+      if (es == 4)
+        reinterpret_cast<uint32_t*>(out)[one] = reinterpret_cast<const uint32_t*>(stage)[one];
+      else
+        reinterpret_cast<uint16_t*>(out)[one] = reinterpret_cast<const uint16_t*>(stage)[one];
     }
     __syncwarp();
   }
