@@ -43,14 +43,16 @@ struct Gemm {
   // a stage: A codes and scales, this block's B codes, the scales of all of the tile's B rows
   static constexpr int kBCodes = zr::kMxTileBytes, kBScales = kBCodes + zr::kMxCodeBytes;
   static constexpr int kStageBytes = kBScales + kTiles * zr::kMxScaleBytes;
-  static constexpr int kStages = 6;
+  static constexpr int kStages = PAIR ? 6 : 5;
   // Tensor memory: two accumulators of kCols columns, 8 columns of A's scales, 8 for each tile of B's.
   // The pair's accumulators share 24 columns, or the scales would find no room in the 512: those are
   // read first, and the next tile's products wait for them alone.
   static constexpr int kD1 = PAIR ? 232 : 128, kScaleA = PAIR ? 488 : 256, kScaleB = kScaleA + 8;
   static constexpr int kLag = PAIR ? 1 : 2;   // an accumulator waits for the one so many turns before it
-  static constexpr int kStageOut = 32 * 128;  // an epilogue warp's rows on their way out
-  static constexpr int kSmem = kStages * kStageBytes + kOutWarps * kStageOut + 256;
+  // an epilogue warp's rows on their way out, 4 KB a time: a block alone has the room for three times,
+  // so that it need not wait for each copy (a third of a short product); between a pair's tiles there is time
+  static constexpr int kOutBuffers = PAIR ? 1 : 3, kOutBytes = 32 * 128;
+  static constexpr int kSmem = kStages * kStageBytes + kOutWarps * kOutBuffers * kOutBytes + 256;
 };
 
 struct GemmArgs {
@@ -89,13 +91,13 @@ __device__ __forceinline__ void tile_of(const GemmArgs& g, int id, int& m, int& 
 // warp's staging rows in the order of the 128-byte swizzle (16-byte word j of a row at j ^ (row % 8),
 // so that no two lanes write to a bank), from where one copy takes them; where the rows of out do not
 // begin on 16-byte boundaries, a row at a time by the lanes.
-template <int DT>
+template <int DT, int BUFFERS>
 __device__ __forceinline__ void rows_out(const GemmArgs& g, const CUtensorMap* map, char* stage, const uint32_t* v,
                                          int64_t row0, int64_t col) {
   constexpr int es = DT == zr::DT_F32 ? 4 : 2, kCols = 128 / es;
   const int lane = threadIdx.x & 31;
-  if (g.vec) {  // the copy before has read the staging rows
-    if (lane == 0) zr::stores_read();
+  if (g.vec) {  // the copy that used these staging rows last has read them
+    if (lane == 0) zr::stores_read<BUFFERS - 1>();
     __syncwarp();
   }
   uint4* mine = reinterpret_cast<uint4*>(stage + lane * 128);
@@ -117,20 +119,17 @@ __device__ __forceinline__ void rows_out(const GemmArgs& g, const CUtensorMap* m
     return;
   }
   __syncwarp();
-  char* out = static_cast<char*>(g.out);
-  const int rows = (int)(g.M - row0 < 32 ? g.M - row0 : 32);
-#pragma unroll 4
-  for (int r = 0; r < rows; ++r)
+  using T = typename std::conditional<DT == zr::DT_F32, uint32_t, uint16_t>::type;
+  constexpr int kEach = kCols / 32;  // values of a row in a lane, 32 apart
+  T* out = static_cast<T*>(g.out) + row0 * g.ldo + col + lane;
+  const int rows = (int)(g.M - row0 < 32 ? g.M - row0 : 32), left = (int)(g.N - col < kCols ? g.N - col : kCols) - lane;
+#pragma unroll 8
+  for (int r = 0; r < 32; ++r, out += g.ldo) {
 #pragma unroll
-    for (int c = lane; c < kCols; c += 32)
-      if (col + c < g.N) {
-        char* to = out + ((row0 + r) * g.ldo + col + c) * es;
-        const char* from = stage + r * 128 + ((c * es) ^ ((r & 7) << 4));
-        if (DT == zr::DT_F32)
-          *reinterpret_cast<float*>(to) = *reinterpret_cast<const float*>(from);
-        else
-          *reinterpret_cast<uint16_t*>(to) = *reinterpret_cast<const uint16_t*>(from);
-      }
+    for (int i = 0; i < kEach; ++i)
+      if (r < rows && 32 * i < left)
+        out[32 * i] = *reinterpret_cast<const T*>(stage + r * 128 + (((lane + 32 * i) * es) ^ ((r & 7) << 4)));
+  }
   __syncwarp();
 }
 
@@ -144,7 +143,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   extern __shared__ __align__(kSwizzle) char smem[];
   const uint32_t stages = zr::smem_u32(smem);
   char* staging = smem + G::kStages * G::kStageBytes;  // (a multiple of the swizzle, too)
-  char* tail = staging + kOutWarps * G::kStageOut;
+  char* tail = staging + kOutWarps * G::kOutBuffers * G::kOutBytes;
   // full: a stage's copies have landed (a pair's, in both blocks: the first block's barrier counts them
   // all); empty: its products are done; done: an accumulator is complete; freed: the turn kLag later
   // may begin
@@ -279,7 +278,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
   } else {
     const int lanes = (warp & 3) * 32;  // the lanes of tensor memory that this warp may read
-    char* stage = staging + (warp & 3) * G::kStageOut;
+    char* stage = staging + (warp & 3) * G::kOutBuffers * G::kOutBytes;
+    int buffer = 0;
     constexpr int kOnce = DT == zr::DT_F32 ? 32 : 64, kChunks = G::kCols / kOnce;
     auto tell = [&](uint32_t bar) {  // the thread that issues the products
       zr::tmem_fence_before();
@@ -311,7 +311,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         else
           zr::tmem_load64(d + at * kOnce, v);
         if (c == (PAIR ? 0 : kChunks - 1)) tell(freed + 8 * (turn & 1));
-        if (row0 < g.M && col < g.N) rows_out<DT>(g, &maps.out, stage, v, row0, col);
+        if (row0 < g.M && col < g.N) {
+          rows_out<DT, G::kOutBuffers>(g, &maps.out, stage + buffer * G::kOutBytes, v, row0, col);
+          buffer = buffer + 1 < G::kOutBuffers ? buffer + 1 : 0;
+        }
       }
     }
     if ((threadIdx.x & 31) == 0) zr::stores_done();  // out of this block's shared memory

@@ -312,12 +312,12 @@ struct DequantArgs {
 constexpr int kDequantRows = 32, kRowsPerWarp = kDequantRows / (kDequantThreads / 32);
 
 // A block takes 32 rows of a tile, a warp four of them at once (their loads in flight together), a
-// lane eight values of a row. A row that does not begin on a 16-byte boundary goes through shared
-// memory, so that it still leaves in whole aligned words but for its ends.
-template <int DT>
+// lane eight values of a row. ALIGNED: the rows of out begin on 16-byte boundaries; others go through
+// shared memory, so that they still leave in whole aligned words but for their ends.
+template <int DT, bool ALIGNED>
 __global__ void __launch_bounds__(kDequantThreads) dequant_kernel(const __grid_constant__ DequantArgs a) {
   constexpr int es = DT == zr::DT_F32 ? 4 : 2, kRowBytes = zr::kMxCols * es;
-  __shared__ __align__(16) char staging[kDequantThreads / 32][kRowBytes + 16];
+  __shared__ __align__(16) char staging[ALIGNED ? 1 : kDequantThreads / 32][ALIGNED ? 16 : kRowBytes + 16];
   const int64_t t = blockIdx.x >> 2, rt = t / a.tiles, ct = t - rt * a.tiles;
   const uint8_t* tile = a.q + t * zr::kMxTileBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane >> 2;
@@ -349,12 +349,23 @@ __global__ void __launch_bounds__(kDequantThreads) dequant_kernel(const __grid_c
       w[0] = zr::pack8<DT>(v);
     }
     char* out = static_cast<char*>(a.out) + (row * a.ld + c0) * es;
-    const int lead = (int)(reinterpret_cast<uintptr_t>(out) & 15);
-    if (lead == 0 && n == zr::kMxCols) {
+    if (ALIGNED) {
+      if (lane * 8 + 8 <= n) {
 #pragma unroll
-      for (int k = 0; k < es / 2; ++k) zr::st_once(out + (lane * (es / 2) + k) * 16, w[k]);
+        for (int k = 0; k < es / 2; ++k) zr::st_once(out + (lane * (es / 2) + k) * 16, w[k]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (lane * 8 + k < n) {
+            if constexpr (DT == zr::DT_F32)
+              reinterpret_cast<float*>(out)[lane * 8 + k] = v[k];
+            else
+              reinterpret_cast<uint16_t*>(out)[lane * 8 + k] = zr::from_f32<DT>(v[k]);
+          }
+      }
       continue;
     }
+    const int lead = (int)(reinterpret_cast<uintptr_t>(out) & 15);
     char* stage = staging[warp];
 #pragma unroll
     for (int k = 0; k < es / 2; ++k) *reinterpret_cast<uint4*>(stage + (lane * (es / 2) + k) * 16) = w[k];
@@ -376,6 +387,14 @@ __global__ void __launch_bounds__(kDequantThreads) dequant_kernel(const __grid_c
     }
     __syncwarp();
   }
+}
+
+template <int DT>
+void launch_dequant(const DequantArgs& a, int64_t blocks, bool aligned, cudaStream_t s) {
+  if (aligned)
+    dequant_kernel<DT, true><<<(unsigned)blocks, kDequantThreads, 0, s>>>(a);
+  else
+    dequant_kernel<DT, false><<<(unsigned)blocks, kDequantThreads, 0, s>>>(a);
 }
 
 template <int DT, bool CHANCE>
@@ -451,8 +470,9 @@ extern "C" zr_status zr_mx4_dequantize(const void* q, int64_t rows, int64_t cols
   const int64_t blocks = zr::mx_tiles(rows, zr::kMxRows) * a.tiles * (zr::kMxRows / kDequantRows);
   if (blocks > 0x7FFFFFFF) return fail(ZR_ERR_UNSUPPORTED, "zr_mx4_dequantize: matrix too large for one launch");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (dt == ZR_F16) dequant_kernel<zr::DT_F16><<<(unsigned)blocks, kDequantThreads, 0, s>>>(a);
-  else if (dt == ZR_BF16) dequant_kernel<zr::DT_BF16><<<(unsigned)blocks, kDequantThreads, 0, s>>>(a);
-  else dequant_kernel<zr::DT_F32><<<(unsigned)blocks, kDequantThreads, 0, s>>>(a);
+  const bool aligned = ld * (dt == ZR_F32 ? 4 : 2) % 16 == 0;
+  if (dt == ZR_F16) launch_dequant<zr::DT_F16>(a, blocks, aligned, s);
+  else if (dt == ZR_BF16) launch_dequant<zr::DT_BF16>(a, blocks, aligned, s);
+  else launch_dequant<zr::DT_F32>(a, blocks, aligned, s);
   return zr::launch_status("zr_mx4_dequantize");
 }

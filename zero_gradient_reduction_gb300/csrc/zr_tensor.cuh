@@ -96,8 +96,11 @@ __device__ __forceinline__ void box_store(const void* map, int x, int y, uint32_
                : "memory");
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
-// This thread's stores have read their shared memory; have been written.
-__device__ __forceinline__ void stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+// This thread's stores, all but the last PENDING, have read their shared memory; all have been written.
+template <int PENDING>
+__device__ __forceinline__ void stores_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(PENDING) : "memory");
+}
 __device__ __forceinline__ void stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // Shared-memory writes of this thread become visible to bulk copies and products.
