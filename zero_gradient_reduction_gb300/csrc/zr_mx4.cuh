@@ -66,22 +66,22 @@ __device__ __forceinline__ uint32_t mx_codes8(const float t[8]) {
 // the spacing is 1/2, which is what t/2 + 1/2 has in its leading two bits, with the exponents that
 // continue the others'; that sum is the larger of the two exactly there, and it is rounded up, which
 // keeps the condition's sign because the thresholds are representable. On t/4 the leading bits run
-// from 248 (for 0) to 255 (for 6) without a wrap in their byte.
+// from 248 (for 0) to 255 (for 6), so the code is the upper byte's lower three bits.
 __device__ __forceinline__ uint32_t mx_codes8_by_chance(const float x[8], float quarter, const uint32_t dither[8]) {
-  uint32_t c = 0u - 248u * 0x11111111u;
+  uint32_t four, s[8], bits[8];
+  asm("mov.u32 %0, 4;" : "=r"(four));  // unknown to the compiler: a multiply-add, off the busier pipe
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float t = __fmul_rn(fabsf(x[j]), quarter);
-    const uint32_t y = __float_as_uint(fmaxf(t, __fmaf_ru(t, 0.5f, 0.125f)));
-    c += ((y * 4u + dither[j]) >> 24) << (4 * j);
+    s[j] = __float_as_uint(fmaxf(t, __fmaf_ru(t, 0.5f, 0.125f))) * four + dither[j];
+    bits[j] = __float_as_uint(x[j]);
   }
-  // the signs: the upper bytes of the even values and of the odd ones, a byte to each pair of codes
-  auto upper = [&](int j) {
-    const uint32_t a = __byte_perm(__float_as_uint(x[j]), __float_as_uint(x[j + 2]), 0x0073);
-    const uint32_t b = __byte_perm(__float_as_uint(x[j + 4]), __float_as_uint(x[j + 6]), 0x7300);
-    return __byte_perm(a, b, 0x7610);
+  // the upper bytes of the even words, or of the odd ones: a byte to each pair of codes
+  auto upper = [](const uint32_t* w) {
+    return __byte_perm(__byte_perm(w[0], w[2], 0x0073), __byte_perm(w[4], w[6], 0x7300), 0x7610);
   };
-  return c | (upper(0) >> 4 & 0x08080808u) | (upper(1) & 0x80808080u);
+  return (upper(s) & 0x07070707u) | (upper(s + 1) << 4 & 0x70707070u) | (upper(bits) >> 4 & 0x08080808u) |
+         (upper(bits + 1) & 0x80808080u);
 }
 // 2^16 r + 2^15 - 4 for r = byte k of w.
 __device__ __forceinline__ uint32_t mx_dither(uint32_t w, int k) { return __byte_perm(w, 0x7FFCu, 0x6054 | k << 8); }
