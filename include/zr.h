@@ -582,7 +582,8 @@ zr_status zr_mx4_matmul(const void* a, int64_t M, const void* b, int64_t N, int6
  * few tokens may be split over K and joined, in an order that the sizes decide). Up to ZR_MX4_FEW tokens
  * take one launch that reads the weights once, and xq may be NULL; more of them need xq, a
  * device buffer of zr_mx4_bytes(M, K), which then holds MX4(x). (Rows of more than about
- * 300,000 columns need it for few tokens, too.)
+ * 170,000 columns need it for few tokens, too; where it is given it is also used for several tokens
+ * of many outputs, which quantises them once instead of once in each block.)
  * Errors: as the two calls; ZR_ERR_INVALID for a missing xq. */
 zr_status zr_mx4_linear(const void* x, zr_dtype xdt, int64_t M, int64_t ldx, const void* w, int64_t N, int64_t K,
                         void* out, zr_dtype dt, int64_t ldo, void* xq, void* stream);
@@ -590,6 +591,10 @@ zr_status zr_mx4_linear(const void* x, zr_dtype xdt, int64_t M, int64_t ldx, con
 /* Synchronises `stream` and returns ZR_ERR_TIMEOUT if a product on this device gave up a wait
  * since the last call (whose outputs are then not valid), ZR_OK otherwise. */
 zr_status zr_mx4_status(void* stream);
+
+/* Test hook: while `on`, every stage of the products launched expects 16 bytes more than are
+ * copied to it, so that their waits run out; zr_mx4_status reports it. Off after loading. */
+zr_status zr_mx4_stall_waits(int on);
 
 #define ZR_DISTILL_MAX_TOP 1024
 

@@ -170,10 +170,11 @@ def test_matmul(M, N, K, dtype):
         assert bool((room[:, N:] == 7.0).all())
 
 
-@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
 def test_matmul_more_tiles_than_multiprocessors(dtype):
-    """Sizes past both tile shapes' thresholds: blocks that take several tiles, the last ones ragged."""
-    for M, N, K in ((2600, 3000, 512), (1100, 2700, 300), (2945, 2818, 256)):
+    """Sizes past both tile shapes' thresholds: blocks that take several tiles, the last ones ragged; a last round that
+    is taken in halves (9 x 9 tiles of 256 on 76 pairs), with a last column that is whole or a row short."""
+    for M, N, K in ((2600, 3000, 512), (1100, 2700, 300), (2945, 2818, 256), (2300, 2304, 700), (2180, 2296, 512), (2304, 2180, 300)):
         (a, av), (b, bv) = quantised(M, K, 3), quantised(N, K, 4)
         out = torch.full((M, N), float("nan"), dtype=dtype, device="cuda")
         zr.mx4_matmul(a, b, out)
@@ -308,3 +309,26 @@ def test_linear_layer_gradients():
     difference = (h[2] * (ys[0] - ys[1])).sum() / 2
     formula = (h[2].T @ xv)[5, 9]
     assert abs(difference - formula) <= 2.0 ** -20 * (np.abs(h[2].T) @ np.abs(xv))[5, 9]
+
+
+@pytest.mark.parametrize("kind", ["few", "few in clusters", "few, tokens quantised before", "alone", "pairs"])
+def test_waits_end_and_say_so(kind):
+    """Stages that expect bytes which nothing copies: every wait gives up after its two seconds, the status says so
+    once, and the next product is right."""
+    M, N, K = {"few": (2, 50000, 300), "few in clusters": (2, 500, 2048), "few, tokens quantised before": (16, 50000, 2048),
+               "alone": (100, 300, 2048), "pairs": (2304, 2304, 2048)}[kind]
+    x = matrix(M, K, BF16, seed=1, wide=False)
+    w, wv = quantised(N, K, 2)
+    xq, out = zr.Mx4(M, K), torch.empty(M, N, device="cuda")
+    torch.cuda.synchronize()
+    zr.lib().zr_mx4_stall_waits(1)
+    try:
+        zr.mx4_linear(x, w, out, xq=xq)
+    finally:
+        zr.lib().zr_mx4_stall_waits(0)
+    with pytest.raises(zr.ZrError) as e:
+        zr.mx4_status()
+    assert e.value.status == 5
+    zr.mx4_status()
+    zr.mx4_linear(x, w, out, xq=xq)
+    check(out[:, :400], ref.values(*ref.quantise(on_host(x)), K), wv[:400])

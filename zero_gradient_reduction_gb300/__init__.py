@@ -136,6 +136,7 @@ def lib():
                 "zr_mx4_matmul": (st, [vp, i64, vp, i64, i64, vp, i32, i64, vp]),
                 "zr_mx4_linear": (st, [vp, i32, i64, i64, vp, i64, i64, vp, i32, i64, vp, vp]),
                 "zr_mx4_status": (st, [vp]),
+                "zr_mx4_stall_waits": (st, [i32]),
                 "zr_distill_topk": (st, [vp, i32, i64, i64, i64, vp, i32, vp, i32, i32, i64, vp, ctypes.c_float,
                                          ctypes.c_float, vp, vp, vp, i64, vp]),
                 "zr_model_state_bytes": (i64, [i32, i64, i32]),

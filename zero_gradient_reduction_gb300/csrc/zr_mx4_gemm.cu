@@ -9,6 +9,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <type_traits>
 
@@ -24,6 +25,8 @@ namespace {
 
 // Set by a kernel whose wait ran out of time; read and cleared by zr_mx4_status.
 __device__ int g_gave_up;
+// Test hook (zr_mx4_stall_waits): bytes that every stage expects beyond those copied.
+std::atomic<int> g_stall{0};
 
 // ------------------------------------------------------------------ the general product
 // Persistent blocks of six warps: a producer fills a ring of stages (256 columns of K each), one
@@ -62,6 +65,8 @@ struct GemmArgs {
   int64_t M, N, ldo;
   int kt;          // tiles of 256 along K
   int mt, nt;      // output tiles
+  int whole;       // tiles up to here are taken whole; the others, of a pair's last round, in two halves of 128 columns
+  uint32_t stall;  // test hook: bytes expected that never come
   int vec;         // rows of out begin on 16-byte boundaries, and a map can address it
 };
 
@@ -70,7 +75,7 @@ struct GemmArgs {
 // barrier; the tile's bytes are in their place already, so the maps say nothing of swizzles.
 constexpr int kTileLines = zr::kMxTileBytes / 128;
 struct PairMaps {
-  CUtensorMap out, a_tile, b_codes, b_scales;
+  CUtensorMap out, a_tile, b_codes, b_half, b_scales;
 };
 // The output as a box of 32 rows of 128 bytes takes it, swizzled (unused where vec is 0).
 struct OutMap {
@@ -78,14 +83,26 @@ struct OutMap {
 };
 
 // Output tile of a number: groups of up to 32 tiles of rows, and within a group the rows first, so
-// that the blocks at work at one time share few tiles of B and a band of A.
-__device__ __forceinline__ void tile_of(const GemmArgs& g, int id, int& m, int& n) {
+// that the blocks at work at one time share few tiles of B and a band of A. `half`: 0 or 1 for one of
+// a tile's halves, -1 for all of it.
+struct Tile {
+  int m, n, half;
+};
+__device__ __forceinline__ Tile tile_of(const GemmArgs& g, int id) {
   constexpr int kBand = 32;
+  Tile t;
+  t.half = -1;
+  if (id >= g.whole) {
+    t.half = (id - g.whole) & 1;
+    id = g.whole + ((id - g.whole) >> 1);
+  }
   const int per = kBand * g.nt, band = id / per, at = id - band * per;
   const int rows = min(kBand, g.mt - band * kBand);
-  n = at / rows;
-  m = band * kBand + (at - n * rows);
+  t.n = at / rows;
+  t.m = band * kBand + (at - t.n * rows);
+  return t;
 }
+__device__ __forceinline__ int tile_count(const GemmArgs& g) { return 2 * g.mt * g.nt - g.whole; }
 
 // The values of 128 bytes of 32 rows, a row in each lane's registers, to memory. They go through this
 // warp's staging rows in the order of the 128-byte swizzle (16-byte word j of a row at j ^ (row % 8),
@@ -178,7 +195,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     __syncthreads();
   zr::tmem_fence_after();
   const uint32_t tmem = *tmem_at;
-  const int tiles = g.mt * g.nt;
+  const int tiles = tile_count(g);
   const int64_t row_bytes = (int64_t)g.kt * zr::kMxTileBytes;  // a row of MX4 tiles
 
   if (warp == 0) {
@@ -187,19 +204,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       bool ok = true;
       zr::wait_for_previous();
       for (int id = first; id < tiles && ok; id += step) {
-        int m, n;
-        tile_of(g, id, m, n);
+        const Tile t = tile_of(g, id);
+        const bool halved = PAIR && t.half >= 0;
         // a pair's tile may reach past the rows of A or B by an MX4 tile, which is not read then:
         // what the products make of the bytes in its place is not stored
-        const int64_t am = PAIR ? 2 * (int64_t)m + rank : m, bn = PAIR ? 2 * (int64_t)n : n;
-        const bool has_a = !PAIR || am * 128 < g.M, second = PAIR && (bn + 1) * 128 < g.N;
+        const int64_t am = PAIR ? 2 * (int64_t)t.m + rank : t.m, bn = PAIR ? 2 * (int64_t)t.n + (halved ? t.half : 0) : t.n;
+        const bool has_a = !PAIR || am * 128 < g.M, second = PAIR && !halved && (bn + 1) * 128 < g.N;
         const uint8_t *a = g.a + am * row_bytes, *b = g.b + bn * row_bytes;
         const int a_line = (int)(am * g.kt) * kTileLines, b_line = (int)(bn * g.kt) * kTileLines;
         // the first block expects the pair's bytes
         const bool peer_a = PAIR && (am + 1) * 128 < g.M;
-        const uint32_t bytes = PAIR ? zr::kMxTileBytes * (peer_a ? 2 : 1) +
+        const uint32_t bytes = g.stall + (PAIR ? zr::kMxTileBytes * (peer_a ? 2 : 1) +
                                           (zr::kMxCodeBytes + 2 * zr::kMxScaleBytes) * (second ? 2 : 1)
-                                    : 2 * zr::kMxTileBytes;
+                                    : 2 * zr::kMxTileBytes);
         for (int k = 0; k < g.kt; ++k, ++it) {
           const int s = it % G::kStages;
           if (it >= G::kStages && !(ok = zr::bar_wait(empty + 8 * s, (it / G::kStages - 1) & 1, gave_up))) break;
@@ -210,7 +227,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             if (rank == 0) zr::bar_expect(full + 8 * s, bytes);
             if (has_a) zr::pair_copy(at, &maps.a_tile, 0, a_line + line, bar);
             const int next = g.kt * kTileLines;  // the tile's second rows of B
-            if (rank == 0 || second) zr::pair_copy(at + G::kBCodes, &maps.b_codes, 0, b_line + line + rank * next, bar);
+            if (halved)  // 64 rows of it in each block
+              zr::pair_copy(at + G::kBCodes, &maps.b_half, 0, b_line + line + rank * 64, bar);
+            else if (rank == 0 || second)
+              zr::pair_copy(at + G::kBCodes, &maps.b_codes, 0, b_line + line + rank * next, bar);
             zr::pair_copy(at + G::kBScales, &maps.b_scales, 0, b_line + line + 128, bar);
             if (second)
               zr::pair_copy(at + G::kBScales + zr::kMxScaleBytes, &maps.b_scales, 0, b_line + next + line + 128, bar);
@@ -243,6 +263,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       };
       for (int id = first; id < tiles && ok; id += step, ++turn) {
         const uint32_t d = tmem + (turn & 1) * G::kD1, past = turn - G::kLag;
+        const bool halved = PAIR && id >= g.whole;
         if (turn >= G::kLag && !(ok = zr::bar_wait(freed + 8 * (past & 1), (past >> 1) & 1, gave_up))) break;
         zr::tmem_fence_after();
         for (int k = 0; k < g.kt; ++k, ++it) {
@@ -255,13 +276,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             zr::copy_scales<PAIR>(tmem + G::kScaleA + 4 * h, zr::scale_rows(at + zr::kMxCodeBytes + 512 * h));
 #pragma unroll
             for (int t = 0; t < G::kTiles; ++t)
-              zr::copy_scales<PAIR>(tmem + G::kScaleB + 4 * (G::kTiles * h + t),
-                                    zr::scale_rows(at + G::kBScales + t * zr::kMxScaleBytes + 512 * h));
+              if (t == 0 || !halved)
+                zr::copy_scales<PAIR>(tmem + G::kScaleB + 4 * (G::kTiles * h + t),
+                                      zr::scale_rows(at + G::kBScales + t * zr::kMxScaleBytes + 512 * h));
           }
           const uint64_t da = zr::swizzled_operand(at), db = zr::swizzled_operand(at + G::kBCodes);
 #pragma unroll
           for (int q = 0; q < 4; ++q)  // 64 columns, 32 bytes of each row, at a time
-            zr::mx_mma<PAIR>(d, da + 2 * q, db + 2 * q, zr::mx_product(G::kRows, G::kCols, q & 1),
+            zr::mx_mma<PAIR>(d, da + 2 * q, db + 2 * q, zr::mx_product(G::kRows, halved ? 128 : G::kCols, q & 1),
                              tmem + G::kScaleA + 4 * (q >> 1), tmem + G::kScaleB + 4 * G::kTiles * (q >> 1), (k | q) != 0);
           release(empty + 8 * s);
         }
@@ -294,17 +316,18 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     uint32_t turn = 0;
     zr::wait_for_previous();
     for (int id = first; id < tiles; id += step, ++turn) {
-      int m, n;
-      tile_of(g, id, m, n);
+      const Tile t = tile_of(g, id);
       if (!__all_sync(0xFFFFFFFFu, zr::bar_wait(done + 8 * (turn & 1), (turn >> 1) & 1, gave_up))) break;
       zr::tmem_fence_after();
       const uint32_t d = tmem + (turn & 1) * G::kD1 + ((uint32_t)lanes << 16);
-      const int64_t row0 = (int64_t)m * G::kRows + rank * 128 + lanes;
+      const int64_t row0 = (int64_t)t.m * G::kRows + rank * 128 + lanes;
+      const int64_t col0 = (int64_t)t.n * G::kCols + (t.half == 1 ? 128 : 0);
+      const int chunks = PAIR && t.half >= 0 ? kChunks / 2 : kChunks;
 #pragma unroll 1
-      for (int c = 0; c < kChunks; ++c) {
+      for (int c = 0; c < chunks; ++c) {
         // the first accumulator's last columns are the second's first
-        const int at = (turn & 1) ? c : kChunks - 1 - c;
-        const int64_t col = (int64_t)n * G::kCols + at * kOnce;
+        const int at = (turn & 1) ? c : chunks - 1 - c;
+        const int64_t col = col0 + at * kOnce;
         uint32_t v[kOnce];
         if constexpr (kOnce == 32)
           zr::tmem_load32(d + at * kOnce, v);
@@ -350,6 +373,7 @@ struct FewArgs {
   int64_t M, K, N, ldx, ldo;
   int kt, xdt, odt;
   int stages;  // of a block's ring
+  uint32_t stall;  // test hook: bytes expected that never come
 };
 
 __host__ __device__ constexpr int few_smem(int k_tiles, int stages) {
@@ -431,7 +455,7 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
     zr::proxy_fence();
     *gave_up = 0;
     for (int k = 0; k < nk && k < g.stages; ++k) {
-      zr::bar_expect(full + 8 * k, zr::kMxTileBytes);
+      zr::bar_expect(full + 8 * k, zr::kMxTileBytes + g.stall);
       zr::bulk_copy(stages + k * zr::kMxTileBytes, w + (int64_t)k * zr::kMxTileBytes, zr::kMxTileBytes, full + 8 * k);
     }
   }
@@ -512,9 +536,10 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
                      scale_b + 4 * (q >> 1), (k | q) != 0);
         if (k + g.stages < nk) zr::mma_commit(empty + 8 * s);
       }
-      if (*gave_up && g.xq) {  // nothing may be in flight at the end: the tokens, too
+      if (k < nk || *gave_up) {  // no copy may be in flight at the end
         int never = 0;
-        zr::bar_wait(tokens, 0, &never);
+        if (g.xq) zr::bar_wait(tokens, 0, &never);
+        for (int i = 0; i < nk && nk <= g.stages; ++i) zr::bar_wait(full + 8 * i, 0, &never);
       }
       zr::mma_commit(done);  // after a wait that gave up too: nothing may be in flight at the end
     }
@@ -524,7 +549,7 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
       for (; k < nk; ++k) {
         const int s = k % g.stages;
         if (!zr::bar_wait(empty + 8 * s, (k / g.stages - 1) & 1, gave_up)) break;
-        zr::bar_expect(full + 8 * s, zr::kMxTileBytes);
+        zr::bar_expect(full + 8 * s, zr::kMxTileBytes + g.stall);
         zr::bulk_copy(stages + s * zr::kMxTileBytes, w + (int64_t)k * zr::kMxTileBytes, zr::kMxTileBytes, full + 8 * s);
       }
       int never = 0;
@@ -646,6 +671,7 @@ zr_status launch_gemm(const GemmArgs& g, int blocks, bool early, cudaStream_t s)
     const int64_t a_tiles = zr::mx_tiles(g.M, zr::kMxRows) * g.kt, b_tiles = zr::mx_tiles(g.N, zr::kMxRows) * g.kt;
     if (!encode_lines(&maps.a_tile, g.a, a_tiles, kTileLines) ||
         !encode_lines(&maps.b_codes, g.b, b_tiles, zr::kMxRows) ||
+        (g.whole < g.mt * g.nt && !encode_lines(&maps.b_half, g.b, b_tiles, zr::kMxRows / 2)) ||
         !encode_lines(&maps.b_scales, g.b, b_tiles, zr::kMxScaleBytes / 128))
       return fail(ZR_ERR_CUDA, "zr_mx4_matmul: the driver gave no tensor map");
   }
@@ -669,6 +695,7 @@ zr_status matmul(const char* what, const void* a, int64_t M, const void* b, int6
   g.b = static_cast<const uint8_t*>(b);
   g.out = out;
   g.M = M; g.N = N; g.ldo = ldo;
+  g.stall = g_stall.load(std::memory_order_relaxed) ? 16 : 0;
   const int64_t kt = zr::mx_tiles(K, zr::kMxCols);
   // pairs where each gets a tile (and 32 bits hold a matrix's lines)
   const int64_t most = 0x7FFFFFFF / kTileLines;
@@ -679,8 +706,12 @@ zr_status matmul(const char* what, const void* a, int64_t M, const void* b, int6
     return fail(ZR_ERR_UNSUPPORTED, "%s: the product has too many tiles", what);
   g.kt = (int)kt; g.mt = (int)mt; g.nt = (int)nt;
   g.vec = ldo * es % 16 == 0 && ldo < (int64_t)1 << 36 && M <= 0x7FFFFFFF && N <= 0x7FFFFFFF;
+  g.whole = g.mt * g.nt;
   if (pair) {
-    const int blocks = 2 * (int)(mt * nt < sms / 2 ? mt * nt : sms / 2);
+    const int pairs = sms / 2, last = g.whole % pairs, blocks = 2 * (g.whole < pairs ? g.whole : pairs);
+    // a last round that fewer than half of the pairs would be busy with, in halves (2048 x 8192 x 8192:
+    // 48.2 us in 4 rounds, 45.6 in 3.5); not where the last column of tiles has no second half
+    if (last > 0 && 2 * last <= pairs && (int64_t)nt * 256 - N < 128) g.whole -= last;
     if (dt == ZR_F16) return launch_gemm<true, zr::DT_F16>(g, blocks, early, s);
     if (dt == ZR_BF16) return launch_gemm<true, zr::DT_BF16>(g, blocks, early, s);
     return launch_gemm<true, zr::DT_F32>(g, blocks, early, s);
@@ -743,6 +774,7 @@ extern "C" zr_status zr_mx4_linear(const void* x, zr_dtype xdt, int64_t M, int64
     g.x = x; g.w = static_cast<const uint8_t*>(w); g.out = out;
     g.M = M; g.K = K; g.N = N; g.ldx = ldx; g.ldo = ldo;
     g.kt = (int)kt; g.xdt = (int)xdt; g.odt = (int)dt;
+    g.stall = g_stall.load(std::memory_order_relaxed) ? 16 : 0;
     const int blocks = (int)(nt * split);
     // as many stages as fit where every block that there is, up to three to a multiprocessor, is resident
     // at once: one more wave costs more than a shorter ring
@@ -783,4 +815,10 @@ extern "C" zr_status zr_mx4_status(void* stream) {
       return fail(ZR_ERR_TIMEOUT, "zr_mx4_status: a product gave up a wait; outputs since the last check are not valid");
   }
   return e == cudaSuccess ? ZR_OK : fail(ZR_ERR_CUDA, "zr_mx4_status: %s", cudaGetErrorString(e));
+}
+
+extern "C" zr_status zr_mx4_stall_waits(int on) {
+  zr::clear_error();
+  g_stall.store(on ? 1 : 0, std::memory_order_relaxed);
+  return ZR_OK;
 }
