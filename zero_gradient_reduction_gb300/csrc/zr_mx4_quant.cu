@@ -41,7 +41,7 @@ struct Shape {
   __host__ __device__ static constexpr int at(int r) { return r * pitch + (r >> 5) * 64; }
   static constexpr int bytes = kRows * pitch + 64;
 };
-constexpr int kRandPitch = kCols + 8;
+constexpr int kRandPitch = kCols + 16;
 __host__ __device__ constexpr int rand_at(int r) { return r * kRandPitch + (r >> 5) * 32; }
 constexpr int kRandBytes = kRows * kRandPitch + 32;
 
@@ -87,6 +87,33 @@ __device__ __forceinline__ uint32_t lane_bytes(int byte) {
   return w;
 }
 
+// The memory words that hold a patch's rows, WORDS + 1 for each (the first may begin before the row),
+// to its places in shared memory; zeros for what lies past `bytes` of a row and past `rows`.
+template <int WORDS>
+__device__ __forceinline__ void fetch(int (*at)(int), char* to, const char* from, int64_t pitch, int rows, int bytes) {
+  for (int k = threadIdx.x; k < kRows * (WORDS + 1); k += kThreads) {
+    const int r = k / (WORDS + 1), j = k - r * (WORDS + 1);
+    const char* row = from + (r < rows ? r : 0) * pitch;
+    const int before = (int)(reinterpret_cast<uintptr_t>(row) & 15), left = bytes + before - 16 * j;
+    const int valid = r < rows ? (left < 16 ? (left > 0 ? left : 0) : 16) : 0;
+    zr::copy16_of(zr::smem_u32(to + at(r) + 16 * j), valid ? row - before + 16 * j : row - before, valid);
+  }
+}
+// Moves each of those rows to the beginning of its place.
+template <int WORDS>
+__device__ __forceinline__ void align(int (*at)(int), char* rows, const char* from, int64_t pitch) {
+  constexpr int kAtOnce = 32 / WORDS;  // rows of a warp
+  const int lane = threadIdx.x & 31, j = lane % WORDS;
+#pragma unroll 4
+  for (int r = (threadIdx.x >> 5) * kAtOnce + lane / WORDS; r < kRows; r += kThreads / WORDS) {
+    uint4* row = reinterpret_cast<uint4*>(rows + at(r));
+    const uint32_t before = (uint32_t)(reinterpret_cast<uintptr_t>(from + r * pitch) & 15);
+    const uint4 v = zr::shift16(row[j], row[j + 1], before);
+    __syncwarp();
+    if (before) row[j] = v;
+  }
+}
+
 template <int DT, bool CHANCE>
 __global__ void __launch_bounds__(kThreads, DT == zr::DT_F32 ? (CHANCE ? 5 : 6) : 8) quant_kernel(const __grid_constant__ QuantArgs a) {
   using S = Shape<DT>;
@@ -98,79 +125,35 @@ __global__ void __launch_bounds__(kThreads, DT == zr::DT_F32 ? (CHANCE ? 5 : 6) 
   zr::let_next_begin();  // a product of what this writes (it waits for that before it reads)
 
   // ---- the patch to shared memory as it is, zeros outside the matrix
-  constexpr int kPer = 16 / S::es, kVecs = kCols / kPer, kLoads = kRows * kVecs / kThreads;
-  const char* xb = static_cast<const char*>(a.x);
+  constexpr int kWords = kCols * S::es / 16, kRandWords = kCols / 16;  // 16-byte words of a row
+  const char* x = static_cast<const char*>(a.x) + (r0 * a.ldx + c0) * S::es;
+  const char* rnd0 = reinterpret_cast<const char*>(a.rand) + r0 * a.ldr + c0;
   if (a.whole && r0 + kRows <= a.rows && c0 + kCols <= a.cols) {
-    // a patch inside a matrix of aligned rows: copies, all of them in flight
-    constexpr int kStep = kThreads / kVecs;  // rows between a thread's words; a divisor of 32
-    const char* from = xb + ((r0 + tid / kVecs) * a.ldx + c0) * S::es + (tid % kVecs) * 16;
-    const uint32_t to = zr::smem_u32(smem) + (tid / kVecs) * S::pitch + (tid % kVecs) * 16;
+    // a patch inside a matrix of aligned rows
+    constexpr int kStep = kThreads / kWords, kRandStep = kThreads / kRandWords;  // rows between a thread's words
+    const char* from = x + (tid / kWords) * a.ldx * S::es + (tid % kWords) * 16;
+    const uint32_t to = zr::smem_u32(smem) + (tid / kWords) * S::pitch + (tid % kWords) * 16;
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i)
-      zr::copy16(to + S::at(i * kStep), from + i * kStep * a.ldx * S::es);
+    for (int i = 0; i < kRows / kStep; ++i) zr::copy16(to + S::at(i * kStep), from + i * kStep * a.ldx * S::es);
     if (CHANCE) {
-      const uint8_t* rfrom = a.rand + (r0 + (tid >> 4)) * a.ldr + c0 + (tid & 15) * 8;
-      const uint32_t rto = zr::smem_u32(srand) + (tid >> 4) * kRandPitch + (tid & 15) * 8;
+      from = rnd0 + (tid / kRandWords) * a.ldr + (tid % kRandWords) * 16;
+      const uint32_t rto = zr::smem_u32(srand) + (tid / kRandWords) * kRandPitch + (tid % kRandWords) * 16;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) zr::copy8(rto + rand_at(i * 8), rfrom + i * 8 * a.ldr);
+      for (int i = 0; i < kRows / kRandStep; ++i) zr::copy16(rto + rand_at(i * kRandStep), from + i * kRandStep * a.ldr);
     }
     zr::copies_done();
   } else {
-#pragma unroll
-  for (int half = 0; half < kLoads; half += 8) {
-    uint4 v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int k = tid + (half + i) * kThreads, r = k / kVecs, c = (k % kVecs) * kPer;
-      v[i] = make_uint4(0, 0, 0, 0);
-      if (r0 + r < a.rows && c0 + c < a.cols) {
-        const int64_t e = (r0 + r) * a.ldx + c0 + c;
-        if (c0 + c + kPer <= a.cols) {
-          v[i] = zr::load16(xb + e * S::es);
-        } else {
-          uint32_t w[4] = {0, 0, 0, 0};
-          const int left = (int)(a.cols - c0 - c);
-#pragma unroll
-          for (int j = 0; j < kPer; ++j)
-            if (j < left) {
-              if (S::es == 4)
-                w[j] = static_cast<const uint32_t*>(a.x)[e + j];
-              else
-                w[j / 2] |= (uint32_t)static_cast<const uint16_t*>(a.x)[e + j] << (16 * (j & 1));
-            }
-          v[i] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-      }
+    const int64_t down = a.rows - r0, right = a.cols - c0;
+    const int rows = (int)(down < kRows ? (down > 0 ? down : 0) : kRows);
+    const int cols = (int)(right < kCols ? (right > 0 ? right : 0) : kCols);
+    fetch<kWords>(S::at, smem, x, a.ldx * S::es, rows, cols * S::es);
+    if (CHANCE) fetch<kRandWords>(rand_at, reinterpret_cast<char*>(srand), rnd0, a.ldr, rows, cols);
+    zr::copies_done();
+    __syncthreads();
+    if (!a.whole) {
+      align<kWords>(S::at, smem, x, a.ldx * S::es);
+      if (CHANCE) align<kRandWords>(rand_at, reinterpret_cast<char*>(srand), rnd0, a.ldr);
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int k = tid + (half + i) * kThreads, r = k / kVecs, c = k % kVecs;
-      *reinterpret_cast<uint4*>(smem + S::at(r) + c * 16) = v[i];
-    }
-  }
-  if (CHANCE) {
-#pragma unroll
-    for (int i = 0; i < kRows * kCols / 16 / kThreads; ++i) {
-      const int k = tid + i * kThreads, r = k / 8, c = (k % 8) * 16;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (r0 + r < a.rows && c0 + c < a.cols) {
-        const uint8_t* p = a.rand + (r0 + r) * a.ldr + c0 + c;
-        if (c0 + c + 16 <= a.cols) {
-          v = zr::load16(reinterpret_cast<const char*>(p));
-        } else {
-          uint32_t w[4] = {0, 0, 0, 0};
-          const int left = (int)(a.cols - c0 - c);
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (j < left) w[j / 4] |= (uint32_t)p[j] << (8 * (j & 3));
-          v = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-      }
-      uint2* d = reinterpret_cast<uint2*>(srand + rand_at(r) + c);
-      d[0] = make_uint2(v.x, v.y);
-      d[1] = make_uint2(v.z, v.w);
-    }
-  }
   }
   __syncthreads();
 
