@@ -91,12 +91,17 @@ __device__ __forceinline__ uint32_t lane_bytes(int byte) {
 // to its places in shared memory; zeros for what lies past `bytes` of a row and past `rows`.
 template <int WORDS>
 __device__ __forceinline__ void fetch(int (*at)(int), char* to, const char* from, int64_t pitch, int rows, int bytes) {
-  for (int k = threadIdx.x; k < kRows * (WORDS + 1); k += kThreads) {
-    const int r = k / (WORDS + 1), j = k - r * (WORDS + 1);
-    const char* row = from + (r < rows ? r : 0) * pitch;
-    const int before = (int)(reinterpret_cast<uintptr_t>(row) & 15), left = bytes + before - 16 * j;
-    const int valid = r < rows ? (left < 16 ? (left > 0 ? left : 0) : 16) : 0;
-    zr::copy16_of(zr::smem_u32(to + at(r) + 16 * j), valid ? row - before + 16 * j : row - before, valid);
+  constexpr int kEach = WORDS + 1, kDown = kThreads / kEach, kOver = kThreads % kEach;
+  int r = threadIdx.x / kEach, j = threadIdx.x % kEach;
+  const char* row = from + r * pitch;
+#pragma unroll 3
+  for (; r < kRows;) {
+    const int before = (int)(reinterpret_cast<uintptr_t>(row) & 15), left = r < rows ? bytes + before - 16 * j : 0;
+    zr::copy16_of(zr::smem_u32(to + at(r) + 16 * j), left > 0 ? row - before + 16 * j : from, left < 16 ? (left > 0 ? left : 0) : 16);
+    const int down = j + kOver >= kEach ? kDown + 1 : kDown;
+    j += j + kOver >= kEach ? kOver - kEach : kOver;
+    r += down;
+    row += down * pitch;
   }
 }
 // Moves each of those rows to the beginning of its place.
