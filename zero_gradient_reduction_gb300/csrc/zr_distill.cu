@@ -6,6 +6,13 @@
 // is read once into shared memory (of one block, or of a cluster that shares the row), its
 // maximum, its sum of exponentials and its gradient come from there, and the gradient is written
 // once. All arithmetic is fp32; sums are taken in an order that the sizes alone decide.
+//
+// Two bytes (or four) a logit each way bind it: 8192 x 50304 bf16 in 262 us, 6.3 TB/s of the 6.8 that
+// a copy reaches, with two rows at work on each multiprocessor (101 KB each), one read while the
+// other is summed. A first form with loads through registers and fp32 one at a time took 724 us;
+// asynchronous copies 344, two exponentials' arithmetic in one instruction and results under 2^-126 to
+// zero 310, the teacher's entries in a warp of their own 263. 13 x 50257 fp32, a cluster of 8 blocks to
+// a row: 9.4 us, of which a launch is 2.5 and each wait of the cluster about 1.
 #include <cuda_runtime.h>
 
 #include <cstdint>

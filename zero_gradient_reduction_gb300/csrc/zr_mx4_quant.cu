@@ -1,5 +1,14 @@
 // Quantisation of a matrix to the microscaled 4-bit format (by its rows, by its columns, or
 // both from one read) and back to the values that the codes stand for.
+//
+// Quantising reads a value once and writes 17/32 byte of it for each direction; a block brings a
+// patch to shared memory by asynchronous copies and lets each thread take whole blocks of 32 from
+// there, along the rows and then along the columns, so that no scale needs a reduction between
+// threads. To nearest it is bound by memory: fp32 50304 x 2048 both ways in 80 us, 6.5 TB/s of the
+// 6.8 that a copy reaches. By chance, with a random byte more per value, the rounding's whole-number
+// steps bind it: bf16 8192 x 8192 both ways in 64 us, 4.3 TB/s with the integer pipe at 75 %.
+// Dequantising bf16 50304 x 2048 takes 39 us, 6.7 TB/s; with rows of odd length 4099 x 2049 in
+// 7.6 us, 2.8 TB/s, where 4096 x 2048 takes 3.9.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -16,7 +25,7 @@ namespace {
 
 // A block quantises 64 x 128 values: half a tile's rows by half its columns in q, half a tile's rows by
 // a quarter of its columns in qt. Blocks of twice the rows and threads left a longer last wave (4099 x
-// 2049 in bf16 by chance both ways 21.1 us; now XXX).
+// 2049 in bf16 by chance both ways 21.1 us, then; 16.9 now).
 constexpr int kThreads = 128, kRows = 64, kCols = 128;
 constexpr int kDequantThreads = 256;
 
