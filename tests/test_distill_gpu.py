@@ -88,6 +88,44 @@ def test_loss_and_gradient(T, V, K, dtype):
         check(*case(T, V, K, dtype, seed=T + V + i, ids_type=(torch.int32, torch.int64)[i % 2], tdt=(F32, BF16, F16)[i]), tau=tau, scale=3.0)
 
 
+@pytest.mark.parametrize("centre,tau,V", [(5000.0, 0.01, 900), (7000.0, 0.01, 900), (6931.0, 0.01, 60_000), (-3e4, 1e-3, 500), (1e30, 1.0, 300)])
+def test_logits_far_from_zero_at_low_temperatures(centre, tau, V):
+    """Exponents whose common part is from 10^5 to 10^30: only the differences count. The spread, not the magnitude,
+    decides what fp32 may cost: the differences are exact up to two roundings of an exponent of at most A."""
+    g = torch.Generator().manual_seed(V)
+    ulp = float(np.spacing(np.float32(abs(centre))))
+    z = (centre + max(ulp, tau) * torch.randint(-6, 7, (6, V), generator=g).double()).float().cuda()
+    ids = torch.stack([torch.randperm(V, generator=g)[:9] for _ in range(6)]).int().cuda()
+    teacher = (tau * torch.randn(6, 9, generator=g)).cuda()
+    weight, loss, grad = torch.ones(6, device="cuda"), torch.empty(6, device="cuda"), torch.empty_like(z)
+    zr.distill_topk(z, ids, teacher, loss, grad, weight=weight, temperature=tau)
+    h = [v.double().cpu().numpy() for v in (z, teacher, weight)]
+    l, want, onto = formula(h[0], ids.cpu().numpy(), h[1], h[2], tau, 1.0)
+    spread = (h[0].max(1) - h[0].min(1)).max()
+    bl, bg = bounds(h[0] - h[0].max(1, keepdims=True), h[1], l, want, onto, h[2], tau, 1.0, F32)
+    assert spread > 0
+    assert (np.abs(loss.double().cpu().numpy() - l) <= bl).all()
+    assert (np.abs(grad.double().cpu().numpy() - want) <= bg).all()
+
+
+def test_offsets_past_32_bits():
+    """More than 2^32 bytes and 2^31 logits: the last rows against the formula."""
+    T, V, K = 44_000, 50_304, 4
+    z = torch.empty(T, V, dtype=BF16, device="cuda")
+    assert z.numel() > 1 << 31
+    some = torch.tensor([0, 21_000, T - 2, T - 1])
+    z.normal_()
+    ids = torch.randint(0, V, (T, K), dtype=torch.int64, device="cuda")
+    teacher, loss = torch.randn(T, K, device="cuda"), torch.empty(T, device="cuda")
+    h = [v[some.cuda()].double().cpu().numpy() for v in (z, teacher)]
+    w = np.ones(len(some))
+    l, g, onto = formula(h[0], ids[some.cuda()].cpu().numpy(), h[1], w, 1.0, 1.0)
+    zr.distill_topk(z, ids, teacher, loss, z)
+    bl, bg = bounds(h[0], h[1], l, g, onto, w, 1.0, 1.0, BF16)
+    assert (np.abs(loss[some.cuda()].double().cpu().numpy() - l) <= bl).all()
+    assert (np.abs(z[some.cuda()].double().cpu().numpy() - g) <= bg).all()
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_many_rows_and_long_rows(dtype):
     check(*case(400, 2000, 8, dtype, seed=1))       # a block for each row, several waves

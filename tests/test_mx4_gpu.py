@@ -260,6 +260,33 @@ def test_bytes_outside_are_untouched():
     assert bool((raw[:1024] == 7).all()) and bool((raw[1024 + 130 * 131:] == 7).all())
 
 
+def test_offsets_past_32_bits():
+    """Matrices of more than 2^31 values, whose 4-bit forms are read and written past 2^32 bytes of fp32: rows and columns
+    at both ends against the format's definition, and a product of more than 2^31 results."""
+    rows, cols = 70_001, 32_000
+    x = torch.empty(rows, cols, dtype=BF16, device="cuda").normal_()
+    assert x.numel() > 1 << 31
+    q, qt = zr.Mx4(rows, cols), zr.Mx4(cols, rows)
+    zr.mx4_quantize(x, q, qt)
+    out = torch.empty(rows, cols, dtype=BF16, device="cuda")
+    zr.mx4_dequantize(q, out)
+    for at in (slice(0, 2), slice(35_000, 35_002), slice(rows - 2, rows)):
+        want = torch.from_numpy(ref.values(*ref.quantise(on_host(x[at])), cols)).to(BF16)
+        assert torch.equal(out[at].cpu(), want)
+    del out
+    out_t = torch.empty(cols, rows, dtype=BF16, device="cuda")
+    zr.mx4_dequantize(qt, out_t)
+    for at in (slice(0, 2), slice(cols - 2, cols)):
+        want = torch.from_numpy(ref.values(*ref.quantise(on_host(x[:, at]).T), rows)).to(BF16)
+        assert torch.equal(out_t[at].cpu(), want)
+    del out_t, x, q, qt
+    (a, av), (b, bv) = quantised(rows, 96, 1), quantised(cols, 96, 2)
+    y = torch.empty(rows, cols, dtype=BF16, device="cuda")
+    zr.mx4_matmul(a, b, y)
+    for at in (slice(0, 3), slice(rows - 3, rows)):
+        check(y[at], av[at], bv)
+
+
 def test_other_stream_and_graph():
     """A call on its own stream, and a captured quantise + product that follows its inputs."""
     x = matrix(40, 512, BF16, seed=1)

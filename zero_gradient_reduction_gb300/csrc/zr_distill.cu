@@ -151,24 +151,26 @@ __device__ __forceinline__ float warp_max(float v) {
 
 // A sum of exponentials is kept relative to the maximum m of its z, in base 2 and as one
 // multiply-add: sum of 2^(z c - mc), mc = m c rounded. That rounding multiplies every term by the
-// same factor, which cancels in q and in log q. Where m c is not a usable number (a mask of the
-// type's lowest value, which times c overflows) the terms are 2^((z - m) c). A part that is all
-// masked has m = -inf; its terms are taken relative to 0: 0, or NaN where z is.
+// same factor, which cancels in q and in log q. Where m c is so large that the factor would be
+// anything (logits of 10^4 at a temperature of 0.01, a mask of the type's lowest value) the terms are
+// 2^((z - m) c). A part that is all masked has m = -inf; its terms are taken relative to 0: 0, or NaN
+// where z is.
 struct Base {
   float m, mc, c;
   bool fused;
   __device__ Base(float largest, float c_) : c(c_) {
     m = largest == -INFINITY ? 0.0f : largest;
     mc = __fmul_rn(m, c);
-    fused = fabsf(mc) < 1e37f;  // not where m is NaN or infinite either
+    fused = fabsf(mc) < 1e6f;  // a factor of at most 2^(1/32); not where m is NaN or infinite either
   }
   __device__ float exponent(float z) const { return fused ? __fmaf_rn(z, c, -mc) : __fmul_rn(z - m, c); }
 };
-// A sum relative to the maximum m, relative to a larger one.
+// A sum relative to the maximum m, relative to a larger one: each as it is kept.
 __device__ __forceinline__ float rescaled(float m, float sum, const Base& to) {
   if (m == -INFINITY) return sum;
   const Base from(m, to.c);
-  return __fmul_rn(sum, exp2_fast(from.fused && to.fused ? from.mc - to.mc : __fmul_rn(m - to.m, to.c)));
+  const float e = from.fused ? (to.fused ? from.mc - to.mc : __fmaf_rn(-to.m, to.c, from.mc)) : to.exponent(from.m);
+  return __fmul_rn(sum, exp2_fast(e));
 }
 
 struct Shared {      // what the block's warps, and the cluster's blocks, tell each other
@@ -198,6 +200,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) distill_kernel(const __grid_co
   const int64_t v0 = rank * a.share, v1 = v0 + a.share < a.V ? v0 + a.share : a.V;
   const int n = v1 > v0 ? (int)(v1 - v0) : 0;  // this block's columns; the last blocks may have none
 
+  if (C > 1) zr::cluster_arrived();  // a block's shared memory may be written to once it has begun
   const float w = a.weight ? a.weight[row] : 1.0f;
   const float c = __fdiv_rn(kLog2E, a.tau);
   char* grad = a.grad ? static_cast<char*>(a.grad) + (row * a.ldg + v0) * es : nullptr;
@@ -325,6 +328,8 @@ __global__ void __launch_bounds__(kMaxThreads, 2) distill_kernel(const __grid_co
       }
       if (single >= 0) store1<DT>(grad, single, 0.0f);
     }
+    __syncwarp();
+    if (C > 1) zr::cluster_wait();
     return;
   }
 
@@ -332,6 +337,8 @@ __global__ void __launch_bounds__(kMaxThreads, 2) distill_kernel(const __grid_co
   float wm = has ? sh.m[lane & 15] : -INFINITY, m = warp_max(wm);
   float sum = warp_sum(has ? rescaled(wm, sh.sum[lane & 15], Base(m, c)) : 0.0f);
   if (C > 1) {
+    __syncwarp();
+    zr::cluster_wait();
     if (tid < C) {
       zr::cluster_store(zr::cluster_addr(zr::smem_u32(&sh.row_m[rank]), tid), m);
       zr::cluster_store(zr::cluster_addr(zr::smem_u32(&sh.row_sum[rank]), tid), sum);
