@@ -97,16 +97,20 @@ __device__ __forceinline__ uint32_t lane_bytes(int byte) {
 }
 
 // The memory words that hold a patch's rows, WORDS + 1 for each (the first may begin before the row),
-// to its places in shared memory; zeros for what lies past `bytes` of a row and past `rows`.
+// to its places in shared memory; zeros for what lies past `bytes` of a row and past `rows`. A copy of
+// no bytes still names an address, which has to be one that is there: `any`, the matrix's first.
 template <int WORDS>
-__device__ __forceinline__ void fetch(int (*at)(int), char* to, const char* from, int64_t pitch, int rows, int bytes) {
+__device__ __forceinline__ void fetch(int (*at)(int), char* to, const void* any, const char* from, int64_t pitch, int rows,
+                                      int bytes) {
   constexpr int kEach = WORDS + 1, kDown = kThreads / kEach, kOver = kThreads % kEach;
   int r = threadIdx.x / kEach, j = threadIdx.x % kEach;
   const char* row = from + r * pitch;
 #pragma unroll 3
   for (; r < kRows;) {
-    const int before = (int)(reinterpret_cast<uintptr_t>(row) & 15), left = r < rows ? bytes + before - 16 * j : 0;
-    zr::copy16_of(zr::smem_u32(to + at(r) + 16 * j), left > 0 ? row - before + 16 * j : from, left < 16 ? (left > 0 ? left : 0) : 16);
+    const int before = (int)(reinterpret_cast<uintptr_t>(row) & 15);
+    const int left = r < rows && bytes > 0 ? bytes + before - 16 * j : 0;
+    const void* word = left > 0 ? row - before + 16 * j : any;
+    zr::copy16_of(zr::smem_u32(to + at(r) + 16 * j), word, left < 16 ? (left > 0 ? left : 0) : 16);
     const int down = j + kOver >= kEach ? kDown + 1 : kDown;
     j += j + kOver >= kEach ? kOver - kEach : kOver;
     r += down;
@@ -160,8 +164,8 @@ __global__ void __launch_bounds__(kThreads, DT == zr::DT_F32 ? (CHANCE ? 5 : 6) 
     const int64_t down = a.rows - r0, right = a.cols - c0;
     const int rows = (int)(down < kRows ? (down > 0 ? down : 0) : kRows);
     const int cols = (int)(right < kCols ? (right > 0 ? right : 0) : kCols);
-    fetch<kWords>(S::at, smem, x, a.ldx * S::es, rows, cols * S::es);
-    if (CHANCE) fetch<kRandWords>(rand_at, reinterpret_cast<char*>(srand), rnd0, a.ldr, rows, cols);
+    fetch<kWords>(S::at, smem, a.x, x, a.ldx * S::es, rows, cols * S::es);
+    if (CHANCE) fetch<kRandWords>(rand_at, reinterpret_cast<char*>(srand), a.rand, rnd0, a.ldr, rows, cols);
     zr::copies_done();
     __syncthreads();
     if (!a.whole) {
