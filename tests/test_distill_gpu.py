@@ -251,6 +251,21 @@ def test_plan_scales_the_gradient():
     assert torch.equal(grad * 2, before)
 
 
+def test_what_does_not_fit_is_refused():
+    z, ids, teacher, weight = case(4, 50, 3, F32, seed=12)
+    loss, grad = torch.empty(4, device="cuda"), torch.empty_like(z)
+    ok = dict(logits=z, ids=ids, teacher=teacher, loss=loss, grad=grad, weight=weight)
+    for bad in (dict(ids=ids.short()), dict(ids=ids[:, :2]), dict(ids=ids[:3], teacher=teacher[:3]), dict(ids=ids.cpu()),
+                dict(loss=loss[:3]), dict(loss=loss.double()), dict(weight=weight[:3]), dict(grad=grad.half()),
+                dict(grad=grad[:, :49]), dict(logits=z.double(), grad=grad.double()), dict(temperature=0.0),
+                dict(grad_scale=float("inf")), dict(ids=ids.t().contiguous().t()), dict(teacher=teacher.t().contiguous().t()),
+                dict(logits=z[:, 1:], grad=grad[:, 1:])):
+        with pytest.raises(zr.ZrError) as e:
+            zr.distill_topk(**{**ok, **bad})
+        assert e.value.status == 1, bad
+    zr.distill_topk(**ok)
+
+
 def test_other_stream_and_guards():
     z, ids, teacher, weight = case(7, 999, 12, BF16, seed=11)
     raw = torch.full((7 * 999 + 2048,), 7.0, dtype=BF16, device="cuda")

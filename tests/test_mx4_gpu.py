@@ -174,11 +174,13 @@ def test_matmul(M, N, K, dtype):
 def test_matmul_more_tiles_than_multiprocessors(dtype):
     """Sizes past both tile shapes' thresholds: blocks that take several tiles, the last ones ragged; a last round that
     is taken in halves (9 x 9 tiles of 256 on 76 pairs), with a last column that is whole or a row short."""
-    for M, N, K in ((2600, 3000, 512), (1100, 2700, 300), (2945, 2818, 256), (2300, 2304, 700), (2180, 2296, 512), (2304, 2180, 300)):
+    for M, N, K in ((2600, 3000, 512), (1100, 2699, 300), (2945, 2818, 256), (2300, 2304, 700), (2180, 2296, 512), (2304, 2181, 300)):
         (a, av), (b, bv) = quantised(M, K, 3), quantised(N, K, 4)
-        out = torch.full((M, N), float("nan"), dtype=dtype, device="cuda")
-        zr.mx4_matmul(a, b, out)
-        check(out, av, bv)
+        for ld in (N, (N + 15) // 8 * 8):
+            room = torch.full((M, ld), 7.0, dtype=dtype, device="cuda")
+            zr.mx4_matmul(a, b, room[:, :N])
+            check(room[:, :N], av, bv)
+            assert bool((room[:, N:] == 7.0).all())
 
 
 def test_matmul_is_repeatable():
@@ -233,6 +235,25 @@ def test_not_a_number_stays_in_its_rows(M):
     zr.mx4_linear(x, w, clean, xq=zr.Mx4(M, 600))
     keep = ~want
     assert torch.equal(out.cpu()[keep], clean.cpu()[keep])
+
+
+def test_what_does_not_fit_is_refused():
+    """Shapes, types, places and strides that the binding sees, and the library's own refusals through it."""
+    x, q = torch.zeros(8, 64, device="cuda"), zr.Mx4(8, 64)
+    out = torch.empty(8, 8, device="cuda")
+    for call in (lambda: zr.mx4_quantize(x, zr.Mx4(8, 65)), lambda: zr.mx4_quantize(x, None, zr.Mx4(8, 64)),
+                 lambda: zr.mx4_quantize(x), lambda: zr.mx4_quantize(x.t(), zr.Mx4(64, 8)),
+                 lambda: zr.mx4_quantize(x.double(), q), lambda: zr.mx4_quantize(x[:, 1:], zr.Mx4(8, 63)),
+                 lambda: zr.mx4_quantize(x, q, rand=torch.zeros(8, 63, dtype=torch.uint8, device="cuda")),
+                 lambda: zr.mx4_quantize(x, q, rand=x), lambda: zr.mx4_quantize(x[0], q), lambda: zr.mx4_quantize(x.expand(8, 64)[:1].expand(8, 64), q),
+                 lambda: zr.mx4_dequantize(q, out), lambda: zr.mx4_matmul(q, zr.Mx4(8, 32), out),
+                 lambda: zr.mx4_matmul(q, zr.Mx4(9, 64), out), lambda: zr.mx4_linear(x, zr.Mx4(9, 64), out),
+                 lambda: zr.mx4_linear(torch.zeros(17, 64, device="cuda"), q, torch.empty(17, 8, device="cuda")),
+                 lambda: zr.mx4_linear(x, q, out, xq=zr.Mx4(8, 65)), lambda: zr.Mx4(8, 64, data=torch.empty(17407, dtype=torch.uint8, device="cuda")),
+                 lambda: zr.Mx4(8, 64, data=torch.empty(17408, device="cuda")), lambda: zr.Mx4(8, -1)):
+        with pytest.raises(zr.ZrError) as e:
+            call()
+        assert e.value.status == 1
 
 
 def test_empty_sizes():

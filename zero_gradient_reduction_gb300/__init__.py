@@ -744,5 +744,5 @@ def distill_topk(logits, ids, teacher, loss, grad=None, weight=None, temperature
 __all__ = ["lib", "ZrError", "chunk_size", "bucket_plan", "model_state_bytes", "ring_traffic", "reduce_scatter",
            "all_reduce", "adamw_shard_step", "accumulate", "offload_adamw", "all_gather", "AdamW", "Scaler",
            "State", "State1", "Plan", "step_noalloc", "F16", "BF16", "F32", "STAGING_REGISTERS", "STAGING_BULK",
-           "STAGING_BULK_IO", "Mx4", "mx4_bytes", "mx4_quantize", "mx4_dequantize", "mx4_matmul", "mx4_linear", "mx4_status",
-           "distill_topk", "MX4_FEW", "DISTILL_MAX_TOP"]
+           "STAGING_BULK_IO", "Mx4", "mx4_bytes", "mx4_quantize", "mx4_dequantize", "mx4_matmul", "mx4_linear",
+           "mx4_status", "distill_topk", "MX4_FEW", "DISTILL_MAX_TOP"]

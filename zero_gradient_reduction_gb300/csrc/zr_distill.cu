@@ -194,7 +194,8 @@ __global__ void __launch_bounds__(kMaxThreads, 2) distill_kernel(const __grid_co
   float* sp = reinterpret_cast<float*>(sid + a.K4);   // its p
   float* own = sp + a.K4;                             // its log2 p, then the gradient at its column
   Shared& sh = *reinterpret_cast<Shared*>(own + a.K4);
-  const int tid = threadIdx.x, nthr = blockDim.x - 32, lane = tid & 31, warp = tid >> 5;  // nthr: those that share the words
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int nthr = blockDim.x - 32;  // those that share the words
   const int64_t row = blockIdx.x / C;
   const int rank = C > 1 ? (int)zr::cluster_rank() : 0;
   const int64_t v0 = rank * a.share, v1 = v0 + a.share < a.V ? v0 + a.share : a.V;
@@ -220,7 +221,8 @@ __global__ void __launch_bounds__(kMaxThreads, 2) distill_kernel(const __grid_co
 
   bool some = w != 0.0f;
   if (some) {
-    for (int j = first + tid; tid < nthr && j < min(last, a.room); j += nthr) zr::copy16(zr::smem_u32(words + j), zw + j);
+    for (int j = first + tid; tid < nthr && j < min(last, a.room); j += nthr)
+      zr::copy16(zr::smem_u32(words + j), zw + j);
     if (single >= 0) {
       if (single == 0 && first == 1) zr::copy16(zr::smem_u32(words), zw);
       if (single == n - 1 && last >= first && last < min(nw, a.room)) zr::copy16(zr::smem_u32(words + last), zw + last);
@@ -473,10 +475,12 @@ extern "C" zr_status zr_distill_topk(const void* logits, zr_dtype dt, int64_t T,
   zr::clear_error();
   zr::Range range("zr_distill_topk");
   if (!zr::dtype_ok(dt) || !zr::dtype_ok(teacher_dt)) return fail(ZR_ERR_INVALID, "zr_distill_topk: bad dtype");
-  if (T < 0 || V < 1 || V > 0x7FFFFF00) return fail(ZR_ERR_INVALID, "zr_distill_topk: T must be >= 0 and V in [1, 2^31 - 256]");
+  if (T < 0 || V < 1 || V > 0x7FFFFF00)
+    return fail(ZR_ERR_INVALID, "zr_distill_topk: T must be >= 0 and V in [1, 2^31 - 256]");
   if (K < 1 || K > ZR_DISTILL_MAX_TOP)
     return fail(ZR_ERR_INVALID, "zr_distill_topk: K=%d outside [1, %d]", K, ZR_DISTILL_MAX_TOP);
-  if (ldz < V || ldk < K || (grad && ldg < V)) return fail(ZR_ERR_INVALID, "zr_distill_topk: a row stride is under the row");
+  if (ldz < V || ldk < K || (grad && ldg < V))
+    return fail(ZR_ERR_INVALID, "zr_distill_topk: a row stride is under the row");
   if (!(temperature > 0.0f) || temperature > 1e6f || temperature < 1e-6f)
     return fail(ZR_ERR_INVALID, "zr_distill_topk: temperature must lie in [1e-6, 1e6]");
   if (!(grad_scale == grad_scale) || grad_scale - grad_scale != 0.0f)

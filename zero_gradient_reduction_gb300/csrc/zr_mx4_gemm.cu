@@ -148,7 +148,8 @@ __device__ __forceinline__ void rows_out(const GemmArgs& g, const CUtensorMap* m
   using T = typename std::conditional<DT == zr::DT_F32, uint32_t, uint16_t>::type;
   constexpr int kEach = kCols / 32;  // values of a row in a lane, 32 apart
   T* out = static_cast<T*>(g.out) + row0 * g.ldo + col + lane;
-  const int rows = (int)(g.M - row0 < 32 ? g.M - row0 : 32), left = (int)(g.N - col < kCols ? g.N - col : kCols) - lane;
+  const int rows = (int)(g.M - row0 < 32 ? g.M - row0 : 32);
+  const int left = (int)(g.N - col < kCols ? g.N - col : kCols) - lane;
 #pragma unroll 8
   for (int r = 0; r < 32; ++r, out += g.ldo) {
 #pragma unroll
@@ -156,6 +157,7 @@ __device__ __forceinline__ void rows_out(const GemmArgs& g, const CUtensorMap* m
       if (r < rows && 32 * i < left)
         out[32 * i] = *reinterpret_cast<const T*>(stage + r * 128 + (((lane + 32 * i) * es) ^ ((r & 7) << 4)));
   }
+  if (g.vec && lane == 0) zr::no_store();  // the staging rows' turns are counted in stores
   __syncwarp();
 }
 
@@ -217,15 +219,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const bool halved = PAIR && t.half >= 0;
         // a pair's tile may reach past the rows of A or B by an MX4 tile, which is not read then:
         // what the products make of the bytes in its place is not stored
-        const int64_t am = PAIR ? 2 * (int64_t)t.m + rank : t.m, bn = PAIR ? 2 * (int64_t)t.n + (halved ? t.half : 0) : t.n;
+        const int64_t am = PAIR ? 2 * (int64_t)t.m + rank : t.m;
+        const int64_t bn = PAIR ? 2 * (int64_t)t.n + (halved ? t.half : 0) : t.n;
         const bool has_a = !PAIR || am * 128 < g.M, second = PAIR && !halved && (bn + 1) * 128 < g.N;
         const uint8_t *a = g.a + am * row_bytes, *b = g.b + bn * row_bytes;
         const int a_line = (int)(am * g.kt) * kTileLines, b_line = (int)(bn * g.kt) * kTileLines;
         // the first block expects the pair's bytes
         const bool peer_a = PAIR && (am + 1) * 128 < g.M;
-        const uint32_t bytes = g.stall + (PAIR ? zr::kMxTileBytes * (peer_a ? 2 : 1) +
-                                          (zr::kMxCodeBytes + 2 * zr::kMxScaleBytes) * (second ? 2 : 1)
-                                    : 2 * zr::kMxTileBytes);
+        const uint32_t pair_bytes =
+            zr::kMxTileBytes * (peer_a ? 2 : 1) + (zr::kMxCodeBytes + 2 * zr::kMxScaleBytes) * (second ? 2 : 1);
+        const uint32_t bytes = g.stall + (PAIR ? pair_bytes : 2 * zr::kMxTileBytes);
         for (int k = 0; k < g.kt; ++k, ++it) {
           const int s = it % G::kStages;
           if (it >= G::kStages && !(ok = zr::bar_wait(empty + 8 * s, (it / G::kStages - 1) & 1, gave_up))) break;
@@ -293,7 +296,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 #pragma unroll
           for (int q = 0; q < 4; ++q)  // 64 columns, 32 bytes of each row, at a time
             zr::mx_mma<PAIR>(d, da + 2 * q, db + 2 * q, zr::mx_product(G::kRows, halved ? 128 : G::kCols, q & 1),
-                             tmem + G::kScaleA + 4 * (q >> 1), tmem + G::kScaleB + 4 * G::kTiles * (q >> 1), (k | q) != 0);
+                             tmem + G::kScaleA + 4 * (q >> 1), tmem + G::kScaleB + 4 * G::kTiles * (q >> 1),
+                             (k | q) != 0);
           release(empty + 8 * s);
         }
         if (ok) release(done + 8 * (turn & 1));
@@ -445,7 +449,8 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
   char* xscale = xq + k_most * kXCodes;
   char* tail = xscale + k_most * kXScales + 256;
   const uint32_t stages = zr::smem_u32(smem);
-  const uint32_t full = zr::smem_u32(tail), empty = full + 8 * kFewStages, done = empty + 8 * kFewStages, tokens = done + 8;
+  const uint32_t full = zr::smem_u32(tail), empty = full + 8 * kFewStages, done = empty + 8 * kFewStages,
+                 tokens = done + 8;
   volatile int* gave_up = reinterpret_cast<volatile int*>(tail + 192);
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(tail + 200);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -641,7 +646,8 @@ PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
   static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
-    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found);
+    const cudaError_t e =
+        cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found);
     return (PFN_cuTensorMapEncodeTiled_v12000)(e == cudaSuccess && found == cudaDriverEntryPointSuccess ? p : nullptr);
   }();
   return fn;
@@ -684,14 +690,15 @@ zr_status launch_gemm(const GemmArgs& g, int blocks, bool early, cudaStream_t s)
         !encode_lines(&maps.b_scales, g.b, b_tiles, zr::kMxScaleBytes / 128))
       return fail(ZR_ERR_CUDA, "zr_mx4_matmul: the driver gave no tensor map");
   }
-  cudaError_t e = launch(gemm_kernel<PAIR, DT>, blocks, kGemmThreads, Gemm<PAIR>::kSmem, PAIR ? 2 : 1, early, s, g, maps);
+  cudaError_t e =
+      launch(gemm_kernel<PAIR, DT>, blocks, kGemmThreads, Gemm<PAIR>::kSmem, PAIR ? 2 : 1, early, s, g, maps);
   if (e != cudaSuccess) return fail(ZR_ERR_CUDA, "zr_mx4_matmul: launch failed: %s", cudaGetErrorString(e));
   return ZR_OK;
 }
 
 // early: the launch before it is the quantisation of a, in the same call.
-zr_status matmul(const char* what, const void* a, int64_t M, const void* b, int64_t N, int64_t K, void* out, zr_dtype dt,
-                 int64_t ldo, bool early, cudaStream_t s) {
+zr_status matmul(const char* what, const void* a, int64_t M, const void* b, int64_t N, int64_t K, void* out,
+                 zr_dtype dt, int64_t ldo, bool early, cudaStream_t s) {
   const int es = dt == ZR_F32 ? 4 : 2;
   if (K == 0) {  // a sum of nothing
     cudaError_t e = cudaMemset2DAsync(out, (size_t)ldo * es, 0, (size_t)N * es, (size_t)M, s);
@@ -822,7 +829,7 @@ extern "C" zr_status zr_mx4_status(void* stream) {
     e = cudaMemcpyToSymbolAsync(g_gave_up, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, s);
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);
     if (e == cudaSuccess)
-      return fail(ZR_ERR_TIMEOUT, "zr_mx4_status: a product gave up a wait; outputs since the last check are not valid");
+      return fail(ZR_ERR_TIMEOUT, "zr_mx4_status: a product gave up a wait; outputs since the last check are void");
   }
   return e == cudaSuccess ? ZR_OK : fail(ZR_ERR_CUDA, "zr_mx4_status: %s", cudaGetErrorString(e));
 }

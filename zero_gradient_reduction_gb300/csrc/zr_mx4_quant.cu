@@ -60,7 +60,9 @@ template <int DT>
 __device__ __forceinline__ uint32_t amax_word(uint32_t m, uint32_t w) {
   uint32_t r;
   if (DT == zr::DT_F32)
-    asm("{\n .reg .f32 a;\n abs.f32 a, %2;\n max.NaN.f32 %0, %1, a;\n}\n" : "=f"(*reinterpret_cast<float*>(&r)) : "f"(__uint_as_float(m)), "f"(__uint_as_float(w)));
+    asm("{\n .reg .f32 a;\n abs.f32 a, %2;\n max.NaN.f32 %0, %1, a;\n}\n"
+        : "=f"(*reinterpret_cast<float*>(&r))
+        : "f"(__uint_as_float(m)), "f"(__uint_as_float(w)));
   else if (DT == zr::DT_BF16)
     asm("{\n .reg .b32 a;\n abs.bf16x2 a, %2;\n max.NaN.bf16x2 %0, %1, a;\n}\n" : "=r"(r) : "r"(m), "r"(w));
   else
@@ -100,8 +102,8 @@ __device__ __forceinline__ uint32_t lane_bytes(int byte) {
 // to its places in shared memory; zeros for what lies past `bytes` of a row and past `rows`. A copy of
 // no bytes still names an address, which has to be one that is there: `any`, the matrix's first.
 template <int WORDS>
-__device__ __forceinline__ void fetch(int (*at)(int), char* to, const void* any, const char* from, int64_t pitch, int rows,
-                                      int bytes) {
+__device__ __forceinline__ void fetch(int (*at)(int), char* to, const void* any, const char* from, int64_t pitch,
+                                      int rows, int bytes) {
   constexpr int kEach = WORDS + 1, kDown = kThreads / kEach, kOver = kThreads % kEach;
   int r = threadIdx.x / kEach, j = threadIdx.x % kEach;
   const char* row = from + r * pitch;
@@ -133,7 +135,8 @@ __device__ __forceinline__ void align(int (*at)(int), char* rows, const char* fr
 }
 
 template <int DT, bool CHANCE>
-__global__ void __launch_bounds__(kThreads, DT == zr::DT_F32 ? (CHANCE ? 5 : 6) : 8) quant_kernel(const __grid_constant__ QuantArgs a) {
+__global__ void __launch_bounds__(kThreads, DT == zr::DT_F32 ? (CHANCE ? 5 : 6) : 8)
+    quant_kernel(const __grid_constant__ QuantArgs a) {
   using S = Shape<DT>;
   extern __shared__ __align__(16) char smem[];
   uint8_t* srand = reinterpret_cast<uint8_t*>(smem + S::bytes);
@@ -157,7 +160,8 @@ __global__ void __launch_bounds__(kThreads, DT == zr::DT_F32 ? (CHANCE ? 5 : 6) 
       from = rnd0 + (tid / kRandWords) * a.ldr + (tid % kRandWords) * 16;
       const uint32_t rto = zr::smem_u32(srand) + (tid / kRandWords) * kRandPitch + (tid % kRandWords) * 16;
 #pragma unroll
-      for (int i = 0; i < kRows / kRandStep; ++i) zr::copy16(rto + rand_at(i * kRandStep), from + i * kRandStep * a.ldr);
+      for (int i = 0; i < kRows / kRandStep; ++i)
+        zr::copy16(rto + rand_at(i * kRandStep), from + i * kRandStep * a.ldr);
     }
     zr::copies_done();
   } else {
@@ -198,7 +202,8 @@ __global__ void __launch_bounds__(kThreads, DT == zr::DT_F32 ? (CHANCE ? 5 : 6) 
           m = amax_word<DT>(amax_word<DT>(amax_word<DT>(amax_word<DT>(m, u.x), u.y), u.z), u.w);
         }
       }
-      if (DT != zr::DT_F32) m = bits_of_half<DT>((m >> 16) > (m & 0xFFFFu) ? m >> 16 : m & 0xFFFFu);  // (as whole numbers, NaN on top)
+      // (of two 16-bit patterns the larger as whole numbers, with NaN on top)
+      if (DT != zr::DT_F32) m = bits_of_half<DT>((m >> 16) > (m & 0xFFFFu) ? m >> 16 : m & 0xFFFFu);
       const int byte = zr::mx_scale_byte<CHANCE>(m);
       uint32_t o[4];
       if (byte == 255) {

@@ -96,6 +96,8 @@ __device__ __forceinline__ void box_store(const void* map, int x, int y, uint32_
                : "memory");
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
+// A store of nothing.
+__device__ __forceinline__ void no_store() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 // This thread's stores, all but the last PENDING, have read their shared memory; all have been written.
 template <int PENDING>
 __device__ __forceinline__ void stores_read() {
@@ -231,10 +233,10 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
 }
 // The same for a pair's products, on the barrier at this address in each block of `blocks` (a bit each).
 __device__ __forceinline__ void pair_commit(uint32_t bar, uint16_t blocks) {
-  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-                   bar),
-               "h"(blocks)
-               : "memory");
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"(blocks)
+      : "memory");
 }
 
 // ---- a launch that may begin before the one before it in the stream has ended (both no-ops otherwise)
@@ -253,7 +255,9 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // The two halves of cluster_sync: what came before the first can be read after the second.
-__device__ __forceinline__ void cluster_arrived() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrived() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ uint32_t cluster_addr(uint32_t smem, uint32_t rank) {
   uint32_t r;
