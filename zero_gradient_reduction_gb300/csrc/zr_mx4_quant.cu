@@ -318,8 +318,9 @@ struct DequantArgs {
 constexpr int kDequantRows = 32, kRowsPerWarp = kDequantRows / (kDequantThreads / 32);
 
 // A block takes 32 rows of a tile, a warp four of them at once (their loads in flight together), a
-// lane eight values of a row. ALIGNED: the rows of out begin on 16-byte boundaries; others go through
-// shared memory, so that they still leave in whole aligned words but for their ends.
+// lane eight values of a row. ALIGNED: the rows of out begin on 16-byte boundaries; others leave in
+// whole aligned words, too, but for their ends: in 16 bits a lane's word from its own values and the
+// next lane's; in 32, and at the matrix's last columns, by way of shared memory.
 template <int DT, bool ALIGNED>
 __global__ void __launch_bounds__(kDequantThreads) dequant_kernel(const __grid_constant__ DequantArgs a) {
   constexpr int es = DT == zr::DT_F32 ? 4 : 2, kRowBytes = zr::kMxCols * es;
@@ -372,6 +373,22 @@ __global__ void __launch_bounds__(kDequantThreads) dequant_kernel(const __grid_c
       continue;
     }
     const int lead = (int)(reinterpret_cast<uintptr_t>(out) & 15);
+    if (DT != zr::DT_F32 && n == zr::kMxCols && lead != 0) {
+      auto from_lane = [&](int l) {
+        return make_uint4(__shfl_sync(0xFFFFFFFFu, w[0].x, l), __shfl_sync(0xFFFFFFFFu, w[0].y, l),
+                          __shfl_sync(0xFFFFFFFFu, w[0].z, l), __shfl_sync(0xFFFFFFFFu, w[0].w, l));
+      };
+      const int skip = 16 - lead, head = skip / 2;  // what a lane leaves to the word of the one before it
+      const uint4 next = from_lane((lane + 1) & 31);
+      if (lane < 31) zr::st_once(out + skip + lane * 16, zr::shift16(w[0], next, (uint32_t)skip));
+      // the row's first values up to a boundary and its last ones behind one, eight together: a lane each
+      const uint4 end = from_lane(lane < head ? 0 : 31);
+      const uint32_t pick = (lane & 4) ? ((lane & 2) ? end.w : end.z) : ((lane & 2) ? end.y : end.x);
+      if (lane < 8)
+        reinterpret_cast<uint16_t*>(out)[lane < head ? lane : zr::kMxCols - 8 + lane] =
+            (uint16_t)(pick >> (16 * (lane & 1)));
+      continue;
+    }
     char* stage = staging[warp];
 #pragma unroll
     for (int k = 0; k < es / 2; ++k) *reinterpret_cast<uint4*>(stage + (lane * (es / 2) + k) * 16) = w[k];
