@@ -597,35 +597,24 @@ def _refuse(message: str):
 
 
 # A small call costs a few microseconds on the GPU, so these calls look their parts up once: the library's functions,
-# torch's types, the current stream's handle without a Stream object around it.
+# torch's types, and the current stream's handle without a Stream object around it.
 _fns = {}
 _types = {}
 
 
 def _fn(name: str):
-    f = _fns.get(name)
-    if f is None:
-        import torch
-        _types.update({torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32})
-        f = _fns[name] = getattr(lib(), name)
+    import torch
+    _types.update({torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32})
+    _fns["stream"] = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda device: torch.cuda.current_stream(device).cuda_stream)
+    f = _fns[name] = getattr(lib(), name)
     return f
 
 
-def _raw_stream(stream, device: int) -> int:
-    if stream is not None:
-        return int(stream.cuda_stream)
-    of = _fns.get("stream")
-    if of is None:
-        import torch
-        of = _fns["stream"] = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-            lambda d: torch.cuda.current_stream(d).cuda_stream)
-    return of(device)
-
-
 def _matrix(t, what: str):
-    """(pointer, rows, cols, row stride, dtype) of a device matrix whose rows are contiguous."""
-    shape = t.shape
-    if len(shape) != 2 or not t.is_cuda:
+    """(pointer, rows, cols, row stride, dtype, device) of a device matrix whose rows are contiguous."""
+    shape, device = t.shape, t.get_device()
+    if device < 0 or len(shape) != 2:
         _refuse(f"{what} must be a matrix in device memory")
     rows, cols = shape
     ld, step = t.stride()
@@ -638,7 +627,11 @@ def _matrix(t, what: str):
     dt = _types.get(t.dtype)
     if dt is None:
         _refuse(f"{what} must be fp32, fp16 or bf16, not {t.dtype}")
-    return t.data_ptr(), rows, cols, ld, dt
+    return t.data_ptr(), rows, cols, ld, dt, device
+
+
+def _stream_of(stream, device: int) -> int:
+    return _fns["stream"](device) if stream is None else int(stream.cuda_stream)
 
 
 class Mx4:
@@ -661,8 +654,8 @@ class Mx4:
 def mx4_quantize(x, q: Optional[Mx4] = None, q_t: Optional[Mx4] = None, rand=None, stream=None) -> None:
     """Quantises matrix x to q, and its transpose to q_t (zr_mx4_quantize); `rand`: uint8 random bits of x's shape
     for rounding by chance."""
-    fn = _fn("zr_mx4_quantize")
-    p, rows, cols, ld, dt = _matrix(x, "x")
+    fn = _fns.get("zr_mx4_quantize") or _fn("zr_mx4_quantize")
+    p, rows, cols, ld, dt, device = _matrix(x, "x")
     if q is not None and (q.rows != rows or q.cols != cols):
         _refuse(f"mx4_quantize: q is {q.rows} x {q.cols}, x {rows} x {cols}")
     if q_t is not None and (q_t.rows != cols or q_t.cols != rows):
@@ -674,38 +667,38 @@ def mx4_quantize(x, q: Optional[Mx4] = None, q_t: Optional[Mx4] = None, rand=Non
         if not rand.is_contiguous():
             _refuse("mx4_quantize: rand must be contiguous")
         rp, ldr = rand.data_ptr(), cols
-    _check(fn(p, dt, rows, cols, ld, rp, ldr, q and q.ptr, q_t and q_t.ptr, _raw_stream(stream, x.get_device())))
+    _check(fn(p, dt, rows, cols, ld, rp, ldr, q and q.ptr, q_t and q_t.ptr, _stream_of(stream, device)))
 
 
 def mx4_dequantize(q: Mx4, out, stream=None) -> None:
     """out = the values that q stands for (zr_mx4_dequantize)."""
-    fn = _fn("zr_mx4_dequantize")
-    p, rows, cols, ld, dt = _matrix(out, "out")
+    fn = _fns.get("zr_mx4_dequantize") or _fn("zr_mx4_dequantize")
+    p, rows, cols, ld, dt, device = _matrix(out, "out")
     if q.rows != rows or q.cols != cols:
         _refuse(f"mx4_dequantize: q is {q.rows} x {q.cols}, out {rows} x {cols}")
-    _check(fn(q.ptr, rows, cols, p, dt, ld, _raw_stream(stream, out.get_device())))
+    _check(fn(q.ptr, rows, cols, p, dt, ld, _stream_of(stream, device)))
 
 
 def mx4_matmul(a: Mx4, b: Mx4, out, stream=None) -> None:
     """out[M, N] = a[M, K] b[N, K]^T (zr_mx4_matmul)."""
-    fn = _fn("zr_mx4_matmul")
-    p, rows, cols, ld, dt = _matrix(out, "out")
+    fn = _fns.get("zr_mx4_matmul") or _fn("zr_mx4_matmul")
+    p, rows, cols, ld, dt, device = _matrix(out, "out")
     if a.cols != b.cols or a.rows != rows or b.rows != cols:
         _refuse(f"mx4_matmul: a is {a.rows} x {a.cols}, b {b.rows} x {b.cols}, out {rows} x {cols}")
-    _check(fn(a.ptr, rows, b.ptr, cols, a.cols, p, dt, ld, _raw_stream(stream, out.get_device())))
+    _check(fn(a.ptr, rows, b.ptr, cols, a.cols, p, dt, ld, _stream_of(stream, device)))
 
 
 def mx4_linear(x, w: Mx4, out, xq: Optional[Mx4] = None, stream=None) -> None:
     """out[M, N] = x[M, K] w[N, K]^T with x quantised in the call (zr_mx4_linear); more than MX4_FEW tokens need xq,
     a buffer for the quantised x."""
-    fn = _fn("zr_mx4_linear")
-    p, rows, k, ldx, xdt = _matrix(x, "x")
-    o, m, n, ldo, dt = _matrix(out, "out")
+    fn = _fns.get("zr_mx4_linear") or _fn("zr_mx4_linear")
+    p, rows, k, ldx, xdt, _ = _matrix(x, "x")
+    o, m, n, ldo, dt, device = _matrix(out, "out")
     if w.cols != k or m != rows or w.rows != n:
         _refuse(f"mx4_linear: x is {rows} x {k}, w {w.rows} x {w.cols}, out {m} x {n}")
     if xq is not None and (xq.rows != rows or xq.cols != k):
         _refuse(f"mx4_linear: xq is {xq.rows} x {xq.cols}, x {rows} x {k}")
-    _check(fn(p, xdt, rows, ldx, w.ptr, n, k, o, dt, ldo, xq and xq.ptr, _raw_stream(stream, out.get_device())))
+    _check(fn(p, xdt, rows, ldx, w.ptr, n, k, o, dt, ldo, xq and xq.ptr, _stream_of(stream, device)))
 
 
 def mx4_status(stream=None) -> None:
@@ -718,9 +711,9 @@ def distill_topk(logits, ids, teacher, loss, grad=None, weight=None, temperature
     """The distillation loss of each row against a teacher's top logits, and its gradient times grad_scale and the
     plan's loss scale (zr_distill_topk). `grad` may be `logits`."""
     import torch
-    fn = _fn("zr_distill_topk")
-    z, rows, vocab, ldz, dt = _matrix(logits, "logits")
-    t, trows, top, ldk, tdt = _matrix(teacher, "teacher")
+    fn = _fns.get("zr_distill_topk") or _fn("zr_distill_topk")
+    z, rows, vocab, ldz, dt, device = _matrix(logits, "logits")
+    t, trows, top, ldk, tdt, _ = _matrix(teacher, "teacher")
     if ids.dtype not in (torch.int32, torch.int64) or ids.shape != teacher.shape or not ids.is_cuda:
         _refuse("distill_topk: ids must be int32 or int64 of teacher's shape in device memory")
     if trows != rows:
@@ -734,11 +727,11 @@ def distill_topk(logits, ids, teacher, loss, grad=None, weight=None, temperature
     if grad is not None:
         if grad.dtype != logits.dtype or grad.shape != logits.shape:
             _refuse("distill_topk: grad must have the logits' type and shape")
-        g, _, _, ldg, _ = _matrix(grad, "grad")
+        g, _, _, ldg, _, _ = _matrix(grad, "grad")
     _check(fn(z, dt, rows, vocab, ldz, ids.data_ptr(), int(ids.dtype == torch.int64), t, tdt, top, ldk,
               weight.data_ptr() if weight is not None else None, temperature, grad_scale,
               plan.handle if plan is not None else None, loss.data_ptr(), g, ldg,
-              _raw_stream(stream, logits.get_device())))
+              _stream_of(stream, device)))
 
 
 __all__ = ["lib", "ZrError", "chunk_size", "bucket_plan", "model_state_bytes", "ring_traffic", "reduce_scatter",
