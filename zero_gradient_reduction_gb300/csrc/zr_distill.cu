@@ -42,6 +42,7 @@ struct DistillArgs {
   int64_t T, V, ldz, ldg, ldk;
   int64_t share;        // columns of each block of a row's cluster
   int K, K4, wide_ids, tdt;  // K4: K to a multiple of 4
+  int slot_bits;             // log2 of the slots of an entry's column: at least 2 K of them
   int room;             // 16-byte words of a row's share that shared memory holds
   float tau, grad_scale;
 };
@@ -173,6 +174,28 @@ __device__ __forceinline__ float rescaled(float m, float sum, const Base& to) {
   return __fmul_rn(sum, exp2_fast(e));
 }
 
+// Which columns stand in a row's entries more than once: a table of the columns in shared memory,
+// filled by one warp in any order, the sign marking those taken again. Looking through all K
+// entries for each of them cost 8192 rows of 256 entries as much again as the row itself.
+constexpr int kNoColumn = 0x7FFFFFFF;
+__device__ __forceinline__ int slot_of(int id, int bits) { return (int)((uint32_t)id * 2654435761u >> (32 - bits)); }
+__device__ __forceinline__ void take_slot(int* slots, int bits, int id) {
+  const int mask = (1 << bits) - 1;
+  for (int at = slot_of(id, bits);; at = (at + 1) & mask) {  // ends: half the slots stay free
+    const int was = atomicCAS(slots + at, kNoColumn, id);
+    if (was == kNoColumn) return;
+    if ((was & 0x7FFFFFFF) == id) {
+      if (was >= 0) atomicOr(slots + at, (int)0x80000000);
+      return;
+    }
+  }
+}
+__device__ __forceinline__ bool several(const int* slots, int bits, int id) {
+  const int mask = (1 << bits) - 1;
+  for (int at = slot_of(id, bits);; at = (at + 1) & mask)
+    if ((slots[at] & 0x7FFFFFFF) == id) return slots[at] < 0;
+}
+
 struct Shared {      // what the block's warps, and the cluster's blocks, tell each other
   float m[16], sum[16], loss[16];  // of each warp
   float row_m[8], row_sum[8], row_loss[8];  // of the cluster's blocks: each tells all, the loss the first
@@ -193,7 +216,9 @@ __global__ void __launch_bounds__(kMaxThreads, 2) distill_kernel(const __grid_co
   int* sid = reinterpret_cast<int*>(words + a.room);  // an entry's column, or -1
   float* sp = reinterpret_cast<float*>(sid + a.K4);   // its p
   float* own = sp + a.K4;                             // its log2 p, then the gradient at its column
-  Shared& sh = *reinterpret_cast<Shared*>(own + a.K4);
+  float* all = own + a.K4;                            // the p of all entries at its column
+  int* slots = reinterpret_cast<int*>(all + a.K4);    // the columns, by hash
+  Shared& sh = *reinterpret_cast<Shared*>(slots + (1 << a.slot_bits));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int nthr = blockDim.x - 32;  // those that share the words
   const int64_t row = blockIdx.x / C;
@@ -232,6 +257,8 @@ __global__ void __launch_bounds__(kMaxThreads, 2) distill_kernel(const __grid_co
       // ---- the teacher's entries: p over the kept ones
       float t_max = -INFINITY;
       int any = 0, past = 0;
+      for (int i = lane; i < 1 << a.slot_bits; i += 32) slots[i] = kNoColumn;
+      __syncwarp();
       for (int k = lane; k < a.K4; k += 32) {
         int64_t id = -1;
         float t = 0.0f;
@@ -247,6 +274,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) distill_kernel(const __grid_co
         any |= kept && !(t == -INFINITY);  // a masked entry is none
         if (kept) t_max = fmaxf(t_max, t);
         sid[k] = kept && id < a.V ? (int)id : -1;
+        if (kept && id < a.V) take_slot(slots, a.slot_bits, (int)id);
         own[k] = kept ? t : -INFINITY;
       }
       any = __any_sync(0xFFFFFFFFu, any);
@@ -260,6 +288,17 @@ __global__ void __launch_bounds__(kMaxThreads, 2) distill_kernel(const __grid_co
       for (int k = lane; k < a.K4; k += 32) {
         sp[k] = __fdiv_rn(sp[k], p_sum);
         own[k] -= log_p;
+      }
+      __syncwarp();
+      for (int k = lane; k < a.K; k += 32) {
+        const int id = sid[k];
+        float p = sp[k];
+        if (id >= 0 && several(slots, a.slot_bits, id)) {  // each of them finds the same sum
+          p = 0.0f;
+          for (int i = 0; i < a.K; ++i)
+            if (sid[i] == id) p += sp[i];
+        }
+        all[k] = p;
       }
       if (lane == 0) {
         sh.some = any;
@@ -367,15 +406,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) distill_kernel(const __grid_co
     if (id >= v0 && id < v1) {
       const float zc = base.exponent(value((int)(id - v0)));
       if (!(sp[k] == 0.0f)) loss += sp[k] * (own[k] - (zc - log_q)) * kLn2;
-      float p = 0.0f;  // an id may stand twice: each of its entries finds the same sum
-      for (int i = 0; i < a.K4; i += 4) {
-        const int4 four = *reinterpret_cast<const int4*>(sid + i);
-        if (four.x == id) p += sp[i];
-        if (four.y == id) p += sp[i + 1];
-        if (four.z == id) p += sp[i + 2];
-        if (four.w == id) p += sp[i + 3];
-      }
-      own[k] = __fmul_rn(f, __fdiv_rn(exp2_fast(zc), sum) - p);
+      own[k] = __fmul_rn(f, __fdiv_rn(exp2_fast(zc), sum) - all[k]);
     }
   }
   loss = warp_sum(loss);
@@ -506,7 +537,9 @@ extern "C" zr_status zr_distill_topk(const void* logits, zr_dtype dt, int64_t T,
   a.tau = temperature; a.grad_scale = grad_scale;
   // A row goes to one block where two rows fit an SM's shared memory and there are rows for every
   // SM; longer rows, or few of them, are shared by a cluster.
-  const int fixed = ((K + 3) & ~3) * 12 + (int)sizeof(Shared);
+  a.slot_bits = 1;
+  while (1 << a.slot_bits < 2 * K) ++a.slot_bits;
+  const int fixed = a.K4 * 16 + (4 << a.slot_bits) + (int)sizeof(Shared);
   const int64_t half = zr::kSmemMost / 2 - 1024 - fixed;
   int split = 1;
   while (split < 8 && ((V / split) * es > half || (T * split <= sms && V / split >= 4096))) split *= 2;
