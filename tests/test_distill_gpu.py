@@ -277,3 +277,32 @@ def test_other_stream_and_guards():
     side.synchronize()
     assert torch.equal(loss, ref_loss) and torch.equal(grad, ref_grad)
     assert bool((raw[:1024] == 7).all()) and bool((raw[1024 + 7 * 999:] == 7).all())
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("T,V,dtype", [(160, 58_001, BF16), (160, 29_000, F32), (155, 121_000, F16), (154, 62_003, F32)])
+def test_rows_that_shared_memory_holds_a_part_of(T, V, dtype, in_place):
+    """A block's, and a cluster's blocks': more rows than multiprocessors, each a little over what is kept of it. What is
+    read again adds, for each thread, under ten sums of four words and as many changes of its maximum."""
+    check(*case(T, V, 20, dtype, seed=V), tau=2.0, in_place=in_place)
+
+
+@pytest.mark.parametrize("K,columns", [(1024, 1), (1024, 700), (300, 5), (33, 16)])
+def test_columns_that_stand_many_times(K, columns):
+    z, ids, teacher, weight = case(9, 3000, K, BF16, seed=K + columns)
+    keep = ids < 0
+    ids = torch.where(keep, ids, 2990 - ids % columns * 4)
+    check(z, ids, teacher, weight)
+
+
+def test_the_largest_logit_in_the_part_that_is_read_again():
+    """Its sum is relative to its own maximum, which the part kept in shared memory comes to take over, and the other way round."""
+    z, ids, teacher, weight = case(160, 58_000, 20, BF16, seed=5)
+    z[::2, -1] = 60.0
+    z[1::2, 0] = 60.0
+    z[::3, -3000:] = -float("inf")
+    z[1::3, :40_000] = -float("inf")
+    ids[(ids < 40_000) | (ids > 54_000)] = -1
+    z[:, 45_000] = 1.0
+    ids[:, 0] = 45_000
+    check(z, ids, teacher, weight)

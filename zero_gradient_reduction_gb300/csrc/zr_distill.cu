@@ -5,14 +5,18 @@
 // vocabulary, loss = w tau^2 sum_k p_k (log p_k - log q_id(k)) and dloss/dz = w tau (q - p). A row
 // is read once into shared memory (of one block, or of a cluster that shares the row), its
 // maximum, its sum of exponentials and its gradient come from there, and the gradient is written
-// once. All arithmetic is fp32; sums are taken in an order that the sizes alone decide.
+// once; what a long row has beyond that room is summed as it is read, and read again from L2 for its
+// gradient. All arithmetic is fp32; sums are taken in an order that the sizes alone decide.
 //
-// Two bytes (or four) a logit each way bind it: 8192 x 50304 bf16 in 262 us, 6.3 TB/s of the 6.8 that
+// Two bytes (or four) a logit each way bind it: 8192 x 50304 bf16 in 248 us, 6.6 TB/s of the 6.8 that
 // a copy reaches, with two rows at work on each multiprocessor (101 KB each), one read while the
 // other is summed. A first form with loads through registers and fp32 one at a time took 724 us;
 // asynchronous copies 344, two exponentials' arithmetic in one instruction and results under 2^-126 to
-// zero 310, the teacher's entries in a warp of their own 263. 13 x 50257 fp32, a cluster of 8 blocks to
-// a row: 9.4 us, of which a launch is 2.5 and each wait of the cluster about 1.
+// zero 310, the teacher's entries in a warp of their own 263. Shorter rows have as many at work as fit:
+// 8192 x 8000 bf16 in 55 us with ten, 104 with three. Blocks that stay and fetch the next row's words
+// into the places of the gradient's were slower (307 and 67 us): they all read, then all sum, together.
+// 13 x 50257 fp32, a cluster of 8 blocks to a row: 8.8 us, of which a launch is 2.5 and each wait of the
+// cluster about 1.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -28,7 +32,7 @@ using zr::fail;
 
 namespace {
 
-constexpr int kMaxThreads = 512;  // 15 warps for a row's words and one for the teacher's entries
+constexpr int kMaxThreads = 1024;  // the last warp for the teacher's entries, the others for a row's words
 constexpr float kLog2E = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
 
 struct DistillArgs {
@@ -196,8 +200,65 @@ __device__ __forceinline__ bool several(const int* slots, int bits, int id) {
     if ((slots[at] & 0x7FFFFFFF) == id) return slots[at] < 0;
 }
 
+// The exponentials of a word's logits relative to a maximum, summed: two by two where that is one
+// multiply-add.
+template <int DT>
+__device__ __forceinline__ Two terms(uint4 u, Two c, Two less) {
+  constexpr int per = Word<DT>::per;
+  float f[per];
+  Word<DT>::open(u, f);
+  Two part(0.0f, 0.0f);
+#pragma unroll
+  for (int i = 0; i < per; i += 2) {
+    const Two x = fma2(Two(f[i], f[i + 1]), c, less);
+    part = add2(part, Two(exp2_fast(x.lo()), exp2_fast(x.hi())));
+  }
+  return part;
+}
+template <int DT>
+__device__ __forceinline__ float terms(uint4 u, const Base& base) {
+  if (base.fused) {
+    const Two part = terms<DT>(u, Two(base.c, base.c), Two(-base.mc, -base.mc));
+    return __fadd_rn(part.lo(), part.hi());
+  }
+  constexpr int per = Word<DT>::per;
+  float f[per], sum = 0.0f;
+  Word<DT>::open(u, f);
+#pragma unroll
+  for (int i = 0; i < per; ++i) sum = __fadd_rn(sum, exp2_fast(base.exponent(f[i])));
+  return sum;
+}
+
+// A lane's entries k0, k0 + 32, ... as they stand in memory. They are asked for before the row is, all
+// together, and as words of 32 bits that nothing looks at before the last is asked for: behind a row's
+// copies each turn of loads waits for 100 KB.
+struct RawEntries {
+  static constexpr int many = 4;
+  uint32_t lo[many], hi[many], t[many];
+  __device__ void load(const DistillArgs& a, int64_t row, int k0) {
+    const int half = a.tdt != zr::DT_F32;
+#pragma unroll
+    for (int i = 0; i < many; ++i) {
+      const int64_t at = row * a.ldk + k0 + 32 * i;
+      if (k0 + 32 * i < a.K) {
+        lo[i] = __ldg(static_cast<const uint32_t*>(a.ids) + (at << a.wide_ids));
+        if (a.wide_ids) hi[i] = __ldg(static_cast<const uint32_t*>(a.ids) + 2 * at + 1);
+        t[i] = __ldg(static_cast<const uint32_t*>(a.teacher) + (at >> half));
+      }
+    }
+  }
+  __device__ int64_t id(const DistillArgs& a, int i) const {
+    return a.wide_ids ? (int64_t)((uint64_t)hi[i] << 32 | lo[i]) : (int64_t)(int32_t)lo[i];
+  }
+  __device__ float logit(const DistillArgs& a, int64_t row, int k, int i) const {
+    if (a.tdt == zr::DT_F32) return __uint_as_float(t[i]);
+    const uint16_t v = (uint16_t)(t[i] >> ((row * a.ldk + k) & 1) * 16);
+    return a.tdt == zr::DT_BF16 ? zr::to_f32<zr::DT_BF16>(v) : zr::to_f32<zr::DT_F16>(v);
+  }
+};
+
 struct Shared {      // what the block's warps, and the cluster's blocks, tell each other
-  float m[16], sum[16], loss[16];  // of each warp
+  float m[32], sum[32], loss[32];  // of each warp
   float row_m[8], row_sum[8], row_loss[8];  // of the cluster's blocks: each tells all, the loss the first
   int some, beyond;
 };
@@ -208,7 +269,7 @@ struct Shared {      // what the block's warps, and the cluster's blocks, tell e
 // and stores the same words, so the passes need no barrier between them; the last warp has no words
 // and reads the teacher's entries while the row is on its way.
 template <int DT, int C>
-__global__ void __launch_bounds__(kMaxThreads, 2) distill_kernel(const __grid_constant__ DistillArgs a) {
+__global__ void __launch_bounds__(kMaxThreads) distill_kernel(const __grid_constant__ DistillArgs a) {
   using W = Word<DT>;
   constexpr int per = W::per, es = 16 / per;
   extern __shared__ __align__(16) char smem[];
@@ -241,9 +302,11 @@ __global__ void __launch_bounds__(kMaxThreads, 2) distill_kernel(const __grid_co
   // those go to one thread each, which keeps its value in a register
   const int first = lead > 0 ? 1 : 0, last = (lead + n) / per;
   const int head = lead > 0 ? min(n, per - lead) : 0, behind = max(head, last * per - lead);
-  const int single = tid < head ? tid : tid >= 32 && tid - 32 < n - behind ? behind + tid - 32 : -1;
+  const int single = tid < head ? tid : tid >= 8 && tid - 8 < n - behind ? behind + tid - 8 : -1;
   float z_single = -INFINITY;
 
+  RawEntries raw;
+  if (tid >= nthr) raw.load(a, row, lane);
   bool some = w != 0.0f;
   if (some) {
     for (int j = first + tid; tid < nthr && j < min(last, a.room); j += nthr)
@@ -258,31 +321,33 @@ __global__ void __launch_bounds__(kMaxThreads, 2) distill_kernel(const __grid_co
       float t_max = -INFINITY;
       int any = 0, past = 0;
       for (int i = lane; i < 1 << a.slot_bits; i += 32) slots[i] = kNoColumn;
-      __syncwarp();
-      for (int k = lane; k < a.K4; k += 32) {
-        int64_t id = -1;
-        float t = 0.0f;
-        if (k < a.K) {
-          const int64_t at = row * a.ldk + k;
-          id = a.wide_ids ? static_cast<const int64_t*>(a.ids)[at] : static_cast<const int32_t*>(a.ids)[at];
-          t = a.tdt == zr::DT_F32    ? zr::load1<zr::DT_F32>(a.teacher, at)
-              : a.tdt == zr::DT_BF16 ? zr::load1<zr::DT_BF16>(a.teacher, at)
-                                     : zr::load1<zr::DT_F16>(a.teacher, at);
+      for (int k0 = lane; k0 < a.K4; k0 += 32 * RawEntries::many) {
+        if (k0 != lane) raw.load(a, row, k0);
+#pragma unroll
+        for (int i = 0; i < RawEntries::many; ++i) {
+          const int k = k0 + 32 * i;
+          const int64_t id = k < a.K ? raw.id(a, i) : -1;
+          const float t = raw.logit(a, row, k, i);
+          const bool kept = id >= 0;
+          past |= id >= a.V;
+          any |= kept && !(t == -INFINITY);  // a masked entry is none
+          if (kept) t_max = fmaxf(t_max, t);
+          if (k < a.K4) {
+            sid[k] = kept && id < a.V ? (int)id : -1;
+            own[k] = kept ? t : -INFINITY;
+          }
         }
-        const bool kept = id >= 0;
-        past |= id >= a.V;
-        any |= kept && !(t == -INFINITY);  // a masked entry is none
-        if (kept) t_max = fmaxf(t_max, t);
-        sid[k] = kept && id < a.V ? (int)id : -1;
-        if (kept && id < a.V) take_slot(slots, a.slot_bits, (int)id);
-        own[k] = kept ? t : -INFINITY;
       }
+      __syncwarp();
       any = __any_sync(0xFFFFFFFFu, any);
       past = __any_sync(0xFFFFFFFFu, past);
       t_max = warp_max(t_max);
       // an entry of -inf has p = 0; +inf or NaN leaves every p not a number
       float p_sum = 0.0f;
-      for (int k = lane; k < a.K4; k += 32) p_sum += sp[k] = exp2_fast(own[k] = (own[k] - t_max) * c);
+      for (int k = lane; k < a.K4; k += 32) {
+        if (sid[k] >= 0) take_slot(slots, a.slot_bits, sid[k]);
+        p_sum += sp[k] = exp2_fast(own[k] = (own[k] - t_max) * c);
+      }
       p_sum = warp_sum(p_sum);
       const float log_p = log2f(p_sum);
       for (int k = lane; k < a.K4; k += 32) {
@@ -305,44 +370,51 @@ __global__ void __launch_bounds__(kMaxThreads, 2) distill_kernel(const __grid_co
         sh.beyond = past;
       }
     }
-    zr::copies_done();
   }
 
-  auto word = [&](int j) { return j < a.room ? words[j] : ld_row(zw + j); };
   auto value = [&](int i) {  // the i-th logit of this block's columns
     i += lead;
     return i / per < a.room ? zr::load1<DT>(smem, i) : zr::load1<DT>(zw, i);
   };
+  // the words that shared memory holds, and the first of this thread's that it does not
+  const int kept = min(last, a.room);
+  const int more = first + tid + max(kept - first - tid + nthr - 1, 0) / nthr * nthr;
+  constexpr int kOnce = 4;  // of the others, on their way together
 
   if (some && tid < nthr) {
-    // ---- each thread's maximum, and its sum relative to it
+    // ---- each thread's maximum, and its sum relative to it: of the words without room first, while
+    // the others are on their way
+    float m = -INFINITY, sum = 0.0f;
+    for (int j = more; j < last; j += kOnce * nthr) {
+      uint4 u[kOnce];
+      uint32_t most = W::lowest();
+#pragma unroll
+      for (int i = 0; i < kOnce; ++i)
+        u[i] = j + i * nthr < last ? ld_row(zw + j + i * nthr)
+                                   : make_uint4(W::lowest(), W::lowest(), W::lowest(), W::lowest());
+#pragma unroll
+      for (int i = 0; i < kOnce; ++i) most = W::larger(most, u[i]);
+      const float m_all = fmaxf(m, W::largest(most));
+      const Base mine(m_all, c);
+      if (m_all != m) sum = rescaled(m, sum, mine);
+      m = m_all;
+#pragma unroll
+      for (int i = 0; i < kOnce; ++i) sum = __fadd_rn(sum, terms<DT>(u[i], mine));
+    }
+    zr::copies_done();
     uint32_t most = W::lowest();
-    for (int j = first + tid; j < last; j += nthr) most = W::larger(most, word(j));
-    const float m = fmaxf(W::largest(most), z_single);
+    for (int j = first + tid; j < kept; j += nthr) most = W::larger(most, words[j]);
+    const float m_over = m;
+    m = fmaxf(fmaxf(m, W::largest(most)), z_single);
     const Base mine(m, c);
-    float sum = 0.0f;
+    sum = rescaled(m_over, sum, mine);
     if (mine.fused) {
       const Two cc(c, c), less(-mine.mc, -mine.mc);
       Two total(0.0f, 0.0f);
-      for (int j = first + tid; j < last; j += nthr) {
-        float f[per];
-        W::open(word(j), f);
-        Two part(0.0f, 0.0f);
-#pragma unroll
-        for (int i = 0; i < per; i += 2) {
-          const Two x = fma2(Two(f[i], f[i + 1]), cc, less);
-          part = add2(part, Two(exp2_fast(x.lo()), exp2_fast(x.hi())));
-        }
-        total = add2(total, part);
-      }
-      sum = __fadd_rn(total.lo(), total.hi());
+      for (int j = first + tid; j < kept; j += nthr) total = add2(total, terms<DT>(words[j], cc, less));
+      sum = __fadd_rn(sum, __fadd_rn(total.lo(), total.hi()));
     } else {
-      for (int j = first + tid; j < last; j += nthr) {
-        float f[per];
-        W::open(word(j), f);
-#pragma unroll
-        for (int i = 0; i < per; ++i) sum = __fadd_rn(sum, exp2_fast(mine.exponent(f[i])));
-      }
+      for (int j = first + tid; j < kept; j += nthr) sum = __fadd_rn(sum, terms<DT>(words[j], mine));
     }
     sum = __fadd_rn(sum, exp2_fast(mine.exponent(z_single)));
     const float wm = warp_max(m);
@@ -375,8 +447,8 @@ __global__ void __launch_bounds__(kMaxThreads, 2) distill_kernel(const __grid_co
   }
 
   const bool has = lane < (nthr >> 5);
-  float wm = has ? sh.m[lane & 15] : -INFINITY, m = warp_max(wm);
-  float sum = warp_sum(has ? rescaled(wm, sh.sum[lane & 15], Base(m, c)) : 0.0f);
+  float wm = has ? sh.m[lane] : -INFINITY, m = warp_max(wm);
+  float sum = warp_sum(has ? rescaled(wm, sh.sum[lane], Base(m, c)) : 0.0f);
   if (C > 1) {
     __syncwarp();
     zr::cluster_wait();
@@ -414,7 +486,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) distill_kernel(const __grid_co
   if (C > 1 || nw > a.room) __syncthreads();  // the entries' logits are read before the gradient may replace them
   if (C > 1) {  // the blocks' parts of the loss travel while the gradient is written
     if (warp == 0) {
-      loss = warp_sum(lane <= (nthr >> 5) ? sh.loss[lane & 15] : 0.0f);
+      loss = warp_sum(lane <= (nthr >> 5) ? sh.loss[lane] : 0.0f);
       if (lane == 0) zr::cluster_store(zr::cluster_addr(zr::smem_u32(&sh.row_loss[rank]), 0), loss);
     }
     __syncwarp();
@@ -425,9 +497,9 @@ __global__ void __launch_bounds__(kMaxThreads, 2) distill_kernel(const __grid_co
   if (grad) {
     const float fq = __fdiv_rn(f, sum);
     const Two cc(c, c), less(-base.mc, -base.mc), by(fq, fq);
-    for (int j = first + tid; tid < nthr && j < last; j += nthr) {
+    auto put = [&](int j, uint4 u) {
       float v[per];
-      W::open(word(j), v);
+      W::open(u, v);
       if (base.fused) {
 #pragma unroll
         for (int i = 0; i < per; i += 2) {
@@ -447,6 +519,18 @@ __global__ void __launch_bounds__(kMaxThreads, 2) distill_kernel(const __grid_co
 #pragma unroll
         for (int i = 0; i < per; ++i) store1<DT>(to, i, v[i]);
       }
+    };
+    if (tid < nthr) {
+      for (int j = more; j < last; j += kOnce * nthr) {
+        uint4 u[kOnce];
+#pragma unroll
+        for (int i = 0; i < kOnce; ++i)
+          if (j + i * nthr < last) u[i] = ld_row(zw + j + i * nthr);
+#pragma unroll
+        for (int i = 0; i < kOnce; ++i)
+          if (j + i * nthr < last) put(j + i * nthr, u[i]);
+      }
+      for (int j = first + tid; j < kept; j += nthr) put(j, words[j]);
     }
     if (single >= 0) store1<DT>(grad, single, __fmul_rn(exp2_fast(base.exponent(z_single)), fq));
   }
@@ -464,7 +548,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) distill_kernel(const __grid_co
 #pragma unroll
       for (int r = 0; r < C; ++r) loss = __fadd_rn(loss, sh.row_loss[r]);
     } else {
-      loss = warp_sum(lane <= (nthr >> 5) ? sh.loss[lane & 15] : 0.0f);
+      loss = warp_sum(lane <= (nthr >> 5) ? sh.loss[lane] : 0.0f);
     }
     if (lane == 0) a.loss[row] = sh.beyond ? NAN : __fmul_rn(loss, __fmul_rn(w, __fmul_rn(a.tau, a.tau)));
   }
@@ -535,23 +619,36 @@ extern "C" zr_status zr_distill_topk(const void* logits, zr_dtype dt, int64_t T,
   a.T = T; a.V = V; a.ldz = ldz; a.ldg = ldg; a.ldk = ldk;
   a.K = K; a.K4 = (K + 3) & ~3; a.wide_ids = ids64; a.tdt = (int)teacher_dt;
   a.tau = temperature; a.grad_scale = grad_scale;
-  // A row goes to one block where two rows fit an SM's shared memory and there are rows for every
-  // SM; longer rows, or few of them, are shared by a cluster.
+  // How many blocks share a row, and how many an SM has at once. Its memory holds so many words of a row
+  // each; what a row has beyond them is read again, from L2. One block takes a row of up to 1.2 times
+  // what two blocks to an SM hold (7229 x 57000 bf16 in 270 us, 372 with one) or of what one holds;
+  // longer rows go to as few blocks as have up to 1.2 times the half each. Where rows leave SMs free
+  // each is shared as far as those go and its parts stay 24 KB long.
   a.slot_bits = 1;
   while (1 << a.slot_bits < 2 * K) ++a.slot_bits;
   const int fixed = a.K4 * 16 + (4 << a.slot_bits) + (int)sizeof(Shared);
-  const int64_t half = zr::kSmemMost / 2 - 1024 - fixed;
+  auto held = [&](int blocks) { return ((zr::kSmemMost + 1024) / blocks - 1024 - fixed) / 16; };
+  const int unit = 16 / es;
+  auto words = [&](int split) { return (V + split * unit - 1) / (split * unit) + 1; };  // 1: it may begin inside a word
+  auto nearly = [&](int64_t n, int blocks) { return n * 5 <= (int64_t)held(blocks) * 6; };
   int split = 1;
-  while (split < 8 && ((V / split) * es > half || (T * split <= sms && V / split >= 4096))) split *= 2;
+  if (words(1) > held(1) && !nearly(words(1), 2))
+    while (split < 8 && !nearly(words(split), 2)) split *= 2;
+  while (split < 8 && T * split * 2 <= sms && words(split) > 3000) split *= 2;
   if (T > 0x7FFFFFFF / split) return fail(ZR_ERR_UNSUPPORTED, "zr_distill_topk: too many rows for one launch");
-  const int64_t unit = 16 / es;
-  a.share = (V + split * unit - 1) / (split * unit) * unit;
-  int64_t room = a.share / unit + 1;  // one more word where the row does not begin on a boundary
-  const int64_t most = (zr::kSmemMost - fixed) / 16;
-  a.room = (int)(room < most ? room : most);  // what does not fit is read again
-  int threads = 64;
-  while (threads < 256 && threads * 4 < room) threads *= 2;
-  threads = threads * 4 < room ? kMaxThreads : threads + 32;
+  const int64_t room = words(split);
+  a.share = (room - 1) * unit;
+  // One more block than fit whole where it nearly does: for a row of its own the second only, in a
+  // cluster, which waits more, others too (1373 x 150000 fp32 in 296 us with 3, 348 with 2). A thread has
+  // 20 words at most: 8192 x 8000 bf16 in 55 us with 10 blocks of 2 warps, 71 with 14 of one.
+  int blocks = 1;
+  while (blocks < 16 && T * split > (int64_t)blocks * sms && room <= 20 * (1024 / (blocks + 1) / 32 * 32 - 32) &&
+         (room <= held(blocks + 1) || ((blocks == 1 || split > 1) && nearly(room, blocks + 1)))) ++blocks;
+  a.room = (int)(room < held(blocks) ? room : held(blocks));
+  // They share the SM's registers, 64 a thread. A row that has its SM to itself takes fewer threads, as
+  // barriers cost more than words then (13 x 50257 fp32 in 9.0 us with 384, 9.9 with 1024).
+  int threads = T * split <= sms ? 384 : 1024 / blocks / 32 * 32;
+  if (threads > (room + 31) / 32 * 32 + 32) threads = (int)((room + 31) / 32 * 32 + 32);
   const int smem = a.room * 16 + fixed;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dt == ZR_F16) return launch_split<zr::DT_F16>(a, split, threads, smem, s);
