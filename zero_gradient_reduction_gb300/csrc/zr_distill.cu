@@ -558,17 +558,7 @@ template <int DT, int C>
 zr_status launch(const DistillArgs& a, int threads, int smem, cudaStream_t s) {
   static zr::SmemAllowance allowance;
   if (zr_status st = allowance.allow("zr_distill_topk", (const void*)distill_kernel<DT, C>, zr::kSmemMost)) return st;
-  cudaLaunchConfig_t c{};
-  c.gridDim = dim3((unsigned)(a.T * C));
-  c.blockDim = dim3((unsigned)threads);
-  c.dynamicSmemBytes = (size_t)smem;
-  c.stream = s;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim = {C, 1, 1};
-  c.attrs = &at;
-  c.numAttrs = C > 1 ? 1 : 0;
-  cudaError_t e = cudaLaunchKernelEx(&c, distill_kernel<DT, C>, a);
+  cudaError_t e = zr::launch(distill_kernel<DT, C>, a.T * C, threads, smem, C, false, s, a);
   if (e != cudaSuccess) return fail(ZR_ERR_CUDA, "zr_distill_topk: launch failed: %s", cudaGetErrorString(e));
   return ZR_OK;
 }

@@ -39,6 +39,34 @@ class SmemAllowance {
   std::atomic<uint64_t> done_{0};
 };
 
+// A launch of blocks, or clusters of them. `early`: it may begin while the launch before it in the stream
+// still runs, where that one lets it; the kernel waits for that one's end before it reads or writes
+// what another may write or read. That hides the 1 us of a launch in a chain of short ones.
+template <class Kernel, class... Args>
+cudaError_t launch(Kernel kernel, int64_t blocks, int threads, int smem, int cluster, bool early, cudaStream_t s,
+                   const Args&... args) {
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3((unsigned)blocks);
+  c.blockDim = dim3((unsigned)threads);
+  c.dynamicSmemBytes = (size_t)smem;
+  c.stream = s;
+  cudaLaunchAttribute at[2] = {};
+  int n = 0;
+  if (cluster > 1) {
+    at[n].id = cudaLaunchAttributeClusterDimension;
+    at[n].val.clusterDim.x = (unsigned)cluster;
+    at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (early) {
+    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  c.attrs = at;
+  c.numAttrs = (unsigned)n;
+  return cudaLaunchKernelEx(&c, kernel, args...);
+}
+
 // Streaming multiprocessors of the current device (0 and a recorded error on failure).
 inline int sm_count(const char* what) {
   static std::atomic<int> known[64];

@@ -207,6 +207,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   zr::tmem_fence_after();
   const uint32_t tmem = *tmem_at;
   const int tiles = tile_count(g);
+  zr::let_next_begin();  // it waits for this one's end before it reads or writes
   const int64_t row_bytes = (int64_t)g.kt * zr::kMxTileBytes;  // a row of MX4 tiles
 
   if (warp == 0) {
@@ -617,30 +618,6 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
   if (warp == 0) zr::tmem_free(tmem, 32);
 }
 
-// A launch of clusters that may begin while the launch before it (in the same call) still runs.
-template <class Kernel, class... Args>
-cudaError_t launch(Kernel kernel, int blocks, int threads, int smem, int cluster, bool early, cudaStream_t s,
-                   const Args&... args) {
-  cudaLaunchConfig_t c{};
-  c.gridDim = dim3((unsigned)blocks);
-  c.blockDim = dim3((unsigned)threads);
-  c.dynamicSmemBytes = (size_t)smem;
-  c.stream = s;
-  cudaLaunchAttribute at[2] = {};
-  int n = 0;
-  if (cluster > 1) {
-    at[n].id = cudaLaunchAttributeClusterDimension;
-    at[n++].val.clusterDim = {(unsigned)cluster, 1, 1};
-  }
-  if (early) {
-    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[n++].val.programmaticStreamSerializationAllowed = 1;
-  }
-  c.attrs = at;
-  c.numAttrs = n;
-  return cudaLaunchKernelEx(&c, kernel, args...);
-}
-
 // The driver's encoder of tensor maps, looked up once.
 PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
   static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
@@ -676,7 +653,7 @@ bool encode_out(CUtensorMap* map, const GemmArgs& g, int dt) {
 }
 
 template <bool PAIR, int DT>
-zr_status launch_gemm(const GemmArgs& g, int blocks, bool early, cudaStream_t s) {
+zr_status launch_gemm(const GemmArgs& g, int blocks, cudaStream_t s) {
   static zr::SmemAllowance allowance;
   if (zr_status st = allowance.allow("zr_mx4_matmul", (const void*)gemm_kernel<PAIR, DT>, Gemm<PAIR>::kSmem)) return st;
   Maps<PAIR> maps;
@@ -690,15 +667,14 @@ zr_status launch_gemm(const GemmArgs& g, int blocks, bool early, cudaStream_t s)
         !encode_lines(&maps.b_scales, g.b, b_tiles, zr::kMxScaleBytes / 128))
       return fail(ZR_ERR_CUDA, "zr_mx4_matmul: the driver gave no tensor map");
   }
-  cudaError_t e =
-      launch(gemm_kernel<PAIR, DT>, blocks, kGemmThreads, Gemm<PAIR>::kSmem, PAIR ? 2 : 1, early, s, g, maps);
+  cudaError_t e = zr::launch(gemm_kernel<PAIR, DT>, blocks, kGemmThreads, Gemm<PAIR>::kSmem, PAIR ? 2 : 1, true, s, g,
+                             maps);
   if (e != cudaSuccess) return fail(ZR_ERR_CUDA, "zr_mx4_matmul: launch failed: %s", cudaGetErrorString(e));
   return ZR_OK;
 }
 
-// early: the launch before it is the quantisation of a, in the same call.
 zr_status matmul(const char* what, const void* a, int64_t M, const void* b, int64_t N, int64_t K, void* out,
-                 zr_dtype dt, int64_t ldo, bool early, cudaStream_t s) {
+                 zr_dtype dt, int64_t ldo, cudaStream_t s) {
   const int es = dt == ZR_F32 ? 4 : 2;
   if (K == 0) {  // a sum of nothing
     cudaError_t e = cudaMemset2DAsync(out, (size_t)ldo * es, 0, (size_t)N * es, (size_t)M, s);
@@ -728,21 +704,21 @@ zr_status matmul(const char* what, const void* a, int64_t M, const void* b, int6
     // a last round that fewer than half of the pairs would be busy with, in halves (2048 x 8192 x 8192:
     // 48.2 us in 4 rounds, 45.6 in 3.5); not where the last column of tiles has no second half
     if (last > 0 && 2 * last <= pairs && (int64_t)nt * 256 - N < 128) g.whole -= last;
-    if (dt == ZR_F16) return launch_gemm<true, zr::DT_F16>(g, blocks, early, s);
-    if (dt == ZR_BF16) return launch_gemm<true, zr::DT_BF16>(g, blocks, early, s);
-    return launch_gemm<true, zr::DT_F32>(g, blocks, early, s);
+    if (dt == ZR_F16) return launch_gemm<true, zr::DT_F16>(g, blocks, s);
+    if (dt == ZR_BF16) return launch_gemm<true, zr::DT_BF16>(g, blocks, s);
+    return launch_gemm<true, zr::DT_F32>(g, blocks, s);
   }
   const int blocks = (int)(mt * nt < sms ? mt * nt : sms);
-  if (dt == ZR_F16) return launch_gemm<false, zr::DT_F16>(g, blocks, early, s);
-  if (dt == ZR_BF16) return launch_gemm<false, zr::DT_BF16>(g, blocks, early, s);
-  return launch_gemm<false, zr::DT_F32>(g, blocks, early, s);
+  if (dt == ZR_F16) return launch_gemm<false, zr::DT_F16>(g, blocks, s);
+  if (dt == ZR_BF16) return launch_gemm<false, zr::DT_BF16>(g, blocks, s);
+  return launch_gemm<false, zr::DT_F32>(g, blocks, s);
 }
 
 template <int S>
 zr_status launch_few(const FewArgs& g, int blocks, int smem, cudaStream_t s) {
   static zr::SmemAllowance allowance;
   if (zr_status st = allowance.allow("zr_mx4_linear", (const void*)few_kernel<S>, zr::kSmemMost)) return st;
-  cudaError_t e = launch(few_kernel<S>, blocks, kFewThreads, smem, S, g.xq != nullptr, s, g);
+  cudaError_t e = zr::launch(few_kernel<S>, blocks, kFewThreads, smem, S, g.xq != nullptr, s, g);
   if (e != cudaSuccess) return fail(ZR_ERR_CUDA, "zr_mx4_linear: launch failed: %s", cudaGetErrorString(e));
   return ZR_OK;
 }
@@ -760,7 +736,7 @@ extern "C" zr_status zr_mx4_matmul(const void* a, int64_t M, const void* b, int6
   if (!out || (K > 0 && (!a || !b))) return fail(ZR_ERR_INVALID, "zr_mx4_matmul: null pointer");
   if (!zr::aligned16(a) || !zr::aligned16(b) || !zr::aligned16(out))
     return fail(ZR_ERR_INVALID, "zr_mx4_matmul: a pointer is not 16-byte aligned");
-  return matmul("zr_mx4_matmul", a, M, b, N, K, out, dt, ldo, false, static_cast<cudaStream_t>(stream));
+  return matmul("zr_mx4_matmul", a, M, b, N, K, out, dt, ldo, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" zr_status zr_mx4_linear(const void* x, zr_dtype xdt, int64_t M, int64_t ldx, const void* w, int64_t N,
@@ -815,7 +791,7 @@ extern "C" zr_status zr_mx4_linear(const void* x, zr_dtype xdt, int64_t M, int64
     if (!xq) return fail(ZR_ERR_INVALID, "zr_mx4_linear: more than %d tokens (or a very long K) need xq", kFewTokens);
     if (zr_status st = zr_mx4_quantize(x, xdt, M, K, ldx, nullptr, 0, xq, nullptr, stream)) return st;
   }
-  return matmul("zr_mx4_linear", xq, M, w, N, K, out, dt, ldo, true, s);
+  return matmul("zr_mx4_linear", xq, M, w, N, K, out, dt, ldo, s);
 }
 
 extern "C" zr_status zr_mx4_status(void* stream) {

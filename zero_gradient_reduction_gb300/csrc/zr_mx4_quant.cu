@@ -331,6 +331,8 @@ __global__ void __launch_bounds__(kDequantThreads) dequant_kernel(const __grid_c
   const int64_t c0 = ct * zr::kMxCols;
   const int n = (int)(a.cols - c0 < zr::kMxCols ? a.cols - c0 : zr::kMxCols);  // columns of this tile
   const int r0 = (int)(blockIdx.x & 3) * kDequantRows + warp;
+  zr::wait_for_previous();
+  zr::let_next_begin();
   uint32_t codes[kRowsPerWarp];
   int byte[kRowsPerWarp];
 #pragma unroll
@@ -413,11 +415,9 @@ __global__ void __launch_bounds__(kDequantThreads) dequant_kernel(const __grid_c
 }
 
 template <int DT>
-void launch_dequant(const DequantArgs& a, int64_t blocks, bool aligned, cudaStream_t s) {
-  if (aligned)
-    dequant_kernel<DT, true><<<(unsigned)blocks, kDequantThreads, 0, s>>>(a);
-  else
-    dequant_kernel<DT, false><<<(unsigned)blocks, kDequantThreads, 0, s>>>(a);
+cudaError_t launch_dequant(const DequantArgs& a, int64_t blocks, bool aligned, cudaStream_t s) {
+  return aligned ? zr::launch(dequant_kernel<DT, true>, blocks, kDequantThreads, 0, 1, true, s, a)
+                 : zr::launch(dequant_kernel<DT, false>, blocks, kDequantThreads, 0, 1, true, s, a);
 }
 
 template <int DT, bool CHANCE>
@@ -425,8 +425,10 @@ zr_status launch_quant(const QuantArgs& a, int64_t patches, cudaStream_t s) {
   constexpr int smem = Shape<DT>::bytes + (CHANCE ? kRandBytes : 0);
   static zr::SmemAllowance allowance;
   if (zr_status st = allowance.allow("zr_mx4_quantize", (const void*)quant_kernel<DT, CHANCE>, smem)) return st;
-  quant_kernel<DT, CHANCE><<<(unsigned)patches, kThreads, smem, s>>>(a);
-  return zr::launch_status("zr_mx4_quantize");
+  // Not early: its blocks would crowd onto the SMs that the launch before leaves room on (592 x 2789 x 1238 there
+  // and back 26.2 us, 18.8 like this), and a product may read its weights before this one's end.
+  cudaError_t e = zr::launch(quant_kernel<DT, CHANCE>, patches, kThreads, smem, 1, false, s, a);
+  return e == cudaSuccess ? ZR_OK : fail(ZR_ERR_CUDA, "zr_mx4_quantize: launch failed: %s", cudaGetErrorString(e));
 }
 
 }  // namespace
@@ -494,8 +496,8 @@ extern "C" zr_status zr_mx4_dequantize(const void* q, int64_t rows, int64_t cols
   if (blocks > 0x7FFFFFFF) return fail(ZR_ERR_UNSUPPORTED, "zr_mx4_dequantize: matrix too large for one launch");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool aligned = ld * (dt == ZR_F32 ? 4 : 2) % 16 == 0;
-  if (dt == ZR_F16) launch_dequant<zr::DT_F16>(a, blocks, aligned, s);
-  else if (dt == ZR_BF16) launch_dequant<zr::DT_BF16>(a, blocks, aligned, s);
-  else launch_dequant<zr::DT_F32>(a, blocks, aligned, s);
-  return zr::launch_status("zr_mx4_dequantize");
+  const cudaError_t e = dt == ZR_F16    ? launch_dequant<zr::DT_F16>(a, blocks, aligned, s)
+                        : dt == ZR_BF16 ? launch_dequant<zr::DT_BF16>(a, blocks, aligned, s)
+                                        : launch_dequant<zr::DT_F32>(a, blocks, aligned, s);
+  return e == cudaSuccess ? ZR_OK : fail(ZR_ERR_CUDA, "zr_mx4_dequantize: launch failed: %s", cudaGetErrorString(e));
 }
