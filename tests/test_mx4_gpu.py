@@ -380,3 +380,56 @@ def test_waits_end_and_say_so(kind):
     zr.mx4_status()
     zr.mx4_linear(x, w, out, xq=xq)
     check(out[:, :400], ref.values(*ref.quantise(on_host(x)), K), wv[:400])
+
+
+@pytest.mark.parametrize("M,N,K", [(1100, 2699, 4100), (2300, 2304, 3900), (2304, 2181, 4096), (2180, 2296, 4096), (1024, 4096, 4096)])
+def test_matmul_of_a_long_k_by_pairs(M, N, K):
+    """Where K is long pairs of blocks take 256 x 256 tiles: a round that leaves pairs free, ragged last tiles, and a
+    last round in halves with a last column that is whole or a row short."""
+    (a, av), (b, bv) = quantised(M, K, 7), quantised(N, K, 8)
+    for dtype in (F32, F16, BF16):
+        for ld in (N, (N + 15) // 8 * 8):
+            room = torch.full((M, ld), 7.0, dtype=dtype, device="cuda")
+            zr.mx4_matmul(a, b, room[:, :N])
+            check(room[:, :N], av, bv)
+            assert bool((room[:, N:] == 7.0).all())
+
+
+def test_waits_of_pairs_end_and_say_so():
+    (a, av), (b, bv) = quantised(2304, 4096, 1), quantised(2304, 4096, 2)
+    out = torch.empty(2304, 2304, device="cuda")
+    torch.cuda.synchronize()
+    zr.lib().zr_mx4_stall_waits(1)
+    try:
+        zr.mx4_matmul(a, b, out)
+    finally:
+        zr.lib().zr_mx4_stall_waits(0)
+    with pytest.raises(zr.ZrError) as e:
+        zr.mx4_status()
+    assert e.value.status == 5
+    zr.mx4_status()
+    zr.mx4_matmul(a, b, out)
+    check(out[:, :400], av, bv[:400])
+
+
+def test_a_chain_of_launches_reads_what_the_one_before_wrote():
+    """Products and dequantisations begin while the launch before them ends: each of a chain reads its output."""
+    (w, wv), x = quantised(512, 512, 3), matrix(512, 512, BF16, seed=4, wide=False)
+    q, y, back = zr.Mx4(512, 512), torch.empty(512, 512, device="cuda"), torch.empty(512, 512, device="cuda")
+    want = None
+    for turn in range(20):
+        zr.mx4_quantize(x, q)
+        zr.mx4_matmul(q, w, y)
+        zr.mx4_quantize(y, q)
+        zr.mx4_dequantize(q, back)
+        zr.mx4_matmul(q, w, y)
+        got = (y.clone(), back.clone())
+        if turn == 0:
+            torch.cuda.synchronize()
+            want = got
+            first = np.zeros((512, 512))
+            first[:] = ref.values(*ref.quantise(on_host(x)), 512) @ wv.T
+            qv = ref.values(*ref.quantise(first.astype(np.float32).astype(np.float64)), 512)
+            assert (np.abs(on_host(back) - qv) > 0).mean() < 0.01  # a rounding of fp32 sums apart
+            check(y, on_host(back), wv)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

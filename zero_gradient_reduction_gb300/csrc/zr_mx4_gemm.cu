@@ -673,6 +673,32 @@ zr_status launch_gemm(const GemmArgs& g, int blocks, cudaStream_t s) {
   return ZR_OK;
 }
 
+// Tiles of 256 x 256 that pairs take in rounds. A last round that fewer than half of the pairs would be
+// busy with is taken in halves (2048 x 8192 x 8192: 48.2 us in 4 rounds, 45.6 in 3.5); not where the last
+// column of tiles has no second half, and not for want of a first round (256 x 8192 x 8192 in halves
+// 20.5 us, where as many whole tiles take 14.3).
+bool halves_last(int64_t M, int64_t N, int sms) {
+  const int64_t nt = zr::mx_tiles(N, 256), tiles = zr::mx_tiles(M, 256) * nt, pairs = sms / 2, last = tiles % pairs;
+  return tiles > pairs && last > 0 && 2 * last <= pairs && nt * 256 - N < 128;
+}
+
+// Whether pairs with their larger tiles are faster than single blocks. A pair's round costs about 1.3
+// times a block's and does twice the work, but its start and its last output take longer, so that few
+// rounds, or few of K, favour blocks. The times, in 10 ns: a start, then for each round 256 columns of K
+// at a time and what of the output does not overlap (measured; blocks and pairs at 2048 x 2048 x 2048 7.0
+// and 7.7 us, 2048 x 2048 x 8192 16.7 and 14.3, 2135 x 2109 x 8192 18.1 and 22.2, 2048 x 6144 x 512 to
+// fp32 11.2 and 14.5).
+bool pairs_faster(int64_t M, int64_t N, int64_t kt, zr_dtype dt, int sms) {
+  const int64_t m1 = zr::mx_tiles(M, 128), n1 = zr::mx_tiles(N, 128), m2 = zr::mx_tiles(M, 256), n2 = zr::mx_tiles(N, 256);
+  const int64_t most = 0x7FFFFFFF / kTileLines;
+  if (m1 > most / kt || n1 > most / kt) return false;  // 32 bits hold a matrix's lines
+  const int64_t pairs = sms / 2;
+  const int64_t rounds = (m1 * n1 + sms - 1) / sms, twice = 2 * ((m2 * n2 + pairs - 1) / pairs) - halves_last(M, N, sms);
+  const bool wide = dt == ZR_F32;
+  const int64_t single = 22 * kt + (wide ? 80 : 30), paired = 29 * kt + (wide ? 210 : kt < 6 ? 200 - 29 * kt : 40);
+  return 470 + twice * paired / 2 < 290 + rounds * single;
+}
+
 zr_status matmul(const char* what, const void* a, int64_t M, const void* b, int64_t N, int64_t K, void* out,
                  zr_dtype dt, int64_t ldo, cudaStream_t s) {
   const int es = dt == ZR_F32 ? 4 : 2;
@@ -689,10 +715,7 @@ zr_status matmul(const char* what, const void* a, int64_t M, const void* b, int6
   g.M = M; g.N = N; g.ldo = ldo;
   g.stall = g_stall.load(std::memory_order_relaxed) ? 16 : 0;
   const int64_t kt = zr::mx_tiles(K, zr::kMxCols);
-  // pairs where each gets a tile (and 32 bits hold a matrix's lines)
-  const int64_t most = 0x7FFFFFFF / kTileLines;
-  const bool pair = zr::mx_tiles(M, 256) * zr::mx_tiles(N, 256) >= sms / 2 && zr::mx_tiles(M, 128) <= most / kt &&
-                    zr::mx_tiles(N, 128) <= most / kt;
+  const bool pair = pairs_faster(M, N, kt, dt, sms);
   const int64_t mt = zr::mx_tiles(M, pair ? 256 : 128), nt = zr::mx_tiles(N, pair ? 256 : 128);
   if (kt > 0x7FFFFFFF || nt > (1 << 25) || mt > 0x3FFFFFFF / nt)
     return fail(ZR_ERR_UNSUPPORTED, "%s: the product has too many tiles", what);
@@ -701,9 +724,7 @@ zr_status matmul(const char* what, const void* a, int64_t M, const void* b, int6
   g.whole = g.mt * g.nt;
   if (pair) {
     const int pairs = sms / 2, last = g.whole % pairs, blocks = 2 * (g.whole < pairs ? g.whole : pairs);
-    // a last round that fewer than half of the pairs would be busy with, in halves (2048 x 8192 x 8192:
-    // 48.2 us in 4 rounds, 45.6 in 3.5); not where the last column of tiles has no second half
-    if (last > 0 && 2 * last <= pairs && (int64_t)nt * 256 - N < 128) g.whole -= last;
+    if (halves_last(M, N, sms)) g.whole -= last;
     if (dt == ZR_F16) return launch_gemm<true, zr::DT_F16>(g, blocks, s);
     if (dt == ZR_BF16) return launch_gemm<true, zr::DT_BF16>(g, blocks, s);
     return launch_gemm<true, zr::DT_F32>(g, blocks, s);
