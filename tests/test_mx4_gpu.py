@@ -433,3 +433,35 @@ def test_a_chain_of_launches_reads_what_the_one_before_wrote():
             assert (np.abs(on_host(back) - qv) > 0).mean() < 0.01  # a rounding of fp32 sums apart
             check(y, on_host(back), wv)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("M,N,K", [(17, 300, 4100), (40, 77, 5000), (64, 2048, 8192), (129, 901, 8192), (640, 1100, 8200), (1, 5, 100_001)])
+def test_matmul_of_few_tiles_and_a_long_k(M, N, K):
+    """Clusters of 2, 4 and 8 blocks share K: parts of unequal length, tiles of one row and of 128, every output type."""
+    (a, av), (b, bv) = quantised(M, K, 9), quantised(N, K, 10)
+    for dtype in (F32, F16, BF16):
+        for ld in (N, N + 3, (N + 15) // 8 * 8):
+            room = torch.full((M, ld), 7.0, dtype=dtype, device="cuda")
+            zr.mx4_matmul(a, b, room[:, :N])
+            check(room[:, :N], av, bv)
+            assert bool((room[:, N:] == 7.0).all())
+            again = torch.empty_like(room)
+            zr.mx4_matmul(a, b, again[:, :N])
+            assert torch.equal(again[:, :N], room[:, :N])
+
+
+def test_waits_of_blocks_that_share_k_end_and_say_so():
+    (a, av), (b, bv) = quantised(64, 8192, 1), quantised(512, 8192, 2)
+    out = torch.empty(64, 512, device="cuda")
+    torch.cuda.synchronize()
+    zr.lib().zr_mx4_stall_waits(1)
+    try:
+        zr.mx4_matmul(a, b, out)
+    finally:
+        zr.lib().zr_mx4_stall_waits(0)
+    with pytest.raises(zr.ZrError) as e:
+        zr.mx4_status()
+    assert e.value.status == 5
+    zr.mx4_status()
+    zr.mx4_matmul(a, b, out)
+    check(out, av, bv)

@@ -75,6 +75,7 @@ struct GemmArgs {
   int kt;          // tiles of 256 along K
   int mt, nt;      // output tiles
   int whole;       // tiles up to here are taken whole; the others, of a pair's last round, in two halves of 128 columns
+  int split;       // blocks, a cluster of them, that share a tile's K (of the form with single blocks)
   uint32_t stall;  // test hook: bytes expected that never come
   int vec;         // rows of out begin on 16-byte boundaries, and a map can address it
 };
@@ -161,6 +162,66 @@ __device__ __forceinline__ void rows_out(const GemmArgs& g, const CUtensorMap* m
   __syncwarp();
 }
 
+// A tile of which each block of a cluster has the products of a part of K, in its shared memory: the
+// blocks take its rows in equal shares, add the parts in the order of the blocks and store them. 64 x
+// 2048 x 8192 to bf16 in 6.4 us by fours, 9.5 by blocks alone; two waits of the cluster and 64 KB through
+// its network cost 1 to 3 us.
+constexpr int kPartPitch = 132;  // floats: rows four banks apart
+template <int S, int DT>
+__device__ __forceinline__ void join_parts(const GemmArgs& g, const float* part, int rank, const Tile& t) {
+  using T = typename std::conditional<DT == zr::DT_F32, uint32_t, uint16_t>::type;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t row0 = (int64_t)t.m * 128, col = (int64_t)t.n * 128 + lane * 4;
+  const int rows = (int)(g.M - row0 < 128 ? g.M - row0 : 128), share = (rows + S - 1) / S;
+  const int end = min(rows, (rank + 1) * share);
+  auto put = [&](int64_t row, const float v[4]) {
+    T u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (DT == zr::DT_F32)
+        u[i] = __float_as_uint(v[i]);
+      else
+        u[i] = zr::from_f32<DT>(v[i]);
+    }
+    T* out = static_cast<T*>(g.out) + row * g.ldo + col;
+    if (g.vec && col + 4 <= g.N) {
+      if constexpr (DT == zr::DT_F32)
+        *reinterpret_cast<uint4*>(out) = make_uint4(u[0], u[1], u[2], u[3]);
+      else
+        *reinterpret_cast<uint2*>(out) = make_uint2(u[0] | (uint32_t)u[1] << 16, u[2] | (uint32_t)u[3] << 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (col + i < g.N) out[i] = u[i];
+    }
+  };
+  constexpr int kWarps = kGemmThreads / 32, kOnce = S == 2 ? 8 : 2;  // a warp's rows on their way together
+  float4 p[kOnce][S];
+  for (int r0 = rank * share + warp; r0 < end; r0 += kOnce * kWarps) {
+#pragma unroll
+    for (int i = 0; i < kOnce; ++i) {
+      const int r = r0 + i * kWarps;
+      const uint32_t at = zr::smem_u32(part + r * kPartPitch + lane * 4);
+#pragma unroll
+      for (int q = 0; q < S; ++q)
+        if (r < end) p[i][q] = zr::cluster_load4(zr::cluster_addr(at, q));
+    }
+#pragma unroll
+    for (int i = 0; i < kOnce; ++i)
+      if (r0 + i * kWarps < end) {
+        float v[4] = {p[i][0].x, p[i][0].y, p[i][0].z, p[i][0].w};
+#pragma unroll
+        for (int q = 1; q < S; ++q) {
+          v[0] += p[i][q].x;
+          v[1] += p[i][q].y;
+          v[2] += p[i][q].z;
+          v[3] += p[i][q].w;
+        }
+        put(row0 + r0 + i * kWarps, v);
+      }
+  }
+}
+
 template <bool PAIR>
 using Maps = typename std::conditional<PAIR, PairMaps, OutMap>::type;
 
@@ -180,8 +241,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   volatile int* gave_up = reinterpret_cast<volatile int*>(tail + 224);
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(tail + 232);
   const int warp = threadIdx.x >> 5;
-  const int rank = PAIR ? (int)zr::cluster_rank() : 0;
-  const int first = PAIR ? blockIdx.x >> 1 : blockIdx.x, step = PAIR ? gridDim.x >> 1 : gridDim.x;
+  const bool split = !PAIR && g.split > 1;  // a tile to a cluster: each block has a part of K
+  const int rank = PAIR || split ? (int)zr::cluster_rank() : 0;
+  const int first = PAIR ? blockIdx.x >> 1 : blockIdx.x / g.split, step = PAIR ? gridDim.x >> 1 : gridDim.x / g.split;
+  const int k0 = split ? (int)((int64_t)g.kt * rank / g.split) : 0;
+  const int k1 = split ? (int)((int64_t)g.kt * (rank + 1) / g.split) : g.kt;
 
   if (warp == 0) {
     zr::tmem_alloc<PAIR>(zr::smem_u32(tmem_at), 512);
@@ -230,7 +294,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const uint32_t pair_bytes =
             zr::kMxTileBytes * (peer_a ? 2 : 1) + (zr::kMxCodeBytes + 2 * zr::kMxScaleBytes) * (second ? 2 : 1);
         const uint32_t bytes = g.stall + (PAIR ? pair_bytes : 2 * zr::kMxTileBytes);
-        for (int k = 0; k < g.kt; ++k, ++it) {
+        for (int k = k0; k < k1; ++k, ++it) {
           const int s = it % G::kStages;
           if (it >= G::kStages && !(ok = zr::bar_wait(empty + 8 * s, (it / G::kStages - 1) & 1, gave_up))) break;
           const uint32_t at = stages + s * G::kStageBytes;
@@ -259,13 +323,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const uint32_t from = it < G::kStages ? 0 : it - G::kStages;
       for (uint32_t i = from; i < it && ok; ++i)
         ok = zr::bar_wait(empty + 8 * (i % G::kStages), (i / G::kStages) & 1, gave_up);
-      if (!ok && rank == 0) {  // (the first block waits for the pair's copies; the other ends after it)
+      if (!ok && (!PAIR || rank == 0)) {  // (the first block waits for the pair's copies; the other ends after it)
         int never = 0;
         for (uint32_t i = from; i < it; ++i) zr::bar_wait(full + 8 * (i % G::kStages), (i / G::kStages) & 1, &never);
       }
     }
   } else if (warp == 1) {
-    if (rank == 0 && zr::elect_one()) {  // a pair's products are issued by its first block
+    if ((!PAIR || rank == 0) && zr::elect_one()) {  // a pair's products are issued by its first block
       uint32_t it = 0, turn = 0;
       bool ok = true;
       auto release = [&](uint32_t bar) {
@@ -279,7 +343,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const bool halved = PAIR && id >= g.whole;
         if (turn >= G::kLag && !(ok = zr::bar_wait(freed + 8 * (past & 1), (past >> 1) & 1, gave_up))) break;
         zr::tmem_fence_after();
-        for (int k = 0; k < g.kt; ++k, ++it) {
+        for (int k = k0; k < k1; ++k, ++it) {
           const int s = it % G::kStages;
           if (!(ok = zr::bar_wait(full + 8 * s, (it / G::kStages) & 1, gave_up))) break;
           zr::tmem_fence_after();
@@ -298,7 +362,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           for (int q = 0; q < 4; ++q)  // 64 columns, 32 bytes of each row, at a time
             zr::mx_mma<PAIR>(d, da + 2 * q, db + 2 * q, zr::mx_product(G::kRows, halved ? 128 : G::kCols, q & 1),
                              tmem + G::kScaleA + 4 * (q >> 1), tmem + G::kScaleB + 4 * G::kTiles * (q >> 1),
-                             (k | q) != 0);
+                             k > k0 || q > 0);
           release(empty + 8 * s);
         }
         if (ok) release(done + 8 * (turn & 1));
@@ -334,7 +398,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       if (!__all_sync(0xFFFFFFFFu, zr::bar_wait(done + 8 * (turn & 1), (turn >> 1) & 1, gave_up))) break;
       zr::tmem_fence_after();
       const uint32_t d = tmem + (turn & 1) * G::kD1 + ((uint32_t)lanes << 16);
-      const int64_t row0 = (int64_t)t.m * G::kRows + rank * 128 + lanes;
+      const int64_t row0 = (int64_t)t.m * G::kRows + (PAIR ? rank * 128 : 0) + lanes;
       const int64_t col0 = (int64_t)t.n * G::kCols + (t.half == 1 ? 128 : 0);
       const int chunks = PAIR && t.half >= 0 ? kChunks / 2 : kChunks;
 #pragma unroll 1
@@ -348,7 +412,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         else
           zr::tmem_load64(d + at * kOnce, v);
         if (c == (PAIR ? 0 : kChunks - 1)) tell(freed + 8 * (turn & 1));
-        if (row0 < g.M && col < g.N) {
+        if (split) {  // over the stages, which are used up
+          float* part = reinterpret_cast<float*>(smem) + (lanes + (threadIdx.x & 31)) * kPartPitch + at * kOnce;
+#pragma unroll
+          for (int i = 0; i < kOnce; i += 4) *reinterpret_cast<uint4*>(part + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        } else if (row0 < g.M && col < g.N) {
           rows_out<DT, G::kOutBuffers>(g, &maps.out, stage + buffer * G::kOutBytes, v, row0, col);
           buffer = buffer + 1 < G::kOutBuffers ? buffer + 1 : 0;
         }
@@ -357,8 +425,20 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     if ((threadIdx.x & 31) == 0) zr::stores_done();  // out of this block's shared memory
   }
   __syncwarp();
+  if (split) {
+    zr::cluster_sync();
+    const Tile t = tile_of(g, first);
+    const float* part = reinterpret_cast<const float*>(smem);
+    if (g.split == 2)
+      join_parts<2, DT>(g, part, rank, t);
+    else if (g.split == 4)
+      join_parts<4, DT>(g, part, rank, t);
+    else
+      join_parts<8, DT>(g, part, rank, t);
+    __syncwarp();
+  }
   zr::tmem_fence_before();
-  if (PAIR)
+  if (PAIR || split)
     zr::cluster_sync();  // neither block's shared or tensor memory goes before the other is done with it
   else
     __syncthreads();
@@ -667,7 +747,7 @@ zr_status launch_gemm(const GemmArgs& g, int blocks, cudaStream_t s) {
         !encode_lines(&maps.b_scales, g.b, b_tiles, zr::kMxScaleBytes / 128))
       return fail(ZR_ERR_CUDA, "zr_mx4_matmul: the driver gave no tensor map");
   }
-  cudaError_t e = zr::launch(gemm_kernel<PAIR, DT>, blocks, kGemmThreads, Gemm<PAIR>::kSmem, PAIR ? 2 : 1, true, s, g,
+  cudaError_t e = zr::launch(gemm_kernel<PAIR, DT>, blocks, kGemmThreads, Gemm<PAIR>::kSmem, PAIR ? 2 : g.split, true, s, g,
                              maps);
   if (e != cudaSuccess) return fail(ZR_ERR_CUDA, "zr_mx4_matmul: launch failed: %s", cudaGetErrorString(e));
   return ZR_OK;
@@ -699,6 +779,21 @@ bool pairs_faster(int64_t M, int64_t N, int64_t kt, zr_dtype dt, int sms) {
   return 470 + twice * paired / 2 < 290 + rounds * single;
 }
 
+// How many blocks share a tile's K, where there are more of them than tiles: what it saves at 0.22 us for
+// 256 columns against what it costs, which grows with the rows (measured for 17, 64 and 128). The blocks
+// of a cluster lie on neighbouring SMs, so that not all SMs find a place in one of four, and only half in
+// one of eight (128 of those took two rounds).
+int shares_of_k(int64_t M, int64_t tiles, int64_t kt, int sms) {
+  const int64_t rows = M < 128 ? M : 128;
+  int best = 1;
+  int64_t gain = 20;
+  for (int s = 2; s <= 8 && s <= kt && tiles * s <= (s == 2 ? sms : s == 4 ? sms * 6 / 7 : sms / 2); s *= 2) {
+    const int64_t g = (kt < 1000 ? 22 * kt : 22000) * (s - 1) / s - 85 - rows * (100 + 8 * s) / 100;
+    if (g > gain) gain = g, best = s;
+  }
+  return best;
+}
+
 zr_status matmul(const char* what, const void* a, int64_t M, const void* b, int64_t N, int64_t K, void* out,
                  zr_dtype dt, int64_t ldo, cudaStream_t s) {
   const int es = dt == ZR_F32 ? 4 : 2;
@@ -722,6 +817,7 @@ zr_status matmul(const char* what, const void* a, int64_t M, const void* b, int6
   g.kt = (int)kt; g.mt = (int)mt; g.nt = (int)nt;
   g.vec = ldo * es % 16 == 0 && ldo < (int64_t)1 << 36 && M <= 0x7FFFFFFF && N <= 0x7FFFFFFF;
   g.whole = g.mt * g.nt;
+  g.split = 1;
   if (pair) {
     const int pairs = sms / 2, last = g.whole % pairs, blocks = 2 * (g.whole < pairs ? g.whole : pairs);
     if (halves_last(M, N, sms)) g.whole -= last;
@@ -729,7 +825,8 @@ zr_status matmul(const char* what, const void* a, int64_t M, const void* b, int6
     if (dt == ZR_BF16) return launch_gemm<true, zr::DT_BF16>(g, blocks, s);
     return launch_gemm<true, zr::DT_F32>(g, blocks, s);
   }
-  const int blocks = (int)(mt * nt < sms ? mt * nt : sms);
+  g.split = shares_of_k(M, mt * nt, kt, sms);
+  const int blocks = g.split > 1 ? (int)(mt * nt) * g.split : (int)(mt * nt < sms ? mt * nt : sms);
   if (dt == ZR_F16) return launch_gemm<false, zr::DT_F16>(g, blocks, s);
   if (dt == ZR_BF16) return launch_gemm<false, zr::DT_BF16>(g, blocks, s);
   return launch_gemm<false, zr::DT_F32>(g, blocks, s);
