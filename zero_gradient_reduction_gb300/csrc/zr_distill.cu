@@ -183,21 +183,22 @@ __device__ __forceinline__ float rescaled(float m, float sum, const Base& to) {
 // entries for each of them cost 8192 rows of 256 entries as much again as the row itself.
 constexpr int kNoColumn = 0x7FFFFFFF;
 __device__ __forceinline__ int slot_of(int id, int bits) { return (int)((uint32_t)id * 2654435761u >> (32 - bits)); }
-__device__ __forceinline__ void take_slot(int* slots, int bits, int id) {
+// Goes on from a slot that held `was` when an entry came to it.
+__device__ __forceinline__ void take_slot(int* slots, int bits, int id, int at, int was) {
   const int mask = (1 << bits) - 1;
-  for (int at = slot_of(id, bits);; at = (at + 1) & mask) {  // ends: half the slots stay free
-    const int was = atomicCAS(slots + at, kNoColumn, id);
-    if (was == kNoColumn) return;
+  while (was != kNoColumn) {  // ends: half the slots stay free
     if ((was & 0x7FFFFFFF) == id) {
       if (was >= 0) atomicOr(slots + at, (int)0x80000000);
       return;
     }
+    at = (at + 1) & mask;
+    was = atomicCAS(slots + at, kNoColumn, id);
   }
 }
-__device__ __forceinline__ bool several(const int* slots, int bits, int id) {
+__device__ __forceinline__ bool several(const int* slots, int bits, int id, int at, int there) {
   const int mask = (1 << bits) - 1;
-  for (int at = slot_of(id, bits);; at = (at + 1) & mask)
-    if ((slots[at] & 0x7FFFFFFF) == id) return slots[at] < 0;
+  while ((there & 0x7FFFFFFF) != id) there = slots[at = (at + 1) & mask];
+  return there < 0;
 }
 
 // The exponentials of a word's logits relative to a maximum, summed: two by two where that is one
@@ -229,33 +230,26 @@ __device__ __forceinline__ float terms(uint4 u, const Base& base) {
   return sum;
 }
 
-// A lane's entries k0, k0 + 32, ... as they stand in memory. They are asked for before the row is, all
-// together, and as words of 32 bits that nothing looks at before the last is asked for: behind a row's
-// copies each turn of loads waits for 100 KB.
-struct RawEntries {
-  static constexpr int many = 4;
-  uint32_t lo[many], hi[many], t[many];
-  __device__ void load(const DistillArgs& a, int64_t row, int k0) {
-    const int half = a.tdt != zr::DT_F32;
-#pragma unroll
-    for (int i = 0; i < many; ++i) {
-      const int64_t at = row * a.ldk + k0 + 32 * i;
-      if (k0 + 32 * i < a.K) {
-        lo[i] = __ldg(static_cast<const uint32_t*>(a.ids) + (at << a.wide_ids));
-        if (a.wide_ids) hi[i] = __ldg(static_cast<const uint32_t*>(a.ids) + 2 * at + 1);
-        t[i] = __ldg(static_cast<const uint32_t*>(a.teacher) + (at >> half));
-      }
-    }
+// A row's entries as they stand in memory, to shared memory: ids of 4 or 8 bytes, and the words of 4
+// bytes that hold the logits. They are asked for before the row is, and all together: behind a row's
+// copies each turn of loads waits for 100 KB (8192 rows of 50304 with 256 entries each took 413 us in
+// eight turns).
+__device__ __forceinline__ void ask_for_entries(const DistillArgs& a, int64_t row, int lane, void* ids, void* logits) {
+  const int half = a.tdt != zr::DT_F32;
+  for (int k = lane; k < a.K; k += 32) {
+    const int64_t at = row * a.ldk + k;
+    if (a.wide_ids)
+      zr::copy8(zr::smem_u32(static_cast<int64_t*>(ids) + k), static_cast<const int64_t*>(a.ids) + at);
+    else
+      zr::copy4(zr::smem_u32(static_cast<int32_t*>(ids) + k), static_cast<const int32_t*>(a.ids) + at);
+    zr::copy4(zr::smem_u32(static_cast<uint32_t*>(logits) + k), static_cast<const uint32_t*>(a.teacher) + (at >> half));
   }
-  __device__ int64_t id(const DistillArgs& a, int i) const {
-    return a.wide_ids ? (int64_t)((uint64_t)hi[i] << 32 | lo[i]) : (int64_t)(int32_t)lo[i];
-  }
-  __device__ float logit(const DistillArgs& a, int64_t row, int k, int i) const {
-    if (a.tdt == zr::DT_F32) return __uint_as_float(t[i]);
-    const uint16_t v = (uint16_t)(t[i] >> ((row * a.ldk + k) & 1) * 16);
-    return a.tdt == zr::DT_BF16 ? zr::to_f32<zr::DT_BF16>(v) : zr::to_f32<zr::DT_F16>(v);
-  }
-};
+}
+__device__ __forceinline__ float teacher_logit(const DistillArgs& a, int64_t row, int k, uint32_t w) {
+  if (a.tdt == zr::DT_F32) return __uint_as_float(w);
+  const uint16_t v = (uint16_t)(w >> ((row * a.ldk + k) & 1) * 16);
+  return a.tdt == zr::DT_BF16 ? zr::to_f32<zr::DT_BF16>(v) : zr::to_f32<zr::DT_F16>(v);
+}
 
 struct Shared {      // what the block's warps, and the cluster's blocks, tell each other
   float m[32], sum[32], loss[32];  // of each warp
@@ -305,8 +299,7 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(const __grid_const
   const int single = tid < head ? tid : tid >= 8 && tid - 8 < n - behind ? behind + tid - 8 : -1;
   float z_single = -INFINITY;
 
-  RawEntries raw;
-  if (tid >= nthr) raw.load(a, row, lane);
+  if (tid >= nthr) ask_for_entries(a, row, lane, own, sp);  // (ids of 8 bytes reach over `all`)
   bool some = w != 0.0f;
   if (some) {
     for (int j = first + tid; tid < nthr && j < min(last, a.room); j += nthr)
@@ -321,32 +314,45 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(const __grid_const
       float t_max = -INFINITY;
       int any = 0, past = 0;
       for (int i = lane; i < 1 << a.slot_bits; i += 32) slots[i] = kNoColumn;
-      for (int k0 = lane; k0 < a.K4; k0 += 32 * RawEntries::many) {
-        if (k0 != lane) raw.load(a, row, k0);
-#pragma unroll
-        for (int i = 0; i < RawEntries::many; ++i) {
-          const int k = k0 + 32 * i;
-          const int64_t id = k < a.K ? raw.id(a, i) : -1;
-          const float t = raw.logit(a, row, k, i);
-          const bool kept = id >= 0;
-          past |= id >= a.V;
-          any |= kept && !(t == -INFINITY);  // a masked entry is none
-          if (kept) t_max = fmaxf(t_max, t);
-          if (k < a.K4) {
-            sid[k] = kept && id < a.V ? (int)id : -1;
-            own[k] = kept ? t : -INFINITY;
-          }
+      zr::copies_done();
+      for (int k = lane; k < a.K4; k += 32) {  // (an entry's bytes are this lane's own copies)
+        int64_t id = -1;
+        float t = 0.0f;
+        if (k < a.K) {
+          id = a.wide_ids ? reinterpret_cast<const int64_t*>(own)[k] : reinterpret_cast<const int32_t*>(own)[k];
+          t = teacher_logit(a, row, k, __float_as_uint(sp[k]));
         }
+        const bool kept = id >= 0;
+        past |= id >= a.V;
+        any |= kept && !(t == -INFINITY);  // a masked entry is none
+        if (kept) t_max = fmaxf(t_max, t);
+        sid[k] = kept && id < a.V ? (int)id : -1;
+        sp[k] = kept ? t : -INFINITY;
       }
       __syncwarp();
       any = __any_sync(0xFFFFFFFFu, any);
       past = __any_sync(0xFFFFFFFFu, past);
       t_max = warp_max(t_max);
       // an entry of -inf has p = 0; +inf or NaN leaves every p not a number
+      constexpr int kEntries = 4;  // of a lane, so that their first looks at the table overlap
       float p_sum = 0.0f;
-      for (int k = lane; k < a.K4; k += 32) {
-        if (sid[k] >= 0) take_slot(slots, a.slot_bits, sid[k]);
-        p_sum += sp[k] = exp2_fast(own[k] = (own[k] - t_max) * c);
+      for (int k0 = lane; k0 < a.K4; k0 += 32 * kEntries) {
+        int id[kEntries], at[kEntries], was[kEntries];
+#pragma unroll
+        for (int i = 0; i < kEntries; ++i) {
+          const int k = k0 + 32 * i;
+          id[i] = k < a.K4 ? sid[k] : -1;
+          at[i] = slot_of(id[i], a.slot_bits);
+          was[i] = id[i] >= 0 ? atomicCAS(slots + at[i], kNoColumn, id[i]) : kNoColumn;
+        }
+#pragma unroll
+        for (int i = 0; i < kEntries; ++i) {
+          const int k = k0 + 32 * i;
+          if (k < a.K4) p_sum += sp[k] = exp2_fast(own[k] = (sp[k] - t_max) * c);
+        }
+#pragma unroll
+        for (int i = 0; i < kEntries; ++i)
+          if (id[i] >= 0) take_slot(slots, a.slot_bits, id[i], at[i], was[i]);
       }
       p_sum = warp_sum(p_sum);
       const float log_p = log2f(p_sum);
@@ -355,15 +361,27 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(const __grid_const
         own[k] -= log_p;
       }
       __syncwarp();
-      for (int k = lane; k < a.K; k += 32) {
-        const int id = sid[k];
-        float p = sp[k];
-        if (id >= 0 && several(slots, a.slot_bits, id)) {  // each of them finds the same sum
-          p = 0.0f;
-          for (int i = 0; i < a.K; ++i)
-            if (sid[i] == id) p += sp[i];
+      for (int k0 = lane; k0 < a.K; k0 += 32 * kEntries) {
+        int id[kEntries], at[kEntries], there[kEntries];
+#pragma unroll
+        for (int i = 0; i < kEntries; ++i) {
+          const int k = k0 + 32 * i;
+          id[i] = k < a.K ? sid[k] : -1;
+          at[i] = slot_of(id[i], a.slot_bits);
+          there[i] = slots[at[i]];
         }
-        all[k] = p;
+#pragma unroll
+        for (int i = 0; i < kEntries; ++i) {
+          const int k = k0 + 32 * i;
+          if (k >= a.K) break;
+          float p = sp[k];
+          if (id[i] >= 0 && several(slots, a.slot_bits, id[i], at[i], there[i])) {  // each of them finds the same sum
+            p = 0.0f;
+            for (int j = 0; j < a.K; ++j)
+              if (sid[j] == id[i]) p += sp[j];
+          }
+          all[k] = p;
+        }
       }
       if (lane == 0) {
         sh.some = any;
@@ -429,6 +447,7 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(const __grid_const
     some = sh.some;
   }
 
+  if (!some && tid >= nthr) zr::copies_done();
   if (!some) {  // no weight, or nothing kept: no loss and no gradient (the same in the whole cluster)
     if (rank == 0 && tid == 0) a.loss[row] = 0.0f;
     if (grad && tid < nthr) {
@@ -614,8 +633,10 @@ extern "C" zr_status zr_distill_topk(const void* logits, zr_dtype dt, int64_t T,
   // what two blocks to an SM hold (7229 x 57000 bf16 in 270 us, 372 with one) or of what one holds;
   // longer rows go to as few blocks as have up to 1.2 times the half each. Where rows leave SMs free
   // each is shared as far as those go and its parts stay 24 KB long.
+  // A quarter full the table of columns is walked less than half full (256 entries by 8192 x 8000 in 75 us
+  // against 98), as long as it is small.
   a.slot_bits = 1;
-  while (1 << a.slot_bits < 2 * K) ++a.slot_bits;
+  while (1 << a.slot_bits < 2 * K || (1 << a.slot_bits < 4 * K && a.slot_bits < 11)) ++a.slot_bits;  // up to 8 KB
   const int fixed = a.K4 * 16 + (4 << a.slot_bits) + (int)sizeof(Shared);
   auto held = [&](int blocks) { return ((zr::kSmemMost + 1024) / blocks - 1024 - fixed) / 16; };
   const int unit = 16 / es;
