@@ -465,3 +465,49 @@ def test_waits_of_blocks_that_share_k_end_and_say_so():
     zr.mx4_status()
     zr.mx4_matmul(a, b, out)
     check(out, av, bv)
+
+
+def test_captured_behind_copies_and_other_streams():
+    """Products and dequantisations as a graph's first node, behind a copy, a fill and a kernel of torch, and behind a
+    join of two streams: each replay gives what the calls give one by one."""
+    (a, av), (b, bv) = quantised(300, 700, 11), quantised(200, 700, 12)
+    a2 = zr.Mx4(300, 700)
+    out, back, moved = torch.empty(300, 200, device="cuda"), torch.empty(300, 700, device="cuda"), torch.empty(300, 200, device="cuda")
+    x = matrix(300, 700, F32, seed=13, wide=False)
+    side, main = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def work():
+        zr.mx4_matmul(a, b, out)            # first
+        moved.copy_(out)
+        a2.data.copy_(a.data)
+        zr.mx4_dequantize(a2, back)         # behind a copy
+        back.add_(1.0)
+        out.zero_()
+        zr.mx4_matmul(a2, b, out)           # behind a fill
+        out.mul_(2.0)
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            zr.mx4_quantize(x, a2)
+        moved.add_(out)
+        here.wait_stream(side)
+        zr.mx4_matmul(a2, b, out)           # behind a join
+
+    main.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(main):
+        work()
+    main.synchronize()
+    want = [t.clone() for t in (out, back, moved, a2.data)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        work()
+    for _ in range(3):
+        for t in (out, back, moved):
+            t.fill_(7.0)
+        a2.data.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, w in zip((out, back, moved, a2.data), want):
+            assert torch.equal(got, w)
+    check(out, ref.values(*ref.quantise(on_host(x)), 700), bv)
+    assert np.array_equal(on_host(back), (av.astype(np.float32) + np.float32(1)).astype(np.float64))
