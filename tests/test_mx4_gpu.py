@@ -511,3 +511,18 @@ def test_captured_behind_copies_and_other_streams():
             assert torch.equal(got, w)
     check(out, ref.values(*ref.quantise(on_host(x)), 700), bv)
     assert np.array_equal(on_host(back), (av.astype(np.float32) + np.float32(1)).astype(np.float64))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("ld", [320, 322, 324, 328, 321])
+@pytest.mark.parametrize("cols", [304, 312, 308, 306, 301])
+def test_quantise_row_strides_of_values_and_random_bytes(dtype, ld, cols):
+    """Rows that begin on boundaries of 16, 8, 4 and fewer bytes: the values' by ld, the random bytes' by cols."""
+    rows = 131
+    x = matrix(rows, cols, dtype, seed=ld, ld=ld)
+    rand = torch.randint(0, 256, (rows, cols), dtype=torch.uint8, generator=torch.Generator().manual_seed(cols)).cuda()
+    q, qt = zr.Mx4(rows, cols), zr.Mx4(cols, rows)
+    zr.mx4_quantize(x, q, qt, rand=rand)
+    h, r = on_host(x), rand.cpu().numpy()
+    same(q, ref.quantise(h, r), cols)
+    same(qt, ref.quantise(h.T, r.T), rows)

@@ -82,6 +82,16 @@ __device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
 __device__ __forceinline__ void copy8(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
+// `bytes` of STEP (4, 8 or 16) that begin on a boundary of STEP, and zeros behind them.
+template <int STEP>
+__device__ __forceinline__ void copy_of(uint32_t dst, const void* src, int bytes) {
+  if constexpr (STEP == 16)
+    copy16_of(dst, src, bytes);
+  else if constexpr (STEP == 8)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // A box of a tensor map (x = column, y = row of its first element) to shared memory of this block of
