@@ -368,6 +368,8 @@ class Plan:
         h = ctypes.c_void_p()
         _check(lib().zr_plan_create(ctypes.byref(d), ctypes.byref(h)))
         self._h = h
+        import torch
+        self.device = torch.cuda.current_device()  # where the library has put the plan's control block
         self.W, self.A, self.dtype, self.stage = int(W), int(A), int(dtype), int(stage)
         self.fp32_grads = bool(fp32_grads)
         self.numel = int(lib().zr_plan_numel(h))
@@ -605,8 +607,9 @@ _types = {}
 def _fn(name: str):
     import torch
     _types.update({torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32})
-    _fns["stream"] = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-        lambda device: torch.cuda.current_stream(device).cuda_stream)
+    _fns.setdefault("stream", getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda device: torch.cuda.current_stream(device).cuda_stream))
+    _fns.setdefault("device", getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device)
     f = _fns[name] = getattr(lib(), name)
     return f
 
@@ -630,14 +633,25 @@ def _matrix(t, what: str):
     return t.data_ptr(), rows, cols, ld, dt, device
 
 
-def _stream_of(stream, device: int) -> int:
-    return _fns["stream"](device) if stream is None else int(stream.cuda_stream)
+def _stream_of(stream, device: int, *others: int) -> int:
+    """The handle of the stream to launch on, once every operand's device is known to be the current one: a launch goes
+    to the current device whatever stream it names, and there the others' addresses mean nothing."""
+    for d in others:
+        if d != device:
+            _refuse(f"operands on devices {device} and {d}")
+    if _fns["device"]() != device:
+        _refuse(f"operands on device {device}, which is not the current one")
+    if stream is None:
+        return _fns["stream"](device)
+    if getattr(stream, "device_index", device) != device:
+        _refuse(f"operands on device {device}, the stream on {stream.device_index}")
+    return int(stream.cuda_stream)
 
 
 class Mx4:
     """A rows x cols matrix in microscaled 4-bit floating point: its bytes in `data` (layout in include/zr.h)."""
 
-    __slots__ = ("rows", "cols", "data", "ptr")
+    __slots__ = ("rows", "cols", "data", "ptr", "device")
 
     def __init__(self, rows: int, cols: int, data=None, device="cuda"):
         if rows < 0 or cols < 0:
@@ -646,9 +660,9 @@ class Mx4:
         if data is None:
             import torch
             data = torch.empty(need, dtype=torch.uint8, device=device)
-        elif data.element_size() != 1 or data.numel() < need or not data.is_cuda or not data.is_contiguous():
+        if data.element_size() != 1 or data.numel() < need or not data.is_cuda or not data.is_contiguous():
             _refuse(f"Mx4: data must be {need} contiguous bytes in device memory")
-        self.rows, self.cols, self.data, self.ptr = rows, cols, data, data.data_ptr()
+        self.rows, self.cols, self.data, self.ptr, self.device = rows, cols, data, data.data_ptr(), data.get_device()
 
 
 def mx4_quantize(x, q: Optional[Mx4] = None, q_t: Optional[Mx4] = None, rand=None, stream=None) -> None:
@@ -667,7 +681,9 @@ def mx4_quantize(x, q: Optional[Mx4] = None, q_t: Optional[Mx4] = None, rand=Non
         if not rand.is_contiguous():
             _refuse("mx4_quantize: rand must be contiguous")
         rp, ldr = rand.data_ptr(), cols
-    _check(fn(p, dt, rows, cols, ld, rp, ldr, q and q.ptr, q_t and q_t.ptr, _stream_of(stream, device)))
+    s = _stream_of(stream, device, q.device if q is not None else device, q_t.device if q_t is not None else device,
+                   rand.get_device() if rand is not None else device)
+    _check(fn(p, dt, rows, cols, ld, rp, ldr, q and q.ptr, q_t and q_t.ptr, s))
 
 
 def mx4_dequantize(q: Mx4, out, stream=None) -> None:
@@ -676,7 +692,7 @@ def mx4_dequantize(q: Mx4, out, stream=None) -> None:
     p, rows, cols, ld, dt, device = _matrix(out, "out")
     if q.rows != rows or q.cols != cols:
         _refuse(f"mx4_dequantize: q is {q.rows} x {q.cols}, out {rows} x {cols}")
-    _check(fn(q.ptr, rows, cols, p, dt, ld, _stream_of(stream, device)))
+    _check(fn(q.ptr, rows, cols, p, dt, ld, _stream_of(stream, device, q.device)))
 
 
 def mx4_matmul(a: Mx4, b: Mx4, out, stream=None) -> None:
@@ -685,20 +701,21 @@ def mx4_matmul(a: Mx4, b: Mx4, out, stream=None) -> None:
     p, rows, cols, ld, dt, device = _matrix(out, "out")
     if a.cols != b.cols or a.rows != rows or b.rows != cols:
         _refuse(f"mx4_matmul: a is {a.rows} x {a.cols}, b {b.rows} x {b.cols}, out {rows} x {cols}")
-    _check(fn(a.ptr, rows, b.ptr, cols, a.cols, p, dt, ld, _stream_of(stream, device)))
+    _check(fn(a.ptr, rows, b.ptr, cols, a.cols, p, dt, ld, _stream_of(stream, device, a.device, b.device)))
 
 
 def mx4_linear(x, w: Mx4, out, xq: Optional[Mx4] = None, stream=None) -> None:
     """out[M, N] = x[M, K] w[N, K]^T with x quantised in the call (zr_mx4_linear); more than MX4_FEW tokens need xq,
     a buffer for the quantised x."""
     fn = _fns.get("zr_mx4_linear") or _fn("zr_mx4_linear")
-    p, rows, k, ldx, xdt, _ = _matrix(x, "x")
+    p, rows, k, ldx, xdt, x_device = _matrix(x, "x")
     o, m, n, ldo, dt, device = _matrix(out, "out")
     if w.cols != k or m != rows or w.rows != n:
         _refuse(f"mx4_linear: x is {rows} x {k}, w {w.rows} x {w.cols}, out {m} x {n}")
     if xq is not None and (xq.rows != rows or xq.cols != k):
         _refuse(f"mx4_linear: xq is {xq.rows} x {xq.cols}, x {rows} x {k}")
-    _check(fn(p, xdt, rows, ldx, w.ptr, n, k, o, dt, ldo, xq and xq.ptr, _stream_of(stream, device)))
+    s = _stream_of(stream, device, x_device, w.device, xq.device if xq is not None else device)
+    _check(fn(p, xdt, rows, ldx, w.ptr, n, k, o, dt, ldo, xq and xq.ptr, s))
 
 
 def mx4_status(stream=None) -> None:
@@ -713,7 +730,7 @@ def distill_topk(logits, ids, teacher, loss, grad=None, weight=None, temperature
     import torch
     fn = _fns.get("zr_distill_topk") or _fn("zr_distill_topk")
     z, rows, vocab, ldz, dt, device = _matrix(logits, "logits")
-    t, trows, top, ldk, tdt, _ = _matrix(teacher, "teacher")
+    t, trows, top, ldk, tdt, t_device = _matrix(teacher, "teacher")
     if ids.dtype not in (torch.int32, torch.int64) or ids.shape != teacher.shape or not ids.is_cuda:
         _refuse("distill_topk: ids must be int32 or int64 of teacher's shape in device memory")
     if trows != rows:
@@ -723,15 +740,16 @@ def distill_topk(logits, ids, teacher, loss, grad=None, weight=None, temperature
     for name, v in (("loss", loss), ("weight", weight)):
         if v is not None and (v.dtype != torch.float32 or v.numel() != rows or not v.is_contiguous() or not v.is_cuda):
             _refuse(f"distill_topk: {name} must be fp32 [{rows}] in device memory")
-    g, ldg = None, 0
+    g, ldg, g_device = None, 0, device
     if grad is not None:
         if grad.dtype != logits.dtype or grad.shape != logits.shape:
             _refuse("distill_topk: grad must have the logits' type and shape")
-        g, _, _, ldg, _, _ = _matrix(grad, "grad")
+        g, _, _, ldg, _, g_device = _matrix(grad, "grad")
+    s = _stream_of(stream, device, t_device, ids.get_device(), loss.get_device(), g_device,
+                   weight.get_device() if weight is not None else device, plan.device if plan is not None else device)
     _check(fn(z, dt, rows, vocab, ldz, ids.data_ptr(), int(ids.dtype == torch.int64), t, tdt, top, ldk,
               weight.data_ptr() if weight is not None else None, temperature, grad_scale,
-              plan.handle if plan is not None else None, loss.data_ptr(), g, ldg,
-              _stream_of(stream, device)))
+              plan.handle if plan is not None else None, loss.data_ptr(), g, ldg, s))
 
 
 __all__ = ["lib", "ZrError", "chunk_size", "bucket_plan", "model_state_bytes", "ring_traffic", "reduce_scatter",
