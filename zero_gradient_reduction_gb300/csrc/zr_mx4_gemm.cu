@@ -332,6 +332,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     if ((!PAIR || rank == 0) && zr::elect_one()) {  // a pair's products are issued by its first block
       uint32_t it = 0, turn = 0;
       bool ok = true;
+      zr::wait_for_previous();  // nothing is copied before that, and its time is not this product's
       auto release = [&](uint32_t bar) {
         if (PAIR)
           zr::pair_commit(bar, 3);
