@@ -588,8 +588,12 @@ zr_status zr_mx4_matmul(const void* a, int64_t M, const void* b, int64_t N, int6
 zr_status zr_mx4_linear(const void* x, zr_dtype xdt, int64_t M, int64_t ldx, const void* w, int64_t N, int64_t K,
                         void* out, zr_dtype dt, int64_t ldo, void* xq, void* stream);
 
-/* Synchronises `stream` and returns ZR_ERR_TIMEOUT if a product on this device gave up a wait
- * since the last call (whose outputs are then not valid), ZR_OK otherwise. */
+/* Synchronises `stream` and returns ZR_ERR_TIMEOUT if a product on this device, on any stream,
+ * gave up a wait since the last call for this stream (since the library was loaded for a stream's
+ * first call); the outputs of this stream's products since then may not be valid. ZR_OK otherwise:
+ * they are. A report is not lost to other streams, each hears of it; threads that share a stream
+ * share its reports. Products of a replayed graph count for the stream that it is replayed on.
+ * Errors: ZR_ERR_CUDA, ZR_ERR_OOM (a stream's first call). */
 zr_status zr_mx4_status(void* stream);
 
 /* Test hook: while `on`, every stage of the products launched expects 16 bytes more than are

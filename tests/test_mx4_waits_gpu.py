@@ -46,3 +46,43 @@ def test_the_launch_before_does_not_use_up_a_products_time(M, N, K):
     assert e.value.status == 5  # the first one's
     zr.mx4_status()
     check(out[:, :400], cv, dv[:400])
+
+
+def test_every_stream_hears_of_a_wait_that_ran_out():
+    """A report that one stream has had is not lost to another: the product's own, above all."""
+    (a, _), (b, _) = quantised(64, 200, 1), quantised(64, 200, 2)
+    out, side, other = torch.empty(64, 64, device="cuda"), torch.cuda.Stream(), torch.cuda.Stream()
+    for s in (None, side, other):
+        try:
+            zr.mx4_status(stream=s)
+        except zr.ZrError:
+            pass  # of another test, if at all
+    torch.cuda.synchronize()
+    stalled(lambda: zr.mx4_matmul(a, b, out, stream=side))
+    side.synchronize()
+    for s in (None, other, side):
+        with pytest.raises(zr.ZrError) as e:
+            zr.mx4_status(stream=s)
+        assert e.value.status == 5
+    for s in (side, None, other):
+        zr.mx4_status(stream=s)
+
+
+def test_a_replayed_product_is_heard_of_where_it_ran():
+    """Captured on one stream, replayed on another: the stream of the replay hears of it."""
+    (a, _), (b, _) = quantised(64, 200, 1), quantised(64, 200, 2)
+    out, side, graph = torch.empty(64, 64, device="cuda"), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    zr.mx4_matmul(a, b, out)
+    torch.cuda.synchronize()
+
+    def capture():
+        with torch.cuda.graph(graph, stream=side):
+            zr.mx4_matmul(a, b, out, stream=side)
+
+    stalled(capture)
+    zr.mx4_status()
+    graph.replay()
+    with pytest.raises(zr.ZrError) as e:
+        zr.mx4_status()
+    assert e.value.status == 5
+    zr.mx4_status()

@@ -719,7 +719,7 @@ def mx4_linear(x, w: Mx4, out, xq: Optional[Mx4] = None, stream=None) -> None:
 
 
 def mx4_status(stream=None) -> None:
-    """Synchronises the stream and raises if a product gave up a wait since the last call (zr_mx4_status)."""
+    """Synchronises the stream and raises if a product gave up a wait since this stream's last call (zr_mx4_status)."""
     _check(lib().zr_mx4_status(_stream_handle(stream)))
 
 

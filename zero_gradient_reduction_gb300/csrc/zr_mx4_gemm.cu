@@ -20,7 +20,11 @@
 
 #include <atomic>
 #include <cstdint>
+#include <exception>
+#include <map>
+#include <mutex>
 #include <type_traits>
+#include <utility>
 
 #include "zr_internal.h"
 #include "zr_launch.h"
@@ -32,8 +36,12 @@ using zr::fail;
 
 namespace {
 
-// Set by a kernel whose wait ran out of time; read and cleared by zr_mx4_status.
-__device__ int g_gave_up;
+// Counts the blocks, ever, whose wait ran out of time. It is never set back: what one stream has heard of
+// another may still have to.
+__device__ unsigned long long g_gave_up;
+// The count that each stream (by device and id) has heard of by zr_mx4_status.
+std::mutex g_heard_mu;
+std::map<std::pair<int, unsigned long long>, unsigned long long> g_heard;
 // Test hook (zr_mx4_stall_waits): bytes that every stage expects beyond those copied.
 std::atomic<int> g_stall{0};
 
@@ -444,7 +452,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   else
     __syncthreads();
   zr::tmem_fence_after();
-  if (threadIdx.x == 0 && *gave_up) g_gave_up = 1;
+  if (threadIdx.x == 0 && *gave_up) atomicAdd(&g_gave_up, 1ull);
   if (warp == 0) zr::tmem_free<PAIR>(tmem, 512);
 }
 
@@ -695,7 +703,7 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
     __syncthreads();
   }
   zr::tmem_fence_after();
-  if (threadIdx.x == 0 && *gave_up) g_gave_up = 1;
+  if (threadIdx.x == 0 && *gave_up) atomicAdd(&g_gave_up, 1ull);
   if (warp == 0) zr::tmem_free(tmem, 32);
 }
 
@@ -916,17 +924,25 @@ extern "C" zr_status zr_mx4_linear(const void* x, zr_dtype xdt, int64_t M, int64
 extern "C" zr_status zr_mx4_status(void* stream) {
   zr::clear_error();
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  int gave_up = 0;
-  cudaError_t e = cudaMemcpyFromSymbolAsync(&gave_up, g_gave_up, sizeof gave_up, 0, cudaMemcpyDeviceToHost, s);
+  int device = 0;
+  unsigned long long id = 0, count = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e == cudaSuccess) e = cudaStreamGetId(s, &id);  // (a handle may come again for another stream)
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbolAsync(&count, g_gave_up, sizeof count, 0, cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  if (e == cudaSuccess && gave_up) {
-    const int zero = 0;
-    e = cudaMemcpyToSymbolAsync(g_gave_up, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, s);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    if (e == cudaSuccess)
-      return fail(ZR_ERR_TIMEOUT, "zr_mx4_status: a product gave up a wait; outputs since the last check are void");
+  if (e != cudaSuccess) return fail(ZR_ERR_CUDA, "zr_mx4_status: %s", cudaGetErrorString(e));
+  bool more = false;
+  try {
+    std::lock_guard<std::mutex> lock(g_heard_mu);
+    unsigned long long& heard = g_heard[{device, id}];
+    more = count > heard;
+    if (more) heard = count;
+  } catch (const std::exception&) {
+    return fail(ZR_ERR_OOM, "zr_mx4_status: no memory for the stream's record");
   }
-  return e == cudaSuccess ? ZR_OK : fail(ZR_ERR_CUDA, "zr_mx4_status: %s", cudaGetErrorString(e));
+  if (more)
+    return fail(ZR_ERR_TIMEOUT, "zr_mx4_status: a product gave up a wait; outputs since this stream's last check are void");
+  return ZR_OK;
 }
 
 extern "C" zr_status zr_mx4_stall_waits(int on) {
