@@ -613,8 +613,9 @@ zr_status zr_mx4_stall_waits(int on);
  * the ring; one that overflows dt is what the step's flag is for.
  * An entry with a negative id, or with a teacher logit of -inf, is not kept. A row without
  * weight or without kept entries has loss 0 and gradient 0, whatever its logits hold. Logits
- * of -inf have q = 0. A row with NaN or +inf, with every logit -inf, or with an id >= V has
- * loss and gradient NaN. An id may stand more than once in a row.
+ * of -inf have q = 0. A row with NaN or +inf among its logits or its kept entries, with every
+ * logit -inf, or with an id >= V has loss NaN and gradient NaN in every column. An id may stand
+ * more than once in a row.
  * logits: device, T x V of type dt, row stride ldz; ids: device, T x K of int32 (int64 with
  * ids64), teacher: device, T x K of type teacher_dt, both with row stride ldk; weight: device
  * fp32[T] or NULL (all 1); loss: device fp32[T]; grad: device, T x V of type dt with row stride

@@ -254,7 +254,7 @@ __device__ __forceinline__ float teacher_logit(const DistillArgs& a, int64_t row
 struct Shared {      // what the block's warps, and the cluster's blocks, tell each other
   float m[32], sum[32], loss[32];  // of each warp
   float row_m[8], row_sum[8], row_loss[8];  // of the cluster's blocks: each tells all, the loss the first
-  int some, beyond;
+  int some, no_answer;
 };
 
 // A row is handled in the 16-byte words of memory that hold it: word 0 begins at the boundary at
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(const __grid_const
     if (tid >= nthr) {
       // ---- the teacher's entries: p over the kept ones
       float t_max = -INFINITY;
-      int any = 0, past = 0;
+      int any = 0, no_answer = 0;
       for (int i = lane; i < 1 << a.slot_bits; i += 32) slots[i] = kNoColumn;
       zr::copies_done();
       for (int k = lane; k < a.K4; k += 32) {  // (an entry's bytes are this lane's own copies)
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(const __grid_const
           t = teacher_logit(a, row, k, __float_as_uint(sp[k]));
         }
         const bool kept = id >= 0;
-        past |= id >= a.V;
+        no_answer |= id >= a.V || (kept && !(t < INFINITY));
         any |= kept && !(t == -INFINITY);  // a masked entry is none
         if (kept) t_max = fmaxf(t_max, t);
         sid[k] = kept && id < a.V ? (int)id : -1;
@@ -331,9 +331,9 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(const __grid_const
       }
       __syncwarp();
       any = __any_sync(0xFFFFFFFFu, any);
-      past = __any_sync(0xFFFFFFFFu, past);
+      no_answer = __any_sync(0xFFFFFFFFu, no_answer);
       t_max = warp_max(t_max);
-      // an entry of -inf has p = 0; +inf or NaN leaves every p not a number
+      // an entry of -inf has p = 0
       constexpr int kEntries = 4;  // of a lane, so that their first looks at the table overlap
       float p_sum = 0.0f;
       for (int k0 = lane; k0 < a.K4; k0 += 32 * kEntries) {
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(const __grid_const
       }
       if (lane == 0) {
         sh.some = any;
-        sh.beyond = past;
+        sh.no_answer = no_answer;
       }
     }
   }
@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(const __grid_const
     for (int r = 0; r < C; ++r) sum = __fadd_rn(sum, rescaled(sh.row_m[r], sh.row_sum[r], Base(m, c)));
   }
   const Base base(m, c);
-  if (sh.beyond) sum = NAN;  // an entry past the vocabulary: the row says so in its loss and its gradient
+  if (sh.no_answer) sum = NAN;  // an entry past the vocabulary, or no number: so are the loss and the whole gradient
 
   // ---- the entries in this block's columns: their loss, and the gradient there
   const float scale = a.scale ? __fmul_rn(a.grad_scale, *a.scale) : a.grad_scale;
@@ -569,7 +569,7 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(const __grid_const
     } else {
       loss = warp_sum(lane <= (nthr >> 5) ? sh.loss[lane] : 0.0f);
     }
-    if (lane == 0) a.loss[row] = sh.beyond ? NAN : __fmul_rn(loss, __fmul_rn(w, __fmul_rn(a.tau, a.tau)));
+    if (lane == 0) a.loss[row] = sh.no_answer ? NAN : __fmul_rn(loss, __fmul_rn(w, __fmul_rn(a.tau, a.tau)));
   }
 }
 
