@@ -231,9 +231,9 @@ __device__ __forceinline__ float terms(uint4 u, const Base& base) {
 }
 
 // A row's entries as they stand in memory, to shared memory: ids of 4 or 8 bytes, and the words of 4
-// bytes that hold the logits. They are asked for before the row is, and all together: behind a row's
-// copies each turn of loads waits for 100 KB (8192 rows of 50304 with 256 entries each took 413 us in
-// eight turns).
+// bytes that hold the logits (of a word that the row's last entry begins, 2 bytes: the array may end
+// there). They are asked for before the row is, and all together: behind a row's copies each turn of
+// loads waits for 100 KB (8192 rows of 50304 with 256 entries each took 413 us in eight turns).
 __device__ __forceinline__ void ask_for_entries(const DistillArgs& a, int64_t row, int lane, void* ids, void* logits) {
   const int half = a.tdt != zr::DT_F32;
   for (int k = lane; k < a.K; k += 32) {
@@ -242,7 +242,8 @@ __device__ __forceinline__ void ask_for_entries(const DistillArgs& a, int64_t ro
       zr::copy8(zr::smem_u32(static_cast<int64_t*>(ids) + k), static_cast<const int64_t*>(a.ids) + at);
     else
       zr::copy4(zr::smem_u32(static_cast<int32_t*>(ids) + k), static_cast<const int32_t*>(a.ids) + at);
-    zr::copy4(zr::smem_u32(static_cast<uint32_t*>(logits) + k), static_cast<const uint32_t*>(a.teacher) + (at >> half));
+    zr::copy_of<4>(zr::smem_u32(static_cast<uint32_t*>(logits) + k), static_cast<const uint32_t*>(a.teacher) + (at >> half),
+                   half && k == a.K - 1 && !(at & 1) ? 2 : 4);
   }
 }
 __device__ __forceinline__ float teacher_logit(const DistillArgs& a, int64_t row, int k, uint32_t w) {
