@@ -583,7 +583,10 @@ zr_status zr_mx4_matmul(const void* a, int64_t M, const void* b, int64_t N, int6
  * take one launch that reads the weights once, and xq may be NULL; more of them need xq, a
  * device buffer of zr_mx4_bytes(M, K), which then holds MX4(x). (Rows of more than about
  * 170,000 columns need it for few tokens, too; where it is given it is also used for several tokens
- * of many outputs, which quantises them once instead of once in each block.)
+ * of many outputs, which quantises them once instead of once in each block. Up to ZR_MX4_FEW tokens it
+ * is a workspace: whether it holds anything after the call depends on the sizes and the GPU.) Few
+ * tokens off 16-byte boundaries are read as the 16-byte words that hold them, up to 14 bytes behind
+ * the last one with it.
  * Errors: as the two calls; ZR_ERR_INVALID for a missing xq. */
 zr_status zr_mx4_linear(const void* x, zr_dtype xdt, int64_t M, int64_t ldx, const void* w, int64_t N, int64_t K,
                         void* out, zr_dtype dt, int64_t ldo, void* xq, void* stream);

@@ -706,7 +706,7 @@ def mx4_matmul(a: Mx4, b: Mx4, out, stream=None) -> None:
 
 def mx4_linear(x, w: Mx4, out, xq: Optional[Mx4] = None, stream=None) -> None:
     """out[M, N] = x[M, K] w[N, K]^T with x quantised in the call (zr_mx4_linear); more than MX4_FEW tokens need xq,
-    a buffer for the quantised x."""
+    a buffer that holds the quantised x then (for fewer it is a workspace, whose contents say nothing)."""
     fn = _fns.get("zr_mx4_linear") or _fn("zr_mx4_linear")
     p, rows, k, ldx, xdt, x_device = _matrix(x, "x")
     o, m, n, ldo, dt, device = _matrix(out, "out")
