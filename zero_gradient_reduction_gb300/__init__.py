@@ -678,9 +678,11 @@ def mx4_quantize(x, q: Optional[Mx4] = None, q_t: Optional[Mx4] = None, rand=Non
     if rand is not None:
         if rand.element_size() != 1 or rand.shape != x.shape or not rand.is_cuda:
             _refuse("mx4_quantize: rand must be bytes of x's shape in device memory")
-        if not rand.is_contiguous():
-            _refuse("mx4_quantize: rand must be contiguous")
-        rp, ldr = rand.data_ptr(), cols
+        rp, (ldr, step) = rand.data_ptr(), rand.stride()
+        if step != 1 and cols > 1:
+            _refuse("mx4_quantize: the rows of rand must be contiguous")
+        if rows <= 1:  # (as in _matrix)
+            ldr = cols
     s = _stream_of(stream, device, q.device if q is not None else device, q_t.device if q_t is not None else device,
                    rand.get_device() if rand is not None else device)
     _check(fn(p, dt, rows, cols, ld, rp, ldr, q and q.ptr, q_t and q_t.ptr, s))
@@ -735,8 +737,9 @@ def distill_topk(logits, ids, teacher, loss, grad=None, weight=None, temperature
         _refuse("distill_topk: ids must be int32 or int64 of teacher's shape in device memory")
     if trows != rows:
         _refuse(f"distill_topk: {rows} rows of logits, {trows} of the teacher")
-    if not ids.is_contiguous() or ldk != top:
-        _refuse("distill_topk: ids and teacher must be contiguous")
+    ld, step = ids.stride()
+    if (step != 1 and top > 1) or (ld != ldk and rows > 1):
+        _refuse("distill_topk: the rows of ids must be contiguous, and as far apart as teacher's")
     for name, v in (("loss", loss), ("weight", weight)):
         if v is not None and (v.dtype != torch.float32 or v.numel() != rows or not v.is_contiguous() or not v.is_cuda):
             _refuse(f"distill_topk: {name} must be fp32 [{rows}] in device memory")
