@@ -122,3 +122,10 @@ def test_a_matrix_in_host_memory():
         zr.Mx4(4, 64, device="cpu")
     with pytest.raises(zr.ZrError):
         mx4(4, 64, device=-1)
+
+
+def test_no_loss(calls):
+    fn, makers = operands("distill")
+    with pytest.raises(zr.ZrError) as e:
+        fn(**{**{k: make(0) for k, make in makers.items()}, "loss": None})
+    assert e.value.status == 1 and not calls

@@ -740,6 +740,8 @@ def distill_topk(logits, ids, teacher, loss, grad=None, weight=None, temperature
     ld, step = ids.stride()
     if (step != 1 and top > 1) or (ld != ldk and rows > 1):
         _refuse("distill_topk: the rows of ids must be contiguous, and as far apart as teacher's")
+    if loss is None:
+        _refuse("distill_topk: no loss given")
     for name, v in (("loss", loss), ("weight", weight)):
         if v is not None and (v.dtype != torch.float32 or v.numel() != rows or not v.is_contiguous() or not v.is_cuda):
             _refuse(f"distill_topk: {name} must be fp32 [{rows}] in device memory")
