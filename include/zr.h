@@ -54,7 +54,7 @@ typedef enum {
     ZR_ERR_UNSUPPORTED = 2, /* valid request the library does not handle */
     ZR_ERR_CUDA = 3,        /* a CUDA runtime call failed */
     ZR_ERR_OOM = 4,         /* the library could not allocate its own small buffers */
-    ZR_ERR_TIMEOUT = 5      /* reserved: no call waits on the device without a bound */
+    ZR_ERR_TIMEOUT = 5      /* a kernel's bounded wait ran out */
 } zr_status;
 
 typedef enum { ZR_F16 = 0, ZR_BF16 = 1, ZR_F32 = 2 } zr_dtype;
@@ -533,7 +533,10 @@ zr_status zr_step_noalloc(const zr_bucket* buckets, int nbuckets, int W, int A, 
  *   then the scale byte of (r, j) at (j/4)*512 + (r % 32)*16 + (r/32)*4 + j % 4.
  * Rows and columns past the matrix hold zero codes and finite scales; zr_mx4_quantize writes
  * whole tiles. In memory nothing else belongs to the matrix, so it can be kept, copied and
- * saved as those bytes. */
+ * saved as those bytes.
+ *
+ * Every pointer that the calls of this section take to device memory begins on a 16-byte boundary
+ * (ids, weights and losses, too); row strides may be any that a row fits in. */
 #define ZR_MX4_FEW 16 /* tokens up to which zr_mx4_linear needs no buffer for them */
 
 /* Bytes of a rows x cols MX4 matrix (0 for an empty one, -1 for a negative size). */
@@ -569,8 +572,11 @@ zr_status zr_mx4_dequantize(const void* q, int64_t rows, int64_t cols, void* out
  * stride ldo. Products and sums in fp32 on the tensor cores, one rounding to dt. K == 0
  * gives zeros. The three products of a linear layer y = x W^T are
  * (x, W), then dx = (dy, W transposed) and dW = (dy transposed, x transposed).
- * Every wait in the kernel is bounded (2 s); one that gives up leaves out undefined and is
- * reported by zr_mx4_status. The first call on a device sets kernel attributes there; make it
+ * Every wait of the kernel for its copies, products and results is bounded: 2 s, which begin after
+ * the launch before it has ended; one that gives up leaves out undefined and is reported by
+ * zr_mx4_status. What else its blocks wait for has no clock and ends with what it waits for: the
+ * launch before, the blocks of a cluster, whose own waits are bounded, and tensor memory that a
+ * block of another kernel on the same multiprocessor holds. The first call on a device sets kernel attributes there; make it
  * before any stream capture.
  * Errors: ZR_ERR_INVALID for a bad dtype, negative sizes, ldo under N, null or misaligned
  * pointers; ZR_ERR_UNSUPPORTED past 2^30 output tiles. */
@@ -617,8 +623,8 @@ zr_status zr_mx4_stall_waits(int on);
  * An entry with a negative id, or with a teacher logit of -inf, is not kept. A row without
  * weight or without kept entries has loss 0 and gradient 0, whatever its logits hold. Logits
  * of -inf have q = 0. A row with NaN or +inf among its logits or its kept entries, with every
- * logit -inf, or with an id >= V has loss NaN and gradient NaN in every column. An id may stand
- * more than once in a row.
+ * logit -inf, or with an id >= V (an entry's of -inf, too) has loss NaN and gradient NaN in every
+ * column. An id may stand more than once in a row.
  * logits: device, T x V of type dt, row stride ldz; ids: device, T x K of int32 (int64 with
  * ids64), teacher: device, T x K of type teacher_dt, both with row stride ldk; weight: device
  * fp32[T] or NULL (all 1); loss: device fp32[T]; grad: device, T x V of type dt with row stride

@@ -44,3 +44,17 @@ def test_whole_rows(T, V, dtype, in_place):
     if not in_place:
         zr.distill_topk(z, ids, teacher, alone, weight=weight)
         assert torch.equal(torch.isnan(alone), want)
+
+
+def test_an_id_past_the_vocabulary_counts_without_being_kept():
+    """An entry of -inf is not kept, but its id has to be one; in a row with nothing kept no id is looked at."""
+    z, ids, teacher, weight = case(4, 130, 5, F32, seed=3)
+    weight[:] = 1.0
+    ids = ids.clamp(min=0)
+    ids[1, 2], teacher[1, 2] = 130, -float("inf")
+    ids[2, 2], teacher[2] = 130, -float("inf")
+    loss, grad = torch.empty(4, device="cuda"), torch.empty_like(z)
+    zr.distill_topk(z, ids, teacher, loss, grad, weight=weight)
+    assert torch.equal(torch.isnan(loss).cpu(), torch.arange(4) == 1)
+    assert torch.equal(torch.isnan(grad).all(1).cpu(), torch.arange(4) == 1)
+    assert float(loss[2]) == 0 and bool((grad[2] == 0).all())

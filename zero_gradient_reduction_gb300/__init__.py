@@ -728,7 +728,8 @@ def mx4_status(stream=None) -> None:
 def distill_topk(logits, ids, teacher, loss, grad=None, weight=None, temperature: float = 1.0,
                  grad_scale: float = 1.0, plan: Optional[Plan] = None, stream=None) -> None:
     """The distillation loss of each row against a teacher's top logits, and its gradient times grad_scale and the
-    plan's loss scale (zr_distill_topk). `grad` may be `logits`."""
+    plan's loss scale (zr_distill_topk). `grad` may be `logits`; `ids` and `teacher` may be the first columns of wider
+    ones, as far apart."""
     import torch
     fn = _fns.get("zr_distill_topk") or _fn("zr_distill_topk")
     z, rows, vocab, ldz, dt, device = _matrix(logits, "logits")

@@ -6,11 +6,15 @@
 // read, and their scales already in the order that one copy takes to tensor memory. Products
 // accumulate in fp32.
 //
-// Measured: pairs of blocks 8192^3 to bf16 in 139 us (7.9 PFLOP/s; the products' own rate, issued
-// without a pause, is 9.9), 8192 x 50304 x 2048 in 248 us (6.8); there the tensor pipe is active 72 %
-// of the time and shared memory, which the copies write and the products read, is what is nearest to
-// its limit: 84 KB a stage at 128 bytes a cycle are 656 cycles of the 750 that a stage takes. Blocks
-// alone 2304 x 768 x 777 to fp32 in 5.6 us, of which 1.1 us until the first stage has landed and 1.5 us
+// Measured: pairs of blocks 8192^3 to bf16 in 146 us (7.5 PFLOP/s; the products' own rate, issued
+// without a pause, is 9.9 in steps of K = 64, the ones used here), 8192 x 50304 x 2048 in 253 us (6.7).
+// Both are bursts; back to back for seconds the power limit lowers the clock, to 1.67 GHz for the
+// latter, which takes 281 us then. There the tensor pipe is active 72 % of the cycles, and counters say
+// that shared memory is not what the rest waits for: of a stage's 712 cycles the tensor cores' reads
+// take 280 (16 KB of A, 16 KB of B, of which a pair's block holds half, and 3 KB of scales), and the
+// banks are at 24 % of their rate for reads and at 24 % for writes. What it is has not been settled; the
+// scales' copies, to columns that the stage before still reads, cannot overlap its products. Blocks
+// alone 2304 x 768 x 777 to fp32 in 5.1 us, of which 1.1 us until the first stage has landed and 1.5 us
 // for the results. Few tokens: 1 x 2048 by 8192 x 2048 in 5.2 us, 8 x 2048 by 50304 x 2048 in 12.7 us,
 // 4.3 TB/s. (K = 2048 with A's rows kept in shared memory for a run of tiles read half as much and
 // was no faster, 294 us: its ring of 4 stages no longer covered a copy's latency.)

@@ -5,7 +5,7 @@
 // patch to shared memory by asynchronous copies and lets each thread take whole blocks of 32 from
 // there, along the rows and then along the columns, so that no scale needs a reduction between
 // threads. To nearest it is bound by memory: fp32 50304 x 2048 both ways in 80 us, 6.5 TB/s of the
-// 6.8 that a copy reaches. By chance, with a random byte more per value, the rounding's whole-number
+// 6.7 that a copy reaches. By chance, with a random byte more per value, the rounding's whole-number
 // steps bind it: bf16 8192 x 8192 both ways in 64 us, 4.3 TB/s with the integer pipe at 75 %.
 // Dequantising bf16 50304 x 2048 takes 39 us, 6.7 TB/s; with rows of odd length 4099 x 2049 in
 // 7.0 us, 3.0 TB/s, where 4096 x 2048 takes 3.9.
