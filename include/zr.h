@@ -539,7 +539,7 @@ zr_status zr_step_noalloc(const zr_bucket* buckets, int nbuckets, int W, int A, 
  * (ids, weights and losses, too); row strides may be any that a row fits in. */
 #define ZR_MX4_FEW 16 /* tokens up to which zr_mx4_linear needs no buffer for them */
 
-/* Bytes of a rows x cols MX4 matrix (0 for an empty one, -1 for a negative size). */
+/* Bytes of a rows x cols MX4 matrix (0 for an empty one, -1 for a negative size or more than 2^63). */
 int64_t zr_mx4_bytes(int64_t rows, int64_t cols);
 
 /* Quantises x (device, rows x cols of type dt, row stride ldx elements) to q, blocks along
@@ -564,7 +564,7 @@ zr_status zr_mx4_quantize(const void* x, zr_dtype dt, int64_t rows, int64_t cols
  * (but for 2^128, to which the largest fp32 values may be rounded by chance: infinite); in
  * F16 values past its range become infinite. out: device, rows x cols, row stride ld.
  * Errors: ZR_ERR_INVALID for a bad dtype, negative sizes, ld under cols, null or misaligned
- * pointers. */
+ * pointers; ZR_ERR_UNSUPPORTED past 2^31 pieces of 32 x 256. */
 zr_status zr_mx4_dequantize(const void* q, int64_t rows, int64_t cols, void* out, zr_dtype dt, int64_t ld,
                             void* stream);
 

@@ -27,7 +27,8 @@ constexpr int kMxCodeBytes = kMxRows * kMxCols / 2;      // 16384
 constexpr int kMxScaleBytes = kMxRows * kMxCols / 32;    // 1024
 constexpr int kMxTileBytes = kMxCodeBytes + kMxScaleBytes;
 
-__host__ __device__ inline int64_t mx_tiles(int64_t n, int per) { return (n + per - 1) / per; }
+// (No sum that could pass 63 bits.)
+__host__ __device__ inline int64_t mx_tiles(int64_t n, int per) { return n / per + (n % per != 0); }
 
 // Offset of the 16-byte chunk of (row in tile, block of 32 columns in tile) in its tile.
 __device__ __forceinline__ int mx_chunk_at(int r, int j) { return r * 128 + ((j ^ (r & 7)) << 4); }

@@ -10,7 +10,7 @@
 // without a pause, is 9.9 in steps of K = 64, the ones used here), 8192 x 50304 x 2048 in 253 us (6.7).
 // Both are bursts; back to back for seconds the power limit lowers the clock, to 1.67 GHz for the
 // latter, which takes 281 us then. There the tensor pipe is active 72 % of the cycles, and counters say
-// that shared memory is not what the rest waits for: of a stage's 712 cycles the tensor cores' reads
+// that shared memory is not what the rest waits for: of a stage's 707 cycles the tensor cores' reads
 // take 280 (16 KB of A, 16 KB of B, of which a pair's block holds half, and 3 KB of scales), and the
 // banks are at 24 % of their rate for reads and at 24 % for writes. What it is has not been settled; the
 // scales' copies, to columns that the stage before still reads, cannot overlap its products. Blocks

@@ -463,7 +463,9 @@ zr_status launch_quant(const QuantArgs& a, int64_t patches, cudaStream_t s) {
 
 extern "C" int64_t zr_mx4_bytes(int64_t rows, int64_t cols) {
   if (rows < 0 || cols < 0) return -1;
-  return zr::mx_tiles(rows, zr::kMxRows) * zr::mx_tiles(cols, zr::kMxCols) * zr::kMxTileBytes;
+  const int64_t down = zr::mx_tiles(rows, zr::kMxRows), over = zr::mx_tiles(cols, zr::kMxCols);
+  if (over > 0 && down > INT64_MAX / zr::kMxTileBytes / over) return -1;
+  return down * over * zr::kMxTileBytes;
 }
 
 extern "C" zr_status zr_mx4_quantize(const void* x, zr_dtype dt, int64_t rows, int64_t cols, int64_t ldx,
@@ -491,8 +493,8 @@ extern "C" zr_status zr_mx4_quantize(const void* x, zr_dtype dt, int64_t rows, i
   const int64_t row128 = 2 * zr::mx_tiles(rows, 128), col128 = zr::mx_tiles(cols, kCols);
   const int64_t row_patches = qt ? 4 * a.qt_tiles : row128;
   a.col_patches = q ? 2 * a.q_tiles : col128;
+  if (row_patches > 0x7FFFFFFF / a.col_patches) return fail(ZR_ERR_UNSUPPORTED, "zr_mx4_quantize: matrix too large for one launch");
   const int64_t patches = row_patches * a.col_patches;
-  if (patches > 0x7FFFFFFF) return fail(ZR_ERR_UNSUPPORTED, "zr_mx4_quantize: matrix too large for one launch");
   a.q_row_patches = (int)row128;
   a.qt_col_patches = (int)col128;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -522,8 +524,10 @@ extern "C" zr_status zr_mx4_dequantize(const void* q, int64_t rows, int64_t cols
   a.out = out;
   a.rows = rows; a.cols = cols; a.ld = ld;
   a.tiles = zr::mx_tiles(cols, zr::kMxCols);
-  const int64_t blocks = zr::mx_tiles(rows, zr::kMxRows) * a.tiles * (zr::kMxRows / kDequantRows);
-  if (blocks > 0x7FFFFFFF) return fail(ZR_ERR_UNSUPPORTED, "zr_mx4_dequantize: matrix too large for one launch");
+  const int64_t row_blocks = zr::mx_tiles(rows, zr::kMxRows) * (zr::kMxRows / kDequantRows);
+  if (row_blocks > 0x7FFFFFFF / a.tiles)
+    return fail(ZR_ERR_UNSUPPORTED, "zr_mx4_dequantize: matrix too large for one launch");
+  const int64_t blocks = row_blocks * a.tiles;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool aligned = ld * (dt == ZR_F32 ? 4 : 2) % 16 == 0;
   const cudaError_t e = dt == ZR_F16    ? launch_dequant<zr::DT_F16>(a, blocks, aligned, s)
