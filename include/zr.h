@@ -639,6 +639,79 @@ zr_status zr_distill_topk(const void* logits, zr_dtype dt, int64_t T, int64_t V,
                           void* grad, int64_t ldg, void* stream);
 
 /* ------------------------------------------------------------------------- */
+/* Post-training: log-probabilities, policy and preference losses              */
+/* ------------------------------------------------------------------------- */
+
+/* Losses of a model that is trained from rewards or preferences, taken from its logits as
+ * zr_distill_topk takes them: forward and backward in one call, the gradient in the logits' type
+ * under the plan's loss scale, ready for backward and the ring. With z a row of V logits,
+ * q = softmax(z / temperature) and a = ids[t] the row's chosen column,
+ *   logp[t] = log q_a.
+ * Sums are fp32, relative to the row's maximum; 1 - q_a and a logp near 0 are taken from the sum of
+ * the other columns, so that an almost certain token keeps its accuracy. A row of which a is
+ * negative is not scored and not read (a prompt's, padding). Logits of -inf have q = 0; chosen,
+ * logp = -inf. A row with NaN or +inf among its logits, with every logit -inf or with a >= V has
+ * logp NaN.
+ * For every call of this section: logits are device, T x V of type dt, row stride ldz, beginning
+ * on a 16-byte boundary, as a gradient does (T x V, row stride ldg; the logits themselves, with
+ * ldg = ldz, or apart from them; NULL for the loss alone); ids: device int32[T] (int64 with ids64);
+ * other arrays are device memory and begin on a boundary of their type. grad_scale is multiplied
+ * by the plan's current loss scale (plan NULL: alone), read on the device, so that a captured
+ * graph follows it. Errors of each: ZR_ERR_INVALID for a bad dtype, T < 0, V outside
+ * [1, 2^31 - 256], a row stride under its row, a temperature outside [1e-6, 1e6], a number that is not
+ * finite where one is needed, null or misaligned pointers, a gradient that overlaps the logits without being
+ * them; ZR_ERR_UNSUPPORTED for more rows than a launch takes (2^31 / 8 are always taken). */
+
+/* logp: device fp32[T], 0 in rows that are not scored. entropy: device fp32[T] or NULL, the
+ * entropy -sum q log q of each scored row, NaN where the row has no answer (a masked choice has one).
+ * One read of the scored rows. */
+zr_status zr_token_logprobs(const void* logits, zr_dtype dt, int64_t T, int64_t V, int64_t ldz, const void* ids,
+                            int ids64, float temperature, float* logp, float* entropy, void* stream);
+
+/* The clipped policy loss with a KL term, of each token, and its gradient. With
+ * r = exp(logp - old_logp[t]), A = advantage[t], d = ref_logp[t] - logp:
+ *   loss[t] = weight[t] (-min(r A, clamp(r, 1 - clip_low, 1 + clip_high) A) + kl (exp(d) - d - 1))
+ *   grad[t][v] = s f_t (1[v = a] - q_v) / temperature,  f_t = dloss[t] / dlogp, s = grad_scale and plan
+ * where the clamped product is the smaller one it adds nothing to f_t; where both are equal r's
+ * does. old_logp, advantage, loss: fp32[T]; weight: fp32[T] or NULL (all 1); ref_logp: fp32[T], NULL
+ * only with kl = 0, and not read then; logp: fp32[T] or NULL, written. A row that is not scored,
+ * or has weight 0, has loss, logp and gradient 0, whatever its logits hold; where logp is NaN so
+ * are the loss and every column of the gradient. A loss or factor that overflows fp32 (an
+ * old_logp of -inf) gives what the formulas give, infinities and NaN.
+ * Errors besides: ZR_ERR_INVALID for clip_low outside [0, 1] or clip_high outside [0, 1e30]. */
+zr_status zr_policy_loss(const void* logits, zr_dtype dt, int64_t T, int64_t V, int64_t ldz, const void* ids, int ids64,
+                         const float* old_logp, const float* advantage, const float* weight, float clip_low,
+                         float clip_high, const float* ref_logp, float kl, float temperature, float grad_scale,
+                         const zr_plan* plan, float* loss, float* logp, void* grad, int64_t ldg, void* stream);
+
+/* Device bytes of a preference loss's workspace (-1 for sizes that it does not take). */
+int64_t zr_preference_bytes(int64_t T, int64_t pairs);
+
+/* The loss of pairs of sequences by their log-probability ratios, and its gradient. Sequence s
+ * has the rows starts[s] to starts[s + 1] - 1; pair i prefers sequence 2i to 2i + 1. With the sums over a
+ * sequence's scored rows and the logistic function S:
+ *   rewards[s] = beta sum (logp[t] - ref_logp[t]),  m = rewards[2i] - rewards[2i + 1]
+ *   loss[i] = -weight[i] ((1 - smoothing) log S(m) + smoothing log S(-m))
+ * and in a scored row of the pair, with f = dloss[i] / dlogp (beta dloss[i] / dm, negative for 2i + 1),
+ *   grad[t][v] = s f (1[v = a] - q_v) / temperature,  s = grad_scale and plan.
+ * starts: device int32[2 pairs + 1] (int64 with starts64), ascending within [0, T]; a sequence may
+ * be empty, its reward is 0. Rows before the first sequence and behind the last are left as they are, in
+ * the gradient too. A pair whose own starts do not ascend within [0, T] has loss and rewards NaN; if
+ * any do not, the gradient says nothing, but no call reads or writes outside the arrays.
+ * ref_logp: fp32[T]; weight: fp32[pairs] or NULL (all 1); loss: fp32[pairs]; rewards:
+ * fp32[2 pairs] or NULL, written. Rows that are not scored have gradient 0. A pair of weight 0 has loss,
+ * rewards and gradients 0, and its rows are not read. Where a scored row's logp is NaN so are
+ * its sequence's reward, the pair's loss and all gradients of its scored rows.
+ * work: zr_preference_bytes of device memory beginning on a 16-byte boundary, overwritten; calls (and
+ * graphs) that may run at the same time need one each.
+ * Errors besides: ZR_ERR_INVALID for pairs < 0, smoothing outside [0, 1]. */
+zr_status zr_preference_loss(const void* logits, zr_dtype dt, int64_t T, int64_t V, int64_t ldz, const void* ids,
+                             int ids64, const void* starts, int starts64, int64_t pairs, const float* ref_logp,
+                             const float* weight, float beta, float smoothing, float temperature, float grad_scale,
+                             const zr_plan* plan, float* loss, float* rewards, void* grad, int64_t ldg, void* work,
+                             void* stream);
+
+/* ------------------------------------------------------------------------- */
 /* Accounting                                                                 */
 /* ------------------------------------------------------------------------- */
 

@@ -139,6 +139,13 @@ def lib():
                 "zr_mx4_stall_waits": (st, [i32]),
                 "zr_distill_topk": (st, [vp, i32, i64, i64, i64, vp, i32, vp, i32, i32, i64, vp, ctypes.c_float,
                                          ctypes.c_float, vp, vp, vp, i64, vp]),
+                "zr_token_logprobs": (st, [vp, i32, i64, i64, i64, vp, i32, ctypes.c_float, vp, vp, vp]),
+                "zr_policy_loss": (st, [vp, i32, i64, i64, i64, vp, i32, vp, vp, vp, ctypes.c_float, ctypes.c_float, vp,
+                                        ctypes.c_float, ctypes.c_float, ctypes.c_float, vp, vp, vp, vp, i64, vp]),
+                "zr_preference_bytes": (i64, [i64, i64]),
+                "zr_preference_loss": (st, [vp, i32, i64, i64, i64, vp, i32, vp, i32, i64, vp, vp, ctypes.c_float,
+                                            ctypes.c_float, ctypes.c_float, ctypes.c_float, vp, vp, vp, vp, i64, vp,
+                                            vp]),
                 "zr_model_state_bytes": (i64, [i32, i64, i32]),
                 "zr_ring_traffic": (st, [i64, i32, i32, vp, vp, vp, vp]),
                 "zr_status_str": (ctypes.c_char_p, [st]),
@@ -607,6 +614,7 @@ _types = {}
 def _fn(name: str):
     import torch
     _types.update({torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32})
+    _fns.update(f32=torch.float32, i32=torch.int32, i64=torch.int64)
     _fns.setdefault("stream", getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda device: torch.cuda.current_stream(device).cuda_stream))
     _fns.setdefault("device", getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device)
@@ -758,8 +766,104 @@ def distill_topk(logits, ids, teacher, loss, grad=None, weight=None, temperature
               plan.handle if plan is not None else None, loss.data_ptr(), g, ldg, s))
 
 
+# ----------------------------------------------------------------------------- post-training losses
+def _vector(t, what: str, n: int, device: int):
+    """The pointer of a contiguous fp32 vector of n values on the matrix's device, None for None."""
+    if t is None:
+        return None
+    if t.dtype is not _fns["f32"] or t.numel() != n or not t.is_contiguous() or not t.is_cuda:
+        _refuse(f"{what} must be fp32 [{n}] in device memory")
+    if t.get_device() != device:
+        _refuse(f"{what} on device {t.get_device()}, the matrix on {device}")
+    return t.data_ptr()
+
+
+def _whole(t, what: str, n: int, device: int):
+    """(pointer, whether of 64 bits) of a contiguous vector of n whole numbers on the matrix's device."""
+    wide = t.dtype is _fns["i64"]
+    if not (wide or t.dtype is _fns["i32"]) or t.numel() != n or not t.is_contiguous() or not t.is_cuda:
+        _refuse(f"{what} must be int32 or int64 [{n}] in device memory")
+    if t.get_device() != device:
+        _refuse(f"{what} on device {t.get_device()}, the matrix on {device}")
+    return t.data_ptr(), int(wide)
+
+
+def _gradient(grad, logits, what: str):
+    """(pointer, row stride, device) of a gradient like the logits."""
+    if grad.dtype is not logits.dtype or grad.shape != logits.shape:
+        _refuse(f"{what}: grad must have the logits' type and shape")
+    g, _, _, ldg, _, device = _matrix(grad, "grad")
+    return g, ldg, device
+
+
+def token_logprobs(logits, ids, logp, entropy=None, temperature: float = 1.0, stream=None) -> None:
+    """logp = the log-probability of each row's column ids[t] under softmax(logits / temperature), 0 where it is
+    negative; `entropy` of each scored row on request (zr_token_logprobs)."""
+    fn = _fns.get("zr_token_logprobs") or _fn("zr_token_logprobs")
+    z, rows, vocab, ldz, dt, device = _matrix(logits, "logits")
+    i, wide = _whole(ids, "token_logprobs: ids", rows, device)
+    if logp is None:
+        _refuse("token_logprobs: no logp given")
+    lp, h = _vector(logp, "token_logprobs: logp", rows, device), _vector(entropy, "token_logprobs: entropy", rows, device)
+    _check(fn(z, dt, rows, vocab, ldz, i, wide, temperature, lp, h, _stream_of(stream, device)))
+
+
+def policy_loss(logits, ids, old_logp, advantage, loss, grad=None, weight=None, clip=(0.2, 0.2), ref_logp=None,
+                kl: float = 0.0, logp=None, temperature: float = 1.0, grad_scale: float = 1.0,
+                plan: Optional[Plan] = None, stream=None) -> None:
+    """The clipped policy loss of each token with kl times a KL term against ref_logp, and its gradient at the logits
+    times grad_scale and the plan's loss scale (zr_policy_loss). `clip`: how far under and over 1 the ratio to
+    old_logp counts; `grad` may be `logits`; `logp` receives the tokens' log-probabilities."""
+    fn = _fns.get("zr_policy_loss") or _fn("zr_policy_loss")
+    z, rows, vocab, ldz, dt, device = _matrix(logits, "logits")
+    i, wide = _whole(ids, "policy_loss: ids", rows, device)
+    if old_logp is None or advantage is None or loss is None:
+        _refuse("policy_loss: old_logp, advantage and loss are needed")
+    old, adv, out, w, ref, lp = [_vector(v, name, rows, device) for v, name in (
+        (old_logp, "policy_loss: old_logp"), (advantage, "policy_loss: advantage"), (loss, "policy_loss: loss"),
+        (weight, "policy_loss: weight"), (ref_logp, "policy_loss: ref_logp"), (logp, "policy_loss: logp"))]
+    low, high = clip
+    g, ldg, g_device = (None, 0, device) if grad is None else _gradient(grad, logits, "policy_loss")
+    s = _stream_of(stream, device, g_device, plan.device if plan is not None else device)
+    _check(fn(z, dt, rows, vocab, ldz, i, wide, old, adv, w, low, high, ref, kl, temperature, grad_scale,
+              plan.handle if plan is not None else None, out, lp, g, ldg, s))
+
+
+def preference_bytes(tokens: int, pairs: int) -> int:
+    """Device bytes of the workspace that preference_loss needs (zr_preference_bytes)."""
+    return int(lib().zr_preference_bytes(int(tokens), int(pairs)))
+
+
+def preference_loss(logits, ids, starts, ref_logp, loss, work, grad=None, weight=None, beta: float = 0.1,
+                    smoothing: float = 0.0, rewards=None, temperature: float = 1.0, grad_scale: float = 1.0,
+                    plan: Optional[Plan] = None, stream=None) -> None:
+    """The loss of each pair of sequences by beta times their log-probability ratios to ref_logp, and its gradient at
+    the logits times grad_scale and the plan's loss scale (zr_preference_loss). Sequence s has the rows starts[s] to
+    starts[s + 1] - 1, pair i prefers sequence 2 i to 2 i + 1; `work`: preference_bytes bytes, the call's own while it
+    runs; `grad` may be `logits`; `rewards` receives each sequence's reward."""
+    fn = _fns.get("zr_preference_loss") or _fn("zr_preference_loss")
+    z, rows, vocab, ldz, dt, device = _matrix(logits, "logits")
+    i, wide = _whole(ids, "preference_loss: ids", rows, device)
+    if ref_logp is None or loss is None:
+        _refuse("preference_loss: ref_logp and loss are needed")
+    pairs = loss.numel()
+    at, wide_starts = _whole(starts, "preference_loss: starts", 2 * pairs + 1, device)
+    ref = _vector(ref_logp, "preference_loss: ref_logp", rows, device)
+    out, w, r = [_vector(v, name, n, device) for v, name, n in (
+        (loss, "preference_loss: loss", pairs), (weight, "preference_loss: weight", pairs),
+        (rewards, "preference_loss: rewards", 2 * pairs))]
+    need = preference_bytes(rows, pairs)
+    if work.element_size() != 1 or work.numel() < need or not work.is_cuda or not work.is_contiguous():
+        _refuse(f"preference_loss: work must be {need} contiguous bytes in device memory")
+    g, ldg, g_device = (None, 0, device) if grad is None else _gradient(grad, logits, "preference_loss")
+    s = _stream_of(stream, device, work.get_device(), g_device, plan.device if plan is not None else device)
+    _check(fn(z, dt, rows, vocab, ldz, i, wide, at, wide_starts, pairs, ref, w, beta, smoothing, temperature, grad_scale,
+              plan.handle if plan is not None else None, out, r, g, ldg, work.data_ptr(), s))
+
+
 __all__ = ["lib", "ZrError", "chunk_size", "bucket_plan", "model_state_bytes", "ring_traffic", "reduce_scatter",
            "all_reduce", "adamw_shard_step", "accumulate", "offload_adamw", "all_gather", "AdamW", "Scaler",
            "State", "State1", "Plan", "step_noalloc", "F16", "BF16", "F32", "STAGING_REGISTERS", "STAGING_BULK",
            "STAGING_BULK_IO", "Mx4", "mx4_bytes", "mx4_quantize", "mx4_dequantize", "mx4_matmul", "mx4_linear",
-           "mx4_status", "distill_topk", "MX4_FEW", "DISTILL_MAX_TOP"]
+           "mx4_status", "distill_topk", "MX4_FEW", "DISTILL_MAX_TOP", "token_logprobs", "policy_loss", "preference_loss",
+           "preference_bytes"]
