@@ -62,7 +62,8 @@ __global__ void __launch_bounds__(384, 4) logprob_kernel(const __grid_constant__
     all = zr::rebased<ENTROPY>(all, fmaxf(all.m, z_chosen), a.scale);
     const zr::Base base(all.m, a.scale);
     const float rest = ENTROPY ? all.trimmed(a.scale) : all.sum;
-    a.logp[row] = id < a.V ? zr::log_chosen<!ENTROPY>(z_chosen, rest, base, a.scale) : NAN;
+    const zr::Pair logp = zr::log_chosen<!ENTROPY>(z_chosen, rest, base, a.scale);
+    a.logp[row] = id < a.V ? logp.value + logp.rest : NAN;
     if (ENTROPY) {
       zr::add_term<false, true>(all, base, a.scale, z_chosen);
       a.entropy[row] = id < a.V ? __fmul_rn(zr::kLn2, log2f(all.sum) - __fdiv_rn(all.ex, all.sum)) : NAN;
@@ -169,7 +170,8 @@ __global__ void __launch_bounds__(1024) policy_kernel(const __grid_constant__ Po
   rest = zr::rebased<false>(rest, fmaxf(rest.m, z_chosen), a.scale);
   const zr::Base base(rest.m, a.scale);
   const float sum = known ? __fadd_rn(rest.sum, zr::exp2_fast(base.exponent<false>(z_chosen, a.scale))) : NAN;
-  const float logp = known ? zr::log_chosen<false>(z_chosen, rest.sum, base, a.scale) : NAN;
+  const zr::Pair of = zr::log_chosen<false>(z_chosen, rest.sum, base, a.scale);
+  const float logp = known ? of.value + of.rest : NAN;
   const float ratio = expf(logp - old_logp), free = __fmul_rn(ratio, advantage);
   const float bound = __fmul_rn(fminf(fmaxf(ratio, a.low), a.high), advantage);
   const bool clipped = free > bound;  // (not where one is no number, which stays so)

@@ -95,7 +95,8 @@ __global__ void __launch_bounds__(384, 4) score_kernel(const __grid_constant__ P
     rest = zr::rebased<false>(rest, fmaxf(rest.m, z_chosen), a.scale);
     const zr::Base base(rest.m, a.scale);
     const float sum = __fadd_rn(rest.sum, zr::exp2_fast(base.exponent<true>(z_chosen, a.scale)));
-    a.ratio[row] = id < a.V ? zr::log_chosen<true>(z_chosen, rest.sum, base, a.scale) - a.ref_logp[row] : NAN;
+    const zr::Pair logp = zr::log_chosen<true>(z_chosen, rest.sum, base, a.scale);
+    a.ratio[row] = id < a.V ? (logp.value - a.ref_logp[row]) + logp.rest : NAN;
     a.sums[row] = RowSum{rest.m, sum, __fdiv_rn(rest.sum, sum), 0.0f};
   }
 }

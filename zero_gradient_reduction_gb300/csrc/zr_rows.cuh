@@ -369,24 +369,59 @@ __device__ __forceinline__ Part join_all(const Part& mine, const Scale& k, Parts
   return all;
 }
 
-// log softmax at the chosen value z from the sum of all other terms. Where the chosen one has most of the
-// sum, the sum's logarithm would keep nothing of the rest. Elsewhere it is z's exponent less the sum's logarithm:
-// of fine exponents z c - M itself, in two words; of others the difference to m, which c's error leaves as it
-// is. ex2.approx gives results that are too small by 5.0e-8 of themselves on average (as measured here over a
-// million arguments in each of eight intervals), which the sum's logarithm gets back.
+// a + b, and what rounding has taken from it.
+struct Pair {
+  float value, rest;
+};
+__device__ __forceinline__ Pair exact_sum(float a, float b) {
+  const float s = a + b, t = s - a;
+  return Pair{s, (a - (s - t)) + (b - t)};
+}
+
+// ln s in two words: with s = 2^k f and t = (f - 1)/(f + 1), k ln 2 + 2 (t + t^3/3 + t^5/5 + ...), of which k ln 2
+// and 2 t are taken to twice 24 bits. One number's last half unit would be much the same for rows of much the
+// same sum.
+constexpr float kLn2Rest = -1.904654323148236e-9f;  // ln 2 less kLn2
+__device__ __forceinline__ Pair log_pair(float s) {
+  if (!(s > 1e-37f)) return Pair{logf(s), 0.0f};
+  const int bits = __float_as_int(s), k = (bits - 0x3F3504F3) >> 23;  // f from about sqrt(1/2) to sqrt(2)
+  const float f = __int_as_float(bits - (k << 23)), n = f - 1.0f;
+  const Pair d = exact_sum(f, 1.0f);
+  const float t = __fdiv_rn(n, d.value), t2 = __fmul_rn(t, t);
+  const float t_rest = __fdiv_rn(__fmaf_rn(-t, d.value, n) - __fmul_rn(t, d.rest), d.value);
+  float series = __fmaf_rn(t2, 2.0f / 11.0f, 2.0f / 9.0f);
+  series = __fmaf_rn(t2, series, 2.0f / 7.0f);
+  series = __fmaf_rn(t2, series, 2.0f / 5.0f);
+  series = __fmaf_rn(t2, series, 2.0f / 3.0f);
+  const float kf = (float)k, a = __fmul_rn(kf, kLn2);
+  const Pair sum = exact_sum(a, 2.0f * t);
+  const float low = __fmaf_rn(kf, kLn2Rest, __fmaf_rn(kf, kLn2, -a)) + 2.0f * t_rest;
+  return Pair{sum.value, sum.rest + (low + __fmul_rn(__fmul_rn(t, t2), series))};
+}
+
+// log softmax at the chosen value z from the sum of all other terms, in two words. Where the chosen one has
+// most of the sum, the sum's logarithm would keep nothing of the rest. Elsewhere it is z's exponent less the
+// sum's logarithm: of fine exponents z c - M itself; of others the difference to m, which c's error leaves as
+// it is. ex2.approx gives results that are too small by 5.0e-8 of themselves on average (as measured here over
+// a million arguments in each of eight intervals), which the sum's logarithm gets back.
 template <bool FINE>
-__device__ __forceinline__ float log_chosen(float z, float rest, const Base& base, const Scale& k) {
+__device__ __forceinline__ Pair log_chosen(float z, float rest, const Base& base, const Scale& k) {
   constexpr float kShort = 5.0e-8f;
   const float e = exp2_fast(base.exponent<FINE>(z, k));
-  if (rest < e) return -log1pf(__fdiv_rn(rest, e));
-  const float log_sum = logf(rest + e);
-  if (!(FINE && base.fine) || !(z > -1e30f))
-    return __fdiv_rn(z - base.m, k.tau) - (log_sum - __fmaf_rn(base.below(k), kLn2, -kShort));
-  const float p = __fmul_rn(z, base.hi), x = p - base.M, back = x - p;
-  const float off = (p - (x - back)) - (base.M + back);  // of that difference
-  const float low = __fmaf_rn(z, base.lo, __fmaf_rn(z, base.hi, -p) + off);
-  const float y = x + low, y_low = low - (y - x);
-  return __fmaf_rn(y, kLn2, -log_sum) + __fmaf_rn(y_low, kLn2, -kShort);
+  if (rest < e) return Pair{-log1pf(__fdiv_rn(rest, e)), 0.0f};
+  const Pair log_sum = log_pair(rest + e);
+  if (!(z > -1e30f)) return Pair{z - log_sum.value, 0.0f};  // masked, or no number
+  const float short_of = log_sum.rest + kShort;
+  if (!(FINE && base.fine)) {
+    const Pair d = exact_sum(__fdiv_rn(z - base.m, k.tau), -log_sum.value);
+    return Pair{d.value, d.rest + __fmaf_rn(base.below(k), kLn2, -short_of)};
+  }
+  const float p = __fmul_rn(z, base.hi);
+  const Pair x = exact_sum(p, -base.M);
+  const Pair y = exact_sum(x.value, __fmaf_rn(z, base.lo, __fmaf_rn(z, base.hi, -p) + x.rest));
+  const float q = __fmul_rn(y.value, kLn2), q_rest = __fmaf_rn(y.value, kLn2, -q);
+  const Pair d = exact_sum(q, -log_sum.value);
+  return Pair{d.value, d.rest + (__fmaf_rn(y.rest, kLn2, __fmaf_rn(y.value, kLn2Rest, q_rest)) - short_of)};
 }
 
 // Column ids of 4 or 8 bytes.
