@@ -597,6 +597,45 @@ zr_status zr_mx4_matmul(const void* a, int64_t M, const void* b, int64_t N, int6
 zr_status zr_mx4_linear(const void* x, zr_dtype xdt, int64_t M, int64_t ldx, const void* w, int64_t N, int64_t K,
                         void* out, zr_dtype dt, int64_t ldo, void* xq, void* stream);
 
+/* What the results s of a product go through before their one rounding (fp32 until then):
+ *   h = s + bias[n],  out = act(h) + residual;  or, with `gradient`,  out = s act'(pre).
+ * act: none, max(h, 0), GELU in its tanh form h/2 (1 + tanh(sqrt(2/pi) (h + 0.044715 h^3))), or
+ * SiLU h / (1 + e^-h); their derivatives, relu's at 0 being 0. The three products of a layer
+ * y = act(x W^T + b) are then zr_mx4_linear_finish with bias, activation and pre (h, kept), in the
+ * layer above zr_mx4_matmul_finish with `gradient` and that pre, which gives the gradient at h,
+ * and a plain product for dW; zr_column_sums gives db.
+ * bias: device, N values of type bias_dtype, or NULL. residual: device, M x N of out's type, row
+ * stride ldr, or NULL; it may be out itself (with ldr = ldo). pre: device, M x N of out's type, row
+ * stride ldp: h, written (or NULL), or with `gradient` read, where it may be out itself. Otherwise out,
+ * pre and residual share no memory; rows as far apart may lie between each other's. All
+ * begin on a 16-byte boundary. Infinities and NaN go where the formulas take them. */
+typedef enum { ZR_ACT_NONE = 0, ZR_ACT_RELU = 1, ZR_ACT_GELU = 2, ZR_ACT_SILU = 3 } zr_activation;
+typedef struct {
+    const void* bias;
+    const void* residual;
+    void* pre;
+    int64_t ldr, ldp;
+    zr_dtype bias_dtype;
+    int32_t activation; /* zr_activation */
+    int32_t gradient;   /* 0, or 1: out = s act'(pre); bias and residual are NULL then */
+} zr_mx4_epilogue;
+
+/* zr_mx4_matmul and zr_mx4_linear with an epilogue (host memory, read during the call; NULL for none).
+ * K == 0 is a sum of nothing, which goes through the epilogue. Errors: theirs, and ZR_ERR_INVALID for an unknown
+ * activation, a bad bias_dtype, a row stride under N, a misaligned pointer, a gradient without pre
+ * or with bias or residual, matrices that overlap. */
+zr_status zr_mx4_matmul_finish(const void* a, int64_t M, const void* b, int64_t N, int64_t K, void* out, zr_dtype dt,
+                               int64_t ldo, const zr_mx4_epilogue* epilogue, void* stream);
+zr_status zr_mx4_linear_finish(const void* x, zr_dtype xdt, int64_t M, int64_t ldx, const void* w, int64_t N, int64_t K,
+                               void* out, zr_dtype dt, int64_t ldo, void* xq, const zr_mx4_epilogue* epilogue,
+                               void* stream);
+
+/* out[n] = sum over m of x[m][n]: a bias's gradient from its layer's output gradient. x: device,
+ * M x N of type dt, row stride ldx; out: device fp32[N]. Sums are fp32, in an order that the sizes decide. M == 0
+ * gives zeros. Errors: ZR_ERR_INVALID for a bad dtype, negative sizes, ldx under N, null or
+ * misaligned pointers (x on a 16-byte boundary, out on one of its type). */
+zr_status zr_column_sums(const void* x, zr_dtype dt, int64_t M, int64_t N, int64_t ldx, float* out, void* stream);
+
 /* Synchronises `stream` and returns ZR_ERR_TIMEOUT if a product on this device, on any stream,
  * gave up a wait since the last call for this stream (since the library was loaded for a stream's
  * first call); the outputs of this stream's products since then may not be valid. ZR_OK otherwise:

@@ -60,6 +60,12 @@ class StateC1(ctypes.Structure):
                 ("param", ctypes.c_void_p)]
 
 
+class Epilogue(ctypes.Structure):  # zr_mx4_epilogue
+    _fields_ = [("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("pre", ctypes.c_void_p),
+                ("ldr", ctypes.c_int64), ("ldp", ctypes.c_int64), ("bias_dtype", ctypes.c_int),
+                ("activation", ctypes.c_int32), ("gradient", ctypes.c_int32)]
+
+
 class Checkpoint(ctypes.Structure):
     _fields_ = [("current", ctypes.c_int32), ("scale", ctypes.c_float), ("good", ctypes.c_int64),
                 ("t", ctypes.c_int64), ("steps", ctypes.c_int64), ("skipped", ctypes.c_int64),
@@ -135,6 +141,10 @@ def lib():
                 "zr_mx4_dequantize": (st, [vp, i64, i64, vp, i32, i64, vp]),
                 "zr_mx4_matmul": (st, [vp, i64, vp, i64, i64, vp, i32, i64, vp]),
                 "zr_mx4_linear": (st, [vp, i32, i64, i64, vp, i64, i64, vp, i32, i64, vp, vp]),
+                "zr_mx4_matmul_finish": (st, [vp, i64, vp, i64, i64, vp, i32, i64, ctypes.POINTER(Epilogue), vp]),
+                "zr_mx4_linear_finish": (st, [vp, i32, i64, i64, vp, i64, i64, vp, i32, i64, vp, ctypes.POINTER(Epilogue),
+                                              vp]),
+                "zr_column_sums": (st, [vp, i32, i64, i64, i64, vp, vp]),
                 "zr_mx4_status": (st, [vp]),
                 "zr_mx4_stall_waits": (st, [i32]),
                 "zr_distill_topk": (st, [vp, i32, i64, i64, i64, vp, i32, vp, i32, i32, i64, vp, ctypes.c_float,
@@ -705,19 +715,74 @@ def mx4_dequantize(q: Mx4, out, stream=None) -> None:
     _check(fn(q.ptr, rows, cols, p, dt, ld, _stream_of(stream, device, q.device)))
 
 
-def mx4_matmul(a: Mx4, b: Mx4, out, stream=None) -> None:
-    """out[M, N] = a[M, K] b[N, K]^T (zr_mx4_matmul)."""
-    fn = _fns.get("zr_mx4_matmul") or _fn("zr_mx4_matmul")
+ACTIVATIONS = {None: 0, "relu": 1, "gelu": 2, "silu": 3}  # zr_activation
+
+
+def _epilogue(what: str, out, rows: int, cols: int, device: int, bias, activation, residual, pre, gradient):
+    """zr_mx4_epilogue of a product's keywords; their tensors are on the output's device."""
+    e = Epilogue()
+    act = ACTIVATIONS.get(activation)
+    if act is None:
+        _refuse(f"{what}: activation must be one of {sorted(k for k in ACTIVATIONS if k)} or None, not {activation!r}")
+    e.activation, e.gradient = act, gradient
+    for name, t in (("residual", residual), ("pre", pre)):
+        if t is None:
+            continue
+        if t.dtype is not out.dtype or t.shape != out.shape:
+            _refuse(f"{what}: {name} must have out's type and shape")
+        p, _, _, ld, _, d = _matrix(t, name)
+        if d != device:
+            _refuse(f"{what}: {name} on device {d}, out on {device}")
+        if name == "pre":
+            e.pre, e.ldp = p, ld
+        else:
+            e.residual, e.ldr = p, ld
+    if bias is not None:
+        dt = _types.get(bias.dtype)
+        if dt is None or bias.numel() != cols or not bias.is_contiguous() or not bias.is_cuda:
+            _refuse(f"{what}: bias must be fp32, fp16 or bf16 [{cols}] in device memory")
+        if bias.get_device() != device:
+            _refuse(f"{what}: bias on device {bias.get_device()}, out on {device}")
+        e.bias, e.bias_dtype = bias.data_ptr(), dt
+    return e
+
+
+def mx4_matmul(a: Mx4, b: Mx4, out, stream=None, *, bias=None, activation=None, residual=None, pre=None,
+               gradient_of=None) -> None:
+    """out[M, N] = a[M, K] b[N, K]^T (zr_mx4_matmul). With any of the keywords the results go through an epilogue
+    (zr_mx4_matmul_finish): out = act(h) + residual with h = a b^T + bias, stored to `pre` if given; or, with
+    `gradient_of` naming an activation, out = a b^T times that activation's derivative at `pre`. `residual`, or the
+    `pre` of a gradient, may be `out`. Activations: "relu", "gelu" (in its tanh form), "silu"."""
+    name = "zr_mx4_matmul"
+    plain = bias is None and activation is None and residual is None and pre is None and gradient_of is None
+    if not plain:
+        name = "zr_mx4_matmul_finish"
+    fn = _fns.get(name) or _fn(name)
     p, rows, cols, ld, dt, device = _matrix(out, "out")
     if a.cols != b.cols or a.rows != rows or b.rows != cols:
         _refuse(f"mx4_matmul: a is {a.rows} x {a.cols}, b {b.rows} x {b.cols}, out {rows} x {cols}")
-    _check(fn(a.ptr, rows, b.ptr, cols, a.cols, p, dt, ld, _stream_of(stream, device, a.device, b.device)))
+    s = _stream_of(stream, device, a.device, b.device)
+    if plain:
+        _check(fn(a.ptr, rows, b.ptr, cols, a.cols, p, dt, ld, s))
+        return
+    if gradient_of is not None and activation is not None:
+        _refuse("mx4_matmul: an activation and a gradient of one")
+    e = _epilogue("mx4_matmul", out, rows, cols, device, bias, gradient_of if gradient_of is not None else activation,
+                  residual, pre, int(gradient_of is not None))
+    _check(fn(a.ptr, rows, b.ptr, cols, a.cols, p, dt, ld, ctypes.byref(e), s))
 
 
-def mx4_linear(x, w: Mx4, out, xq: Optional[Mx4] = None, stream=None) -> None:
+def mx4_linear(x, w: Mx4, out, xq: Optional[Mx4] = None, stream=None, *, bias=None, activation=None, residual=None,
+               pre=None) -> None:
     """out[M, N] = x[M, K] w[N, K]^T with x quantised in the call (zr_mx4_linear); more than MX4_FEW tokens need xq,
-    a buffer that holds the quantised x then (for fewer it is a workspace, whose contents say nothing)."""
-    fn = _fns.get("zr_mx4_linear") or _fn("zr_mx4_linear")
+    a buffer that holds the quantised x then (for fewer it is a workspace, whose contents say nothing). With any of
+    the keywords out = act(h) + residual, h = x w^T + bias, and h is stored to `pre` if given (zr_mx4_linear_finish;
+    as in mx4_matmul)."""
+    name = "zr_mx4_linear"
+    plain = bias is None and activation is None and residual is None and pre is None
+    if not plain:
+        name = "zr_mx4_linear_finish"
+    fn = _fns.get(name) or _fn(name)
     p, rows, k, ldx, xdt, x_device = _matrix(x, "x")
     o, m, n, ldo, dt, device = _matrix(out, "out")
     if w.cols != k or m != rows or w.rows != n:
@@ -725,7 +790,21 @@ def mx4_linear(x, w: Mx4, out, xq: Optional[Mx4] = None, stream=None) -> None:
     if xq is not None and (xq.rows != rows or xq.cols != k):
         _refuse(f"mx4_linear: xq is {xq.rows} x {xq.cols}, x {rows} x {k}")
     s = _stream_of(stream, device, x_device, w.device, xq.device if xq is not None else device)
-    _check(fn(p, xdt, rows, ldx, w.ptr, n, k, o, dt, ldo, xq and xq.ptr, s))
+    if plain:
+        _check(fn(p, xdt, rows, ldx, w.ptr, n, k, o, dt, ldo, xq and xq.ptr, s))
+        return
+    e = _epilogue("mx4_linear", out, rows, n, device, bias, activation, residual, pre, 0)
+    _check(fn(p, xdt, rows, ldx, w.ptr, n, k, o, dt, ldo, xq and xq.ptr, ctypes.byref(e), s))
+
+
+def column_sums(x, out, stream=None) -> None:
+    """out[N] = the sums of x's columns in fp32: a bias's gradient (zr_column_sums)."""
+    fn = _fns.get("zr_column_sums") or _fn("zr_column_sums")
+    p, rows, cols, ld, dt, device = _matrix(x, "x")
+    if out is None:
+        _refuse("column_sums: no out given")
+    o = _vector(out, "column_sums: out", cols, device)
+    _check(fn(p, dt, rows, cols, ld, o, _stream_of(stream, device)))
 
 
 def mx4_status(stream=None) -> None:
@@ -866,4 +945,4 @@ __all__ = ["lib", "ZrError", "chunk_size", "bucket_plan", "model_state_bytes", "
            "State", "State1", "Plan", "step_noalloc", "F16", "BF16", "F32", "STAGING_REGISTERS", "STAGING_BULK",
            "STAGING_BULK_IO", "Mx4", "mx4_bytes", "mx4_quantize", "mx4_dequantize", "mx4_matmul", "mx4_linear",
            "mx4_status", "distill_topk", "MX4_FEW", "DISTILL_MAX_TOP", "token_logprobs", "policy_loss", "preference_loss",
-           "preference_bytes"]
+           "preference_bytes", "column_sums", "ACTIVATIONS"]

@@ -60,6 +60,118 @@ std::atomic<int> g_stall{0};
 constexpr int kOutWarps = 4, kGemmThreads = 64 + 32 * kOutWarps;
 constexpr int kSwizzle = 1024;  // the operands' swizzle repeats every 1024 bytes
 
+// What a product's results go through on their way out (EPI; zr_mx4_epilogue): h = s + bias, out = act(h) +
+// residual, h stored on request; or out = s act'(h) for a stored h. Each is taken in fp32 from the sum itself and
+// rounded once.
+struct Finish {
+  const void* bias;
+  const void* residual;
+  void* pre;
+  int64_t ldr, ldp;
+  int bias_dt, act, gradient;
+  int vec_residual, vec_pre;  // rows begin on 16-byte boundaries (of pre as of out, GemmArgs::vec)
+};
+struct NoFinish {};
+template <bool EPI>
+using FinishOf = typename std::conditional<EPI, Finish, NoFinish>::type;
+
+// 1/(1 + e^-u): of the side that does not overflow, and 1 less it, which does not cancel.
+__device__ __forceinline__ void logistic(float u, float& up, float& down) {
+  float t, p;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(__fmul_rn(-fabsf(u), 1.44269504088896340736f)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(1.0f + t));
+  const float q = __fmul_rn(t, p);
+  up = u >= 0.0f ? p : q;
+  down = u >= 0.0f ? q : p;
+}
+constexpr float kGelu1 = 1.59576912160573071176f, kGelu3 = 0.07135481282553181f;  // sqrt(8/pi), 0.044715 of it
+
+// The activation. GELU in its tanh form is h S(u), u = sqrt(8/pi) (h + 0.044715 h^3), S the logistic function.
+template <int ACT>
+__device__ __forceinline__ float activated(float h) {
+  if (ACT == ZR_ACT_RELU) return h < 0.0f ? 0.0f : h;
+  if (ACT == ZR_ACT_NONE) return h;
+  const float u = ACT == ZR_ACT_SILU ? h : __fmul_rn(h, __fmaf_rn(__fmul_rn(h, h), kGelu3, kGelu1));
+  float t, p;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(__fmul_rn(u, -1.44269504088896340736f)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(1.0f + t));
+  return __fmul_rn(h, p);
+}
+// Its derivative: S + h S (1 - S) u'. Far out it is 0 or 1, without what overflows on the way.
+template <int ACT>
+__device__ __forceinline__ float slope(float h) {
+  if (ACT == ZR_ACT_NONE) return 1.0f;
+  const float far = h > 0.0f ? 1.0f : h <= 0.0f ? 0.0f : h;
+  if (ACT == ZR_ACT_RELU) return far;
+  const float h2 = __fmul_rn(h, h);
+  const float u = ACT == ZR_ACT_SILU ? h : __fmul_rn(h, __fmaf_rn(h2, kGelu3, kGelu1));
+  const float du = ACT == ZR_ACT_SILU ? 1.0f : __fmaf_rn(h2, 3.0f * kGelu3, kGelu1);
+  float up, down;
+  logistic(u, up, down);
+  return fabsf(h) < 100.0f ? __fmul_rn(up, __fmaf_rn(__fmul_rn(h, down), du, 1.0f)) : far;
+}
+
+__device__ __forceinline__ float load_as(const void* p, int dt, int64_t i) {
+  if (dt == zr::DT_F32) return static_cast<const float*>(p)[i];
+  const uint16_t v = static_cast<const uint16_t*>(p)[i];
+  return dt == zr::DT_BF16 ? zr::to_f32<zr::DT_BF16>(v) : zr::to_f32<zr::DT_F16>(v);
+}
+__device__ __forceinline__ void store_as(void* out, int dt, int64_t i, float v) {
+  if (dt == zr::DT_F32)
+    static_cast<float*>(out)[i] = v;
+  else
+    static_cast<uint16_t*>(out)[i] = dt == zr::DT_BF16 ? zr::from_f32<zr::DT_BF16>(v) : zr::from_f32<zr::DT_F16>(v);
+}
+
+template <class Each>
+__device__ __forceinline__ void by_activation(int act, Each each) {
+  if (act == ZR_ACT_GELU)
+    each(std::integral_constant<int, ZR_ACT_GELU>());
+  else if (act == ZR_ACT_SILU)
+    each(std::integral_constant<int, ZR_ACT_SILU>());
+  else if (act == ZR_ACT_RELU)
+    each(std::integral_constant<int, ZR_ACT_RELU>());
+  else
+    each(std::integral_constant<int, ZR_ACT_NONE>());
+}
+
+// One result, with h stored if it is wanted.
+__device__ __forceinline__ float finished(const Finish& e, int dt, int64_t row, int64_t col, float s) {
+  float r = s;
+  if (e.gradient) {
+    const float h = load_as(e.pre, dt, row * e.ldp + col);
+    by_activation(e.act, [&](auto act) { r = __fmul_rn(s, slope<act.value>(h)); });
+    return r;
+  }
+  const float h = e.bias ? __fadd_rn(s, load_as(e.bias, e.bias_dt, col)) : s;
+  by_activation(e.act, [&](auto act) { r = activated<act.value>(h); });
+  if (e.residual) r = __fadd_rn(r, load_as(e.residual, dt, row * e.ldr + col));
+  if (e.pre) store_as(e.pre, dt, row * e.ldp + col, h);
+  return r;
+}
+
+// The values of 128 bytes of a row from column col on, `left` of them in the row, as fp32.
+template <int DT>
+__device__ __forceinline__ void load_row(const void* p, int64_t at, int left, bool vec, float* f) {
+  constexpr int es = DT == zr::DT_F32 ? 4 : 2, kCols = 128 / es;
+  const char* from = static_cast<const char*>(p) + at * es;
+  if (vec && left >= kCols) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint4 u = *reinterpret_cast<const uint4*>(from + 16 * j);
+      if constexpr (DT == zr::DT_F32) {
+        f[4 * j] = __uint_as_float(u.x), f[4 * j + 1] = __uint_as_float(u.y);
+        f[4 * j + 2] = __uint_as_float(u.z), f[4 * j + 3] = __uint_as_float(u.w);
+      } else {
+        zr::unpack8<DT>(u, f + 8 * j);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) f[i] = i < left ? zr::load1<DT>(from, i) : 0.0f;
+  }
+}
+
 template <bool PAIR>
 struct Gemm {
   static constexpr int kTiles = PAIR ? 2 : 1;                       // MX4 tiles along M and along N
@@ -131,8 +243,8 @@ __device__ __forceinline__ int tile_count(const GemmArgs& g) { return 2 * g.mt *
 // so that no two lanes write to a bank), from where one copy takes them; where the rows of out do not
 // begin on 16-byte boundaries, a row at a time by the lanes.
 template <int DT, int BUFFERS>
-__device__ __forceinline__ void rows_out(const GemmArgs& g, const CUtensorMap* map, char* stage, const uint32_t* v,
-                                         int64_t row0, int64_t col) {
+__device__ __forceinline__ void rows_out(const GemmArgs& g, void* to, int64_t ld, const CUtensorMap* map, char* stage,
+                                         const uint32_t* v, int64_t row0, int64_t col) {
   constexpr int es = DT == zr::DT_F32 ? 4 : 2, kCols = 128 / es;
   const int lane = threadIdx.x & 31;
   if (g.vec) {  // the copy that used these staging rows last has read them
@@ -160,11 +272,11 @@ __device__ __forceinline__ void rows_out(const GemmArgs& g, const CUtensorMap* m
   __syncwarp();
   using T = typename std::conditional<DT == zr::DT_F32, uint32_t, uint16_t>::type;
   constexpr int kEach = kCols / 32;  // values of a row in a lane, 32 apart
-  T* out = static_cast<T*>(g.out) + row0 * g.ldo + col + lane;
+  T* out = static_cast<T*>(to) + row0 * ld + col + lane;
   const int rows = (int)(g.M - row0 < 32 ? g.M - row0 : 32);
   const int left = (int)(g.N - col < kCols ? g.N - col : kCols) - lane;
 #pragma unroll 8
-  for (int r = 0; r < 32; ++r, out += g.ldo) {
+  for (int r = 0; r < 32; ++r, out += ld) {
 #pragma unroll
     for (int i = 0; i < kEach; ++i)
       if (r < rows && 32 * i < left)
@@ -179,15 +291,20 @@ __device__ __forceinline__ void rows_out(const GemmArgs& g, const CUtensorMap* m
 // 2048 x 8192 to bf16 in 6.4 us by fours, 9.5 by blocks alone; two waits of the cluster and 64 KB through
 // its network cost 1 to 3 us.
 constexpr int kPartPitch = 132;  // floats: rows four banks apart
-template <int S, int DT>
-__device__ __forceinline__ void join_parts(const GemmArgs& g, const float* part, int rank, const Tile& t) {
+template <int S, int DT, bool EPI>
+__device__ __forceinline__ void join_parts(const GemmArgs& g, const FinishOf<EPI>& e, const float* part, int rank, const Tile& t) {
   using T = typename std::conditional<DT == zr::DT_F32, uint32_t, uint16_t>::type;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t row0 = (int64_t)t.m * 128, col = (int64_t)t.n * 128 + lane * 4;
   const int rows = (int)(g.M - row0 < 128 ? g.M - row0 : 128), share = (rows + S - 1) / S;
   const int end = min(rows, (rank + 1) * share);
-  auto put = [&](int64_t row, const float v[4]) {
+  auto put = [&](int64_t row, float v[4]) {
     T u[4];
+    if constexpr (EPI) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (col + i < g.N) v[i] = finished(e, DT, row, col + i, v[i]);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if constexpr (DT == zr::DT_F32)
@@ -236,10 +353,14 @@ __device__ __forceinline__ void join_parts(const GemmArgs& g, const float* part,
 
 template <bool PAIR>
 using Maps = typename std::conditional<PAIR, PairMaps, OutMap>::type;
+// How a stored h is stored, as the output is.
+template <bool EPI>
+using PreMap = typename std::conditional<EPI, OutMap, NoFinish>::type;
 
-template <bool PAIR, int DT>
+template <bool PAIR, int DT, bool EPI>
 __global__ void __launch_bounds__(kGemmThreads, 1)
-    gemm_kernel(const __grid_constant__ GemmArgs g, const __grid_constant__ Maps<PAIR> maps) {
+    gemm_kernel(const __grid_constant__ GemmArgs g, const __grid_constant__ Maps<PAIR> maps,
+                const __grid_constant__ FinishOf<EPI> e, const __grid_constant__ PreMap<EPI> pre_map) {
   using G = Gemm<PAIR>;
   extern __shared__ __align__(kSwizzle) char smem[];
   const uint32_t stages = zr::smem_u32(smem);
@@ -425,13 +546,53 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         else
           zr::tmem_load64(d + at * kOnce, v);
         if (c == (PAIR ? 0 : kChunks - 1)) tell(freed + 8 * (turn & 1));
+        if constexpr (EPI) {
+          if (g.kt == 0) {  // a sum of nothing
+#pragma unroll
+            for (int i = 0; i < kOnce; ++i) v[i] = 0;
+          }
+        }
         if (split) {  // over the stages, which are used up
           float* part = reinterpret_cast<float*>(smem) + (lanes + (threadIdx.x & 31)) * kPartPitch + at * kOnce;
 #pragma unroll
           for (int i = 0; i < kOnce; i += 4) *reinterpret_cast<uint4*>(part + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
         } else if (row0 < g.M && col < g.N) {
-          rows_out<DT, G::kOutBuffers>(g, &maps.out, stage + buffer * G::kOutBytes, v, row0, col);
-          buffer = buffer + 1 < G::kOutBuffers ? buffer + 1 : 0;
+          auto store = [&](void* to, int64_t ld, const CUtensorMap* map) {
+            rows_out<DT, G::kOutBuffers>(g, to, ld, map, stage + buffer * G::kOutBytes, v, row0, col);
+            buffer = buffer + 1 < G::kOutBuffers ? buffer + 1 : 0;
+          };
+          if constexpr (EPI) {
+            const int64_t row = row0 + (threadIdx.x & 31);
+            const int left = (int)(g.N - col < kOnce ? g.N - col : kOnce);
+            if (e.gradient) {
+              float h[kOnce];
+              load_row<DT>(e.pre, row * e.ldp + col, row < g.M ? left : 0, e.vec_pre, h);
+              by_activation(e.act, [&](auto act) {
+#pragma unroll
+                for (int i = 0; i < kOnce; ++i) v[i] = __float_as_uint(__fmul_rn(__uint_as_float(v[i]), slope<act.value>(h[i])));
+              });
+            } else {
+              if (e.bias) {
+                float b[kOnce];
+#pragma unroll
+                for (int i = 0; i < kOnce; ++i) b[i] = i < left ? load_as(e.bias, e.bias_dt, col + i) : 0.0f;
+#pragma unroll
+                for (int i = 0; i < kOnce; ++i) v[i] = __float_as_uint(__fadd_rn(__uint_as_float(v[i]), b[i]));
+              }
+              if (e.pre) store(e.pre, e.ldp, &pre_map.out);
+              by_activation(e.act, [&](auto act) {
+#pragma unroll
+                for (int i = 0; i < kOnce; ++i) v[i] = __float_as_uint(activated<act.value>(__uint_as_float(v[i])));
+              });
+              if (e.residual) {
+                float r[kOnce];
+                load_row<DT>(e.residual, row * e.ldr + col, row < g.M ? left : 0, e.vec_residual, r);
+#pragma unroll
+                for (int i = 0; i < kOnce; ++i) v[i] = __float_as_uint(__fadd_rn(__uint_as_float(v[i]), r[i]));
+              }
+            }
+          }
+          store(g.out, g.ldo, &maps.out);
         }
       }
     }
@@ -443,11 +604,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const Tile t = tile_of(g, first);
     const float* part = reinterpret_cast<const float*>(smem);
     if (g.split == 2)
-      join_parts<2, DT>(g, part, rank, t);
+      join_parts<2, DT, EPI>(g, e, part, rank, t);
     else if (g.split == 4)
-      join_parts<4, DT>(g, part, rank, t);
+      join_parts<4, DT, EPI>(g, e, part, rank, t);
     else
-      join_parts<8, DT>(g, part, rank, t);
+      join_parts<8, DT, EPI>(g, e, part, rank, t);
     __syncwarp();
   }
   zr::tmem_fence_before();
@@ -526,15 +687,9 @@ __device__ __forceinline__ void open_eight(const Eight& u, int dt, float v[8]) {
   }
 }
 
-__device__ __forceinline__ void store_as(void* out, int dt, int64_t i, float v) {
-  if (dt == zr::DT_F32)
-    static_cast<float*>(out)[i] = v;
-  else
-    static_cast<uint16_t*>(out)[i] = dt == zr::DT_BF16 ? zr::from_f32<zr::DT_BF16>(v) : zr::from_f32<zr::DT_F16>(v);
-}
-
-template <int S>
-__global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant__ FewArgs g) {
+template <int S, bool EPI>
+__global__ void __launch_bounds__(kFewThreads)
+    few_kernel(const __grid_constant__ FewArgs g, const __grid_constant__ FinishOf<EPI> e) {
   extern __shared__ __align__(kSwizzle) char smem[];
   const int n = blockIdx.x / S, rank = S > 1 ? (int)zr::cluster_rank() : 0;
   const int k0 = (int)((int64_t)g.kt * rank / S), nk = (int)((int64_t)g.kt * (rank + 1) / S) - k0;
@@ -549,6 +704,10 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(tail + 200);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint8_t* w = g.w + ((int64_t)n * g.kt + k0) * zr::kMxTileBytes;
+  auto put = [&](int64_t token, int64_t col, float v) {
+    if constexpr (EPI) v = finished(e, g.odt, token, col, v);
+    store_as(g.out, g.odt, token * g.ldo + col, v);
+  };
 
   if (warp == 0) {
     zr::tmem_alloc(zr::smem_u32(tmem_at), 32);
@@ -680,7 +839,7 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
           if (S > 1)
             part[t * 128 + warp * 32 + lane] = __uint_as_float(v[t]);
           else if (col < g.N)
-            store_as(g.out, g.odt, t * g.ldo + col, __uint_as_float(v[t]));
+            put(t, col, __uint_as_float(v[t]));
         }
     }
     zr::tmem_fence_before();
@@ -689,8 +848,8 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
   if (S > 1) {
     zr::cluster_sync();
     constexpr int kShare = 128 / S;
-    for (int e = threadIdx.x; e < (int)g.M * kShare; e += kFewThreads) {
-      const int t = e / kShare, c = rank * kShare + e % kShare;
+    for (int i = threadIdx.x; i < (int)g.M * kShare; i += kFewThreads) {
+      const int t = i / kShare, c = rank * kShare + i % kShare;
       const uint32_t at = zr::smem_u32(part + t * 128 + c);
       float sum = 0.0f;
 #pragma unroll
@@ -699,7 +858,7 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
         sum = r ? sum + p : p;
       }
       const int64_t col = (int64_t)n * 128 + c;
-      if (col < g.N) store_as(g.out, g.odt, t * g.ldo + col, sum);
+      if (col < g.N) put(t, col, sum);
     }
     __syncwarp();
     zr::cluster_sync();  // a block's shared memory stays until the others have read it
@@ -732,37 +891,41 @@ bool encode_lines(CUtensorMap* map, const void* q, int64_t tiles, int lines) {
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A map of the output.
-bool encode_out(CUtensorMap* map, const GemmArgs& g, int dt) {
+// A map of the output, or of another matrix of its size and type.
+bool encode_out(CUtensorMap* map, const GemmArgs& g, void* out, int64_t ld, int dt) {
   const int es = dt == zr::DT_F32 ? 4 : 2;
   const CUtensorMapDataType type = dt == zr::DT_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                    : dt == zr::DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  const cuuint64_t size[2] = {(cuuint64_t)g.N, (cuuint64_t)g.M}, stride[1] = {(cuuint64_t)g.ldo * es};
+  const cuuint64_t size[2] = {(cuuint64_t)g.N, (cuuint64_t)g.M}, stride[1] = {(cuuint64_t)ld * es};
   const cuuint32_t box[2] = {(cuuint32_t)(128 / es), 32}, step[2] = {1, 1};
-  return map_encoder()(map, type, 2, g.out, size, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+  return map_encoder()(map, type, 2, out, size, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool PAIR, int DT>
-zr_status launch_gemm(const GemmArgs& g, int blocks, cudaStream_t s) {
+template <bool PAIR, int DT, bool EPI>
+zr_status launch_gemm(const char* what, const GemmArgs& g, const FinishOf<EPI>& e, int blocks, cudaStream_t s) {
   static zr::SmemAllowance allowance;
-  if (zr_status st = allowance.allow("zr_mx4_matmul", (const void*)gemm_kernel<PAIR, DT>, Gemm<PAIR>::kSmem)) return st;
+  if (zr_status st = allowance.allow(what, (const void*)gemm_kernel<PAIR, DT, EPI>, Gemm<PAIR>::kSmem)) return st;
   Maps<PAIR> maps;
-  if (!map_encoder() || (g.vec && !encode_out(&maps.out, g, DT)))
-    return fail(ZR_ERR_CUDA, "zr_mx4_matmul: the driver gave no tensor map");
-  if constexpr (PAIR) {
-    const int64_t a_tiles = zr::mx_tiles(g.M, zr::kMxRows) * g.kt, b_tiles = zr::mx_tiles(g.N, zr::kMxRows) * g.kt;
-    if (!encode_lines(&maps.a_tile, g.a, a_tiles, kTileLines) ||
-        !encode_lines(&maps.b_codes, g.b, b_tiles, zr::kMxRows) ||
-        (g.whole < g.mt * g.nt && !encode_lines(&maps.b_half, g.b, b_tiles, zr::kMxRows / 2)) ||
-        !encode_lines(&maps.b_scales, g.b, b_tiles, zr::kMxScaleBytes / 128))
-      return fail(ZR_ERR_CUDA, "zr_mx4_matmul: the driver gave no tensor map");
+  PreMap<EPI> pre;
+  bool encoded = map_encoder() && (!g.vec || encode_out(&maps.out, g, g.out, g.ldo, DT));
+  if constexpr (EPI)
+    encoded = encoded && (!g.vec || !e.pre || e.gradient || encode_out(&pre.out, g, e.pre, e.ldp, DT));
+  if (encoded && PAIR) {
+    if constexpr (PAIR) {
+      const int64_t a_tiles = zr::mx_tiles(g.M, zr::kMxRows) * g.kt, b_tiles = zr::mx_tiles(g.N, zr::kMxRows) * g.kt;
+      encoded = encode_lines(&maps.a_tile, g.a, a_tiles, kTileLines) &&
+                encode_lines(&maps.b_codes, g.b, b_tiles, zr::kMxRows) &&
+                (g.whole >= g.mt * g.nt || encode_lines(&maps.b_half, g.b, b_tiles, zr::kMxRows / 2)) &&
+                encode_lines(&maps.b_scales, g.b, b_tiles, zr::kMxScaleBytes / 128);
+    }
   }
-  cudaError_t e = zr::launch(gemm_kernel<PAIR, DT>, blocks, kGemmThreads, Gemm<PAIR>::kSmem, PAIR ? 2 : g.split, true, s, g,
-                             maps);
-  if (e != cudaSuccess) return fail(ZR_ERR_CUDA, "zr_mx4_matmul: launch failed: %s", cudaGetErrorString(e));
+  if (!encoded) return fail(ZR_ERR_CUDA, "%s: the driver gave no tensor map", what);
+  cudaError_t err = zr::launch(gemm_kernel<PAIR, DT, EPI>, blocks, kGemmThreads, Gemm<PAIR>::kSmem, PAIR ? 2 : g.split, true, s,
+                               g, maps, e, pre);
+  if (err != cudaSuccess) return fail(ZR_ERR_CUDA, "%s: launch failed: %s", what, cudaGetErrorString(err));
   return ZR_OK;
 }
 
@@ -807,12 +970,13 @@ int shares_of_k(int64_t M, int64_t tiles, int64_t kt, int sms) {
   return best;
 }
 
+template <bool EPI>
 zr_status matmul(const char* what, const void* a, int64_t M, const void* b, int64_t N, int64_t K, void* out,
-                 zr_dtype dt, int64_t ldo, cudaStream_t s) {
+                 zr_dtype dt, int64_t ldo, const FinishOf<EPI>& e, cudaStream_t s) {
   const int es = dt == ZR_F32 ? 4 : 2;
-  if (K == 0) {  // a sum of nothing
-    cudaError_t e = cudaMemset2DAsync(out, (size_t)ldo * es, 0, (size_t)N * es, (size_t)M, s);
-    return e == cudaSuccess ? ZR_OK : fail(ZR_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+  if (K == 0 && !EPI) {  // a sum of nothing
+    cudaError_t err = cudaMemset2DAsync(out, (size_t)ldo * es, 0, (size_t)N * es, (size_t)M, s);
+    return err == cudaSuccess ? ZR_OK : fail(ZR_ERR_CUDA, "%s: %s", what, cudaGetErrorString(err));
   }
   const int sms = zr::sm_count(what);
   if (sms == 0) return ZR_ERR_CUDA;
@@ -823,69 +987,113 @@ zr_status matmul(const char* what, const void* a, int64_t M, const void* b, int6
   g.M = M; g.N = N; g.ldo = ldo;
   g.stall = g_stall.load(std::memory_order_relaxed) ? 16 : 0;
   const int64_t kt = zr::mx_tiles(K, zr::kMxCols);
-  const bool pair = pairs_faster(M, N, kt, dt, sms);
+  const bool pair = kt > 0 && pairs_faster(M, N, kt, dt, sms);
   const int64_t mt = zr::mx_tiles(M, pair ? 256 : 128), nt = zr::mx_tiles(N, pair ? 256 : 128);
   if (kt > 0x7FFFFFFF || nt > (1 << 25) || mt > 0x3FFFFFFF / nt)
     return fail(ZR_ERR_UNSUPPORTED, "%s: the product has too many tiles", what);
   g.kt = (int)kt; g.mt = (int)mt; g.nt = (int)nt;
-  g.vec = ldo * es % 16 == 0 && ldo < (int64_t)1 << 36 && M <= 0x7FFFFFFF && N <= 0x7FFFFFFF;
+  auto vec = [&](int64_t ld) { return ld * es % 16 == 0 && ld < (int64_t)1 << 36 && M <= 0x7FFFFFFF && N <= 0x7FFFFFFF; };
+  g.vec = vec(ldo);
+  if constexpr (EPI)
+    if (e.pre && !e.gradient) g.vec = g.vec && vec(e.ldp);
   g.whole = g.mt * g.nt;
   g.split = 1;
   if (pair) {
     const int pairs = sms / 2, last = g.whole % pairs, blocks = 2 * (g.whole < pairs ? g.whole : pairs);
     if (halves_last(M, N, sms)) g.whole -= last;
-    if (dt == ZR_F16) return launch_gemm<true, zr::DT_F16>(g, blocks, s);
-    if (dt == ZR_BF16) return launch_gemm<true, zr::DT_BF16>(g, blocks, s);
-    return launch_gemm<true, zr::DT_F32>(g, blocks, s);
+    if (dt == ZR_F16) return launch_gemm<true, zr::DT_F16, EPI>(what, g, e, blocks, s);
+    if (dt == ZR_BF16) return launch_gemm<true, zr::DT_BF16, EPI>(what, g, e, blocks, s);
+    return launch_gemm<true, zr::DT_F32, EPI>(what, g, e, blocks, s);
   }
-  g.split = shares_of_k(M, mt * nt, kt, sms);
+  if (kt > 0) g.split = shares_of_k(M, mt * nt, kt, sms);
   const int blocks = g.split > 1 ? (int)(mt * nt) * g.split : (int)(mt * nt < sms ? mt * nt : sms);
-  if (dt == ZR_F16) return launch_gemm<false, zr::DT_F16>(g, blocks, s);
-  if (dt == ZR_BF16) return launch_gemm<false, zr::DT_BF16>(g, blocks, s);
-  return launch_gemm<false, zr::DT_F32>(g, blocks, s);
+  if (dt == ZR_F16) return launch_gemm<false, zr::DT_F16, EPI>(what, g, e, blocks, s);
+  if (dt == ZR_BF16) return launch_gemm<false, zr::DT_BF16, EPI>(what, g, e, blocks, s);
+  return launch_gemm<false, zr::DT_F32, EPI>(what, g, e, blocks, s);
 }
 
-template <int S>
-zr_status launch_few(const FewArgs& g, int blocks, int smem, cudaStream_t s) {
+template <int S, bool EPI>
+zr_status launch_few(const char* what, const FewArgs& g, const FinishOf<EPI>& e, int blocks, int smem, cudaStream_t s) {
   static zr::SmemAllowance allowance;
-  if (zr_status st = allowance.allow("zr_mx4_linear", (const void*)few_kernel<S>, zr::kSmemMost)) return st;
-  cudaError_t e = zr::launch(few_kernel<S>, blocks, kFewThreads, smem, S, g.xq != nullptr, s, g);
-  if (e != cudaSuccess) return fail(ZR_ERR_CUDA, "zr_mx4_linear: launch failed: %s", cudaGetErrorString(e));
+  if (zr_status st = allowance.allow(what, (const void*)few_kernel<S, EPI>, zr::kSmemMost)) return st;
+  cudaError_t err = zr::launch(few_kernel<S, EPI>, blocks, kFewThreads, smem, S, g.xq != nullptr, s, g, e);
+  if (err != cudaSuccess) return fail(ZR_ERR_CUDA, "%s: launch failed: %s", what, cudaGetErrorString(err));
   return ZR_OK;
 }
 
-}  // namespace
-
-extern "C" zr_status zr_mx4_matmul(const void* a, int64_t M, const void* b, int64_t N, int64_t K, void* out,
-                                   zr_dtype dt, int64_t ldo, void* stream) {
-  zr::clear_error();
-  zr::Range range("zr_mx4_matmul");
-  if (!zr::dtype_ok(dt)) return fail(ZR_ERR_INVALID, "zr_mx4_matmul: bad dtype %d", (int)dt);
-  if (M < 0 || N < 0 || K < 0) return fail(ZR_ERR_INVALID, "zr_mx4_matmul: negative size");
-  if (ldo < N) return fail(ZR_ERR_INVALID, "zr_mx4_matmul: the row stride of out is under N");
-  if (M == 0 || N == 0) return ZR_OK;
-  if (!out || (K > 0 && (!a || !b))) return fail(ZR_ERR_INVALID, "zr_mx4_matmul: null pointer");
-  if (!zr::aligned16(a) || !zr::aligned16(b) || !zr::aligned16(out))
-    return fail(ZR_ERR_INVALID, "zr_mx4_matmul: a pointer is not 16-byte aligned");
-  return matmul("zr_mx4_matmul", a, M, b, N, K, out, dt, ldo, static_cast<cudaStream_t>(stream));
+// Whether two matrices of M x N values of `es` bytes share memory: rows as far apart may lie between each other's.
+bool overlap(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t M, int64_t N, int es) {
+  const __int128 x = (__int128)reinterpret_cast<uintptr_t>(a), y = (__int128)reinterpret_cast<uintptr_t>(b);
+  const __int128 row = (__int128)N * es, ends_a = x + (__int128)(M - 1) * lda * es + row,
+                 ends_b = y + (__int128)(M - 1) * ldb * es + row;
+  if (y >= ends_a || x >= ends_b) return false;
+  if (lda != ldb || M == 1) return true;
+  const __int128 ld = (__int128)lda * es, apart = ((y - x) % ld + ld) % ld;
+  return apart < row || ld - apart < row;
 }
 
-extern "C" zr_status zr_mx4_linear(const void* x, zr_dtype xdt, int64_t M, int64_t ldx, const void* w, int64_t N,
-                                   int64_t K, void* out, zr_dtype dt, int64_t ldo, void* xq, void* stream) {
-  zr::clear_error();
-  zr::Range range("zr_mx4_linear");
-  if (!zr::dtype_ok(xdt) || !zr::dtype_ok(dt)) return fail(ZR_ERR_INVALID, "zr_mx4_linear: bad dtype");
-  if (M < 0 || N < 0 || K < 0) return fail(ZR_ERR_INVALID, "zr_mx4_linear: negative size");
-  if (ldx < K || ldo < N) return fail(ZR_ERR_INVALID, "zr_mx4_linear: a row stride is under the row");
+// Refuses what an epilogue may not be; `e` may be null.
+zr_status check_epilogue(const char* what, const zr_mx4_epilogue* e, int64_t M, int64_t N, const void* out, zr_dtype dt,
+                         int64_t ldo) {
+  if (!e) return ZR_OK;
+  const int es = dt == ZR_F32 ? 4 : 2;
+  if (e->activation < ZR_ACT_NONE || e->activation > ZR_ACT_SILU)
+    return fail(ZR_ERR_INVALID, "%s: unknown activation %d", what, (int)e->activation);
+  if (e->bias && !zr::dtype_ok(e->bias_dtype)) return fail(ZR_ERR_INVALID, "%s: bad dtype of the bias", what);
+  if ((e->residual && e->ldr < N) || (e->pre && e->ldp < N))
+    return fail(ZR_ERR_INVALID, "%s: the row stride of pre or residual is under N", what);
+  if (e->gradient && (!e->pre || e->bias || e->residual))
+    return fail(ZR_ERR_INVALID, "%s: a gradient takes pre, and neither bias nor residual", what);
+  if (!zr::aligned16(e->bias) || !zr::aligned16(e->residual) || !zr::aligned16(e->pre))
+    return fail(ZR_ERR_INVALID, "%s: a pointer of the epilogue is not 16-byte aligned", what);
   if (M == 0 || N == 0) return ZR_OK;
-  if (!out || (K > 0 && (!x || !w))) return fail(ZR_ERR_INVALID, "zr_mx4_linear: null pointer");
-  if (!zr::aligned16(x) || !zr::aligned16(w) || !zr::aligned16(out) || !zr::aligned16(xq))
-    return fail(ZR_ERR_INVALID, "zr_mx4_linear: a pointer is not 16-byte aligned");
+  auto clash = [&](const void* p, int64_t ld, const void* q, int64_t ldq, bool may_be) {
+    return p && q && !(may_be && p == q && ld == ldq) && overlap(p, ld, q, ldq, M, N, es);
+  };
+  if (clash(e->residual, e->ldr, out, ldo, true) || clash(e->pre, e->ldp, out, ldo, e->gradient != 0) ||
+      clash(e->pre, e->ldp, e->residual, e->ldr, false))
+    return fail(ZR_ERR_INVALID, "%s: out, pre and residual overlap", what);
+  return ZR_OK;
+}
+Finish finish_of(const zr_mx4_epilogue& e, zr_dtype dt) {
+  const int es = dt == ZR_F32 ? 4 : 2;
+  Finish f{};
+  f.bias = e.bias; f.residual = e.residual; f.pre = e.pre;
+  f.ldr = e.ldr; f.ldp = e.ldp;
+  f.bias_dt = (int)e.bias_dtype; f.act = e.activation; f.gradient = e.gradient != 0;
+  f.vec_residual = e.ldr * es % 16 == 0;
+  f.vec_pre = e.ldp * es % 16 == 0;
+  return f;
+}
+
+template <bool EPI>
+zr_status checked_matmul(const char* what, const void* a, int64_t M, const void* b, int64_t N, int64_t K, void* out,
+                         zr_dtype dt, int64_t ldo, const zr_mx4_epilogue* epilogue, void* stream) {
+  zr::clear_error();
+  zr::Range range(what);
+  if (!zr::dtype_ok(dt)) return fail(ZR_ERR_INVALID, "%s: bad dtype %d", what, (int)dt);
+  if (M < 0 || N < 0 || K < 0) return fail(ZR_ERR_INVALID, "%s: negative size", what);
+  if (ldo < N) return fail(ZR_ERR_INVALID, "%s: the row stride of out is under N", what);
+  if (zr_status st = check_epilogue(what, epilogue, M, N, out, dt, ldo)) return st;
+  if (M == 0 || N == 0) return ZR_OK;
+  if (!out || (K > 0 && (!a || !b))) return fail(ZR_ERR_INVALID, "%s: null pointer", what);
+  if (!zr::aligned16(a) || !zr::aligned16(b) || !zr::aligned16(out))
+    return fail(ZR_ERR_INVALID, "%s: a pointer is not 16-byte aligned", what);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if constexpr (EPI)
+    return matmul<true>(what, a, M, b, N, K, out, dt, ldo, finish_of(*epilogue, dt), s);
+  else
+    return matmul<false>(what, a, M, b, N, K, out, dt, ldo, NoFinish{}, s);
+}
+
+template <bool EPI>
+zr_status linear(const char* what, const void* x, zr_dtype xdt, int64_t M, int64_t ldx, const void* w, int64_t N, int64_t K,
+                 void* out, zr_dtype dt, int64_t ldo, void* xq, const FinishOf<EPI>& e, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t kt = zr::mx_tiles(K, zr::kMxCols), nt = zr::mx_tiles(N, 128);
   // blocks of a cluster share K where the outputs alone would leave multiprocessors idle: two blocks
   // fit on one, so up to twice their number
-  const int sms = zr::sm_count("zr_mx4_linear");
+  const int sms = zr::sm_count(what);
   if (sms == 0) return ZR_ERR_CUDA;
   int split = 1;
   while (split < 8 && nt * split * 2 <= 2 * sms && split * 2 <= kt) split *= 2;
@@ -913,16 +1121,61 @@ extern "C" zr_status zr_mx4_linear(const void* x, zr_dtype xdt, int64_t M, int64
       if (zr_status st = zr_mx4_quantize(x, xdt, M, K, ldx, nullptr, 0, xq, nullptr, stream)) return st;
       g.xq = static_cast<const uint8_t*>(xq);
     }
-    if (split == 8) return launch_few<8>(g, blocks, smem, s);
-    if (split == 4) return launch_few<4>(g, blocks, smem, s);
-    if (split == 2) return launch_few<2>(g, blocks, smem, s);
-    return launch_few<1>(g, blocks, smem, s);
+    if (split == 8) return launch_few<8, EPI>(what, g, e, blocks, smem, s);
+    if (split == 4) return launch_few<4, EPI>(what, g, e, blocks, smem, s);
+    if (split == 2) return launch_few<2, EPI>(what, g, e, blocks, smem, s);
+    return launch_few<1, EPI>(what, g, e, blocks, smem, s);
   }
   if (K > 0) {
-    if (!xq) return fail(ZR_ERR_INVALID, "zr_mx4_linear: more than %d tokens (or a very long K) need xq", kFewTokens);
+    if (!xq) return fail(ZR_ERR_INVALID, "%s: more than %d tokens (or a very long K) need xq", what, kFewTokens);
     if (zr_status st = zr_mx4_quantize(x, xdt, M, K, ldx, nullptr, 0, xq, nullptr, stream)) return st;
   }
-  return matmul("zr_mx4_linear", xq, M, w, N, K, out, dt, ldo, s);
+  return matmul<EPI>(what, xq, M, w, N, K, out, dt, ldo, e, s);
+}
+
+template <bool EPI>
+zr_status checked_linear(const char* what, const void* x, zr_dtype xdt, int64_t M, int64_t ldx, const void* w, int64_t N,
+                         int64_t K, void* out, zr_dtype dt, int64_t ldo, void* xq, const zr_mx4_epilogue* epilogue,
+                         void* stream) {
+  zr::clear_error();
+  zr::Range range(what);
+  if (!zr::dtype_ok(xdt) || !zr::dtype_ok(dt)) return fail(ZR_ERR_INVALID, "%s: bad dtype", what);
+  if (M < 0 || N < 0 || K < 0) return fail(ZR_ERR_INVALID, "%s: negative size", what);
+  if (ldx < K || ldo < N) return fail(ZR_ERR_INVALID, "%s: a row stride is under the row", what);
+  if (zr_status st = check_epilogue(what, epilogue, M, N, out, dt, ldo)) return st;
+  if (M == 0 || N == 0) return ZR_OK;
+  if (!out || (K > 0 && (!x || !w))) return fail(ZR_ERR_INVALID, "%s: null pointer", what);
+  if (!zr::aligned16(x) || !zr::aligned16(w) || !zr::aligned16(out) || !zr::aligned16(xq))
+    return fail(ZR_ERR_INVALID, "%s: a pointer is not 16-byte aligned", what);
+  if constexpr (EPI)
+    return linear<true>(what, x, xdt, M, ldx, w, N, K, out, dt, ldo, xq, finish_of(*epilogue, dt), stream);
+  else
+    return linear<false>(what, x, xdt, M, ldx, w, N, K, out, dt, ldo, xq, NoFinish{}, stream);
+}
+
+}  // namespace
+
+extern "C" zr_status zr_mx4_matmul(const void* a, int64_t M, const void* b, int64_t N, int64_t K, void* out,
+                                   zr_dtype dt, int64_t ldo, void* stream) {
+  return checked_matmul<false>("zr_mx4_matmul", a, M, b, N, K, out, dt, ldo, nullptr, stream);
+}
+
+extern "C" zr_status zr_mx4_linear(const void* x, zr_dtype xdt, int64_t M, int64_t ldx, const void* w, int64_t N,
+                                   int64_t K, void* out, zr_dtype dt, int64_t ldo, void* xq, void* stream) {
+  return checked_linear<false>("zr_mx4_linear", x, xdt, M, ldx, w, N, K, out, dt, ldo, xq, nullptr, stream);
+}
+
+extern "C" zr_status zr_mx4_matmul_finish(const void* a, int64_t M, const void* b, int64_t N, int64_t K, void* out,
+                                          zr_dtype dt, int64_t ldo, const zr_mx4_epilogue* epilogue, void* stream) {
+  if (!epilogue) return zr_mx4_matmul(a, M, b, N, K, out, dt, ldo, stream);
+  return checked_matmul<true>("zr_mx4_matmul_finish", a, M, b, N, K, out, dt, ldo, epilogue, stream);
+}
+
+extern "C" zr_status zr_mx4_linear_finish(const void* x, zr_dtype xdt, int64_t M, int64_t ldx, const void* w, int64_t N,
+                                          int64_t K, void* out, zr_dtype dt, int64_t ldo, void* xq,
+                                          const zr_mx4_epilogue* epilogue, void* stream) {
+  if (!epilogue) return zr_mx4_linear(x, xdt, M, ldx, w, N, K, out, dt, ldo, xq, stream);
+  return checked_linear<true>("zr_mx4_linear_finish", x, xdt, M, ldx, w, N, K, out, dt, ldo, xq, epilogue, stream);
 }
 
 extern "C" zr_status zr_mx4_status(void* stream) {
