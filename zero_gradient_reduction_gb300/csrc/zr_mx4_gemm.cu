@@ -34,6 +34,7 @@
 #include "zr_launch.h"
 #include "zr_mx4.cuh"
 #include "zr_nvtx.h"
+#include "zr_rows.cuh"
 #include "zr_tensor.cuh"
 
 using zr::fail;
@@ -57,7 +58,6 @@ std::atomic<int> g_stall{0};
 //   a pair of blocks (a cluster of two on neighbouring multiprocessors) takes 256 x 256 as one
 //   product of M = 256: each holds 128 rows of A and 128 of the tile's rows of B, so that 32 KB of
 //   codes come in for 128 x 256 of output where a block alone would need 48 KB.
-constexpr int kOutWarps = 4, kGemmThreads = 64 + 32 * kOutWarps;
 constexpr int kSwizzle = 1024;  // the operands' swizzle repeats every 1024 bytes
 
 // What a product's results go through on their way out (EPI; zr_mx4_epilogue): h = s + bias, out = act(h) +
@@ -75,40 +75,40 @@ struct NoFinish {};
 template <bool EPI>
 using FinishOf = typename std::conditional<EPI, Finish, NoFinish>::type;
 
-// 1/(1 + e^-u): of the side that does not overflow, and 1 less it, which does not cancel.
-__device__ __forceinline__ void logistic(float u, float& up, float& down) {
-  float t, p;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(__fmul_rn(-fabsf(u), 1.44269504088896340736f)));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(1.0f + t));
-  const float q = __fmul_rn(t, p);
-  up = u >= 0.0f ? p : q;
-  down = u >= 0.0f ? q : p;
+__device__ __forceinline__ float reciprocal(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
-constexpr float kGelu1 = 1.59576912160573071176f, kGelu3 = 0.07135481282553181f;  // sqrt(8/pi), 0.044715 of it
-
-// The activation. GELU in its tanh form is h S(u), u = sqrt(8/pi) (h + 0.044715 h^3), S the logistic function.
+// The activations as h S(u), S the logistic function: SiLU with u = h, GELU in its tanh form with
+// u = sqrt(8/pi) (h + 0.044715 h^3). What follows has u as an exponent of 2 with the sign turned, -u log2(e) =
+// h (k3 h^2 + k1), so that S = 1/(1 + 2^x). Two values at a time, an instruction for both where there is one.
+constexpr float kGelu1 = -2.302208198144325f, kGelu3 = -0.1029432395800235f, kSilu1 = -1.44269504088896340736f;
 template <int ACT>
-__device__ __forceinline__ float activated(float h) {
-  if (ACT == ZR_ACT_RELU) return h < 0.0f ? 0.0f : h;
-  if (ACT == ZR_ACT_NONE) return h;
-  const float u = ACT == ZR_ACT_SILU ? h : __fmul_rn(h, __fmaf_rn(__fmul_rn(h, h), kGelu3, kGelu1));
-  float t, p;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(__fmul_rn(u, -1.44269504088896340736f)));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(1.0f + t));
-  return __fmul_rn(h, p);
+__device__ __forceinline__ zr::Two activated(zr::Two h) {
+  if constexpr (ACT == ZR_ACT_NONE) {
+    return h;
+  } else if constexpr (ACT == ZR_ACT_RELU) {
+    return zr::Two(h.lo() < 0.0f ? 0.0f : h.lo(), h.hi() < 0.0f ? 0.0f : h.hi());
+  } else {
+    const zr::Two k1(ACT == ZR_ACT_GELU ? kGelu1 : kSilu1, ACT == ZR_ACT_GELU ? kGelu1 : kSilu1), k3(kGelu3, kGelu3);
+    const zr::Two x = zr::mul2(h, ACT == ZR_ACT_GELU ? zr::fma2(zr::mul2(h, h), k3, k1) : k1);
+    const zr::Two d = zr::add2(zr::Two(zr::exp2_fast(x.lo()), zr::exp2_fast(x.hi())), zr::Two(1.0f, 1.0f));
+    return zr::mul2(h, zr::Two(reciprocal(d.lo()), reciprocal(d.hi())));
+  }
 }
-// Its derivative: S + h S (1 - S) u'. Far out it is 0 or 1, without what overflows on the way.
+// The derivative, S + h S (1 - S) u': S and 1 - S from the side of u that does not overflow, 0 or 1 far out.
 template <int ACT>
 __device__ __forceinline__ float slope(float h) {
-  if (ACT == ZR_ACT_NONE) return 1.0f;
+  if constexpr (ACT == ZR_ACT_NONE) return 1.0f;
   const float far = h > 0.0f ? 1.0f : h <= 0.0f ? 0.0f : h;
-  if (ACT == ZR_ACT_RELU) return far;
+  if constexpr (ACT == ZR_ACT_RELU) return far;
   const float h2 = __fmul_rn(h, h);
-  const float u = ACT == ZR_ACT_SILU ? h : __fmul_rn(h, __fmaf_rn(h2, kGelu3, kGelu1));
-  const float du = ACT == ZR_ACT_SILU ? 1.0f : __fmaf_rn(h2, 3.0f * kGelu3, kGelu1);
-  float up, down;
-  logistic(u, up, down);
-  return fabsf(h) < 100.0f ? __fmul_rn(up, __fmaf_rn(__fmul_rn(h, down), du, 1.0f)) : far;
+  const float x = __fmul_rn(h, ACT == ZR_ACT_GELU ? __fmaf_rn(h2, kGelu3, kGelu1) : kSilu1);
+  const float du = ACT == ZR_ACT_GELU ? __fmul_rn(__fmaf_rn(h2, 3.0f * kGelu3, kGelu1), -zr::kLn2) : 1.0f;
+  const float t = zr::exp2_fast(-fabsf(x)), p = reciprocal(1.0f + t), q = __fmul_rn(t, p);
+  const float up = h >= 0.0f ? p : q;  // (x has the other sign of h)
+  return fabsf(h) < 100.0f ? __fmaf_rn(__fmul_rn(h, __fmul_rn(p, q)), du, up) : far;
 }
 
 __device__ __forceinline__ float load_as(const void* p, int dt, int64_t i) {
@@ -144,42 +144,23 @@ __device__ __forceinline__ float finished(const Finish& e, int dt, int64_t row, 
     return r;
   }
   const float h = e.bias ? __fadd_rn(s, load_as(e.bias, e.bias_dt, col)) : s;
-  by_activation(e.act, [&](auto act) { r = activated<act.value>(h); });
+  by_activation(e.act, [&](auto act) { r = activated<act.value>(zr::Two(h, h)).lo(); });
   if (e.residual) r = __fadd_rn(r, load_as(e.residual, dt, row * e.ldr + col));
   if (e.pre) store_as(e.pre, dt, row * e.ldp + col, h);
   return r;
 }
 
-// The values of 128 bytes of a row from column col on, `left` of them in the row, as fp32.
-template <int DT>
-__device__ __forceinline__ void load_row(const void* p, int64_t at, int left, bool vec, float* f) {
-  constexpr int es = DT == zr::DT_F32 ? 4 : 2, kCols = 128 / es;
-  const char* from = static_cast<const char*>(p) + at * es;
-  if (vec && left >= kCols) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint4 u = *reinterpret_cast<const uint4*>(from + 16 * j);
-      if constexpr (DT == zr::DT_F32) {
-        f[4 * j] = __uint_as_float(u.x), f[4 * j + 1] = __uint_as_float(u.y);
-        f[4 * j + 2] = __uint_as_float(u.z), f[4 * j + 3] = __uint_as_float(u.w);
-      } else {
-        zr::unpack8<DT>(u, f + 8 * j);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kCols; ++i) f[i] = i < left ? zr::load1<DT>(from, i) : 0.0f;
-  }
-}
-
-template <bool PAIR>
+template <bool PAIR, bool EPI>
 struct Gemm {
+  // With an epilogue eight warps bring the results out, two to the same lanes, each half of a tile's columns:
+  // its loads and exponentials would keep four longer than the products take.
+  static constexpr int kOutWarps = EPI ? 8 : 4, kThreads = 64 + 32 * kOutWarps;
   static constexpr int kTiles = PAIR ? 2 : 1;                       // MX4 tiles along M and along N
   static constexpr int kRows = 128 * kTiles, kCols = 128 * kTiles;  // output tile
   // a stage: A codes and scales, this block's B codes, the scales of all of the tile's B rows
   static constexpr int kBCodes = zr::kMxTileBytes, kBScales = kBCodes + zr::kMxCodeBytes;
   static constexpr int kStageBytes = kBScales + kTiles * zr::kMxScaleBytes;
-  static constexpr int kStages = PAIR ? 6 : 5;
+  static constexpr int kStages = PAIR && !EPI ? 6 : 5;
   // Tensor memory: two accumulators of kCols columns, 8 columns of A's scales, 8 for each tile of B's.
   // The pair's accumulators share 24 columns, or the scales would find no room in the 512: those are
   // read first, and the next tile's products wait for them alone.
@@ -187,8 +168,9 @@ struct Gemm {
   static constexpr int kLag = PAIR ? 1 : 2;   // an accumulator waits for the one so many turns before it
   // an epilogue warp's rows on their way out, 4 KB a time: a block alone has the room for three times,
   // so that it need not wait for each copy (a third of a short product); between a pair's tiles there is time
-  static constexpr int kOutBuffers = PAIR ? 1 : 3, kOutBytes = 32 * 128;
-  static constexpr int kSmem = kStages * kStageBytes + kOutWarps * kOutBuffers * kOutBytes + 256;
+  static constexpr int kOutBuffers = PAIR || EPI ? 1 : 3, kOutBytes = 32 * 128;
+  static constexpr int kBiasBytes = EPI ? 256 : 0;  // of each such warp: a chunk's bias
+  static constexpr int kSmem = kStages * kStageBytes + kOutWarps * (kOutBuffers * kOutBytes + kBiasBytes) + 256;
 };
 
 struct GemmArgs {
@@ -286,6 +268,89 @@ __device__ __forceinline__ void rows_out(const GemmArgs& g, void* to, int64_t ld
   __syncwarp();
 }
 
+// What a warp's 32 rows of 128 bytes take in from another matrix (a residual, a stored h), asked for before the
+// accumulators are there: a row by eight lanes, which a pass through the staging rows then gives each lane its own
+// of. Where those are not whole 16-byte words, they are read when they are needed.
+template <int DT>
+struct Incoming {
+  static constexpr int es = DT == zr::DT_F32 ? 4 : 2, kCols = 128 / es;
+  const char* from;  // row 0, column 0 of the matrix; null: nothing comes in
+  int64_t ld;
+  bool vec;
+  uint4 u[8];
+  __device__ Incoming(const Finish& e)
+      : from(static_cast<const char*>(e.gradient ? e.pre : e.residual)), ld(e.gradient ? e.ldp : e.ldr),
+        vec(e.gradient ? e.vec_pre : e.vec_residual) {}
+  __device__ bool whole(const GemmArgs& g, int64_t col) const { return vec && (col + kCols <= g.N || g.N * es % 16 == 0); }
+  __device__ void ask(const GemmArgs& g, int64_t row0, int64_t col) {
+    if (!from || !whole(g, col)) return;
+    const int lane = threadIdx.x & 31, r0 = lane >> 3;
+    const int64_t c = col + (lane & 7) * (16 / es);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t row = row0 + r0 + 4 * i;
+      u[i] = row < g.M && c < g.N ? *reinterpret_cast<const uint4*>(from + (row * ld + c) * es) : make_uint4(0, 0, 0, 0);
+    }
+  }
+  // Leaves this lane's row in u.
+  __device__ void take(const GemmArgs& g, char* stage, int64_t row0, int64_t col) {
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) zr::stores_read<0>();  // the copy that used the staging rows last has read them
+    __syncwarp();
+    if (whole(g, col)) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = (lane >> 3) + 4 * i;
+        *reinterpret_cast<uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4)) = u[i];
+      }
+    } else {
+      using T = typename std::conditional<DT == zr::DT_F32, uint32_t, uint16_t>::type;
+      const T* x = reinterpret_cast<const T*>(from) + row0 * ld + col;
+      const int rows = (int)(g.M - row0 < 32 ? g.M - row0 : 32), left = (int)(g.N - col < kCols ? g.N - col : kCols);
+#pragma unroll 8
+      for (int r = 0; r < 32; ++r) {
+#pragma unroll
+        for (int i = lane; i < kCols; i += 32)
+          *reinterpret_cast<T*>(stage + r * 128 + ((i * es) ^ ((r & 7) << 4))) = r < rows && i < left ? x[r * ld + i] : T(0);
+      }
+    }
+    __syncwarp();
+    const uint4* mine = reinterpret_cast<const uint4*>(stage + lane * 128);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) u[j] = mine[j ^ (lane & 7)];
+    __syncwarp();
+  }
+  __device__ void open(int j, float* f) const {  // the values of word j
+    if constexpr (DT == zr::DT_F32) {
+      f[0] = __uint_as_float(u[j].x), f[1] = __uint_as_float(u[j].y);
+      f[2] = __uint_as_float(u[j].z), f[3] = __uint_as_float(u[j].w);
+    } else {
+      zr::unpack8<DT>(u[j], f);
+    }
+  }
+};
+
+// The bias of a chunk of N columns from col on, asked for early as well: a lane's own, then all in shared memory.
+template <int N>
+struct Bias {
+  static constexpr int kEach = N / 32;
+  float mine[kEach];
+  __device__ void ask(const Finish& e, const GemmArgs& g, int64_t col) {
+    if (!e.bias) return;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int64_t c = col + (threadIdx.x & 31) + 32 * i;
+      mine[i] = c < g.N ? load_as(e.bias, e.bias_dt, c) : 0.0f;
+    }
+  }
+  __device__ void share(float* to) const {
+    __syncwarp();  // the last chunk's has been read
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) to[(threadIdx.x & 31) + 32 * i] = mine[i];
+    __syncwarp();
+  }
+};
+
 // A tile of which each block of a cluster has the products of a part of K, in its shared memory: the
 // blocks take its rows in equal shares, add the parts in the order of the blocks and store them. 64 x
 // 2048 x 8192 to bf16 in 6.4 us by fours, 9.5 by blocks alone; two waits of the cluster and 64 KB through
@@ -324,7 +389,7 @@ __device__ __forceinline__ void join_parts(const GemmArgs& g, const FinishOf<EPI
         if (col + i < g.N) out[i] = u[i];
     }
   };
-  constexpr int kWarps = kGemmThreads / 32, kOnce = S == 2 ? 8 : 2;  // a warp's rows on their way together
+  constexpr int kWarps = Gemm<false, EPI>::kThreads / 32, kOnce = S == 2 ? 8 : 2;  // a warp's rows on their way together
   float4 p[kOnce][S];
   for (int r0 = rank * share + warp; r0 < end; r0 += kOnce * kWarps) {
 #pragma unroll
@@ -351,6 +416,14 @@ __device__ __forceinline__ void join_parts(const GemmArgs& g, const FinishOf<EPI
   }
 }
 
+struct NothingIn {
+  __device__ explicit NothingIn(const NoFinish&) {}
+};
+template <bool EPI, int DT>
+using IncomingOf = typename std::conditional<EPI, Incoming<DT>, NothingIn>::type;
+template <bool EPI, int N>
+using BiasOf = typename std::conditional<EPI, Bias<N>, NoFinish>::type;
+
 template <bool PAIR>
 using Maps = typename std::conditional<PAIR, PairMaps, OutMap>::type;
 // How a stored h is stored, as the output is.
@@ -358,14 +431,14 @@ template <bool EPI>
 using PreMap = typename std::conditional<EPI, OutMap, NoFinish>::type;
 
 template <bool PAIR, int DT, bool EPI>
-__global__ void __launch_bounds__(kGemmThreads, 1)
+__global__ void __launch_bounds__(Gemm<PAIR, EPI>::kThreads, 1)
     gemm_kernel(const __grid_constant__ GemmArgs g, const __grid_constant__ Maps<PAIR> maps,
                 const __grid_constant__ FinishOf<EPI> e, const __grid_constant__ PreMap<EPI> pre_map) {
-  using G = Gemm<PAIR>;
+  using G = Gemm<PAIR, EPI>;
   extern __shared__ __align__(kSwizzle) char smem[];
   const uint32_t stages = zr::smem_u32(smem);
   char* staging = smem + G::kStages * G::kStageBytes;  // (a multiple of the swizzle, too)
-  char* tail = staging + kOutWarps * G::kOutBuffers * G::kOutBytes;
+  char* tail = staging + G::kOutWarps * (G::kOutBuffers * G::kOutBytes + G::kBiasBytes);
   // full: a stage's copies have landed (a pair's, in both blocks: the first block's barrier counts them
   // all); empty: its products are done; done: an accumulator is complete; freed: the turn kLag later
   // may begin
@@ -389,7 +462,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     for (int d = 0; d < 2; ++d) {
       zr::bar_init(done + 8 * d, 1);
-      zr::bar_init(freed + 8 * d, G::kTiles * kOutWarps);
+      zr::bar_init(freed + 8 * d, G::kTiles * G::kOutWarps);
     }
     zr::bar_init(drained, 1);
     zr::bar_init_fence();
@@ -512,7 +585,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
   } else {
     const int lanes = (warp & 3) * 32;  // the lanes of tensor memory that this warp may read
-    char* stage = staging + (warp & 3) * G::kOutBuffers * G::kOutBytes;
+    char* stage = staging + (warp - 2) * G::kOutBuffers * G::kOutBytes;
     int buffer = 0;
     constexpr int kOnce = DT == zr::DT_F32 ? 32 : 64, kChunks = G::kCols / kOnce;
     auto tell = [&](uint32_t bar) {  // the thread that issues the products
@@ -525,27 +598,45 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           zr::bar_arrive(bar);
       }
     };
+    IncomingOf<EPI, DT> incoming(e);
+    BiasOf<EPI, kOnce> bias;
+    float* bias_at = reinterpret_cast<float*>(staging + G::kOutWarps * G::kOutBuffers * G::kOutBytes + (warp - 2) * G::kBiasBytes);
+    auto get2 = [](const uint32_t* w) { return zr::Two(__uint_as_float(w[0]), __uint_as_float(w[1])); };
+    auto set2 = [](uint32_t* w, zr::Two f) { w[0] = __float_as_uint(f.lo()), w[1] = __float_as_uint(f.hi()); };
     uint32_t turn = 0;
     zr::wait_for_previous();
     for (int id = first; id < tiles; id += step, ++turn) {
       const Tile t = tile_of(g, id);
-      if (!__all_sync(0xFFFFFFFFu, zr::bar_wait(done + 8 * (turn & 1), (turn >> 1) & 1, gave_up))) break;
-      zr::tmem_fence_after();
       const uint32_t d = tmem + (turn & 1) * G::kD1 + ((uint32_t)lanes << 16);
       const int64_t row0 = (int64_t)t.m * G::kRows + (PAIR ? rank * 128 : 0) + lanes;
       const int64_t col0 = (int64_t)t.n * G::kCols + (t.half == 1 ? 128 : 0);
-      const int chunks = PAIR && t.half >= 0 ? kChunks / 2 : kChunks;
+      const int chunks = (PAIR && t.half >= 0 ? kChunks / 2 : kChunks) / (EPI ? 2 : 1);
+      const int chunk0 = EPI ? ((warp - 2) >> 2) * chunks : 0;  // two warps to the same lanes take half of them each
+      // the first accumulator's last columns are the second's first
+      auto chunk = [&](int c) { return chunk0 + ((turn & 1) ? c : chunks - 1 - c); };
+      auto live = [&](int64_t col) { return !split && row0 < g.M && col < g.N; };
+      if constexpr (EPI) {
+        const int64_t col = col0 + chunk(0) * kOnce;
+        if (live(col)) incoming.ask(g, row0, col), bias.ask(e, g, col);
+      }
+      if (!__all_sync(0xFFFFFFFFu, zr::bar_wait(done + 8 * (turn & 1), (turn >> 1) & 1, gave_up))) break;
+      zr::tmem_fence_after();
 #pragma unroll 1
       for (int c = 0; c < chunks; ++c) {
-        // the first accumulator's last columns are the second's first
-        const int at = (turn & 1) ? c : chunks - 1 - c;
+        const int at = chunk(c);
         const int64_t col = col0 + at * kOnce;
+        if constexpr (EPI) {
+          if (live(col)) {
+            if (incoming.from) incoming.take(g, stage, row0, col);
+            if (e.bias) bias.share(bias_at);
+          }
+        }
         uint32_t v[kOnce];
         if constexpr (kOnce == 32)
           zr::tmem_load32(d + at * kOnce, v);
         else
           zr::tmem_load64(d + at * kOnce, v);
-        if (c == (PAIR ? 0 : kChunks - 1)) tell(freed + 8 * (turn & 1));
+        if (c == (PAIR ? 0 : chunks - 1)) tell(freed + 8 * (turn & 1));
         if constexpr (EPI) {
           if (g.kt == 0) {  // a sum of nothing
 #pragma unroll
@@ -562,37 +653,50 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             buffer = buffer + 1 < G::kOutBuffers ? buffer + 1 : 0;
           };
           if constexpr (EPI) {
-            const int64_t row = row0 + (threadIdx.x & 31);
-            const int left = (int)(g.N - col < kOnce ? g.N - col : kOnce);
+            constexpr int per = DT == zr::DT_F32 ? 4 : 8;
             if (e.gradient) {
-              float h[kOnce];
-              load_row<DT>(e.pre, row * e.ldp + col, row < g.M ? left : 0, e.vec_pre, h);
               by_activation(e.act, [&](auto act) {
 #pragma unroll
-                for (int i = 0; i < kOnce; ++i) v[i] = __float_as_uint(__fmul_rn(__uint_as_float(v[i]), slope<act.value>(h[i])));
+                for (int j = 0; j < 8; ++j) {
+                  float h[per];
+                  incoming.open(j, h);
+#pragma unroll
+                  for (int i = 0; i < per; ++i)
+                    v[per * j + i] = __float_as_uint(__fmul_rn(__uint_as_float(v[per * j + i]), slope<act.value>(h[i])));
+                }
               });
             } else {
               if (e.bias) {
-                float b[kOnce];
 #pragma unroll
-                for (int i = 0; i < kOnce; ++i) b[i] = i < left ? load_as(e.bias, e.bias_dt, col + i) : 0.0f;
-#pragma unroll
-                for (int i = 0; i < kOnce; ++i) v[i] = __float_as_uint(__fadd_rn(__uint_as_float(v[i]), b[i]));
+                for (int i = 0; i < kOnce; i += 4) {
+                  const float4 b = *reinterpret_cast<const float4*>(bias_at + i);
+                  set2(v + i, zr::add2(get2(v + i), zr::Two(b.x, b.y)));
+                  set2(v + i + 2, zr::add2(get2(v + i + 2), zr::Two(b.z, b.w)));
+                }
               }
               if (e.pre) store(e.pre, e.ldp, &pre_map.out);
               by_activation(e.act, [&](auto act) {
 #pragma unroll
-                for (int i = 0; i < kOnce; ++i) v[i] = __float_as_uint(activated<act.value>(__uint_as_float(v[i])));
+                for (int i = 0; i < kOnce; i += 2) set2(v + i, activated<act.value>(get2(v + i)));
               });
               if (e.residual) {
-                float r[kOnce];
-                load_row<DT>(e.residual, row * e.ldr + col, row < g.M ? left : 0, e.vec_residual, r);
 #pragma unroll
-                for (int i = 0; i < kOnce; ++i) v[i] = __float_as_uint(__fadd_rn(__uint_as_float(v[i]), r[i]));
+                for (int j = 0; j < 8; ++j) {
+                  float r[per];
+                  incoming.open(j, r);
+#pragma unroll
+                  for (int i = 0; i < per; i += 2) set2(v + per * j + i, zr::add2(get2(v + per * j + i), zr::Two(r[i], r[i + 1])));
+                }
               }
             }
           }
           store(g.out, g.ldo, &maps.out);
+        }
+        if constexpr (EPI) {
+          if (c + 1 < chunks) {  // the next chunk's, while this one is stored
+            const int64_t next = col0 + chunk(c + 1) * kOnce;
+            if (live(next)) incoming.ask(g, row0, next), bias.ask(e, g, next);
+          }
         }
       }
     }
@@ -907,7 +1011,7 @@ bool encode_out(CUtensorMap* map, const GemmArgs& g, void* out, int64_t ld, int 
 template <bool PAIR, int DT, bool EPI>
 zr_status launch_gemm(const char* what, const GemmArgs& g, const FinishOf<EPI>& e, int blocks, cudaStream_t s) {
   static zr::SmemAllowance allowance;
-  if (zr_status st = allowance.allow(what, (const void*)gemm_kernel<PAIR, DT, EPI>, Gemm<PAIR>::kSmem)) return st;
+  if (zr_status st = allowance.allow(what, (const void*)gemm_kernel<PAIR, DT, EPI>, Gemm<PAIR, EPI>::kSmem)) return st;
   Maps<PAIR> maps;
   PreMap<EPI> pre;
   bool encoded = map_encoder() && (!g.vec || encode_out(&maps.out, g, g.out, g.ldo, DT));
@@ -923,7 +1027,7 @@ zr_status launch_gemm(const char* what, const GemmArgs& g, const FinishOf<EPI>& 
     }
   }
   if (!encoded) return fail(ZR_ERR_CUDA, "%s: the driver gave no tensor map", what);
-  cudaError_t err = zr::launch(gemm_kernel<PAIR, DT, EPI>, blocks, kGemmThreads, Gemm<PAIR>::kSmem, PAIR ? 2 : g.split, true, s,
+  cudaError_t err = zr::launch(gemm_kernel<PAIR, DT, EPI>, blocks, Gemm<PAIR, EPI>::kThreads, Gemm<PAIR, EPI>::kSmem, PAIR ? 2 : g.split, true, s,
                                g, maps, e, pre);
   if (err != cudaSuccess) return fail(ZR_ERR_CUDA, "%s: launch failed: %s", what, cudaGetErrorString(err));
   return ZR_OK;
