@@ -37,29 +37,47 @@ __global__ void __launch_bounds__(kThreads) column_kernel(const __grid_constant_
   const int left = (int)(a.N - col < PER ? (a.N > col ? a.N - col : 0) : PER);
   const char* x = static_cast<const char*>(a.x) + col * es;
   float sum[PER] = {};
-  for (int64_t r = first + r0; r < end; r += kOnce * kRows) {
-    float v[kOnce][PER];
+  auto add = [&](const float v[PER]) {
 #pragma unroll
-    for (int i = 0; i < kOnce; ++i) {
-      const int64_t row = r + i * kRows;
-      const char* from = x + row * a.ld * es;
-      if (PER > 1 && left == PER && row < end) {
-        const uint4 u = zr::ld_once(from);
-        if constexpr (PER == 8) {
-          zr::unpack8<DT>(u, v[i]);
-        } else if constexpr (PER == 4) {
-          v[i][0] = __uint_as_float(u.x), v[i][1] = __uint_as_float(u.y);
-          v[i][2] = __uint_as_float(u.z), v[i][3] = __uint_as_float(u.w);
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < PER; ++k) v[i][k] = row < end && k < left ? zr::load1<DT>(from, k) : 0.0f;
-      }
+    for (int k = 0; k < PER; ++k) sum[k] = __fadd_rn(sum[k], v[k]);
+  };
+  auto open = [&](uint4 u) {
+    float v[PER];
+    if constexpr (PER == 8) {
+      zr::unpack8<DT>(u, v);
+    } else if constexpr (PER == 4) {
+      v[0] = __uint_as_float(u.x), v[1] = __uint_as_float(u.y), v[2] = __uint_as_float(u.z), v[3] = __uint_as_float(u.w);
     }
+    add(v);
+  };
+  const int64_t step = a.ld * es * kRows;
+  const char* from = x + (first + r0) * a.ld * es;
+  int64_t r = first + r0;
+  if (PER > 1 && left == PER) {
+    for (; r + (kOnce - 1) * kRows < end; r += kOnce * kRows, from += kOnce * step) {
+      uint4 u[kOnce];
 #pragma unroll
-    for (int i = 0; i < kOnce; ++i)
+      for (int i = 0; i < kOnce; ++i) u[i] = zr::ld_once(from + i * step);
 #pragma unroll
-      for (int k = 0; k < PER; ++k) sum[k] = __fadd_rn(sum[k], v[i][k]);
+      for (int i = 0; i < kOnce; ++i) open(u[i]);
+    }
+    for (; r < end; r += kRows, from += step) open(zr::ld_once(from));
+  } else if (left > 0) {
+    for (; r + (kOnce - 1) * kRows < end; r += kOnce * kRows, from += kOnce * step) {
+      float v[kOnce][PER];
+#pragma unroll
+      for (int i = 0; i < kOnce; ++i)
+#pragma unroll
+        for (int k = 0; k < PER; ++k) v[i][k] = k < left ? zr::load1<DT>(from + i * step, k) : 0.0f;
+#pragma unroll
+      for (int i = 0; i < kOnce; ++i) add(v[i]);
+    }
+    for (; r < end; r += kRows, from += step) {
+      float v[PER];
+#pragma unroll
+      for (int k = 0; k < PER; ++k) v[k] = k < left ? zr::load1<DT>(from, k) : 0.0f;
+      add(v);
+    }
   }
 #pragma unroll
   for (int k = 0; k < PER; ++k) parts[r0 * kCols + lane * PER + k] = sum[k];
