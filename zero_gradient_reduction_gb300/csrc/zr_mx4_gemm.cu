@@ -97,18 +97,39 @@ __device__ __forceinline__ zr::Two activated(zr::Two h) {
     return zr::mul2(h, zr::Two(reciprocal(d.lo()), reciprocal(d.hi())));
   }
 }
-// The derivative, S + h S (1 - S) u': S and 1 - S from the side of u that does not overflow, 0 or 1 far out.
+__device__ __forceinline__ float clamped(float x, float most) {  // NaN stays
+  float y;
+  asm("{\n .reg .f32 t;\n min.NaN.f32 t, %1, %2;\n max.NaN.f32 %0, t, %3;\n}\n" : "=f"(y) : "f"(x), "f"(most), "f"(-most));
+  return y;
+}
+__device__ __forceinline__ float at_most(float x, float most) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(most));
+  return y;
+}
+// The derivative, S + h S (1 - S) u', with 1 - S = S 2^x, which does not cancel. Past 100 it has long been 0 or 1, and
+// what would overflow on the way is kept from it.
 template <int ACT>
-__device__ __forceinline__ float slope(float h) {
-  if constexpr (ACT == ZR_ACT_NONE) return 1.0f;
-  const float far = h > 0.0f ? 1.0f : h <= 0.0f ? 0.0f : h;
-  if constexpr (ACT == ZR_ACT_RELU) return far;
-  const float h2 = __fmul_rn(h, h);
-  const float x = __fmul_rn(h, ACT == ZR_ACT_GELU ? __fmaf_rn(h2, kGelu3, kGelu1) : kSilu1);
-  const float du = ACT == ZR_ACT_GELU ? __fmul_rn(__fmaf_rn(h2, 3.0f * kGelu3, kGelu1), -zr::kLn2) : 1.0f;
-  const float t = zr::exp2_fast(-fabsf(x)), p = reciprocal(1.0f + t), q = __fmul_rn(t, p);
-  const float up = h >= 0.0f ? p : q;  // (x has the other sign of h)
-  return fabsf(h) < 100.0f ? __fmaf_rn(__fmul_rn(h, __fmul_rn(p, q)), du, up) : far;
+__device__ __forceinline__ zr::Two slope(zr::Two h) {
+  const zr::Two one(1.0f, 1.0f);
+  if constexpr (ACT == ZR_ACT_NONE) {
+    return one;
+  } else if constexpr (ACT == ZR_ACT_RELU) {
+    auto step = [](float f) { return f > 0.0f ? 1.0f : f <= 0.0f ? 0.0f : f; };
+    return zr::Two(step(h.lo()), step(h.hi()));
+  } else {
+    constexpr bool kGelu = ACT == ZR_ACT_GELU;
+    const zr::Two k1(kGelu ? kGelu1 : kSilu1, kGelu ? kGelu1 : kSilu1), k3(kGelu3, kGelu3);
+    h = zr::Two(clamped(h.lo(), 100.0f), clamped(h.hi(), 100.0f));
+    const zr::Two h2 = zr::mul2(h, h), x = zr::mul2(h, kGelu ? zr::fma2(h2, k3, k1) : k1);
+    const zr::Two t(zr::exp2_fast(at_most(x.lo(), 120.0f)), zr::exp2_fast(at_most(x.hi(), 120.0f)));
+    const zr::Two d = zr::add2(t, one), up(reciprocal(d.lo()), reciprocal(d.hi()));
+    constexpr float kTurn = -0.693147180559945309417f;  // from exponents of 2 back to u
+    const zr::Two du3(3.0f * kGelu3 * kTurn, 3.0f * kGelu3 * kTurn), du1(kGelu1 * kTurn, kGelu1 * kTurn);
+    zr::Two r = zr::mul2(h, zr::mul2(up, zr::mul2(t, up)));
+    if (kGelu) r = zr::mul2(r, zr::fma2(h2, du3, du1));
+    return zr::add2(r, up);
+  }
 }
 
 __device__ __forceinline__ float load_as(const void* p, int dt, int64_t i) {
@@ -140,7 +161,7 @@ __device__ __forceinline__ float finished(const Finish& e, int dt, int64_t row, 
   float r = s;
   if (e.gradient) {
     const float h = load_as(e.pre, dt, row * e.ldp + col);
-    by_activation(e.act, [&](auto act) { r = __fmul_rn(s, slope<act.value>(h)); });
+    by_activation(e.act, [&](auto act) { r = __fmul_rn(s, slope<act.value>(zr::Two(h, h)).lo()); });
     return r;
   }
   const float h = e.bias ? __fadd_rn(s, load_as(e.bias, e.bias_dt, col)) : s;
@@ -150,26 +171,29 @@ __device__ __forceinline__ float finished(const Finish& e, int dt, int64_t row, 
   return r;
 }
 
-template <bool PAIR, bool EPI>
+template <bool PAIR, bool EPI, int DT>
 struct Gemm {
-  // With an epilogue eight warps bring the results out, two to the same lanes, each half of a tile's columns:
-  // its loads and exponentials would keep four longer than the products take.
-  static constexpr int kOutWarps = EPI ? 8 : 4, kThreads = 64 + 32 * kOutWarps;
+  // With an epilogue sixteen warps bring the results out, four to the same lanes, a quarter of a tile's columns
+  // each: its loads and exponentials would keep fewer longer than the products take (8192 x 2048 -> 8192 to bf16
+  // with bias, GELU and pre EIGHT_US us with eight).
+  static constexpr int kOutWarps = EPI ? 16 : 4, kSides = kOutWarps / 4, kThreads = 64 + 32 * kOutWarps;
   static constexpr int kTiles = PAIR ? 2 : 1;                       // MX4 tiles along M and along N
   static constexpr int kRows = 128 * kTiles, kCols = 128 * kTiles;  // output tile
   // a stage: A codes and scales, this block's B codes, the scales of all of the tile's B rows
   static constexpr int kBCodes = zr::kMxTileBytes, kBScales = kBCodes + zr::kMxCodeBytes;
   static constexpr int kStageBytes = kBScales + kTiles * zr::kMxScaleBytes;
-  static constexpr int kStages = PAIR && !EPI ? 6 : 5;
+  static constexpr int kStages = EPI ? (DT == zr::DT_F32 ? 4 : 5) : PAIR ? 6 : 5;
   // Tensor memory: two accumulators of kCols columns, 8 columns of A's scales, 8 for each tile of B's.
   // The pair's accumulators share 24 columns, or the scales would find no room in the 512: those are
   // read first, and the next tile's products wait for them alone.
   static constexpr int kD1 = PAIR ? 232 : 128, kScaleA = PAIR ? 488 : 256, kScaleB = kScaleA + 8;
   static constexpr int kLag = PAIR ? 1 : 2;   // an accumulator waits for the one so many turns before it
   // an epilogue warp's rows on their way out, 4 KB a time: a block alone has the room for three times,
-  // so that it need not wait for each copy (a third of a short product); between a pair's tiles there is time
-  static constexpr int kOutBuffers = PAIR || EPI ? 1 : 3, kOutBytes = 32 * 128;
-  static constexpr int kBiasBytes = EPI ? 256 : 0;  // of each such warp: a chunk's bias
+  // so that it need not wait for each copy (a third of a short product); between a pair's tiles there is time.
+  // With an epilogue 32 columns at a time, of 16-bit values 2 KB.
+  static constexpr int kRowBytes = EPI && DT != zr::DT_F32 ? 64 : 128;
+  static constexpr int kOutBuffers = PAIR || EPI ? 1 : 3, kOutBytes = 32 * kRowBytes;
+  static constexpr int kBiasBytes = EPI ? 128 : 0;  // of each such warp: a chunk's bias
   static constexpr int kSmem = kStages * kStageBytes + kOutWarps * (kOutBuffers * kOutBytes + kBiasBytes) + 256;
 };
 
@@ -193,7 +217,7 @@ constexpr int kTileLines = zr::kMxTileBytes / 128;
 struct PairMaps {
   CUtensorMap out, a_tile, b_codes, b_half, b_scales;
 };
-// The output as a box of 32 rows of 128 bytes takes it, swizzled (unused where vec is 0).
+// The output as a box of 32 rows of staging takes it, swizzled (unused where vec is 0).
 struct OutMap {
   CUtensorMap out;
 };
@@ -220,29 +244,35 @@ __device__ __forceinline__ Tile tile_of(const GemmArgs& g, int id) {
 }
 __device__ __forceinline__ int tile_count(const GemmArgs& g) { return 2 * g.mt * g.nt - g.whole; }
 
-// The values of 128 bytes of 32 rows, a row in each lane's registers, to memory. They go through this
-// warp's staging rows in the order of the 128-byte swizzle (16-byte word j of a row at j ^ (row % 8),
-// so that no two lanes write to a bank), from where one copy takes them; where the rows of out do not
-// begin on 16-byte boundaries, a row at a time by the lanes.
-template <int DT, int BUFFERS>
+// Where the 16-byte word j of row r lies among staging rows of ROW (128 or 64) bytes: in the order of the copies'
+// swizzle of that length, so that no two lanes that have a row each meet in a bank.
+template <int ROW>
+__device__ __forceinline__ int staged_at(int r, int j) {
+  return r * ROW + ((ROW == 128 ? j ^ (r & 7) : j ^ ((r >> 1) & 3)) << 4);
+}
+
+// The values of ROW bytes of 32 rows, a row in each lane's registers, to memory. They go through this
+// warp's staging rows, from where one copy takes them; where the rows of out do not begin on 16-byte
+// boundaries, a row at a time by the lanes.
+template <int DT, int BUFFERS, int ROW>
 __device__ __forceinline__ void rows_out(const GemmArgs& g, void* to, int64_t ld, const CUtensorMap* map, char* stage,
                                          const uint32_t* v, int64_t row0, int64_t col) {
-  constexpr int es = DT == zr::DT_F32 ? 4 : 2, kCols = 128 / es;
+  constexpr int es = DT == zr::DT_F32 ? 4 : 2, kCols = ROW / es;
   const int lane = threadIdx.x & 31;
   if (g.vec) {  // the copy that used these staging rows last has read them
     if (lane == 0) zr::stores_read<BUFFERS - 1>();
     __syncwarp();
   }
-  uint4* mine = reinterpret_cast<uint4*>(stage + lane * 128);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int j = 0; j < ROW / 16; ++j) {
+    uint4& word = *reinterpret_cast<uint4*>(stage + staged_at<ROW>(lane, j));
     if (DT == zr::DT_F32) {
-      mine[j ^ (lane & 7)] = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+      word = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
     } else {
       float f[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[8 * j + i]);
-      mine[j ^ (lane & 7)] = zr::pack8<DT == zr::DT_F32 ? zr::DT_BF16 : DT>(f);
+      word = zr::pack8<DT == zr::DT_F32 ? zr::DT_BF16 : DT>(f);
     }
   }
   if (g.vec && (col + kCols <= g.N || g.N * es % 16 == 0)) {  // (copies write whole 16-byte words)
@@ -262,33 +292,33 @@ __device__ __forceinline__ void rows_out(const GemmArgs& g, void* to, int64_t ld
 #pragma unroll
     for (int i = 0; i < kEach; ++i)
       if (r < rows && 32 * i < left)
-        out[32 * i] = *reinterpret_cast<const T*>(stage + r * 128 + (((lane + 32 * i) * es) ^ ((r & 7) << 4)));
+        out[32 * i] = *reinterpret_cast<const T*>(stage + staged_at<ROW>(r, (lane + 32 * i) * es >> 4) + ((lane + 32 * i) * es & 15));
   }
   if (g.vec && lane == 0) zr::no_store();  // the staging rows' turns are counted in stores
   __syncwarp();
 }
 
-// What a warp's 32 rows of 128 bytes take in from another matrix (a residual, a stored h), asked for before the
-// accumulators are there: a row by eight lanes, which a pass through the staging rows then gives each lane its own
+// What a warp's 32 rows of 32 columns take in from another matrix (a residual, a stored h), asked for before the
+// accumulators are there: a row by 4 or 8 lanes, which a pass through the staging rows then gives each lane its own
 // of. Where those are not whole 16-byte words, they are read when they are needed.
 template <int DT>
 struct Incoming {
-  static constexpr int es = DT == zr::DT_F32 ? 4 : 2, kCols = 128 / es;
+  static constexpr int es = DT == zr::DT_F32 ? 4 : 2, kCols = 32, kRow = kCols * es, kWords = kRow / 16, per = 16 / es;
   const char* from;  // row 0, column 0 of the matrix; null: nothing comes in
   int64_t ld;
   bool vec;
-  uint4 u[8];
+  uint4 u[kWords];
   __device__ Incoming(const Finish& e)
       : from(static_cast<const char*>(e.gradient ? e.pre : e.residual)), ld(e.gradient ? e.ldp : e.ldr),
         vec(e.gradient ? e.vec_pre : e.vec_residual) {}
   __device__ bool whole(const GemmArgs& g, int64_t col) const { return vec && (col + kCols <= g.N || g.N * es % 16 == 0); }
   __device__ void ask(const GemmArgs& g, int64_t row0, int64_t col) {
     if (!from || !whole(g, col)) return;
-    const int lane = threadIdx.x & 31, r0 = lane >> 3;
-    const int64_t c = col + (lane & 7) * (16 / es);
+    const int lane = threadIdx.x & 31;
+    const int64_t c = col + lane % kWords * per;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t row = row0 + r0 + 4 * i;
+    for (int i = 0; i < kWords; ++i) {
+      const int64_t row = row0 + lane / kWords + 32 / kWords * i;
       u[i] = row < g.M && c < g.N ? *reinterpret_cast<const uint4*>(from + (row * ld + c) * es) : make_uint4(0, 0, 0, 0);
     }
   }
@@ -299,25 +329,20 @@ struct Incoming {
     __syncwarp();
     if (whole(g, col)) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = (lane >> 3) + 4 * i;
-        *reinterpret_cast<uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4)) = u[i];
-      }
+      for (int i = 0; i < kWords; ++i)
+        *reinterpret_cast<uint4*>(stage + staged_at<kRow>(lane / kWords + 32 / kWords * i, lane % kWords)) = u[i];
     } else {
       using T = typename std::conditional<DT == zr::DT_F32, uint32_t, uint16_t>::type;
-      const T* x = reinterpret_cast<const T*>(from) + row0 * ld + col;
+      const T* x = reinterpret_cast<const T*>(from) + row0 * ld + col + lane;
       const int rows = (int)(g.M - row0 < 32 ? g.M - row0 : 32), left = (int)(g.N - col < kCols ? g.N - col : kCols);
 #pragma unroll 8
-      for (int r = 0; r < 32; ++r) {
-#pragma unroll
-        for (int i = lane; i < kCols; i += 32)
-          *reinterpret_cast<T*>(stage + r * 128 + ((i * es) ^ ((r & 7) << 4))) = r < rows && i < left ? x[r * ld + i] : T(0);
-      }
+      for (int r = 0; r < 32; ++r)
+        *reinterpret_cast<T*>(stage + staged_at<kRow>(r, lane * es >> 4) + (lane * es & 15)) =
+            r < rows && lane < left ? x[r * ld] : T(0);
     }
     __syncwarp();
-    const uint4* mine = reinterpret_cast<const uint4*>(stage + lane * 128);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) u[j] = mine[j ^ (lane & 7)];
+    for (int j = 0; j < kWords; ++j) u[j] = *reinterpret_cast<const uint4*>(stage + staged_at<kRow>(lane, j));
     __syncwarp();
   }
   __device__ void open(int j, float* f) const {  // the values of word j
@@ -330,23 +355,16 @@ struct Incoming {
   }
 };
 
-// The bias of a chunk of N columns from col on, asked for early as well: a lane's own, then all in shared memory.
-template <int N>
+// The bias of a chunk of 32 columns from col on, asked for early as well: a lane's own, then all in shared memory.
 struct Bias {
-  static constexpr int kEach = N / 32;
-  float mine[kEach];
+  float mine;
   __device__ void ask(const Finish& e, const GemmArgs& g, int64_t col) {
-    if (!e.bias) return;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int64_t c = col + (threadIdx.x & 31) + 32 * i;
-      mine[i] = c < g.N ? load_as(e.bias, e.bias_dt, c) : 0.0f;
-    }
+    const int64_t c = col + (threadIdx.x & 31);
+    if (e.bias) mine = c < g.N ? load_as(e.bias, e.bias_dt, c) : 0.0f;
   }
   __device__ void share(float* to) const {
     __syncwarp();  // the last chunk's has been read
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) to[(threadIdx.x & 31) + 32 * i] = mine[i];
+    to[threadIdx.x & 31] = mine;
     __syncwarp();
   }
 };
@@ -389,7 +407,7 @@ __device__ __forceinline__ void join_parts(const GemmArgs& g, const FinishOf<EPI
         if (col + i < g.N) out[i] = u[i];
     }
   };
-  constexpr int kWarps = Gemm<false, EPI>::kThreads / 32, kOnce = S == 2 ? 8 : 2;  // a warp's rows on their way together
+  constexpr int kWarps = Gemm<false, EPI, DT>::kThreads / 32, kOnce = S == 2 ? 8 : 2;  // a warp's rows on their way together
   float4 p[kOnce][S];
   for (int r0 = rank * share + warp; r0 < end; r0 += kOnce * kWarps) {
 #pragma unroll
@@ -421,8 +439,8 @@ struct NothingIn {
 };
 template <bool EPI, int DT>
 using IncomingOf = typename std::conditional<EPI, Incoming<DT>, NothingIn>::type;
-template <bool EPI, int N>
-using BiasOf = typename std::conditional<EPI, Bias<N>, NoFinish>::type;
+template <bool EPI>
+using BiasOf = typename std::conditional<EPI, Bias, NoFinish>::type;
 
 template <bool PAIR>
 using Maps = typename std::conditional<PAIR, PairMaps, OutMap>::type;
@@ -431,10 +449,10 @@ template <bool EPI>
 using PreMap = typename std::conditional<EPI, OutMap, NoFinish>::type;
 
 template <bool PAIR, int DT, bool EPI>
-__global__ void __launch_bounds__(Gemm<PAIR, EPI>::kThreads, 1)
+__global__ void __launch_bounds__(Gemm<PAIR, EPI, DT>::kThreads, 1)
     gemm_kernel(const __grid_constant__ GemmArgs g, const __grid_constant__ Maps<PAIR> maps,
                 const __grid_constant__ FinishOf<EPI> e, const __grid_constant__ PreMap<EPI> pre_map) {
-  using G = Gemm<PAIR, EPI>;
+  using G = Gemm<PAIR, EPI, DT>;
   extern __shared__ __align__(kSwizzle) char smem[];
   const uint32_t stages = zr::smem_u32(smem);
   char* staging = smem + G::kStages * G::kStageBytes;  // (a multiple of the swizzle, too)
@@ -587,7 +605,7 @@ __global__ void __launch_bounds__(Gemm<PAIR, EPI>::kThreads, 1)
     const int lanes = (warp & 3) * 32;  // the lanes of tensor memory that this warp may read
     char* stage = staging + (warp - 2) * G::kOutBuffers * G::kOutBytes;
     int buffer = 0;
-    constexpr int kOnce = DT == zr::DT_F32 ? 32 : 64, kChunks = G::kCols / kOnce;
+    constexpr int kOnce = EPI || DT == zr::DT_F32 ? 32 : 64, kChunks = G::kCols / kOnce;
     auto tell = [&](uint32_t bar) {  // the thread that issues the products
       zr::tmem_fence_before();
       __syncwarp();
@@ -599,7 +617,7 @@ __global__ void __launch_bounds__(Gemm<PAIR, EPI>::kThreads, 1)
       }
     };
     IncomingOf<EPI, DT> incoming(e);
-    BiasOf<EPI, kOnce> bias;
+    BiasOf<EPI> bias;
     float* bias_at = reinterpret_cast<float*>(staging + G::kOutWarps * G::kOutBuffers * G::kOutBytes + (warp - 2) * G::kBiasBytes);
     auto get2 = [](const uint32_t* w) { return zr::Two(__uint_as_float(w[0]), __uint_as_float(w[1])); };
     auto set2 = [](uint32_t* w, zr::Two f) { w[0] = __float_as_uint(f.lo()), w[1] = __float_as_uint(f.hi()); };
@@ -610,8 +628,8 @@ __global__ void __launch_bounds__(Gemm<PAIR, EPI>::kThreads, 1)
       const uint32_t d = tmem + (turn & 1) * G::kD1 + ((uint32_t)lanes << 16);
       const int64_t row0 = (int64_t)t.m * G::kRows + (PAIR ? rank * 128 : 0) + lanes;
       const int64_t col0 = (int64_t)t.n * G::kCols + (t.half == 1 ? 128 : 0);
-      const int chunks = (PAIR && t.half >= 0 ? kChunks / 2 : kChunks) / (EPI ? 2 : 1);
-      const int chunk0 = EPI ? ((warp - 2) >> 2) * chunks : 0;  // two warps to the same lanes take half of them each
+      const int chunks = (PAIR && t.half >= 0 ? kChunks / 2 : kChunks) / G::kSides;
+      const int chunk0 = ((warp - 2) >> 2) * chunks;  // warps of the same lanes take a part of them each
       // the first accumulator's last columns are the second's first
       auto chunk = [&](int c) { return chunk0 + ((turn & 1) ? c : chunks - 1 - c); };
       auto live = [&](int64_t col) { return !split && row0 < g.M && col < g.N; };
@@ -649,20 +667,20 @@ __global__ void __launch_bounds__(Gemm<PAIR, EPI>::kThreads, 1)
           for (int i = 0; i < kOnce; i += 4) *reinterpret_cast<uint4*>(part + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
         } else if (row0 < g.M && col < g.N) {
           auto store = [&](void* to, int64_t ld, const CUtensorMap* map) {
-            rows_out<DT, G::kOutBuffers>(g, to, ld, map, stage + buffer * G::kOutBytes, v, row0, col);
+            rows_out<DT, G::kOutBuffers, G::kRowBytes>(g, to, ld, map, stage + buffer * G::kOutBytes, v, row0, col);
             buffer = buffer + 1 < G::kOutBuffers ? buffer + 1 : 0;
           };
           if constexpr (EPI) {
-            constexpr int per = DT == zr::DT_F32 ? 4 : 8;
+            constexpr int per = Incoming<DT>::per, kWords = Incoming<DT>::kWords;
             if (e.gradient) {
               by_activation(e.act, [&](auto act) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < kWords; ++j) {
                   float h[per];
                   incoming.open(j, h);
 #pragma unroll
-                  for (int i = 0; i < per; ++i)
-                    v[per * j + i] = __float_as_uint(__fmul_rn(__uint_as_float(v[per * j + i]), slope<act.value>(h[i])));
+                  for (int i = 0; i < per; i += 2)
+                    set2(v + per * j + i, zr::mul2(get2(v + per * j + i), slope<act.value>(zr::Two(h[i], h[i + 1]))));
                 }
               });
             } else {
@@ -681,7 +699,7 @@ __global__ void __launch_bounds__(Gemm<PAIR, EPI>::kThreads, 1)
               });
               if (e.residual) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < kWords; ++j) {
                   float r[per];
                   incoming.open(j, r);
 #pragma unroll
@@ -996,27 +1014,28 @@ bool encode_lines(CUtensorMap* map, const void* q, int64_t tiles, int lines) {
 }
 
 // A map of the output, or of another matrix of its size and type.
-bool encode_out(CUtensorMap* map, const GemmArgs& g, void* out, int64_t ld, int dt) {
+bool encode_out(CUtensorMap* map, const GemmArgs& g, void* out, int64_t ld, int dt, int row_bytes) {
   const int es = dt == zr::DT_F32 ? 4 : 2;
   const CUtensorMapDataType type = dt == zr::DT_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                    : dt == zr::DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   const cuuint64_t size[2] = {(cuuint64_t)g.N, (cuuint64_t)g.M}, stride[1] = {(cuuint64_t)ld * es};
-  const cuuint32_t box[2] = {(cuuint32_t)(128 / es), 32}, step[2] = {1, 1};
+  const cuuint32_t box[2] = {(cuuint32_t)(row_bytes / es), 32}, step[2] = {1, 1};
   return map_encoder()(map, type, 2, out, size, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                       row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                       CU_TENSOR_MAP_L2_PROMOTION_NONE,
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <bool PAIR, int DT, bool EPI>
 zr_status launch_gemm(const char* what, const GemmArgs& g, const FinishOf<EPI>& e, int blocks, cudaStream_t s) {
   static zr::SmemAllowance allowance;
-  if (zr_status st = allowance.allow(what, (const void*)gemm_kernel<PAIR, DT, EPI>, Gemm<PAIR, EPI>::kSmem)) return st;
+  if (zr_status st = allowance.allow(what, (const void*)gemm_kernel<PAIR, DT, EPI>, Gemm<PAIR, EPI, DT>::kSmem)) return st;
   Maps<PAIR> maps;
   PreMap<EPI> pre;
-  bool encoded = map_encoder() && (!g.vec || encode_out(&maps.out, g, g.out, g.ldo, DT));
+  bool encoded = map_encoder() && (!g.vec || encode_out(&maps.out, g, g.out, g.ldo, DT, Gemm<PAIR, EPI, DT>::kRowBytes));
   if constexpr (EPI)
-    encoded = encoded && (!g.vec || !e.pre || e.gradient || encode_out(&pre.out, g, e.pre, e.ldp, DT));
+    encoded = encoded && (!g.vec || !e.pre || e.gradient || encode_out(&pre.out, g, e.pre, e.ldp, DT, Gemm<PAIR, EPI, DT>::kRowBytes));
   if (encoded && PAIR) {
     if constexpr (PAIR) {
       const int64_t a_tiles = zr::mx_tiles(g.M, zr::kMxRows) * g.kt, b_tiles = zr::mx_tiles(g.N, zr::kMxRows) * g.kt;
@@ -1027,7 +1046,7 @@ zr_status launch_gemm(const char* what, const GemmArgs& g, const FinishOf<EPI>& 
     }
   }
   if (!encoded) return fail(ZR_ERR_CUDA, "%s: the driver gave no tensor map", what);
-  cudaError_t err = zr::launch(gemm_kernel<PAIR, DT, EPI>, blocks, Gemm<PAIR, EPI>::kThreads, Gemm<PAIR, EPI>::kSmem, PAIR ? 2 : g.split, true, s,
+  cudaError_t err = zr::launch(gemm_kernel<PAIR, DT, EPI>, blocks, Gemm<PAIR, EPI, DT>::kThreads, Gemm<PAIR, EPI, DT>::kSmem, PAIR ? 2 : g.split, true, s,
                                g, maps, e, pre);
   if (err != cudaSuccess) return fail(ZR_ERR_CUDA, "%s: launch failed: %s", what, cudaGetErrorString(err));
   return ZR_OK;
