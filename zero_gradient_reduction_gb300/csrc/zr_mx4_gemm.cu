@@ -39,6 +39,7 @@
 
 using zr::fail;
 
+
 namespace {
 
 // Counts the blocks, ever, whose wait ran out of time. It is never set back: what one stream has heard of
@@ -204,6 +205,8 @@ struct GemmArgs {
   int64_t M, N, ldo;
   int kt;          // tiles of 256 along K
   int mt, nt;      // output tiles
+  uint32_t band_mul;  // id / (kBand nt) as a product's upper half, moved down
+  int band_shift;
   int whole;       // tiles up to here are taken whole; the others, of a pair's last round, in two halves of 128 columns
   int split;       // blocks, a cluster of them, that share a tile's K (of the form with single blocks)
   uint32_t stall;  // test hook: bytes expected that never come
@@ -228,17 +231,17 @@ struct OutMap {
 struct Tile {
   int m, n, half;
 };
+constexpr int kBand = 32;
 __device__ __forceinline__ Tile tile_of(const GemmArgs& g, int id) {
-  constexpr int kBand = 32;
   Tile t;
   t.half = -1;
   if (id >= g.whole) {
     t.half = (id - g.whole) & 1;
     id = g.whole + ((id - g.whole) >> 1);
   }
-  const int per = kBand * g.nt, band = id / per, at = id - band * per;
+  const int band = (int)(__umulhi((uint32_t)id, g.band_mul) >> g.band_shift), at = id - band * kBand * g.nt;
   const int rows = min(kBand, g.mt - band * kBand);
-  t.n = at / rows;
+  t.n = rows == kBand ? at / kBand : at / rows;
   t.m = band * kBand + (at - t.n * rows);
   return t;
 }
@@ -321,6 +324,13 @@ struct Incoming {
       const int64_t row = row0 + lane / kWords + 32 / kWords * i;
       u[i] = row < g.M && c < g.N ? *reinterpret_cast<const uint4*>(from + (row * ld + c) * es) : make_uint4(0, 0, 0, 0);
     }
+  }
+  // A later tile's, from column col to `cols` past it, to L2: a row by each lane.
+  __device__ void expect(const GemmArgs& g, int64_t row0, int64_t col, int cols) const {
+    const int64_t row = row0 + (threadIdx.x & 31), end = col + cols < g.N ? col + cols : g.N;
+    if (!from || row >= g.M) return;
+    for (int64_t c = col; c < end; c += 128 / es)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(from + (row * ld + c) * es));
   }
   // Leaves this lane's row in u.
   __device__ void take(const GemmArgs& g, char* stage, int64_t row0, int64_t col) {
@@ -636,6 +646,12 @@ __global__ void __launch_bounds__(Gemm<PAIR, EPI, DT>::kThreads, 1)
       if constexpr (EPI) {
         const int64_t col = col0 + chunk(0) * kOnce;
         if (live(col)) incoming.ask(g, row0, col), bias.ask(e, g, col);
+        if (incoming.from && id + step < tiles) {
+          const Tile n = tile_of(g, id + step);
+          const int there = (PAIR && n.half >= 0 ? kChunks / 2 : kChunks) / G::kSides * kOnce;
+          incoming.expect(g, (int64_t)n.m * G::kRows + (PAIR ? rank * 128 : 0) + lanes,
+                          (int64_t)n.n * G::kCols + (n.half == 1 ? 128 : 0) + ((warp - 2) >> 2) * there, there);
+        }
       }
       if (!__all_sync(0xFFFFFFFFu, zr::bar_wait(done + 8 * (turn & 1), (turn >> 1) & 1, gave_up))) break;
       zr::tmem_fence_after();
@@ -643,12 +659,6 @@ __global__ void __launch_bounds__(Gemm<PAIR, EPI, DT>::kThreads, 1)
       for (int c = 0; c < chunks; ++c) {
         const int at = chunk(c);
         const int64_t col = col0 + at * kOnce;
-        if constexpr (EPI) {
-          if (live(col)) {
-            if (incoming.from) incoming.take(g, stage, row0, col);
-            if (e.bias) bias.share(bias_at);
-          }
-        }
         uint32_t v[kOnce];
         if constexpr (kOnce == 32)
           zr::tmem_load32(d + at * kOnce, v);
@@ -656,6 +666,10 @@ __global__ void __launch_bounds__(Gemm<PAIR, EPI, DT>::kThreads, 1)
           zr::tmem_load64(d + at * kOnce, v);
         if (c == (PAIR ? 0 : chunks - 1)) tell(freed + 8 * (turn & 1));
         if constexpr (EPI) {
+          if (live(col)) {
+            if (incoming.from) incoming.take(g, stage, row0, col);
+            if (e.bias) bias.share(bias_at);
+          }
           if (g.kt == 0) {  // a sum of nothing
 #pragma unroll
             for (int i = 0; i < kOnce; ++i) v[i] = 0;
@@ -1119,6 +1133,10 @@ zr_status matmul(const char* what, const void* a, int64_t M, const void* b, int6
   g.vec = vec(ldo);
   if constexpr (EPI)
     if (e.pre && !e.gradient) g.vec = g.vec && vec(e.ldp);
+  // for ids under 2^31 and a divisor d, the upper half of id times 2^(31 + l)/d, rounded up, 2^l the power of two at or over d
+  const int64_t band = (int64_t)kBand * g.nt;
+  while ((int64_t)1 << (g.band_shift + 1) < band) ++g.band_shift;
+  g.band_mul = (uint32_t)(((uint64_t)1 << (32 + g.band_shift)) / band + 1);
   g.whole = g.mt * g.nt;
   g.split = 1;
   if (pair) {
