@@ -31,6 +31,8 @@ __global__ void __launch_bounds__(kThreads) column_kernel(const __grid_constant_
   constexpr int es = DT == zr::DT_F32 ? 4 : 2, kCols = LANES * PER, kRows = kThreads / LANES, kOnce = 8;
   __shared__ float parts[kRows * kCols], sums[kCols];
   const int lane = threadIdx.x % LANES, r0 = threadIdx.x / LANES;
+  zr::let_next_begin();
+  zr::wait_for_previous();
   const int rank = C > 1 ? (int)zr::cluster_rank() : 0;
   const int64_t col0 = (int64_t)(blockIdx.x / C) * kCols, col = col0 + lane * PER;
   const int64_t share = (a.M + C - 1) / C, first = share * rank, end = first + share < a.M ? first + share : a.M;
@@ -105,9 +107,9 @@ template <int DT, int LANES, int PER>
 cudaError_t launch(const SumArgs& a, int sms, cudaStream_t s) {
   const int64_t strips = (a.N - 1) / (LANES * PER) + 1;
   // as many blocks to a strip as keep all SMs busy and 64 rows each
-  if (strips * 4 <= sms * 2 && a.M >= 8 * 64) return zr::launch(column_kernel<DT, LANES, PER, 8>, strips * 8, kThreads, 0, 8, false, s, a);
-  if (strips <= sms * 2 && a.M >= 4 * 64) return zr::launch(column_kernel<DT, LANES, PER, 4>, strips * 4, kThreads, 0, 4, false, s, a);
-  return zr::launch(column_kernel<DT, LANES, PER, 1>, strips, kThreads, 0, 1, false, s, a);
+  if (strips * 4 <= sms * 2 && a.M >= 8 * 64) return zr::launch(column_kernel<DT, LANES, PER, 8>, strips * 8, kThreads, 0, 8, true, s, a);
+  if (strips <= sms * 2 && a.M >= 4 * 64) return zr::launch(column_kernel<DT, LANES, PER, 4>, strips * 4, kThreads, 0, 4, true, s, a);
+  return zr::launch(column_kernel<DT, LANES, PER, 1>, strips, kThreads, 0, 1, true, s, a);
 }
 
 template <int DT>
