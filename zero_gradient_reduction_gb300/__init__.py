@@ -718,33 +718,32 @@ def mx4_dequantize(q: Mx4, out, stream=None) -> None:
 ACTIVATIONS = {None: 0, "relu": 1, "gelu": 2, "silu": 3}  # zr_activation
 
 
-def _epilogue(what: str, out, rows: int, cols: int, device: int, bias, activation, residual, pre, gradient):
-    """zr_mx4_epilogue of a product's keywords; their tensors are on the output's device."""
-    e = Epilogue()
+def _beside(what: str, name: str, t, out, device: int):
+    """(pointer, row stride) of an epilogue's matrix, which is like the output."""
+    if t.dtype is not out.dtype or t.shape != out.shape:
+        _refuse(f"{what}: {name} must have out's type and shape")
+    p, _, _, ld, _, d = _matrix(t, name)
+    if d != device:
+        _refuse(f"{what}: {name} on device {d}, out on {device}")
+    return p, ld
+
+
+def _epilogue(what: str, out, cols: int, device: int, bias, activation, residual, pre, gradient: int):
+    """zr_mx4_epilogue of a product's keywords, by reference; their tensors are on the output's device."""
     act = ACTIVATIONS.get(activation)
     if act is None:
         _refuse(f"{what}: activation must be one of {sorted(k for k in ACTIVATIONS if k)} or None, not {activation!r}")
-    e.activation, e.gradient = act, gradient
-    for name, t in (("residual", residual), ("pre", pre)):
-        if t is None:
-            continue
-        if t.dtype is not out.dtype or t.shape != out.shape:
-            _refuse(f"{what}: {name} must have out's type and shape")
-        p, _, _, ld, _, d = _matrix(t, name)
-        if d != device:
-            _refuse(f"{what}: {name} on device {d}, out on {device}")
-        if name == "pre":
-            e.pre, e.ldp = p, ld
-        else:
-            e.residual, e.ldr = p, ld
+    r, ldr = (None, 0) if residual is None else _beside(what, "residual", residual, out, device)
+    h, ldp = (None, 0) if pre is None else _beside(what, "pre", pre, out, device)
+    b, dt = None, 0
     if bias is not None:
         dt = _types.get(bias.dtype)
         if dt is None or bias.numel() != cols or not bias.is_contiguous() or not bias.is_cuda:
             _refuse(f"{what}: bias must be fp32, fp16 or bf16 [{cols}] in device memory")
         if bias.get_device() != device:
             _refuse(f"{what}: bias on device {bias.get_device()}, out on {device}")
-        e.bias, e.bias_dtype = bias.data_ptr(), dt
-    return e
+        b = bias.data_ptr()
+    return ctypes.byref(Epilogue(b, r, h, ldr, ldp, dt, act, gradient))
 
 
 def mx4_matmul(a: Mx4, b: Mx4, out, stream=None, *, bias=None, activation=None, residual=None, pre=None,
@@ -767,9 +766,9 @@ def mx4_matmul(a: Mx4, b: Mx4, out, stream=None, *, bias=None, activation=None, 
         return
     if gradient_of is not None and activation is not None:
         _refuse("mx4_matmul: an activation and a gradient of one")
-    e = _epilogue("mx4_matmul", out, rows, cols, device, bias, gradient_of if gradient_of is not None else activation,
+    e = _epilogue("mx4_matmul", out, cols, device, bias, gradient_of if gradient_of is not None else activation,
                   residual, pre, int(gradient_of is not None))
-    _check(fn(a.ptr, rows, b.ptr, cols, a.cols, p, dt, ld, ctypes.byref(e), s))
+    _check(fn(a.ptr, rows, b.ptr, cols, a.cols, p, dt, ld, e, s))
 
 
 def mx4_linear(x, w: Mx4, out, xq: Optional[Mx4] = None, stream=None, *, bias=None, activation=None, residual=None,
@@ -793,8 +792,8 @@ def mx4_linear(x, w: Mx4, out, xq: Optional[Mx4] = None, stream=None, *, bias=No
     if plain:
         _check(fn(p, xdt, rows, ldx, w.ptr, n, k, o, dt, ldo, xq and xq.ptr, s))
         return
-    e = _epilogue("mx4_linear", out, rows, n, device, bias, activation, residual, pre, 0)
-    _check(fn(p, xdt, rows, ldx, w.ptr, n, k, o, dt, ldo, xq and xq.ptr, ctypes.byref(e), s))
+    e = _epilogue("mx4_linear", out, n, device, bias, activation, residual, pre, 0)
+    _check(fn(p, xdt, rows, ldx, w.ptr, n, k, o, dt, ldo, xq and xq.ptr, e, s))
 
 
 def column_sums(x, out, stream=None) -> None:
