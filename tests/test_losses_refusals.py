@@ -110,7 +110,7 @@ def operands(call):
         return zr.token_logprobs, dict(**z, logp=f32(4), entropy=f32(4))
     if call == "policy":
         return zr.policy_loss, dict(**z, old_logp=f32(4), advantage=f32(4), loss=f32(4), grad=grad, weight=f32(4), ref_logp=f32(4), logp=f32(4), plan=plan)
-    return zr.preference_loss, dict(**z, starts=whole(3), ref_logp=f32(4), loss=f32(1), work=lambda d: Vector((1000,), torch.uint8, d), grad=grad,
+    return zr.preference_loss, dict(**z, starts=whole(3), ref_logp=f32(4), loss=f32(1), work=lambda d: Vector((1 << 16,), torch.uint8, d), grad=grad,
                                     weight=f32(1), rewards=f32(2), plan=plan)
 
 

@@ -236,3 +236,12 @@ def test_no_pairs_and_no_rows():
     zr.preference_loss(z[:0], ids[:0], torch.zeros(5, dtype=torch.int32, device="cuda"), torch.zeros(0, device="cuda"), loss, workspace(0, 2),
                        grad[:0], rewards=r)
     assert np.allclose(loss.cpu().numpy(), np.log(2.0), rtol=1e-6) and bool((r == 0).all())
+
+
+@pytest.mark.parametrize("pairs,rows", [(1, 700), (2, 3000), (700, 2), (40, 60), (3, 1)])
+def test_rows_of_many_shapes_in_order(pairs, rows):
+    """Few long and many short pairs, empty ones among them, on rows that go in parts and in whole: more blocks than run at once."""
+    g = torch.Generator().manual_seed(pairs)
+    lengths = torch.randint(0, 2 * rows, (2 * pairs,), generator=g).tolist()
+    check(*case(lengths, 120, BF16, seed=pairs, before=3, behind=2))
+    check(*case([min(n, 3) for n in lengths[:20]], 40_000, BF16, seed=pairs))

@@ -75,6 +75,8 @@ __global__ void __launch_bounds__(384, 4) score_kernel(const __grid_constant__ P
   const int64_t row = blockIdx.x / C;
   const int rank = C > 1 ? (int)zr::cluster_rank() : 0;
   if (C > 1) zr::cluster_arrived();
+  zr::wait_for_previous();
+  zr::let_next_begin();  // what begins from here on may read what was there before this call
   const int64_t id = zr::id_at(a.ids, a.wide_ids, row);
   const int sequence = sequence_of(a, row);
   if (id < 0 || sequence < 0 || !has_weight(a, sequence)) {
@@ -106,11 +108,13 @@ constexpr int kPairThreads = 256;
 __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constant__ PreferenceArgs a) {
   __shared__ double of_warp[2][kPairThreads / 32];
   const int pair = blockIdx.x, tid = threadIdx.x;
+  zr::let_next_begin();
   int64_t at[3];
 #pragma unroll
   for (int i = 0; i < 3; ++i) at[i] = zr::id_at(a.starts, a.wide_starts, 2 * (int64_t)pair + i);
   const bool sound = at[0] >= 0 && at[0] <= at[1] && at[1] <= at[2] && at[2] <= a.T;
   double sum[2] = {0.0, 0.0};
+  zr::wait_for_previous();
   if (sound) {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -143,22 +147,33 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constan
   a.slope[2 * pair + 1] = f;
 }
 
-// ---- each row's gradient
+// ---- each row's gradient: the last rows first, which were summed last and are in L2 still. A block begins while the
+// pairs are summed up and asks for its first words before it waits for them.
 template <int DT>
 __global__ void __launch_bounds__(384) gradient_kernel(const __grid_constant__ PreferenceArgs a) {
   using W = zr::Word<DT>;
   constexpr int per = W::per, es = 16 / per, kOnce = 4;
   const int tid = threadIdx.x, nthr = blockDim.x;
-  const int64_t row = blockIdx.x / a.split;
-  const int64_t v0 = (blockIdx.x - row * a.split) * a.share, v1 = v0 + a.share < a.V ? v0 + a.share : a.V;
+  const int64_t place = blockIdx.x / a.split, row = a.T - 1 - place;
+  const int64_t v0 = (blockIdx.x - place * a.split) * a.share, v1 = v0 + a.share < a.V ? v0 + a.share : a.V;
   const int n = v1 > v0 ? (int)(v1 - v0) : 0;
-  const int sequence = sequence_of(a, row);
-  if (sequence < 0) return;  // left as it is
   const char* zrow = static_cast<const char*>(a.z) + (row * a.ldz + v0) * es;
   char* grad = static_cast<char*>(a.grad) + (row * a.ldg + v0) * es;
   const zr::RowWords<DT> r(zrow, n, tid);
-  const bool same = (int)(reinterpret_cast<uintptr_t>(grad) & 15) / es == r.lead;
+  uint4 u[kOnce];
+  auto ask = [&](int j) {
+#pragma unroll
+    for (int i = 0; i < kOnce; ++i)
+      if (j + i * nthr < r.last) u[i] = zr::ld_row(r.words + j + i * nthr);
+  };
   const int64_t id = zr::id_at(a.ids, a.wide_ids, row);
+  const int sequence = sequence_of(a, row);
+  const bool live = id >= 0 && sequence >= 0 && has_weight(a, sequence);
+  if (live) ask(r.first + tid);
+  zr::wait_for_previous();
+  if (sequence < 0) return;  // left as it is
+  // the gradient's words are the logits' words, shifted: stored whole only where they coincide
+  const bool same = (int)(reinterpret_cast<uintptr_t>(grad) & 15) / es == r.lead;
   auto store = [&](int j, const float v[per]) {
     char* to = grad + (int64_t)(j * per - r.lead) * es;
     if (same) {
@@ -168,7 +183,7 @@ __global__ void __launch_bounds__(384) gradient_kernel(const __grid_constant__ P
       for (int i = 0; i < per; ++i) zr::store1<DT>(to, i, v[i]);
     }
   };
-  if (id < 0 || !has_weight(a, sequence)) {
+  if (!live) {
     const float zeros[per] = {};
     for (int j = r.first + tid; j < r.last; j += nthr) store(j, zeros);
     if (r.single >= 0) zr::store1<DT>(grad, r.single, 0.0f);
@@ -183,10 +198,7 @@ __global__ void __launch_bounds__(384) gradient_kernel(const __grid_constant__ P
   const zr::Exponents<false> exponents(base, a.scale);
   const zr::Two by2(by, by);
   for (int j = r.first + tid; j < r.last; j += kOnce * nthr) {
-    uint4 u[kOnce];
-#pragma unroll
-    for (int i = 0; i < kOnce; ++i)
-      if (j + i * nthr < r.last) u[i] = zr::ld_row(r.words + j + i * nthr);
+    if (j != r.first + tid) ask(j);
 #pragma unroll
     for (int i = 0; i < kOnce; ++i) {
       if (j + i * nthr >= r.last) break;
@@ -214,7 +226,8 @@ __global__ void __launch_bounds__(384) gradient_kernel(const __grid_constant__ P
   }
   if (r.single >= 0) {
     const float z = zr::load1<DT>(zrow, r.single);
-    zr::store1<DT>(grad, r.single, r.single == chosen ? own : __fmul_rn(zr::exp2_fast(base.exponent<false>(z, a.scale)), by));
+    zr::store1<DT>(grad, r.single,
+                   r.single == chosen ? own : __fmul_rn(zr::exp2_fast(base.exponent<false>(z, a.scale)), by));
   }
 }
 
@@ -225,13 +238,13 @@ zr_status launch(PreferenceArgs& a, int sms, cudaStream_t s) {
   a.split = r.split;
   cudaError_t e = cudaSuccess;
   if (a.T > 0)
-    e = r.split == 8   ? zr::launch(score_kernel<DT, 8>, a.T * 8, r.threads, 0, 8, false, s, a)
-        : r.split == 4 ? zr::launch(score_kernel<DT, 4>, a.T * 4, r.threads, 0, 4, false, s, a)
-        : r.split == 2 ? zr::launch(score_kernel<DT, 2>, a.T * 2, r.threads, 0, 2, false, s, a)
-                       : zr::launch(score_kernel<DT, 1>, a.T, r.threads, 0, 1, false, s, a);
-  if (e == cudaSuccess) e = zr::launch(pair_kernel, a.sequences / 2, kPairThreads, 0, 1, false, s, a);
+    e = r.split == 8   ? zr::launch(score_kernel<DT, 8>, a.T * 8, r.threads, 0, 8, true, s, a)
+        : r.split == 4 ? zr::launch(score_kernel<DT, 4>, a.T * 4, r.threads, 0, 4, true, s, a)
+        : r.split == 2 ? zr::launch(score_kernel<DT, 2>, a.T * 2, r.threads, 0, 2, true, s, a)
+                       : zr::launch(score_kernel<DT, 1>, a.T, r.threads, 0, 1, true, s, a);
+  if (e == cudaSuccess) e = zr::launch(pair_kernel, a.sequences / 2, kPairThreads, 0, 1, true, s, a);
   if (e == cudaSuccess && a.grad && a.T > 0)
-    e = zr::launch(gradient_kernel<DT>, a.T * r.split, r.threads, 0, 1, false, s, a);
+    e = zr::launch(gradient_kernel<DT>, a.T * r.split, r.threads, 0, 1, true, s, a);
   if (e != cudaSuccess) return fail(ZR_ERR_CUDA, "zr_preference_loss: launch failed: %s", cudaGetErrorString(e));
   return ZR_OK;
 }
