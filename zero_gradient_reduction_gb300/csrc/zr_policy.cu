@@ -40,6 +40,7 @@ __global__ void __launch_bounds__(384, 4) logprob_kernel(const __grid_constant__
   const int64_t row = blockIdx.x / C;
   const int rank = C > 1 ? (int)zr::cluster_rank() : 0;
   if (C > 1) zr::cluster_arrived();
+  zr::wait_for_previous();
   const int64_t id = zr::id_at(a.ids, a.wide_ids, row);
   if (id < 0) {  // not scored, and not read (the same in the whole cluster)
     if (C > 1) zr::cluster_wait();
@@ -112,6 +113,7 @@ __global__ void __launch_bounds__(1024) policy_kernel(const __grid_constant__ Po
   const zr::RowWords<DT> r(zrow, n, tid);
   // the gradient's words are the logits' words, shifted: stored whole only where they coincide
   const bool same = grad && (int)(reinterpret_cast<uintptr_t>(grad) & 15) / es == r.lead;
+  zr::wait_for_previous();
   const float w = a.weight ? a.weight[row] : 1.0f;
   const int64_t id = zr::id_at(a.ids, a.wide_ids, row);
 
@@ -237,7 +239,7 @@ template <int DT, int C>
 zr_status launch_policy(const PolicyArgs& a, int threads, int smem, cudaStream_t s) {
   static zr::SmemAllowance allowance;
   if (zr_status st = allowance.allow("zr_policy_loss", (const void*)policy_kernel<DT, C>, zr::kSmemMost)) return st;
-  cudaError_t e = zr::launch(policy_kernel<DT, C>, a.T * C, threads, smem, C, false, s, a);
+  cudaError_t e = zr::launch(policy_kernel<DT, C>, a.T * C, threads, smem, C, true, s, a);
   if (e != cudaSuccess) return fail(ZR_ERR_CUDA, "zr_policy_loss: launch failed: %s", cudaGetErrorString(e));
   return ZR_OK;
 }
@@ -251,10 +253,10 @@ zr_status launch_policy(const PolicyArgs& a, int split, int threads, int smem, c
 
 template <int DT, bool ENTROPY>
 zr_status launch_logprobs(const LogprobArgs& a, const zr::RowShape& r, cudaStream_t s) {
-  cudaError_t e = r.split == 8   ? zr::launch(logprob_kernel<DT, ENTROPY, 8>, a.T * 8, r.threads, 0, 8, false, s, a)
-                  : r.split == 4 ? zr::launch(logprob_kernel<DT, ENTROPY, 4>, a.T * 4, r.threads, 0, 4, false, s, a)
-                  : r.split == 2 ? zr::launch(logprob_kernel<DT, ENTROPY, 2>, a.T * 2, r.threads, 0, 2, false, s, a)
-                                 : zr::launch(logprob_kernel<DT, ENTROPY, 1>, a.T, r.threads, 0, 1, false, s, a);
+  cudaError_t e = r.split == 8   ? zr::launch(logprob_kernel<DT, ENTROPY, 8>, a.T * 8, r.threads, 0, 8, true, s, a)
+                  : r.split == 4 ? zr::launch(logprob_kernel<DT, ENTROPY, 4>, a.T * 4, r.threads, 0, 4, true, s, a)
+                  : r.split == 2 ? zr::launch(logprob_kernel<DT, ENTROPY, 2>, a.T * 2, r.threads, 0, 2, true, s, a)
+                                 : zr::launch(logprob_kernel<DT, ENTROPY, 1>, a.T, r.threads, 0, 1, true, s, a);
   if (e != cudaSuccess) return fail(ZR_ERR_CUDA, "zr_token_logprobs: launch failed: %s", cudaGetErrorString(e));
   return ZR_OK;
 }

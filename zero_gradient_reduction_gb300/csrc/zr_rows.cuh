@@ -459,7 +459,7 @@ inline RowShape held_rows(int64_t T, int64_t V, int es, int fixed, int apart, in
   r.split = split;
   r.share = (room - 1) * unit;
   r.blocks = 1;
-  while (r.blocks < 16 && T * split > (int64_t)r.blocks * sms &&
+  while (r.blocks < (apart ? 16 : 32) && T * split > (int64_t)r.blocks * sms &&
          room <= 20 * (1024 / (r.blocks + 1) / 32 * 32 - apart) &&
          (room <= held(r.blocks + 1) || ((r.blocks == 1 || split > 1) && nearly(room, r.blocks + 1))))
     ++r.blocks;
@@ -471,17 +471,19 @@ inline RowShape held_rows(int64_t T, int64_t V, int es, int fixed, int apart, in
   return r;
 }
 
-// Rows that are read as they come: where they leave SMs free, each is shared by a cluster as far as those
-// go and its parts stay 32 KB long.
+// Rows that are read as they come. A thread has about 16 words (8192 x 8000 bf16 in 25 us, 34 with 4), of rows that
+// leave SMs free 4; those are shared by clusters as far as two blocks to an SM go and the parts stay 32 KB long
+// (100 x 50257 fp32 in 7.0 us, 8.0 with one block to an SM).
 inline RowShape streamed_rows(int64_t T, int64_t V, int es, int sms) {
   const int unit = 16 / es;
   auto words = [&](int split) { return (V + split * unit - 1) / (split * unit) + 1; };
   RowShape r{};
   r.split = 1;
-  while (r.split < 8 && T * r.split * 2 <= sms && words(r.split) > 2000) r.split *= 2;
+  while (r.split < 8 && T * r.split <= sms && words(r.split) > 2000) r.split *= 2;
   const int64_t room = words(r.split);
   r.share = (room - 1) * unit;
-  r.threads = (int)(room < 256 ? (room + 31) / 32 * 32 : T * r.split <= sms ? 384 : 256);
+  const int each = T * r.split <= 2 * sms ? 4 : 16, most = T * r.split <= 2 * sms ? 384 : 256;
+  r.threads = (int)(room < each * most ? (room + each * 32 - 1) / (each * 32) * 32 : most);
   return r;
 }
 
