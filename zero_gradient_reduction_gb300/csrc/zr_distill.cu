@@ -29,14 +29,26 @@
 #include "zr_launch.h"
 #include "zr_nvtx.h"
 #include "zr_plan.h"
+#include "zr_rows.cuh"
 #include "zr_tensor.cuh"
 
+using zr::add2;
+using zr::exp2_fast;
 using zr::fail;
+using zr::fma2;
+using zr::kLn2;
+using zr::kLog2E;
+using zr::ld_row;
+using zr::mul2;
+using zr::store1;
+using zr::Two;
+using zr::warp_max;
+using zr::warp_sum;
+using zr::Word;
 
 namespace {
 
 constexpr int kMaxThreads = 1024;  // the last warp for the teacher's entries, the others for a row's words
-constexpr float kLog2E = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
 
 struct DistillArgs {
   const void* z;
@@ -53,109 +65,6 @@ struct DistillArgs {
   int room;             // 16-byte words of a row's share that shared memory holds
   float tau, grad_scale;
 };
-
-// Not the read-only path: the gradient may replace the logits.
-__device__ __forceinline__ uint4 ld_row(const uint4* p) {
-  uint4 r;
-  asm volatile("ld.global.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "l"(p)
-               : "memory");
-  return r;
-}
-
-// 2^x to 2 ulp, results under 2^-126 to zero.
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// Two fp32 operations in one instruction.
-struct Two {
-  uint64_t v;
-  __device__ Two(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
-  __device__ explicit Two(uint64_t w) : v(w) {}
-  __device__ float lo() const { return __uint_as_float((uint32_t)v); }
-  __device__ float hi() const { return __uint_as_float((uint32_t)(v >> 32)); }
-};
-__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return Two(r);
-}
-__device__ __forceinline__ Two add2(Two a, Two b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a.v), "l"(b.v));
-  return Two(r);
-}
-__device__ __forceinline__ Two mul2(Two a, Two b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a.v), "l"(b.v));
-  return Two(r);
-}
-
-template <int DT>
-struct Word {
-  static constexpr int per = DT == zr::DT_F32 ? 4 : 8;
-  __device__ static void open(uint4 u, float f[per]) {
-    if constexpr (DT == zr::DT_F32) {
-      f[0] = __uint_as_float(u.x); f[1] = __uint_as_float(u.y);
-      f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);
-    } else {
-      zr::unpack8<DT>(u, f);
-    }
-  }
-  // The larger of m and the word's values, two at a time in 16 bits; `m` starts as lowest().
-  __device__ static uint32_t lowest() {
-    return DT == zr::DT_F32 ? 0xFF800000u : DT == zr::DT_BF16 ? 0xFF80FF80u : 0xFC00FC00u;
-  }
-  __device__ static uint32_t larger(uint32_t a, uint32_t b) {
-    if constexpr (DT == zr::DT_F32) {
-      return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
-    } else if constexpr (DT == zr::DT_BF16) {
-      const __nv_bfloat162 r = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
-      return *reinterpret_cast<const uint32_t*>(&r);
-    } else {
-      const __half2 r = __hmax2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
-      return *reinterpret_cast<const uint32_t*>(&r);
-    }
-  }
-  __device__ static uint32_t larger(uint32_t m, uint4 u) {
-    return larger(larger(m, larger(u.x, u.y)), larger(u.z, u.w));
-  }
-  __device__ static float largest(uint32_t m) {
-    if constexpr (DT == zr::DT_F32)
-      return __uint_as_float(m);
-    else
-      return fmaxf(zr::to_f32<DT>((uint16_t)m), zr::to_f32<DT>((uint16_t)(m >> 16)));
-  }
-  __device__ static uint4 close(const float f[per]) {
-    if constexpr (DT == zr::DT_F32)
-      return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-    else
-      return zr::pack8<DT>(f);
-  }
-};
-
-template <int DT>
-__device__ __forceinline__ void store1(void* p, int64_t i, float v) {
-  if (DT == zr::DT_F32)
-    static_cast<float*>(p)[i] = v;
-  else
-    static_cast<uint16_t*>(p)[i] = zr::from_f32<DT == zr::DT_F32 ? zr::DT_BF16 : DT>(v);
-}
-
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-  return v;
-}
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-  return v;
-}
 
 // A sum of exponentials is kept relative to the maximum m of its z, in base 2 and as one
 // multiply-add: sum of 2^(z c - mc), mc = m c rounded. That rounding multiplies every term by the

@@ -316,7 +316,7 @@ extern "C" zr_status zr_policy_loss(const void* logits, zr_dtype dt, int64_t T, 
   const int sms = zr::sm_count("zr_policy_loss");
   if (sms == 0) return ZR_ERR_CUDA;
   const int es = dt == ZR_F32 ? 4 : 2, fixed = (int)sizeof(zr::Parts);
-  const zr::RowShape r = zr::held_rows(T, V, es, fixed, 0, sms);
+  const zr::RowShape r = zr::held_rows(T, V, es, fixed, sms);
   if (T > 0x7FFFFFFF / r.split) return fail(ZR_ERR_UNSUPPORTED, "zr_policy_loss: too many rows for one launch");
   PolicyArgs a{};
   a.z = logits; a.ids = ids; a.old_logp = old_logp; a.advantage = advantage; a.weight = weight;

@@ -438,14 +438,13 @@ struct RowShape {
 
 // Rows that are held in shared memory while their gradient is not known. An SM's memory holds so many
 // words of a row for each of its blocks; what a row has beyond them is read again, from L2. One block takes
-// a row of up to 1.2 times what two blocks to an SM hold (7229 x 57000 bf16 in 270 us, 372 with one) or of
-// what one holds; longer rows go to as few blocks as have up to 1.2 times the half each. Where rows leave
-// SMs free each is shared as far as those go and its parts stay 24 KB long.
+// a row of up to 1.2 times what two blocks to an SM hold or of what one holds; longer rows go to as few
+// blocks as have up to 1.2 times the half each. Where rows leave SMs free each is shared, as far as three
+// blocks to an SM go and its parts stay 24 KB long (200 x 50257 fp32 in 18.6 us, 22.6 with one).
 // One more block than fit whole where it nearly does: for a row of its own the second only, in a
-// cluster, which waits more, others too (1373 x 150000 fp32 in 296 us with 3, 348 with 2). A thread has
-// 20 words at most: 8192 x 8000 bf16 in 55 us with 10 blocks of 2 warps, 71 with 14 of one. (Figures of
-// the distillation loss, with one warp of each block, `apart`, for what else a row has.)
-inline RowShape held_rows(int64_t T, int64_t V, int es, int fixed, int apart, int sms) {
+// cluster, which waits more, others too. A thread has 20 words at most (8192 x 1000 fp32 in 13.8 us with 32
+// blocks, 21.0 with 16).
+inline RowShape held_rows(int64_t T, int64_t V, int es, int fixed, int sms) {
   auto held = [&](int blocks) { return ((kSmemMost + 1024) / blocks - 1024 - fixed) / 16; };
   const int unit = 16 / es;
   auto words = [&](int split) { return (V + split * unit - 1) / (split * unit) + 1; };  // 1: it may begin inside a word
@@ -453,21 +452,20 @@ inline RowShape held_rows(int64_t T, int64_t V, int es, int fixed, int apart, in
   int split = 1;
   if (words(1) > held(1) && !nearly(words(1), 2))
     while (split < 8 && !nearly(words(split), 2)) split *= 2;
-  while (split < 8 && T * split * 2 <= sms && words(split) > 3000) split *= 2;
+  while (split < 8 && T * split * 2 <= 3 * sms && words(split) > 3000) split *= 2;
   const int64_t room = words(split);
   RowShape r{};
   r.split = split;
   r.share = (room - 1) * unit;
   r.blocks = 1;
-  while (r.blocks < (apart ? 16 : 32) && T * split > (int64_t)r.blocks * sms &&
-         room <= 20 * (1024 / (r.blocks + 1) / 32 * 32 - apart) &&
+  while (r.blocks < 32 && T * split > (int64_t)r.blocks * sms && room <= 20 * (1024 / (r.blocks + 1) / 32 * 32) &&
          (room <= held(r.blocks + 1) || ((r.blocks == 1 || split > 1) && nearly(room, r.blocks + 1))))
     ++r.blocks;
   r.room = (int)(room < held(r.blocks) ? room : held(r.blocks));
   // They share the SM's registers, 64 a thread. A row that has its SM to itself takes fewer threads, as
-  // barriers cost more than words then (13 x 50257 fp32 in 9.0 us with 384, 9.9 with 1024).
+  // barriers cost more than words then.
   r.threads = T * split <= sms ? 384 : 1024 / r.blocks / 32 * 32;
-  if (r.threads > (room + 31) / 32 * 32 + apart) r.threads = (int)((room + 31) / 32 * 32 + apart);
+  if (r.threads > (room + 31) / 32 * 32) r.threads = (int)((room + 31) / 32 * 32);
   return r;
 }
 
