@@ -738,10 +738,8 @@ def _epilogue(what: str, out, cols: int, device: int, bias, activation, residual
     b, dt = None, 0
     if bias is not None:
         dt = _types.get(bias.dtype)
-        if dt is None or bias.numel() != cols or not bias.is_contiguous() or not bias.is_cuda:
-            _refuse(f"{what}: bias must be fp32, fp16 or bf16 [{cols}] in device memory")
-        if bias.get_device() != device:
-            _refuse(f"{what}: bias on device {bias.get_device()}, out on {device}")
+        if bias.get_device() != device or dt is None or bias.numel() != cols or not bias.is_contiguous():
+            _misplaced(bias, f"{what}: bias", "fp32, fp16 or bf16", cols, device)
         b = bias.data_ptr()
     return ctypes.byref(Epilogue(b, r, h, ldr, ldp, dt, act, gradient))
 
@@ -845,24 +843,26 @@ def distill_topk(logits, ids, teacher, loss, grad=None, weight=None, temperature
 
 
 # ----------------------------------------------------------------------------- post-training losses
+def _misplaced(t, what: str, kind: str, n: int, device: int):
+    if t.is_cuda and t.get_device() != device:
+        _refuse(f"{what} on device {t.get_device()}, the matrix on {device}")
+    _refuse(f"{what} must be {kind} [{n}] in device memory")
+
+
 def _vector(t, what: str, n: int, device: int):
     """The pointer of a contiguous fp32 vector of n values on the matrix's device, None for None."""
     if t is None:
         return None
-    if t.dtype is not _fns["f32"] or t.numel() != n or not t.is_contiguous() or not t.is_cuda:
-        _refuse(f"{what} must be fp32 [{n}] in device memory")
-    if t.get_device() != device:
-        _refuse(f"{what} on device {t.get_device()}, the matrix on {device}")
+    if t.get_device() != device or t.dtype is not _fns["f32"] or t.numel() != n or not t.is_contiguous():
+        _misplaced(t, what, "fp32", n, device)
     return t.data_ptr()
 
 
 def _whole(t, what: str, n: int, device: int):
     """(pointer, whether of 64 bits) of a contiguous vector of n whole numbers on the matrix's device."""
     wide = t.dtype is _fns["i64"]
-    if not (wide or t.dtype is _fns["i32"]) or t.numel() != n or not t.is_contiguous() or not t.is_cuda:
-        _refuse(f"{what} must be int32 or int64 [{n}] in device memory")
-    if t.get_device() != device:
-        _refuse(f"{what} on device {t.get_device()}, the matrix on {device}")
+    if t.get_device() != device or not (wide or t.dtype is _fns["i32"]) or t.numel() != n or not t.is_contiguous():
+        _misplaced(t, what, "int32 or int64", n, device)
     return t.data_ptr(), int(wide)
 
 
@@ -897,9 +897,10 @@ def policy_loss(logits, ids, old_logp, advantage, loss, grad=None, weight=None, 
     i, wide = _whole(ids, "policy_loss: ids", rows, device)
     if old_logp is None or advantage is None or loss is None:
         _refuse("policy_loss: old_logp, advantage and loss are needed")
-    old, adv, out, w, ref, lp = [_vector(v, name, rows, device) for v, name in (
-        (old_logp, "policy_loss: old_logp"), (advantage, "policy_loss: advantage"), (loss, "policy_loss: loss"),
-        (weight, "policy_loss: weight"), (ref_logp, "policy_loss: ref_logp"), (logp, "policy_loss: logp"))]
+    old = _vector(old_logp, "policy_loss: old_logp", rows, device)
+    adv = _vector(advantage, "policy_loss: advantage", rows, device)
+    out, w = _vector(loss, "policy_loss: loss", rows, device), _vector(weight, "policy_loss: weight", rows, device)
+    ref, lp = _vector(ref_logp, "policy_loss: ref_logp", rows, device), _vector(logp, "policy_loss: logp", rows, device)
     low, high = clip
     g, ldg, g_device = (None, 0, device) if grad is None else _gradient(grad, logits, "policy_loss")
     s = _stream_of(stream, device, g_device, plan.device if plan is not None else device)
@@ -927,9 +928,9 @@ def preference_loss(logits, ids, starts, ref_logp, loss, work, grad=None, weight
     pairs = loss.numel()
     at, wide_starts = _whole(starts, "preference_loss: starts", 2 * pairs + 1, device)
     ref = _vector(ref_logp, "preference_loss: ref_logp", rows, device)
-    out, w, r = [_vector(v, name, n, device) for v, name, n in (
-        (loss, "preference_loss: loss", pairs), (weight, "preference_loss: weight", pairs),
-        (rewards, "preference_loss: rewards", 2 * pairs))]
+    out = _vector(loss, "preference_loss: loss", pairs, device)
+    w = _vector(weight, "preference_loss: weight", pairs, device)
+    r = _vector(rewards, "preference_loss: rewards", 2 * pairs, device)
     need = preference_bytes(rows, pairs)
     if work.element_size() != 1 or work.numel() < need or not work.is_cuda or not work.is_contiguous():
         _refuse(f"preference_loss: work must be {need} contiguous bytes in device memory")
