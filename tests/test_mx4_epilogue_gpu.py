@@ -311,6 +311,35 @@ def test_captured_and_on_another_stream():
     assert all(torch.equal(a, b) for a, b in zip(side, plain))
 
 
+@pytest.mark.parametrize("M,N,K", [(8, 300, 700), (100, 300, 700), (64, 512, 8192), (1024, 4096, 4096)])
+def test_waits_end_and_say_so(M, N, K):
+    """Few tokens, blocks alone, clusters and pairs with all that an epilogue takes in: a wait that runs out ends the call."""
+    x, a, _ = operand(M, K, 1, 1.0)
+    _, b, _ = operand(N, K, 2, 1.5 / math.sqrt(K))
+    bias, residual = torch.randn(N, device="cuda"), torch.randn(M, N, device="cuda").bfloat16()
+    out, pre, xq = torch.empty_like(residual), torch.empty_like(residual), zr.Mx4(M, K)
+
+    def call():
+        zr.mx4_linear(x, b, out, xq=xq, bias=bias, activation="gelu", residual=residual, pre=pre)
+
+    call()
+    want = out.clone(), pre.clone()
+    zr.mx4_status()
+    zr.lib().zr_mx4_stall_waits(1)
+    try:
+        call()
+        zr.mx4_matmul(a, b, out, gradient_of="gelu", pre=residual)
+        torch.cuda.synchronize()
+    finally:
+        zr.lib().zr_mx4_stall_waits(0)
+    with pytest.raises(zr.ZrError) as e:
+        zr.mx4_status()
+    assert e.value.status == 5
+    call()
+    assert torch.equal(out, want[0]) and torch.equal(pre, want[1])
+    zr.mx4_status()
+
+
 def test_a_layer_and_its_gradients_against_differences():
     """y = residual + gelu(x W^T + b) V^T + c in one pass forward and one back, from the 4-bit values: the gradients of the
     bias, of h and of the weights against differences of the loss in 64 bits."""

@@ -116,6 +116,20 @@ def test_logprobs_masks_and_rows_without_an_answer():
         assert float(logp[6]) == 0 and float(entropy[6]) == 0
 
 
+def test_logprobs_masked_at_temperatures_of_every_scale():
+    """log2(e)/tau whose upper bits alone are above it, at or under it: masked logits have no part in any of them."""
+    c = 1.4426950408889634
+    near_12_bits = [np.float32(c / k) for k in (np.arange(2048, 2300) / 2048)]
+    tau = [t for base in near_12_bits for t in (np.nextafter(base, np.float32(0)), base, np.nextafter(base, np.float32(9)))]
+    above = [t for t in tau if np.float32(c / t).view(np.uint32) & 0xFFF == 0 and float(np.float32(c / t)) > c / float(t)]
+    assert above
+    z, ids = ref.logits(8, 700, BF16, torch.Generator().manual_seed(2))
+    ids = ids.clamp(max=300)
+    z[:, 400:] = -INF
+    for t in above[:8] + tau[:8] + [1e-6, 1e6]:
+        check_logprobs(z if t > 1e-3 else (z * 1e-6).to(F32), ids, float(np.float32(t)))
+
+
 @pytest.mark.parametrize("centre,tau,V", [(5000.0, 0.01, 900), (6931.0, 0.01, 60_000), (-3e4, 1e-3, 500), (1e30, 1.0, 300)])
 def test_logprobs_far_from_zero_at_low_temperatures(centre, tau, V):
     """Exponents whose common part is from 10^5 to 10^30: the spread decides what fp32 may cost."""

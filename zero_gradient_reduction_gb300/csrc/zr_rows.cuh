@@ -125,11 +125,13 @@ struct Scale {
 inline Scale scale_of(float tau) {
   const double c = 1.4426950408889634 / tau;
   Scale s{(float)c, 0.0f, 0.0f, 0.0f, tau};
-  uint32_t bits;
-  std::memcpy(&bits, &s.c, 4);
-  bits &= 0xFFFFF000u;
-  std::memcpy(&s.hi, &bits, 4);
-  s.lo = (float)(c - s.hi);
+  uint64_t bits;
+  std::memcpy(&bits, &c, 8);
+  bits &= ~((uint64_t)0x1FFFFFFFFFF);  // downwards, so that the rest is positive: an infinity times it keeps its sign
+  double upper;
+  std::memcpy(&upper, &bits, 8);
+  s.hi = (float)upper;
+  s.lo = c > upper ? (float)(c - upper) : 1e-37f;
   s.trim = (float)((c - s.c) / s.c * 0.6931471805599453);
   return s;
 }
