@@ -73,8 +73,11 @@ struct Finish {
   int vec_residual, vec_pre;  // rows begin on 16-byte boundaries (of pre as of out, GemmArgs::vec)
 };
 struct NoFinish {};
-template <bool EPI>
-using FinishOf = typename std::conditional<EPI, Finish, NoFinish>::type;
+// EPI: 0 for a product without an epilogue, 1 for one whose epilogue takes in no other matrix, 2 for one that does. What
+// a kernel has no code for it need not step around: 8192 x 256 -> 8192 to bf16 with bias and GELU in 47 us as 1, 54 as 2.
+constexpr int kPlain = 0, kAlone = 1, kTakesIn = 2;
+template <int EPI>
+using FinishOf = typename std::conditional<EPI != kPlain, Finish, NoFinish>::type;
 
 __device__ __forceinline__ float reciprocal(float x) {
   float y;
@@ -167,11 +170,11 @@ __device__ __forceinline__ float finished(const Finish& e, int dt, int64_t row, 
   return r;
 }
 
-template <bool PAIR, bool EPI, int DT>
+template <bool PAIR, int EPI, int DT>
 struct Gemm {
   // With an epilogue sixteen warps bring the results out, four to the same lanes, a quarter of a tile's columns
   // each: its loads and exponentials would keep fewer longer than the products take (8192 x 2048 -> 8192 to bf16
-  // with bias, GELU and pre 69 us, 77 with eight of 64 columns).
+  // with bias, GELU and pre 67 us, 77 with eight of 64 columns).
   static constexpr int kOutWarps = EPI ? 16 : 4, kSides = kOutWarps / 4, kThreads = 64 + 32 * kOutWarps;
   static constexpr int kTiles = PAIR ? 2 : 1;                       // MX4 tiles along M and along N
   static constexpr int kRows = 128 * kTiles, kCols = 128 * kTiles;  // output tile
@@ -302,7 +305,7 @@ __device__ __forceinline__ void rows_out(const GemmArgs& g, void* to, int64_t ld
 template <int DT>
 struct Incoming {
   static constexpr int es = DT == zr::DT_F32 ? 4 : 2, kCols = 32, kRow = kCols * es, kWords = kRow / 16, per = 16 / es;
-  const char* from;  // row 0, column 0 of the matrix; null: nothing comes in
+  const char* from;  // row 0, column 0 of the matrix
   int64_t ld;
   bool vec;
   uint4 u[kWords];
@@ -311,7 +314,7 @@ struct Incoming {
         vec(e.gradient ? e.vec_pre : e.vec_residual) {}
   __device__ bool whole(const GemmArgs& g, int64_t col) const { return vec && (col + kCols <= g.N || g.N * es % 16 == 0); }
   __device__ void ask(const GemmArgs& g, int64_t row0, int64_t col) {
-    if (!from || !whole(g, col)) return;
+    if (!whole(g, col)) return;
     const int lane = threadIdx.x & 31;
     const int64_t c = col + lane % kWords * per;
 #pragma unroll
@@ -323,7 +326,7 @@ struct Incoming {
   // A later tile's, from column col to `cols` past it, to L2: a row by each lane.
   __device__ void expect(const GemmArgs& g, int64_t row0, int64_t col, int cols) const {
     const int64_t row = row0 + (threadIdx.x & 31), end = col + cols < g.N ? col + cols : g.N;
-    if (!from || row >= g.M) return;
+    if (row >= g.M) return;
     for (int64_t c = col; c < end; c += 128 / es)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(from + (row * ld + c) * es));
   }
@@ -379,7 +382,7 @@ struct Bias {
 // 2048 x 8192 to bf16 in 6.4 us by fours, 9.5 by blocks alone; two waits of the cluster and 64 KB through
 // its network cost 1 to 3 us.
 constexpr int kPartPitch = 132;  // floats: rows four banks apart
-template <int S, int DT, bool EPI>
+template <int S, int DT, int EPI>
 __device__ __forceinline__ void join_parts(const GemmArgs& g, const FinishOf<EPI>& e, const float* part, int rank, const Tile& t) {
   using T = typename std::conditional<DT == zr::DT_F32, uint32_t, uint16_t>::type;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -440,20 +443,21 @@ __device__ __forceinline__ void join_parts(const GemmArgs& g, const FinishOf<EPI
 }
 
 struct NothingIn {
-  __device__ explicit NothingIn(const NoFinish&) {}
+  template <class E>
+  __device__ explicit NothingIn(const E&) {}
 };
-template <bool EPI, int DT>
-using IncomingOf = typename std::conditional<EPI, Incoming<DT>, NothingIn>::type;
-template <bool EPI>
-using BiasOf = typename std::conditional<EPI, Bias, NoFinish>::type;
+template <int EPI, int DT>
+using IncomingOf = typename std::conditional<EPI == kTakesIn, Incoming<DT>, NothingIn>::type;
+template <int EPI>
+using BiasOf = typename std::conditional<EPI != kPlain, Bias, NoFinish>::type;
 
 template <bool PAIR>
 using Maps = typename std::conditional<PAIR, PairMaps, OutMap>::type;
 // How a stored h is stored, as the output is.
-template <bool EPI>
-using PreMap = typename std::conditional<EPI, OutMap, NoFinish>::type;
+template <int EPI>
+using PreMap = typename std::conditional<EPI != kPlain, OutMap, NoFinish>::type;
 
-template <bool PAIR, int DT, bool EPI>
+template <bool PAIR, int DT, int EPI>
 __global__ void __launch_bounds__(Gemm<PAIR, EPI, DT>::kThreads, 1)
     gemm_kernel(const __grid_constant__ GemmArgs g, const __grid_constant__ Maps<PAIR> maps,
                 const __grid_constant__ FinishOf<EPI> e, const __grid_constant__ PreMap<EPI> pre_map) {
@@ -640,8 +644,12 @@ __global__ void __launch_bounds__(Gemm<PAIR, EPI, DT>::kThreads, 1)
       auto live = [&](int64_t col) { return !split && row0 < g.M && col < g.N; };
       if constexpr (EPI) {
         const int64_t col = col0 + chunk(0) * kOnce;
-        if (live(col)) incoming.ask(g, row0, col), bias.ask(e, g, col);
-        if (incoming.from && id + step < tiles) {
+        if (live(col)) bias.ask(e, g, col);
+      }
+      if constexpr (EPI == kTakesIn) {
+        const int64_t col = col0 + chunk(0) * kOnce;
+        if (live(col)) incoming.ask(g, row0, col);
+        if (id + step < tiles) {
           const Tile n = tile_of(g, id + step);
           const int there = (PAIR && n.half >= 0 ? kChunks / 2 : kChunks) / G::kSides * kOnce;
           incoming.expect(g, (int64_t)n.m * G::kRows + (PAIR ? rank * 128 : 0) + lanes,
@@ -662,7 +670,10 @@ __global__ void __launch_bounds__(Gemm<PAIR, EPI, DT>::kThreads, 1)
         if (c == (PAIR ? 0 : chunks - 1)) tell(freed + 8 * (turn & 1));
         if constexpr (EPI) {
           if (live(col)) {
-            if (incoming.from) incoming.take(g, stage, row0, col);
+            // (There always is one. The branch keeps the compiler from moving its words among the accumulators': 8192 x
+            // 2048 -> 8192 behind GELU in 82 us, 88 without it; barriers in its place do not.)
+            if constexpr (EPI == kTakesIn)
+              if (incoming.from) incoming.take(g, stage, row0, col);
             if (e.bias) bias.share(bias_at);
           }
           if (g.kt == 0) {  // a sum of nothing
@@ -681,17 +692,19 @@ __global__ void __launch_bounds__(Gemm<PAIR, EPI, DT>::kThreads, 1)
           };
           if constexpr (EPI) {
             constexpr int per = Incoming<DT>::per, kWords = Incoming<DT>::kWords;
-            if (e.gradient) {
-              by_activation(e.act, [&](auto act) {
+            if (EPI == kTakesIn && e.gradient) {
+              if constexpr (EPI == kTakesIn) {
+                by_activation(e.act, [&](auto act) {
 #pragma unroll
-                for (int j = 0; j < kWords; ++j) {
-                  float h[per];
-                  incoming.open(j, h);
+                  for (int j = 0; j < kWords; ++j) {
+                    float h[per];
+                    incoming.open(j, h);
 #pragma unroll
-                  for (int i = 0; i < per; i += 2)
-                    set2(v + per * j + i, zr::mul2(get2(v + per * j + i), slope<act.value>(zr::Two(h[i], h[i + 1]))));
-                }
-              });
+                    for (int i = 0; i < per; i += 2)
+                      set2(v + per * j + i, zr::mul2(get2(v + per * j + i), slope<act.value>(zr::Two(h[i], h[i + 1]))));
+                  }
+                });
+              }
             } else {
               if (e.bias) {
 #pragma unroll
@@ -706,7 +719,7 @@ __global__ void __launch_bounds__(Gemm<PAIR, EPI, DT>::kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < kOnce; i += 2) set2(v + i, activated<act.value>(get2(v + i)));
               });
-              if (e.residual) {
+              if constexpr (EPI == kTakesIn) {
 #pragma unroll
                 for (int j = 0; j < kWords; ++j) {
                   float r[per];
@@ -722,7 +735,9 @@ __global__ void __launch_bounds__(Gemm<PAIR, EPI, DT>::kThreads, 1)
         if constexpr (EPI) {
           if (c + 1 < chunks) {  // the next chunk's, while this one is stored
             const int64_t next = col0 + chunk(c + 1) * kOnce;
-            if (live(next)) incoming.ask(g, row0, next), bias.ask(e, g, next);
+            if (live(next)) bias.ask(e, g, next);
+            if constexpr (EPI == kTakesIn)
+              if (live(next)) incoming.ask(g, row0, next);
           }
         }
       }
@@ -1036,7 +1051,7 @@ bool encode_out(CUtensorMap* map, const GemmArgs& g, void* out, int64_t ld, int 
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool PAIR, int DT, bool EPI>
+template <bool PAIR, int DT, int EPI>
 zr_status launch_gemm(const char* what, const GemmArgs& g, const FinishOf<EPI>& e, int blocks, cudaStream_t s) {
   static zr::SmemAllowance allowance;
   if (zr_status st = allowance.allow(what, (const void*)gemm_kernel<PAIR, DT, EPI>, Gemm<PAIR, EPI, DT>::kSmem)) return st;
@@ -1102,11 +1117,11 @@ int shares_of_k(int64_t M, int64_t tiles, int64_t kt, int sms) {
   return best;
 }
 
-template <bool EPI>
+template <int EPI>
 zr_status matmul(const char* what, const void* a, int64_t M, const void* b, int64_t N, int64_t K, void* out,
                  zr_dtype dt, int64_t ldo, const FinishOf<EPI>& e, cudaStream_t s) {
   const int es = dt == ZR_F32 ? 4 : 2;
-  if (K == 0 && !EPI) {  // a sum of nothing
+  if (K == 0 && EPI == kPlain) {  // a sum of nothing
     cudaError_t err = cudaMemset2DAsync(out, (size_t)ldo * es, 0, (size_t)N * es, (size_t)M, s);
     return err == cudaSuccess ? ZR_OK : fail(ZR_ERR_CUDA, "%s: %s", what, cudaGetErrorString(err));
   }
@@ -1146,6 +1161,12 @@ zr_status matmul(const char* what, const void* a, int64_t M, const void* b, int6
   if (dt == ZR_F16) return launch_gemm<false, zr::DT_F16, EPI>(what, g, e, blocks, s);
   if (dt == ZR_BF16) return launch_gemm<false, zr::DT_BF16, EPI>(what, g, e, blocks, s);
   return launch_gemm<false, zr::DT_F32, EPI>(what, g, e, blocks, s);
+}
+
+zr_status matmul_finish(const char* what, const void* a, int64_t M, const void* b, int64_t N, int64_t K, void* out,
+                        zr_dtype dt, int64_t ldo, const Finish& e, cudaStream_t s) {
+  if (e.gradient || e.residual) return matmul<kTakesIn>(what, a, M, b, N, K, out, dt, ldo, e, s);
+  return matmul<kAlone>(what, a, M, b, N, K, out, dt, ldo, e, s);
 }
 
 template <int S, bool EPI>
@@ -1202,7 +1223,7 @@ Finish finish_of(const zr_mx4_epilogue& e, zr_dtype dt) {
   return f;
 }
 
-template <bool EPI>
+template <bool EPILOGUE>
 zr_status checked_matmul(const char* what, const void* a, int64_t M, const void* b, int64_t N, int64_t K, void* out,
                          zr_dtype dt, int64_t ldo, const zr_mx4_epilogue* epilogue, void* stream) {
   zr::clear_error();
@@ -1216,10 +1237,10 @@ zr_status checked_matmul(const char* what, const void* a, int64_t M, const void*
   if (!zr::aligned16(a) || !zr::aligned16(b) || !zr::aligned16(out))
     return fail(ZR_ERR_INVALID, "%s: a pointer is not 16-byte aligned", what);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if constexpr (EPI)
-    return matmul<true>(what, a, M, b, N, K, out, dt, ldo, finish_of(*epilogue, dt), s);
+  if constexpr (EPILOGUE)
+    return matmul_finish(what, a, M, b, N, K, out, dt, ldo, finish_of(*epilogue, dt), s);
   else
-    return matmul<false>(what, a, M, b, N, K, out, dt, ldo, NoFinish{}, s);
+    return matmul<kPlain>(what, a, M, b, N, K, out, dt, ldo, NoFinish{}, s);
 }
 
 template <bool EPI>
@@ -1266,7 +1287,10 @@ zr_status linear(const char* what, const void* x, zr_dtype xdt, int64_t M, int64
     if (!xq) return fail(ZR_ERR_INVALID, "%s: more than %d tokens (or a very long K) need xq", what, kFewTokens);
     if (zr_status st = zr_mx4_quantize(x, xdt, M, K, ldx, nullptr, 0, xq, nullptr, stream)) return st;
   }
-  return matmul<EPI>(what, xq, M, w, N, K, out, dt, ldo, e, s);
+  if constexpr (EPI)
+    return matmul_finish(what, xq, M, w, N, K, out, dt, ldo, e, s);
+  else
+    return matmul<kPlain>(what, xq, M, w, N, K, out, dt, ldo, e, s);
 }
 
 template <bool EPI>
