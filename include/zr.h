@@ -607,8 +607,9 @@ zr_status zr_mx4_linear(const void* x, zr_dtype xdt, int64_t M, int64_t ldx, con
  * bias: device, N values of type bias_dtype, or NULL. residual: device, M x N of out's type, row
  * stride ldr, or NULL; it may be out itself (with ldr = ldo). pre: device, M x N of out's type, row
  * stride ldp: h, written (or NULL), or with `gradient` read, where it may be out itself. Otherwise out,
- * pre and residual share no memory; rows as far apart may lie between each other's. All
- * begin on a 16-byte boundary. Infinities and NaN go where the formulas take them. */
+ * pre and residual share no memory; rows as far apart may lie between each other's. What is written
+ * shares none with the product's own operands (tokens may be the residual). All begin on a 16-byte
+ * boundary. Infinities and NaN go where the formulas take them. */
 typedef enum { ZR_ACT_NONE = 0, ZR_ACT_RELU = 1, ZR_ACT_GELU = 2, ZR_ACT_SILU = 3 } zr_activation;
 typedef struct {
     const void* bias;

@@ -16,7 +16,12 @@
 // scales' copies, to columns that the stage before still reads, cannot overlap its products. Blocks
 // alone 2304 x 768 x 777 to fp32 in 5.1 us, of which 1.1 us until the first stage has landed and 1.5 us
 // for the results. Few tokens: 1 x 2048 by 8192 x 2048 in 5.2 us, 8 x 2048 by 50304 x 2048 in 12.7 us,
-// 4.3 TB/s. (K = 2048 with A's rows kept in shared memory for a run of tiles read half as much and
+// 4.3 TB/s. With an epilogue (bias, activation, a stored h, a residual; or an activation's derivative) pairs
+// 8192 x 2048 -> 8192 to bf16: bias and GELU 58 us, with h stored 66, a residual 68, behind GELU 82, where the
+// product alone takes 46. Its bytes bind none of them (46 us at a copy's rate with h stored): the stores, twice
+// as many, meet the products' own reads of L2 (588 MB of operands), with five stages for six. K = 256 shows the
+// epilogue's arithmetic, 47 us with bias and GELU, 28 without: a reciprocal is eight cycles of a quarter SM, an
+// exponential four. (K = 2048 with A's rows kept in shared memory for a run of tiles read half as much and
 // was no faster, 294 us: its ring of 4 stages no longer covered a copy's latency.)
 #include <cuda.h>
 #include <cudaTypedefs.h>

@@ -4,6 +4,14 @@
 // chosen one's less the rejected one's, its loss -w ((1 - l) log s(m) + l log s(-m)) with the logistic s. The
 // gradient of a row of it is f (1[v = a] - q_v), f = -+ w beta ((1 - l) s(-m) - l s(m)): it is known once all
 // rows of the pair have been summed.
+//
+// So the logits are read twice and the gradient written once, by three launches that overlap at their ends: the
+// rows' sums (139 us at 8192 x 50304 bf16), the pairs' (a block each, in the shadow of the others), the
+// gradients (238 us). 377 us of the 366 that three passes take at a copy's rate; with a quarter of the rows not
+// scored 324. Pairs are too long to stay on the chip between the two (a row is 100 KB, a pair hundreds of
+// them); gradients that follow their pair's sums in one launch, from L2, were slower (409 us: each row's ticket,
+// fence and arrival cost more than its second read from memory). The last rows' gradients come first, their
+// logits are in L2 still. 61 rows of one pair: 12.4 us, three launches' latencies.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -126,14 +134,16 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constan
     if ((tid & 31) == 0) of_warp[i][tid >> 5] = sum[i];
   }
   __syncthreads();
-  if (tid != 0) return;
+  if (tid >= 32) return;
   float reward[2];
+#pragma unroll
   for (int i = 0; i < 2; ++i) {
-    double s = 0.0;
-    for (int k = 0; k < kPairThreads / 32; ++k) s += of_warp[i][k];
+    double s = tid < kPairThreads / 32 ? of_warp[i][tid] : 0.0;
+    for (int o = kPairThreads / 64; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
     reward[i] = sound ? (float)(a.beta * s) : NAN;
-    if (a.rewards) a.rewards[2 * pair + i] = reward[i];
   }
+  if (tid != 0) return;
+  if (a.rewards) a.rewards[2 * pair] = reward[0], a.rewards[2 * pair + 1] = reward[1];
   const float w = a.weight ? a.weight[pair] : 1.0f, m = reward[0] - reward[1];
   // the logistic function on both sides, and the loss -log s(m) + l m from the side that does not cancel
   const float e = expf(-fabsf(m)), small = __fdiv_rn(e, 1.0f + e), large = __fdiv_rn(1.0f, 1.0f + e);
