@@ -112,25 +112,36 @@ __global__ void __launch_bounds__(384, 4) score_kernel(const __grid_constant__ P
 }
 
 // ---- each pair's rewards, loss and slope: a block to a pair
+// Sums in two words of 32 bits: a sequence's thousands of ratios would lose to one, and 64 bits are slow here (8 us a
+// pair of 512 rows, most of them in a few dozen additions).
+__device__ __forceinline__ zr::Pair plus(zr::Pair a, zr::Pair b) {
+  const zr::Pair s = zr::exact_sum(a.value, b.value);
+  return zr::Pair{s.value, s.rest + (a.rest + b.rest)};
+}
+__device__ __forceinline__ zr::Pair across(zr::Pair a, int lanes) {
+  return plus(a, zr::Pair{__shfl_xor_sync(0xFFFFFFFFu, a.value, lanes), __shfl_xor_sync(0xFFFFFFFFu, a.rest, lanes)});
+}
 constexpr int kPairThreads = 256;
 __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constant__ PreferenceArgs a) {
-  __shared__ double of_warp[2][kPairThreads / 32];
+  __shared__ zr::Pair of_warp[2][kPairThreads / 32];
   const int pair = blockIdx.x, tid = threadIdx.x;
   zr::let_next_begin();
   int64_t at[3];
 #pragma unroll
   for (int i = 0; i < 3; ++i) at[i] = zr::id_at(a.starts, a.wide_starts, 2 * (int64_t)pair + i);
   const bool sound = at[0] >= 0 && at[0] <= at[1] && at[1] <= at[2] && at[2] <= a.T;
-  double sum[2] = {0.0, 0.0};
+  zr::Pair sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
   zr::wait_for_previous();
   if (sound) {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      for (int64_t r = at[i] + tid; r < at[i + 1]; r += kPairThreads) sum[i] += a.ratio[r];
+#pragma unroll 4
+      for (int64_t r = at[i] + tid; r < at[i + 1]; r += kPairThreads) sum[i] = plus(sum[i], zr::Pair{a.ratio[r], 0.0f});
   }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    for (int o = 16; o; o >>= 1) sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], o);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum[i] = across(sum[i], o);
     if ((tid & 31) == 0) of_warp[i][tid >> 5] = sum[i];
   }
   __syncthreads();
@@ -138,9 +149,12 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constan
   float reward[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    double s = tid < kPairThreads / 32 ? of_warp[i][tid] : 0.0;
-    for (int o = kPairThreads / 64; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-    reward[i] = sound ? (float)(a.beta * s) : NAN;
+    zr::Pair s = tid < kPairThreads / 32 ? of_warp[i][tid] : zr::Pair{0.0f, 0.0f};
+#pragma unroll
+    for (int o = kPairThreads / 64; o; o >>= 1) s = across(s, o);
+    // (where one is infinite or no number so is the first word, and the second says nothing)
+    const float whole = s.value - s.value == 0.0f ? __fmaf_rn(a.beta, s.rest, __fmul_rn(a.beta, s.value)) : __fmul_rn(a.beta, s.value);
+    reward[i] = sound ? whole : NAN;
   }
   if (tid != 0) return;
   if (a.rewards) a.rewards[2 * pair] = reward[0], a.rewards[2 * pair + 1] = reward[1];
