@@ -161,6 +161,23 @@ def test_vectors_of_other_sizes_and_types(calls, call, name):
     assert not calls
 
 
+@pytest.mark.parametrize("rows,pairs", [(0, 1), (1, 1), (2, 1), (3, 2), (4, 7), (5, 2), (61, 1), (8192, 16), (1000, 999)])
+def test_the_workspace_is_as_large_as_the_library_says(calls, rows, pairs):
+    """A byte less is refused, by the same count."""
+    need = zr.preference_bytes(rows, pairs)
+
+    def call(size):
+        zr.preference_loss(Tensor((rows, 50)), Vector((rows,), torch.int64), Vector((2 * pairs + 1,), torch.int64), Vector((rows,)), Vector((pairs,)),
+                           Vector((size,), torch.uint8))
+
+    call(need)
+    assert len(calls) == 1
+    if need:
+        with pytest.raises(zr.ZrError) as e:
+            call(need - 1)
+        assert str(need) in str(e.value)
+
+
 def test_other_refusals(calls):
     fn, makers = operands("preference")
     with pytest.raises(zr.ZrError):

@@ -931,7 +931,7 @@ def preference_loss(logits, ids, starts, ref_logp, loss, work, grad=None, weight
     out = _vector(loss, "preference_loss: loss", pairs, device)
     w = _vector(weight, "preference_loss: weight", pairs, device)
     r = _vector(rewards, "preference_loss: rewards", 2 * pairs, device)
-    need = preference_bytes(rows, pairs)
+    need = 16 * rows + (rows + 2 * pairs + 3) // 4 * 16  # preference_bytes, without a call
     if work.element_size() != 1 or work.numel() < need or not work.is_cuda or not work.is_contiguous():
         _refuse(f"preference_loss: work must be {need} contiguous bytes in device memory")
     g, ldg, g_device = (None, 0, device) if grad is None else _gradient(grad, logits, "preference_loss")
