@@ -4,7 +4,7 @@
 // columns and, in a cluster of C blocks, 1/C of the rows; a thread adds 16 bytes of each of its rows, and the
 // parts are joined in shared memory, then between the cluster's blocks, in an order that the sizes decide.
 // 8192 x 8192 bf16 in 23 us (5.8 TB/s; 82 with a test between a thread's eight loads), 8192 x 2048 in 6.3; rows off
-// 16-byte boundaries, a value a thread, 8192 x 2049 in 10.9.
+// 16-byte boundaries, a value a thread, 8192 x 2049 in 10.8.
 #include <cuda_runtime.h>
 
 #include <cstdint>

@@ -7,17 +7,17 @@
 // accumulate in fp32.
 //
 // Measured: pairs of blocks 8192^3 to bf16 in 146 us (7.5 PFLOP/s; the products' own rate, issued
-// without a pause, is 9.9 in steps of K = 64, the ones used here), 8192 x 50304 x 2048 in 253 us (6.7).
+// without a pause, is 9.9 in steps of K = 64, the ones used here), 8192 x 50304 x 2048 in 250 us (6.7).
 // Both are bursts; back to back for seconds the power limit lowers the clock, to 1.67 GHz for the
 // latter, which takes 281 us then. There the tensor pipe is active 72 % of the cycles, and counters say
-// that shared memory is not what the rest waits for: of a stage's 707 cycles the tensor cores' reads
+// that shared memory is not what the rest waits for: of a stage's 703 cycles the tensor cores' reads
 // take 280 (16 KB of A, 16 KB of B, of which a pair's block holds half, and 3 KB of scales), and the
 // banks are at 24 % of their rate for reads and at 24 % for writes. What it is has not been settled; the
 // scales' copies, to columns that the stage before still reads, cannot overlap its products. Blocks
 // alone 2304 x 768 x 777 to fp32 in 5.1 us, of which 1.1 us until the first stage has landed and 1.5 us
 // for the results. Few tokens: 1 x 2048 by 8192 x 2048 in 5.2 us, 8 x 2048 by 50304 x 2048 in 12.7 us,
 // 4.3 TB/s. With an epilogue (bias, activation, a stored h, a residual; or an activation's derivative) pairs
-// 8192 x 2048 -> 8192 to bf16: bias and GELU 58 us, with h stored 66, a residual 68, behind GELU 82, where the
+// 8192 x 2048 -> 8192 to bf16: bias and GELU 58 us, with h stored 66, a residual 67, GELU's derivative 82, where the
 // product alone takes 46. Its bytes bind none of them (46 us at a copy's rate with h stored): the stores, twice
 // as many, meet the products' own reads of L2 (588 MB of operands), with five stages for six. K = 256 shows the
 // epilogue's arithmetic, 47 us with bias and GELU, 28 without: a reciprocal is eight cycles of a quarter SM, an

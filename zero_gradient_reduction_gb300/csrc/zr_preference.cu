@@ -7,11 +7,11 @@
 //
 // So the logits are read twice and the gradient written once, by three launches that overlap at their ends: the
 // rows' sums (139 us at 8192 x 50304 bf16), the pairs' (a block each, in the shadow of the others), the
-// gradients (238 us). 377 us of the 366 that three passes take at a copy's rate; with a quarter of the rows not
-// scored 324. Pairs are too long to stay on the chip between the two (a row is 100 KB, a pair hundreds of
+// gradients (234 us). 373 us of the 366 that three passes take at a copy's rate; with a quarter of the rows not
+// scored 321. Pairs are too long to stay on the chip between the two (a row is 100 KB, a pair hundreds of
 // them); gradients that follow their pair's sums in one launch, from L2, were slower (409 us: each row's ticket,
 // fence and arrival cost more than its second read from memory). The last rows' gradients come first, their
-// logits are in L2 still. 61 rows of one pair: 12.4 us, three launches' latencies.
+// logits are in L2 still. 61 rows of one pair: 10.8 us, three launches' latencies.
 #include <cuda_runtime.h>
 
 #include <cstdint>
