@@ -608,7 +608,7 @@ zr_status zr_mx4_linear(const void* x, zr_dtype xdt, int64_t M, int64_t ldx, con
  * stride ldr, or NULL; it may be out itself (with ldr = ldo). pre: device, M x N of out's type, row
  * stride ldp: h, written (or NULL), or with `gradient` read, where it may be out itself. Otherwise out,
  * pre and residual share no memory; rows as far apart may lie between each other's. What is written
- * shares none with the product's own operands (tokens may be the residual). All begin on a 16-byte
+ * shares none with the product's own operands (tokens may be the residual, then not out as well). All begin on a 16-byte
  * boundary. Infinities and NaN go where the formulas take them. */
 typedef enum { ZR_ACT_NONE = 0, ZR_ACT_RELU = 1, ZR_ACT_GELU = 2, ZR_ACT_SILU = 3 } zr_activation;
 typedef struct {
@@ -624,7 +624,7 @@ typedef struct {
 /* zr_mx4_matmul and zr_mx4_linear with an epilogue (host memory, read during the call; NULL for none).
  * K == 0 is a sum of nothing, which goes through the epilogue. Errors: theirs, and ZR_ERR_INVALID for an unknown
  * activation, a bad bias_dtype, a row stride under N, a misaligned pointer, a gradient without pre
- * or with bias or residual, matrices that overlap. */
+ * or with bias or residual, matrices that overlap (zr_mx4_linear_finish: x as well). */
 zr_status zr_mx4_matmul_finish(const void* a, int64_t M, const void* b, int64_t N, int64_t K, void* out, zr_dtype dt,
                                int64_t ldo, const zr_mx4_epilogue* epilogue, void* stream);
 zr_status zr_mx4_linear_finish(const void* x, zr_dtype xdt, int64_t M, int64_t ldx, const void* w, int64_t N, int64_t K,

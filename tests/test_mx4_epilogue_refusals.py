@@ -58,6 +58,19 @@ def test_epilogues(L, call):
     assert call(L, epilogue(), m=0, a=None) == 0
 
 
+def test_tokens_in_the_place_of_results(L):
+    """x as the residual and the output of one call: few tokens would be read after other blocks had replaced them."""
+    refused(L, linear(L, epilogue(residual=OUT), a=OUT), "overlaps x")
+    refused(L, linear(L, epilogue(), a=OUT + 16), "overlaps x")
+    refused(L, linear(L, epilogue(pre=1 << 22), a=(1 << 22) - 16), "overlaps x")
+    # rows of 32 bytes of out between rows of 128 bytes of tokens (no weights then), and too near to either end
+    def between(out):
+        return L.zr_mx4_linear_finish(OUT, 2, M, 40, None, N, K, out, 2, 40, None, ctypes.byref(epilogue()), None)
+    refused(L, between(OUT + 128), "null")
+    refused(L, between(OUT + 112), "overlaps x")
+    refused(L, between(OUT + 144), "overlaps x")
+
+
 def test_column_sums(L):
     c = L.zr_column_sums
     refused(L, c(16, 7, 4, 8, 8, 16, None), "dtype")

@@ -774,7 +774,7 @@ def mx4_linear(x, w: Mx4, out, xq: Optional[Mx4] = None, stream=None, *, bias=No
     """out[M, N] = x[M, K] w[N, K]^T with x quantised in the call (zr_mx4_linear); more than MX4_FEW tokens need xq,
     a buffer that holds the quantised x then (for fewer it is a workspace, whose contents say nothing). With any of
     the keywords out = act(h) + residual, h = x w^T + bias, and h is stored to `pre` if given (zr_mx4_linear_finish;
-    as in mx4_matmul)."""
+    as in mx4_matmul); `residual` may be x, but neither out nor `pre` may share memory with it."""
     name = "zr_mx4_linear"
     plain = bias is None and activation is None and residual is None and pre is None
     if not plain:

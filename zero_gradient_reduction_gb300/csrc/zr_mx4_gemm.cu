@@ -10,7 +10,7 @@
 // without a pause, is 9.9 in steps of K = 64, the ones used here), 8192 x 50304 x 2048 in 250 us (6.7).
 // Both are bursts; back to back for seconds the power limit lowers the clock, to 1.67 GHz for the
 // latter, which takes 281 us then. There the tensor pipe is active 72 % of the cycles, and counters say
-// that shared memory is not what the rest waits for: of a stage's 703 cycles the tensor cores' reads
+// that shared memory is not what the rest waits for: of a stage's 703 to 709 cycles the tensor cores' reads
 // take 280 (16 KB of A, 16 KB of B, of which a pair's block holds half, and 3 KB of scales), and the
 // banks are at 24 % of their rate for reads and at 24 % for writes. What it is has not been settled; the
 // scales' copies, to columns that the stage before still reads, cannot overlap its products. Blocks
@@ -1183,15 +1183,21 @@ zr_status launch_few(const char* what, const FewArgs& g, const FinishOf<EPI>& e,
   return ZR_OK;
 }
 
-// Whether two matrices of M x N values of `es` bytes share memory: rows as far apart may lie between each other's.
-bool overlap(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t M, int64_t N, int es) {
-  const __int128 x = (__int128)reinterpret_cast<uintptr_t>(a), y = (__int128)reinterpret_cast<uintptr_t>(b);
-  const __int128 row = (__int128)N * es, ends_a = x + (__int128)(M - 1) * lda * es + row,
-                 ends_b = y + (__int128)(M - 1) * ldb * es + row;
-  if (y >= ends_a || x >= ends_b) return false;
-  if (lda != ldb || M == 1) return true;
-  const __int128 ld = (__int128)lda * es, apart = ((y - x) % ld + ld) % ld;
-  return apart < row || ld - apart < row;
+// M rows of so many values of `es` bytes, one to `ld` values.
+struct Rows {
+  const void* at;
+  int64_t ld, cols;
+  int es;
+};
+// Whether two matrices share memory: rows as far apart may lie between each other's.
+bool overlap(const Rows& a, const Rows& b, int64_t M) {
+  const __int128 x = (__int128)reinterpret_cast<uintptr_t>(a.at), y = (__int128)reinterpret_cast<uintptr_t>(b.at);
+  const __int128 row_a = (__int128)a.cols * a.es, row_b = (__int128)b.cols * b.es, ld = (__int128)a.ld * a.es,
+                 ld_b = (__int128)b.ld * b.es;
+  if (y >= x + (M - 1) * ld + row_a || x >= y + (M - 1) * ld_b + row_b) return false;
+  if (ld != ld_b || M == 1) return true;
+  const __int128 apart = ((y - x) % ld + ld) % ld;
+  return apart < row_a || ld - apart < row_b;
 }
 
 // Refuses what an epilogue may not be; `e` may be null.
@@ -1210,7 +1216,7 @@ zr_status check_epilogue(const char* what, const zr_mx4_epilogue* e, int64_t M, 
     return fail(ZR_ERR_INVALID, "%s: a pointer of the epilogue is not 16-byte aligned", what);
   if (M == 0 || N == 0) return ZR_OK;
   auto clash = [&](const void* p, int64_t ld, const void* q, int64_t ldq, bool may_be) {
-    return p && q && !(may_be && p == q && ld == ldq) && overlap(p, ld, q, ldq, M, N, es);
+    return p && q && !(may_be && p == q && ld == ldq) && overlap({p, ld, N, es}, {q, ldq, N, es}, M);
   };
   if (clash(e->residual, e->ldr, out, ldo, true) || clash(e->pre, e->ldp, out, ldo, e->gradient != 0) ||
       clash(e->pre, e->ldp, e->residual, e->ldr, false))
@@ -1309,6 +1315,13 @@ zr_status checked_linear(const char* what, const void* x, zr_dtype xdt, int64_t 
   if (ldx < K || ldo < N) return fail(ZR_ERR_INVALID, "%s: a row stride is under the row", what);
   if (zr_status st = check_epilogue(what, epilogue, M, N, out, dt, ldo)) return st;
   if (M == 0 || N == 0) return ZR_OK;
+  if constexpr (EPI) {
+    // Few tokens are read by blocks that others are ahead of, whose results would be in their place.
+    const int es = dt == ZR_F32 ? 4 : 2;
+    const Rows tokens{x, ldx, K, xdt == ZR_F32 ? 4 : 2};
+    if (x && K > 0 && ((out && overlap(tokens, {out, ldo, N, es}, M)) || (epilogue->pre && overlap(tokens, {epilogue->pre, epilogue->ldp, N, es}, M))))
+      return fail(ZR_ERR_INVALID, "%s: out or pre overlaps x", what);
+  }
   if (!out || (K > 0 && (!x || !w))) return fail(ZR_ERR_INVALID, "%s: null pointer", what);
   if (!zr::aligned16(x) || !zr::aligned16(w) || !zr::aligned16(out) || !zr::aligned16(xq))
     return fail(ZR_ERR_INVALID, "%s: a pointer is not 16-byte aligned", what);

@@ -266,7 +266,8 @@ zr_status launch(PreferenceArgs& a, int sms, cudaStream_t s) {
         : r.split == 4 ? zr::launch(score_kernel<DT, 4>, a.T * 4, r.threads, 0, 4, true, s, a)
         : r.split == 2 ? zr::launch(score_kernel<DT, 2>, a.T * 2, r.threads, 0, 2, true, s, a)
                        : zr::launch(score_kernel<DT, 1>, a.T, r.threads, 0, 1, true, s, a);
-  if (e == cudaSuccess) e = zr::launch(pair_kernel, a.sequences / 2, kPairThreads, 0, 1, true, s, a);
+  // (behind a call's own sums it begins early: what it reads before it waits for them was there before the call)
+  if (e == cudaSuccess) e = zr::launch(pair_kernel, a.sequences / 2, kPairThreads, 0, 1, a.T > 0, s, a);
   if (e == cudaSuccess && a.grad && a.T > 0)
     e = zr::launch(gradient_kernel<DT>, a.T * r.split, r.threads, 0, 1, true, s, a);
   if (e != cudaSuccess) return fail(ZR_ERR_CUDA, "zr_preference_loss: launch failed: %s", cudaGetErrorString(e));
