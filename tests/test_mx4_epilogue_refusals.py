@@ -122,6 +122,30 @@ def test_the_binding(calls, call):
     assert not calls
 
 
+def test_the_epilogue_that_the_binding_passes(calls):
+    fn, makers = operands("matmul")
+    good = {k: make(0) for k, make in makers.items()}
+    fn(**good, activation="silu")
+    e = zr.Epilogue.from_buffer_copy(calls.pop()[1][8])
+    assert (e.bias, e.residual, e.pre, e.ldr, e.ldp, e.activation, e.gradient) == (*(good[k].data_ptr() for k in ("bias", "residual", "pre")), N, N, 3, 0)
+    assert e.bias_dtype == zr._types[good["bias"].dtype]
+    fn(good["a"], good["b"], good["out"], gradient_of="relu", pre=good["pre"])
+    e = zr.Epilogue.from_buffer_copy(calls.pop()[1][8])
+    assert (e.bias, e.residual, e.pre, e.ldr, e.ldp, e.activation, e.gradient) == (None, None, good["pre"].data_ptr(), 0, N, 1, 1)
+
+
+def test_a_gradient_of_no_rows(calls):
+    """Matrices without values have no address, which would read as a gradient without pre."""
+    zr.mx4_matmul(mx4(0, K, 0), mx4(N, K, 0), Tensor((0, N)), gradient_of="relu", pre=Tensor((0, N)))
+    assert not calls
+
+
+def test_what_the_binding_packs_is_what_the_library_reads(L):
+    packed = zr._pack_epilogue(0, 0, 0, N, N, 2, 4, 0)
+    refused(L, L.zr_mx4_matmul_finish(16, M, 16, N, K, OUT, 2, N, packed, None), "activation 4")
+    refused(L, L.zr_mx4_matmul_finish(16, M, 16, N, K, OUT, 2, N, zr._pack_epilogue(0, 0, OUT + 16, 0, N, 2, 1, 1), None), "overlap")
+
+
 def test_gradients_through_the_binding(calls):
     fn, makers = operands("matmul")
     good = {k: makers[k](0) for k in ("a", "b", "out", "pre")}

@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes
 import dataclasses
 import os
+import struct
 import threading
 from typing import List, Optional, Sequence
 
@@ -141,9 +142,8 @@ def lib():
                 "zr_mx4_dequantize": (st, [vp, i64, i64, vp, i32, i64, vp]),
                 "zr_mx4_matmul": (st, [vp, i64, vp, i64, i64, vp, i32, i64, vp]),
                 "zr_mx4_linear": (st, [vp, i32, i64, i64, vp, i64, i64, vp, i32, i64, vp, vp]),
-                "zr_mx4_matmul_finish": (st, [vp, i64, vp, i64, i64, vp, i32, i64, ctypes.POINTER(Epilogue), vp]),
-                "zr_mx4_linear_finish": (st, [vp, i32, i64, i64, vp, i64, i64, vp, i32, i64, vp, ctypes.POINTER(Epilogue),
-                                              vp]),
+                "zr_mx4_matmul_finish": (st, [vp, i64, vp, i64, i64, vp, i32, i64, vp, vp]),
+                "zr_mx4_linear_finish": (st, [vp, i32, i64, i64, vp, i64, i64, vp, i32, i64, vp, vp, vp]),
                 "zr_column_sums": (st, [vp, i32, i64, i64, i64, vp, vp]),
                 "zr_mx4_status": (st, [vp]),
                 "zr_mx4_stall_waits": (st, [i32]),
@@ -728,20 +728,23 @@ def _beside(what: str, name: str, t, out, device: int):
     return p, ld
 
 
-def _epilogue(what: str, out, cols: int, device: int, bias, activation, residual, pre, gradient: int):
-    """zr_mx4_epilogue of a product's keywords, by reference; their tensors are on the output's device."""
+_pack_epilogue = struct.Struct("PPPqqiii4x").pack  # Epilogue's bytes, in a fifth of the time
+
+
+def _epilogue(what: str, out, cols: int, device: int, bias, activation, residual, pre, gradient: int) -> bytes:
+    """zr_mx4_epilogue of a product's keywords; their tensors are on the output's device."""
     act = ACTIVATIONS.get(activation)
     if act is None:
         _refuse(f"{what}: activation must be one of {sorted(k for k in ACTIVATIONS if k)} or None, not {activation!r}")
-    r, ldr = (None, 0) if residual is None else _beside(what, "residual", residual, out, device)
-    h, ldp = (None, 0) if pre is None else _beside(what, "pre", pre, out, device)
-    b, dt = None, 0
+    r, ldr = (0, 0) if residual is None else _beside(what, "residual", residual, out, device)
+    h, ldp = (0, 0) if pre is None else _beside(what, "pre", pre, out, device)
+    b, dt = 0, 0
     if bias is not None:
         dt = _types.get(bias.dtype)
         if bias.get_device() != device or dt is None or bias.numel() != cols or not bias.is_contiguous():
             _misplaced(bias, f"{what}: bias", "fp32, fp16 or bf16", cols, device)
         b = bias.data_ptr()
-    return ctypes.byref(Epilogue(b, r, h, ldr, ldp, dt, act, gradient))
+    return _pack_epilogue(b, r, h, ldr, ldp, dt, act, gradient)
 
 
 def mx4_matmul(a: Mx4, b: Mx4, out, stream=None, *, bias=None, activation=None, residual=None, pre=None,
@@ -766,6 +769,8 @@ def mx4_matmul(a: Mx4, b: Mx4, out, stream=None, *, bias=None, activation=None, 
         _refuse("mx4_matmul: an activation and a gradient of one")
     e = _epilogue("mx4_matmul", out, cols, device, bias, gradient_of if gradient_of is not None else activation,
                   residual, pre, int(gradient_of is not None))
+    if rows == 0 or cols == 0:  # a `pre` without values has no address
+        return
     _check(fn(a.ptr, rows, b.ptr, cols, a.cols, p, dt, ld, e, s))
 
 
