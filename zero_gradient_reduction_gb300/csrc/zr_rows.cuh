@@ -412,7 +412,10 @@ __device__ __forceinline__ Pair log_chosen(float z, float rest, const Base& base
   const float e = exp2_fast(base.exponent<FINE>(z, k));
   if (rest < e) return Pair{-log1pf(__fdiv_rn(rest, e)), 0.0f};
   const Pair log_sum = log_pair(rest + e);
-  if (!(z > -1e30f)) return Pair{z - log_sum.value, 0.0f};  // masked, or no number
+  // So far under the maximum that the logarithm is nothing beside the difference, masked, or no number; halves, because
+  // the difference of two that are far from zero may have no number of 32 bits where its share of tau has one.
+  if (!(z - base.m > -1e30f))
+    return Pair{__fdiv_rn(0.5f * z - 0.5f * base.m, 0.5f * k.tau) - log_sum.value, 0.0f};
   const float short_of = log_sum.rest + kShort;
   if (!(FINE && base.fine)) {
     const Pair d = exact_sum(__fdiv_rn(z - base.m, k.tau), -log_sum.value);
