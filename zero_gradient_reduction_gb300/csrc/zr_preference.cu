@@ -159,12 +159,14 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constan
   if (tid != 0) return;
   if (a.rewards) a.rewards[2 * pair] = reward[0], a.rewards[2 * pair + 1] = reward[1];
   const float w = a.weight ? a.weight[pair] : 1.0f, m = reward[0] - reward[1];
-  // the logistic function on both sides, and the loss -log s(m) + l m from the side that does not cancel
+  // the logistic function on both sides, and the loss -log s(m) + l m = log(1 + e^-|m|) + |m| times l, or 1 - l where m < 0:
+  // nothing cancels, and a share of nothing is nothing where the margin is infinite
   const float e = expf(-fabsf(m)), small = __fdiv_rn(e, 1.0f + e), large = __fdiv_rn(1.0f, 1.0f + e);
   const float up = m >= 0.0f ? large : small, down = m >= 0.0f ? small : large;
-  const float soft = log1pf(e) + fmaxf(-m, 0.0f);
+  const float share = m >= 0.0f ? a.smoothing : 1.0f - a.smoothing;
+  const float value = log1pf(e) + (share > 0.0f ? __fmul_rn(share, fabsf(m)) : 0.0f);
   const float scale = a.loss_scale ? __fmul_rn(a.grad_scale, *a.loss_scale) : a.grad_scale;
-  a.loss[pair] = w == 0.0f ? 0.0f : __fmul_rn(w, a.smoothing > 0.0f ? soft + __fmul_rn(a.smoothing, m) : soft);
+  a.loss[pair] = w == 0.0f ? 0.0f : __fmul_rn(w, value);
   const float f = __fmul_rn(__fmul_rn(w, a.beta),
                             __fmul_rn(__fdiv_rn(scale, a.scale.tau), (1.0f - a.smoothing) * down - a.smoothing * up));
   a.slope[2 * pair] = -f;
