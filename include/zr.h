@@ -736,8 +736,8 @@ int64_t zr_preference_bytes(int64_t T, int64_t pairs);
  *   grad[t][v] = s f (1[v = a] - q_v) / temperature,  s = grad_scale and plan.
  * starts: device int32[2 pairs + 1] (int64 with starts64), ascending within [0, T]; a sequence may
  * be empty, its reward is 0. Rows before the first sequence and behind the last are left as they are, in
- * the gradient too. A pair whose own starts do not ascend within [0, T] has loss and rewards NaN; if
- * any do not, the gradient says nothing, but no call reads or writes outside the arrays.
+ * the gradient too. A pair whose own starts do not ascend within [0, T] has loss and rewards NaN (0 where
+ * its weight is 0); if any do not, the gradient says nothing, but no call reads or writes outside the arrays.
  * ref_logp: fp32[T]; weight: fp32[pairs] or NULL (all 1); loss: fp32[pairs]; rewards:
  * fp32[2 pairs] or NULL, written. Rows that are not scored have gradient 0. A pair of weight 0 has loss,
  * rewards and gradients 0, and its rows are not read. Where a scored row's logp is NaN so are

@@ -70,3 +70,15 @@ def test_a_margin_that_is_no_number_stays_so():
         near_ref[0] = NAN
         loss, _, _ = run(z, ids, [0, 1, 2, 3, 4], near_ref, smoothing=smoothing)
         assert torch.isnan(loss).tolist() == [True, False]
+
+
+def test_a_pair_that_does_not_count_says_nothing_of_its_starts():
+    """Weight 0 goes before starts that do not ascend, for the loss and the rewards alike; the other pairs are as they were."""
+    z, ids = ref.logits(9, 30, F32, torch.Generator().manual_seed(4))
+    near_ref = torch.zeros(9, device="cuda")
+    for bad in ([5, 3, 5], [-1, 0, 5], [0, 40, 5]):
+        for weight in ([0.0, 1.0], [1.0, 1.0], [0.0, 0.0]):
+            loss, r, _ = run(z, ids, [*bad, 7, 9], near_ref, weight=torch.tensor(weight, device="cuda"))
+            want = 0.0 if weight[0] == 0 else NAN
+            assert all(np.array_equal(float(v), want, equal_nan=True) for v in (loss[0], r[0], r[1])), (bad, weight, loss, r)
+            assert bool(torch.isfinite(loss[1])) and bool(torch.isfinite(r[2:]).all()) and (float(loss[1]) > 0) == (weight[1] > 0)

@@ -146,6 +146,7 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constan
   }
   __syncthreads();
   if (tid >= 32) return;
+  const float w = a.weight ? a.weight[pair] : 1.0f;
   float reward[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -154,11 +155,11 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constan
     for (int o = kPairThreads / 64; o; o >>= 1) s = across(s, o);
     // (where one is infinite or no number so is the first word, and the second says nothing)
     const float whole = s.value - s.value == 0.0f ? __fmaf_rn(a.beta, s.rest, __fmul_rn(a.beta, s.value)) : __fmul_rn(a.beta, s.value);
-    reward[i] = sound ? whole : NAN;
+    reward[i] = w == 0.0f ? 0.0f : sound ? whole : NAN;  // (a pair that does not count says nothing of its starts either)
   }
   if (tid != 0) return;
   if (a.rewards) a.rewards[2 * pair] = reward[0], a.rewards[2 * pair + 1] = reward[1];
-  const float w = a.weight ? a.weight[pair] : 1.0f, m = reward[0] - reward[1];
+  const float m = reward[0] - reward[1];
   // the logistic function on both sides, and the loss -log s(m) + l m = log(1 + e^-|m|) + |m| times l, or 1 - l where m < 0:
   // nothing cancels, and a share of nothing is nothing where the margin is infinite
   const float e = expf(-fabsf(m)), small = __fdiv_rn(e, 1.0f + e), large = __fdiv_rn(1.0f, 1.0f + e);
