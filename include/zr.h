@@ -703,8 +703,9 @@ zr_status zr_distill_topk(const void* logits, zr_dtype dt, int64_t T, int64_t V,
  * them; ZR_ERR_UNSUPPORTED for more rows than a launch takes (2^31 / 8 are always taken). */
 
 /* logp: device fp32[T], 0 in rows that are not scored. entropy: device fp32[T] or NULL, the
- * entropy -sum q log q of each scored row, NaN where the row has no answer (a masked choice has one).
- * One read of the scored rows. */
+ * entropy -sum q log q of each scored row, NaN where the row has no answer (a masked choice has one). It is
+ * never under 0; where the chosen token has most of q its error is relative, elsewhere that of fp32 sums
+ * of the size of 1 + log V. One read of the scored rows. */
 zr_status zr_token_logprobs(const void* logits, zr_dtype dt, int64_t T, int64_t V, int64_t ldz, const void* ids,
                             int ids64, float temperature, float* logp, float* entropy, void* stream);
 

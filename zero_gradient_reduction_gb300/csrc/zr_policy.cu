@@ -74,8 +74,20 @@ __global__ void __launch_bounds__(384, 4) logprob_kernel(const __grid_constant__
     const zr::Pair logp = zr::log_chosen<!ENTROPY>(z_chosen, rest, base, a.scale);
     a.logp[row] = id < a.V ? logp.value + logp.rest : NAN;
     if (ENTROPY) {
-      zr::add_term<false, true>(all, base, a.scale, z_chosen);
-      a.entropy[row] = id < a.V ? __fmul_rn(zr::kLn2, log2f(all.sum) - __fdiv_rn(all.ex, all.sum)) : NAN;
+      // log sum less the mean exponent: two numbers of up to 1 in size where one token has nearly everything, so that what
+      // rounding leaves of a smaller entropy may be under 0. Where it is the chosen one, e of its own against the
+      // `rest`, the same without the difference: log(1 + rest/e) and how far the others' exponents lie under its own.
+      const float x = base.exponent<false>(z_chosen, a.scale), e = zr::exp2_fast(x);
+      float entropy;
+      if (rest < e) {
+        const float under = fmaxf(__fmaf_rn(x, rest, -all.ex), 0.0f);
+        entropy = __fmaf_rn(zr::kLn2, __fdiv_rn(under, __fadd_rn(rest, e)), log1pf(__fdiv_rn(rest, e)));
+      } else {
+        zr::add_term<false, true>(all, base, a.scale, z_chosen);
+        entropy = __fmul_rn(zr::kLn2, log2f(all.sum) - __fdiv_rn(all.ex, all.sum));
+        entropy = entropy < 0.0f ? 0.0f : entropy;  // (no number stays so)
+      }
+      a.entropy[row] = id < a.V ? entropy : NAN;
     }
   }
 }
