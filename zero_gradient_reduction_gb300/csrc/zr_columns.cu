@@ -13,6 +13,7 @@
 #include "zr_internal.h"
 #include "zr_launch.h"
 #include "zr_nvtx.h"
+#include "zr_rows.cuh"
 #include "zr_tensor.cuh"
 
 using zr::fail;
@@ -57,15 +58,15 @@ __global__ void __launch_bounds__(kThreads) column_kernel(const __grid_constant_
   const int64_t step = a.ld * es * kRows;
   const char* from = x + (first + r0) * a.ld * es;
   int64_t r = first + r0;
-  if (PER > 1 && left == PER) {
+  if (PER > 1 && left == PER) {  // (not by the read-only path: the launch before may have written x since this one began)
     for (; r + (kOnce - 1) * kRows < end; r += kOnce * kRows, from += kOnce * step) {
       uint4 u[kOnce];
 #pragma unroll
-      for (int i = 0; i < kOnce; ++i) u[i] = zr::ld_once(from + i * step);
+      for (int i = 0; i < kOnce; ++i) u[i] = zr::ld_row(from + i * step);
 #pragma unroll
       for (int i = 0; i < kOnce; ++i) open(u[i]);
     }
-    for (; r < end; r += kRows, from += step) open(zr::ld_once(from));
+    for (; r < end; r += kRows, from += step) open(zr::ld_row(from));
   } else if (left > 0) {
     for (; r + (kOnce - 1) * kRows < end; r += kOnce * kRows, from += kOnce * step) {
       float v[kOnce][PER];

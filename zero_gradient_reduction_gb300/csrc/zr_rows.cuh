@@ -14,8 +14,9 @@ namespace zr {
 
 constexpr float kLog2E = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
 
-// Not the read-only path: the gradient may replace the logits.
-__device__ __forceinline__ uint4 ld_row(const uint4* p) {
+// Not the read-only path: the gradient may replace the logits, and a launch that begins early may find them still being
+// written. Nor is it moved across a wait.
+__device__ __forceinline__ uint4 ld_row(const void* p) {
   uint4 r;
   asm volatile("ld.global.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
