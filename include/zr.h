@@ -632,8 +632,8 @@ zr_status zr_mx4_linear_finish(const void* x, zr_dtype xdt, int64_t M, int64_t l
                                void* stream);
 
 /* out[n] = sum over m of x[m][n]: a bias's gradient from its layer's output gradient. x: device,
- * M x N of type dt, row stride ldx; out: device fp32[N]. Sums are fp32, in an order that the sizes decide. M == 0
- * gives zeros. Errors: ZR_ERR_INVALID for a bad dtype, negative sizes, ldx under N, null or
+ * M x N of type dt, row stride ldx; out: device fp32[N]. Eight rows are added in fp32, their sums in two words
+ * of it, in an order that the sizes decide: the number of rows costs no accuracy. M == 0 gives zeros. Errors: ZR_ERR_INVALID for a bad dtype, negative sizes, ldx under N, null or
  * misaligned pointers (x on a 16-byte boundary, out on one of its type). */
 zr_status zr_column_sums(const void* x, zr_dtype dt, int64_t M, int64_t N, int64_t ldx, float* out, void* stream);
 

@@ -114,12 +114,8 @@ __global__ void __launch_bounds__(384, 4) score_kernel(const __grid_constant__ P
 // ---- each pair's rewards, loss and slope: a block to a pair
 // Sums in two words of 32 bits: a sequence's thousands of ratios would lose to one, and 64 bits are slow here (8 us a
 // pair of 512 rows, most of them in a few dozen additions).
-__device__ __forceinline__ zr::Pair plus(zr::Pair a, zr::Pair b) {
-  const zr::Pair s = zr::exact_sum(a.value, b.value);
-  return zr::Pair{s.value, s.rest + (a.rest + b.rest)};
-}
 __device__ __forceinline__ zr::Pair across(zr::Pair a, int lanes) {
-  return plus(a, zr::Pair{__shfl_xor_sync(0xFFFFFFFFu, a.value, lanes), __shfl_xor_sync(0xFFFFFFFFu, a.rest, lanes)});
+  return zr::plus(a, zr::Pair{__shfl_xor_sync(0xFFFFFFFFu, a.value, lanes), __shfl_xor_sync(0xFFFFFFFFu, a.rest, lanes)});
 }
 constexpr int kPairThreads = 256;
 __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constant__ PreferenceArgs a) {
@@ -136,7 +132,7 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constan
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll 4
-      for (int64_t r = at[i] + tid; r < at[i + 1]; r += kPairThreads) sum[i] = plus(sum[i], zr::Pair{a.ratio[r], 0.0f});
+      for (int64_t r = at[i] + tid; r < at[i + 1]; r += kPairThreads) sum[i] = zr::plus(sum[i], zr::Pair{a.ratio[r], 0.0f});
   }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {

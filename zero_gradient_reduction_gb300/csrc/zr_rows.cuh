@@ -380,6 +380,10 @@ __device__ __forceinline__ Pair exact_sum(float a, float b) {
   const float s = a + b, t = s - a;
   return Pair{s, (a - (s - t)) + (b - t)};
 }
+__device__ __forceinline__ Pair plus(Pair a, Pair b) {
+  const Pair s = exact_sum(a.value, b.value);
+  return Pair{s.value, s.rest + (a.rest + b.rest)};
+}
 
 // ln s in two words: with s = 2^k f and t = (f - 1)/(f + 1), k ln 2 + 2 (t + t^3/3 + t^5/5 + ...), of which k ln 2
 // and 2 t are taken to twice 24 bits. One number's last half unit would be much the same for rows of much the
