@@ -753,15 +753,18 @@ def mx4_matmul(a: Mx4, b: Mx4, out, stream=None, *, bias=None, activation=None, 
     (zr_mx4_matmul_finish): out = act(h) + residual with h = a b^T + bias, stored to `pre` if given; or, with
     `gradient_of` naming an activation, out = a b^T times that activation's derivative at `pre`. `residual`, or the
     `pre` of a gradient, may be `out`. Activations: "relu", "gelu" (in its tanh form), "silu"."""
-    name = "zr_mx4_matmul"
     plain = bias is None and activation is None and residual is None and pre is None and gradient_of is None
-    if not plain:
-        name = "zr_mx4_matmul_finish"
-    fn = _fns.get(name) or _fn(name)
+    if plain:
+        fn = _fns.get("zr_mx4_matmul") or _fn("zr_mx4_matmul")
+    else:
+        fn = _fns.get("zr_mx4_matmul_finish") or _fn("zr_mx4_matmul_finish")
     p, rows, cols, ld, dt, device = _matrix(out, "out")
     if a.cols != b.cols or a.rows != rows or b.rows != cols:
         _refuse(f"mx4_matmul: a is {a.rows} x {a.cols}, b {b.rows} x {b.cols}, out {rows} x {cols}")
-    s = _stream_of(stream, device, a.device, b.device)
+    if stream is None and a.device == device and b.device == device and _fns["device"]() == device:  # _stream_of, in line
+        s = _fns["stream"](device)
+    else:
+        s = _stream_of(stream, device, a.device, b.device)
     if plain:
         _check(fn(a.ptr, rows, b.ptr, cols, a.cols, p, dt, ld, s))
         return
@@ -780,18 +783,22 @@ def mx4_linear(x, w: Mx4, out, xq: Optional[Mx4] = None, stream=None, *, bias=No
     a buffer that holds the quantised x then (for fewer it is a workspace, whose contents say nothing). With any of
     the keywords out = act(h) + residual, h = x w^T + bias, and h is stored to `pre` if given (zr_mx4_linear_finish;
     as in mx4_matmul); `residual` may be x, but neither out nor `pre` may share memory with it."""
-    name = "zr_mx4_linear"
     plain = bias is None and activation is None and residual is None and pre is None
-    if not plain:
-        name = "zr_mx4_linear_finish"
-    fn = _fns.get(name) or _fn(name)
+    if plain:
+        fn = _fns.get("zr_mx4_linear") or _fn("zr_mx4_linear")
+    else:
+        fn = _fns.get("zr_mx4_linear_finish") or _fn("zr_mx4_linear_finish")
     p, rows, k, ldx, xdt, x_device = _matrix(x, "x")
     o, m, n, ldo, dt, device = _matrix(out, "out")
     if w.cols != k or m != rows or w.rows != n:
         _refuse(f"mx4_linear: x is {rows} x {k}, w {w.rows} x {w.cols}, out {m} x {n}")
     if xq is not None and (xq.rows != rows or xq.cols != k):
         _refuse(f"mx4_linear: xq is {xq.rows} x {xq.cols}, x {rows} x {k}")
-    s = _stream_of(stream, device, x_device, w.device, xq.device if xq is not None else device)
+    xq_device = device if xq is None else xq.device
+    if stream is None and x_device == w.device == xq_device == device == _fns["device"]():  # _stream_of, in line
+        s = _fns["stream"](device)
+    else:
+        s = _stream_of(stream, device, x_device, w.device, xq_device)
     if plain:
         _check(fn(p, xdt, rows, ldx, w.ptr, n, k, o, dt, ldo, xq and xq.ptr, s))
         return
