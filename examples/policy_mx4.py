@@ -102,6 +102,9 @@ class Network:
 
 def train(loss="policy", tokens=1024, dim=256, hidden=512, vocab=2000, steps=30, seed=0, report=print):
     """Mean reward, or mean loss, of each step."""
+    length = 16  # of a sequence of a pair
+    if loss == "preference" and tokens < 2 * length:
+        raise ValueError(f"a pair of sequences has {2 * length} tokens, not {tokens}")
     g = torch.Generator(device="cuda").manual_seed(seed)
     net, hyper = Network(tokens, dim, hidden, vocab, g), zr.AdamW(lr=1e-3, weight_decay=0.0)
     x = torch.randn(tokens, dim, generator=g, device="cuda").to(BF16)
@@ -110,7 +113,6 @@ def train(loss="policy", tokens=1024, dim=256, hidden=512, vocab=2000, steps=30,
     first = net.forward(x).clone()  # the reference's logits
     history = []
     if loss == "preference":
-        length = 16
         pairs = tokens // (2 * length)
         starts = torch.arange(0, 2 * pairs + 1, dtype=torch.int32, device="cuda") * length
         ids = torch.randint(0, vocab, (tokens,), generator=g, device="cuda")
