@@ -632,8 +632,9 @@ zr_status zr_mx4_linear_finish(const void* x, zr_dtype xdt, int64_t M, int64_t l
                                void* stream);
 
 /* out[n] = sum over m of x[m][n]: a bias's gradient from its layer's output gradient. x: device,
- * M x N of type dt, row stride ldx; out: device fp32[N]. Eight rows are added in fp32, their sums in two words
- * of it, in an order that the sizes decide: the number of rows costs no accuracy. M == 0 gives zeros. Errors: ZR_ERR_INVALID for a bad dtype, negative sizes, ldx under N, null or
+ * M x N of type dt, row stride ldx; out: device fp32[N]. Eight rows are added in fp32, their sums in two
+ * words of it, in an order that the sizes decide: the number of rows costs no accuracy. M == 0 gives
+ * zeros. Errors: ZR_ERR_INVALID for a bad dtype, negative sizes, ldx under N, null or
  * misaligned pointers (x on a 16-byte boundary, out on one of its type). */
 zr_status zr_column_sums(const void* x, zr_dtype dt, int64_t M, int64_t N, int64_t ldx, float* out, void* stream);
 
@@ -737,8 +738,9 @@ int64_t zr_preference_bytes(int64_t T, int64_t pairs);
  *   grad[t][v] = s f (1[v = a] - q_v) / temperature,  s = grad_scale and plan.
  * starts: device int32[2 pairs + 1] (int64 with starts64), ascending within [0, T]; a sequence may
  * be empty, its reward is 0. Rows before the first sequence and behind the last are left as they are, in
- * the gradient too. A pair whose own starts do not ascend within [0, T] has loss and rewards NaN (0 where
- * its weight is 0); if any do not, the gradient says nothing, but no call reads or writes outside the arrays.
+ * the gradient too (where that is the logits themselves, they stay logits). A pair whose own starts do
+ * not ascend within [0, T] has loss and rewards NaN (0 where its weight is 0); if any do not, the gradient
+ * says nothing, but no call reads or writes outside the arrays.
  * ref_logp: fp32[T]; weight: fp32[pairs] or NULL (all 1); loss: fp32[pairs]; rewards:
  * fp32[2 pairs] or NULL, written. Rows that are not scored have gradient 0. A pair of weight 0 has loss,
  * rewards and gradients 0, and its rows are not read. Where a scored row's logp is NaN so are

@@ -931,7 +931,7 @@ def preference_loss(logits, ids, starts, ref_logp, loss, work, grad=None, weight
     """The loss of each pair of sequences by beta times their log-probability ratios to ref_logp, and its gradient at
     the logits times grad_scale and the plan's loss scale (zr_preference_loss). Sequence s has the rows starts[s] to
     starts[s + 1] - 1, pair i prefers sequence 2 i to 2 i + 1; `work`: preference_bytes bytes, the call's own while it
-    runs; `grad` may be `logits`; `rewards` receives each sequence's reward."""
+    runs; `grad` may be `logits` (rows of no sequence keep what they hold); `rewards` receives each sequence's reward."""
     fn = _fns.get("zr_preference_loss") or _fn("zr_preference_loss")
     z, rows, vocab, ldz, dt, device = _matrix(logits, "logits")
     i, wide = _whole(ids, "preference_loss: ids", rows, device)

@@ -18,9 +18,11 @@
 // for the results. Few tokens: 1 x 2048 by 8192 x 2048 in 5.2 us, 8 x 2048 by 50304 x 2048 in 12.7 us,
 // 4.3 TB/s. With an epilogue (bias, activation, a stored h, a residual; or an activation's derivative) pairs
 // 8192 x 2048 -> 8192 to bf16: bias and GELU 58 us, with h stored 66, a residual 67, GELU's derivative 82, where the
-// product alone takes 46. Its bytes bind none of them (46 us at a copy's rate with h stored): the stores, twice
-// as many, meet the products' own reads of L2 (588 MB of operands), with five stages for six. K = 256 shows the
-// epilogue's arithmetic, 47 us with bias and GELU, 28 without: a reciprocal is eight cycles of a quarter SM, an
+// product alone takes 46. Its bytes bind none of them (46 us at a copy's rate with h stored), nor does any unit: the
+// tensor pipe is active 37 to 45 % of the cycles, L2 is at 40 to 48 % of its rate, the ALUs at a third of theirs. With K = 256, an
+// eighth of the operands, h stored still takes 58 us and GELU's derivative 72, so most of it is the epilogue's own chain, a
+// tensor-memory load, arithmetic and one staging buffer's stores after one another for each 32 columns. K = 256 shows its
+// arithmetic, too, 47 us with bias and GELU, 28 without: a reciprocal is eight cycles of a quarter SM, an
 // exponential four. (K = 2048 with A's rows kept in shared memory for a run of tiles read half as much and
 // was no faster, 294 us: its ring of 4 stages no longer covered a copy's latency.)
 #include <cuda.h>
@@ -179,7 +181,8 @@ template <bool PAIR, int EPI, int DT>
 struct Gemm {
   // With an epilogue sixteen warps bring the results out, four to the same lanes, a quarter of a tile's columns
   // each: its loads and exponentials would keep fewer longer than the products take (8192 x 2048 -> 8192 to bf16
-  // with bias, GELU and pre 67 us, 77 with eight of 64 columns).
+  // with bias, GELU and pre 67 us, 77 with eight of 64 columns). Eighteen warps have 96 registers a thread: blocks alone
+  // spill 96 to 136 bytes of them, a pair's form to fp32 that takes in a matrix 84, its others 8 at most.
   static constexpr int kOutWarps = EPI ? 16 : 4, kSides = kOutWarps / 4, kThreads = 64 + 32 * kOutWarps;
   static constexpr int kTiles = PAIR ? 2 : 1;                       // MX4 tiles along M and along N
   static constexpr int kRows = 128 * kTiles, kCols = 128 * kTiles;  // output tile
