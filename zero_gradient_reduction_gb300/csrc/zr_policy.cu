@@ -8,9 +8,9 @@
 //
 // A logit's bytes once, and for the loss its gradient's, bind both. Log-probabilities are summed as the rows
 // come, through registers, four words of a thread on their way together and six blocks of 256 threads on an SM
-// (the registers are held to 40 for that: 127 us at 8192 x 50304 bf16, 150 with the 56 that the compiler would
-// take): 6.5 TB/s; with entropies 136 us, the exponentials' arithmetic in the way. The policy loss holds a row
-// in shared memory between its sum and its gradient, 8192 x 50304 bf16 in 271 us, 6.1 TB/s, and 259 where a
+// (the registers are held to 40 for that: 128 us at 8192 x 50304 bf16, 150 with the 56 that the compiler would
+// take): 6.4 TB/s; with entropies 137 us, the exponentials' arithmetic in the way. The policy loss holds a row
+// in shared memory between its sum and its gradient, 8192 x 50304 bf16 in 270 us, 6.1 TB/s, and 258 where a
 // tenth of the rows carries no weight; shorter rows have as many at work as fit, 8192 x 8000 in 49 us, 1000 fp32
 // in 14. 11 x 50257 fp32, a cluster of 8 blocks to a row: 5.5 us, the cluster's two waits about 1 each.
 #include <cuda_runtime.h>
